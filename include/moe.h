@@ -383,6 +383,190 @@ enum { MOE_TRACE_OFF = 0, MOE_TRACE_ALL = 1, MOE_TRACE_GEMM1 = 2 };
 moe_status moe_trace_enable(int32_t mode);
 moe_status moe_trace_read(float* stage_ms, int32_t nstages, int32_t* calls);
 
+/* ---------------------------------------------------------------- training
+ * The router of a layer whose experts stay packed can be trained, and
+ * low-rank adapters beside the layer can be trained and served.  With z the
+ * router's logits and w the routing weights of moe_route, a step runs:
+ *   moe_run_ws            forward (ids, w, y2 and slot_row stay in its
+ *                         workspace, see moe_ws_layout)
+ *   moe_router_loss       balance loss, z-loss and per-expert counts
+ *   moe_finalize_backward dw (and the gradient of the expert rows) from dout
+ *   moe_router_backward   dz from the losses and from dw
+ *
+ * Conventions as above: every call is asynchronous on `stream`, allocates and
+ * synchronises nothing, issues no memset and can be captured into a HIP
+ * graph; results are the same bits on every run.  Pointers are 16-byte
+ * aligned device pointers on the current device.  Outputs overlap no input
+ * unless stated. */
+
+/* Element types of the outputs that come in more than one. */
+typedef enum { MOE_T_BF16 = 0, MOE_T_F32 = 1 } moe_type;
+
+/* Workspace bytes of moe_router_loss for num_tokens tokens in num_seqs
+ * sequences.  Errors: MOE_ERR_INVALID_ARG for bad dims, num_tokens outside
+ * [0, 2^26], num_seqs outside [1, 65535] or a null output pointer. */
+moe_status moe_router_loss_query(const moe_dims* dims, int64_t num_tokens, int32_t num_seqs,
+                                 size_t* bytes);
+
+/* Losses of the router.  With p[t] the softmax of token t's logits over all
+ * experts and lse[t] their log-sum-exp; for sequence s with n_s tokens,
+ * c_s[e] how often they selected expert e and P_s[e] the mean of p[t, e]:
+ *   balance = mean over the sequences that have tokens of
+ *             sum_e (num_experts * c_s[e] / (top_k * n_s)) * P_s[e]
+ *   z       = mean over all tokens of lse[t]^2
+ * (balance is 1 where experts are used and expected evenly; 0 for no tokens).
+ *   router_logits: device float [num_tokens, num_experts]
+ *   ids:           device int32 [num_tokens, top_k], as moe_route writes them
+ *                  (ids outside [0, num_experts) are not counted)
+ *   seq_offsets:   device int32 [num_seqs + 1], ascending: sequence s is the
+ *                  tokens [seq_offsets[s], seq_offsets[s + 1]), and tokens
+ *                  before the first or behind the last count nowhere; null
+ *                  (num_seqs 1): one sequence of all tokens
+ *   token_mask:    device uint8 [num_tokens], 0 for a token that counts
+ *                  nowhere (padding; its logits may hold anything); or null
+ *   losses:        device float [2] out: balance, z
+ *   counts:        device int32 [num_seqs, num_experts] out: c_s
+ *   mean_probs:    device float [num_seqs, num_experts] out: P_s (0 without
+ *                  tokens)
+ *   seq_tokens:    device int32 [num_seqs + 2] out: n_s, then all tokens, then
+ *                  the sequences that have tokens
+ *   workspace:     device buffer of moe_router_loss_query bytes; needs no
+ *                  initialisation
+ * NaN logits rank as -inf as in moe_route; a token with no logit above -inf
+ * has p = 0 and lse = 0; a logit of +inf makes the losses NaN.  num_tokens = 0
+ * writes zeros.  Errors as moe_run_ws. */
+moe_status moe_router_loss(const moe_dims* dims, const float* router_logits, const int32_t* ids,
+                           int64_t num_tokens, int32_t top_k, const int32_t* seq_offsets,
+                           int32_t num_seqs, const uint8_t* token_mask, float* losses,
+                           int32_t* counts, float* mean_probs, int32_t* seq_tokens,
+                           void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Gradient of the logits from the losses of moe_router_loss (the counts held
+ * constant) and from the routing weights, the softmax over the selected
+ * logits; one pass.
+ *   router_logits, ids, seq_offsets, num_seqs, token_mask: as there
+ *   weights, dweights: device float [num_tokens, top_k], moe_route's weights
+ *                  and their gradient; dweights null: none from the weights
+ *   dlosses:       device float [2], gradient of (balance, z): the losses'
+ *                  coefficients; null: none from the losses
+ *   counts, seq_tokens: as moe_router_loss wrote them (with dlosses)
+ *   dlogits:       device float [num_tokens, num_experts] out.  Zero for
+ *                  masked tokens and for tokens with no logit above -inf; the
+ *                  rows of tokens in no sequence are left as they were
+ * dlogits may be router_logits.  num_tokens = 0 returns MOE_OK without
+ * launching.  Errors as moe_run_ws, and MOE_ERR_INVALID_ARG when both
+ * gradients are null. */
+moe_status moe_router_backward(const moe_dims* dims, const float* router_logits,
+                               const int32_t* ids, int64_t num_tokens, int32_t top_k,
+                               const int32_t* seq_offsets, int32_t num_seqs,
+                               const uint8_t* token_mask, const float* weights,
+                               const float* dweights, const float* dlosses, const int32_t* counts,
+                               const int32_t* seq_tokens, float* dlogits, hipStream_t stream);
+
+/* Gradient of the layer's last step, out[t] = sum_j weights[t, j] *
+ * y2[slot_row[t, j]]:
+ *   dweights[t, j] = <dout[t], y2[slot_row[t, j]]>
+ *   dy2[slot_row[t, j]] = weights[t, j] * dout[t]
+ *   dout:     device bf16 bits [num_tokens, hidden]
+ *   weights, y2, slot_row: topk_w, y2 and slot_row of a moe_run_ws workspace
+ *             (slot_row entries outside [0, num_tokens * top_k) are left out,
+ *             their dweights 0)
+ *   dweights: device float [num_tokens, top_k] out
+ *   dy2:      device out [num_tokens * top_k, hidden], float or bf16 bits by
+ *             dy2_type (moe_type; rounded once, to nearest even), or null when
+ *             not wanted; float dy2 may be y2
+ * num_tokens = 0 returns MOE_OK without launching.  Errors as moe_run_ws. */
+moe_status moe_finalize_backward(const moe_dims* dims, const void* dout, int64_t num_tokens,
+                                 int32_t top_k, const float* weights, const float* y2,
+                                 const int32_t* slot_row, float* dweights, void* dy2,
+                                 int32_t dy2_type, hipStream_t stream);
+
+/* ---------------------------------------------------------------- adapters
+ * Low-rank adapters of many requests beside one projection: token t with
+ * adapter a adds scale[a] * (x[t] A_a^T) B_a to what the projection gave.  The
+ * projection may be the layer (x = hidden, out = the layer's bf16 output) or
+ * the router (out = its float logits).  A is bf16 [num_adapters, rank,
+ * in_features], B bf16 [num_adapters, rank, out_features]: the rank comes first
+ * in both (B is the transpose of the usual [out_features, rank]).  An adapter
+ * of a smaller rank has zero rows behind its own.
+ *
+ * A plan groups a batch's tokens by adapter.  It depends on the adapter ids
+ * alone, so one plan serves every projection of every layer, and the backward
+ * pass.  1 <= num_adapters <= 1023, 1 <= rank <= 128, features multiples of 8
+ * up to 2^20, num_tokens up to 2^26. */
+typedef struct {
+  int32_t num_adapters;
+  int32_t rank;
+  int32_t in_features;
+  int32_t out_features;
+  int32_t out_type; /* moe_type of base, out and dout */
+} moe_adapter_dims;
+
+moe_status moe_adapter_plan_query(int32_t num_adapters, int64_t num_tokens, size_t* bytes);
+
+/*   adapter_ids: device int32 [num_tokens]; ids outside [0, num_adapters) mean
+ *                no adapter
+ *   plan:        device buffer of moe_adapter_plan_query bytes, opaque
+ * The order of a group's rows is the order of its tokens.  num_tokens = 0
+ * returns MOE_OK without launching (the calls below then read no plan). */
+moe_status moe_adapter_plan(int32_t num_adapters, const int32_t* adapter_ids, int64_t num_tokens,
+                            void* plan, size_t plan_bytes, hipStream_t stream);
+
+/* Bytes of the workspace of moe_adapter_apply and moe_adapter_backward, and of
+ * what the forward pass saves for the backward pass. */
+moe_status moe_adapter_workspace_query(const moe_adapter_dims* dims, int64_t num_tokens,
+                                       size_t* bytes);
+moe_status moe_adapter_saved_query(const moe_adapter_dims* dims, int64_t num_tokens,
+                                   size_t* bytes);
+
+/* out[t] = base[t] + scale[a] * (x[t] A_a^T) B_a, summed in float32 and rounded
+ * once; out[t] = base[t] for a token without an adapter.
+ *   x:     device bf16 [num_tokens, in_features], x_stride elements between
+ *          rows (all strides: multiples of 8, at least the features)
+ *   plan:  of the same num_adapters and num_tokens.  (With a buffer that holds
+ *          another plan the results are undefined, but no access leaves the
+ *          given buffers.)
+ *   scale: device float [num_adapters]
+ *   base:  device [num_tokens, out_features] of out_type; may be out (with the
+ *          same stride); null: 0
+ *   saved: device buffer of moe_adapter_saved_query bytes for the backward
+ *          pass, or null
+ *   workspace: device buffer of moe_adapter_workspace_query bytes, needs no
+ *          initialisation; calls that may run at the same time need their own
+ * The low-rank rows are float32; where they enter the second product they are
+ * split into two bf16 halves (relative error at most 2^-17).
+ * num_tokens = 0 returns MOE_OK without launching.  Errors as moe_run_ws. */
+moe_status moe_adapter_apply(const moe_adapter_dims* dims, const void* x, int64_t x_stride,
+                             int64_t num_tokens, const void* plan, size_t plan_bytes,
+                             const void* a, const void* b, const float* scale, const void* base,
+                             int64_t base_stride, void* out, int64_t out_stride, void* saved,
+                             size_t saved_bytes, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream);
+
+/* Gradients of moe_adapter_apply, with v[t] = scale[a] * dout[t] B_a^T:
+ *   dx[t] = dx_base[t] + v[t] A_a        bf16; a token without an adapter:
+ *                                        dx_base[t]
+ *   da[a] = sum over its tokens of v[t]^T x[t]
+ *   db[a] = sum over its tokens of scale[a] * (x[t] A_a^T)^T dout[t]
+ *   dout:   device [num_tokens, out_features] of out_type
+ *   saved:  as moe_adapter_apply wrote it (with da and db)
+ *   da, db: device float [num_adapters, rank, in_features] and [num_adapters,
+ *           rank, out_features] out, fully overwritten (zeros for an adapter
+ *           without tokens); both null when the factors are not trained
+ *   dx:     device bf16 [num_tokens, in_features] out, or null
+ *   dx_base: device bf16 [num_tokens, in_features]; may be dx (with the same
+ *           stride); null: 0
+ * num_tokens = 0 writes zeros into da and db.  Errors as moe_run_ws, and
+ * MOE_ERR_INVALID_ARG when no gradient is wanted. */
+moe_status moe_adapter_backward(const moe_adapter_dims* dims, const void* dout,
+                                int64_t dout_stride, const void* x, int64_t x_stride,
+                                int64_t num_tokens, const void* plan, size_t plan_bytes,
+                                const void* a, const void* b, const float* scale,
+                                const void* saved, size_t saved_bytes, float* da, float* db,
+                                const void* dx_base, int64_t dx_base_stride, void* dx,
+                                int64_t dx_stride, void* workspace, size_t workspace_bytes,
+                                hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -26,8 +26,13 @@ EXPORTS = ("moe_abi_version", "moe_last_error", "moe_weights_query", "moe_prepar
            "moe_unpack_weights", "moe_workspace_query", "moe_workspace_layout", "moe_run_ws",
            "moe_run", "moe_route", "moe_quantize_tokens", "moe_tune_set", "moe_tune_clear",
            "moe_autotune", "moe_trace_enable", "moe_trace_read", "moe_release_arenas",
-           "moe_set_fc2_fused", "moe_run_noalloc")
+           "moe_set_fc2_fused", "moe_run_noalloc", "moe_router_loss_query", "moe_router_loss",
+           "moe_router_backward", "moe_finalize_backward", "moe_adapter_plan_query",
+           "moe_adapter_plan", "moe_adapter_workspace_query", "moe_adapter_saved_query",
+           "moe_adapter_apply", "moe_adapter_backward")
 NOALLOC_SCRATCH_BYTES = 64 << 20  # MOE_NOALLOC_SCRATCH_BYTES
+T_BF16, T_F32 = 0, 1
+OUT_TYPE = {"bf16": T_BF16, "f32": T_F32}
 STAGES = ("route", "quant", "gemm1", "requant", "gemm2", "finalize")
 
 
@@ -40,6 +45,12 @@ class MoeError(RuntimeError):
 class Dims(ctypes.Structure):
     _fields_ = [("num_experts", ctypes.c_int32), ("hidden", ctypes.c_int32),
                 ("inter", ctypes.c_int32), ("wfmt", ctypes.c_int32), ("afmt", ctypes.c_int32)]
+
+
+class CAdapterDims(ctypes.Structure):
+    _fields_ = [("num_adapters", ctypes.c_int32), ("rank", ctypes.c_int32),
+                ("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32),
+                ("out_type", ctypes.c_int32)]
 
 
 class WsLayout(ctypes.Structure):
@@ -70,7 +81,7 @@ def lib():
         import torch  # noqa: F401
         L = ctypes.CDLL(LIB_PATH)
         P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
-        DP = ctypes.POINTER(Dims)
+        DP, AP = ctypes.POINTER(Dims), ctypes.POINTER(CAdapterDims)
         L.moe_abi_version.restype = I32
         L.moe_last_error.restype = ctypes.c_char_p
         sig = {
@@ -92,6 +103,17 @@ def lib():
             "moe_release_arenas": [],
             "moe_set_fc2_fused": [I32],
             "moe_trace_read": [ctypes.POINTER(ctypes.c_float), I32, ctypes.POINTER(I32)],
+            "moe_router_loss_query": [DP, I64, I32, ctypes.POINTER(SZ)],
+            "moe_router_loss": [DP, P, P, I64, I32, P, I32, P, P, P, P, P, P, SZ, P],
+            "moe_router_backward": [DP, P, P, I64, I32, P, I32, P, P, P, P, P, P, P, P],
+            "moe_finalize_backward": [DP, P, I64, I32, P, P, P, P, P, I32, P],
+            "moe_adapter_plan_query": [I32, I64, ctypes.POINTER(SZ)],
+            "moe_adapter_plan": [I32, P, I64, P, SZ, P],
+            "moe_adapter_workspace_query": [AP, I64, ctypes.POINTER(SZ)],
+            "moe_adapter_saved_query": [AP, I64, ctypes.POINTER(SZ)],
+            "moe_adapter_apply": [AP, P, I64, I64, P, SZ, P, P, P, P, I64, P, I64, P, SZ, P, SZ, P],
+            "moe_adapter_backward": [AP, P, I64, P, I64, I64, P, SZ, P, P, P, P, SZ, P, P, P, I64,
+                                     P, I64, P, SZ, P],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -271,3 +293,245 @@ def set_fc2_fused(enable: bool):
     quantiser run for every format (process-wide; changes the workspace
     layout)."""
     _check(lib().moe_set_fc2_fused(1 if enable else 0))
+
+
+# ---------------------------------------------------------------- training and adapters
+# These calls check their tensors before the library sees a pointer: a wrong
+# element type, shape, stride or device raises MoeError (MOE_ERR_INVALID_ARG).
+
+def _refuse(msg: str):
+    raise MoeError(1, msg)
+
+
+def _tensor(name, t, dtype, shape, device, rows=False):
+    """Checks tensor t (None passes); rows: 2-d with any row stride, else
+    contiguous.  dtype: the one, or a tuple of those that share the bits."""
+    if t is None:
+        return
+    if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+        _refuse(f"{name} is {t.dtype}, {dtype} is needed")
+    if tuple(t.shape) != shape:
+        _refuse(f"{name} has shape {tuple(t.shape)}, {shape} is needed")
+    if t.device != device:
+        _refuse(f"{name} is on {t.device}, the call runs on {device}")
+    if not t.is_contiguous() and not (rows and (shape[1] == 1 or t.stride(1) == 1)):
+        _refuse(f"{name} is not contiguous")
+
+
+def _buffer(name, t, device):
+    if t is None:
+        return 0
+    if t.device != device or not t.is_contiguous():
+        _refuse(f"{name} must be a contiguous buffer on {device}")
+    return t.numel() * t.element_size()
+
+
+def _current(t, stream):
+    """The device of tensor t, which has to be the current one (the library
+    launches on it) and the stream's."""
+    import torch
+
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        _refuse(f"tensors on {t.device}, but the current device is another one")
+    if stream is not None and stream.device != t.device:
+        _refuse(f"stream of {stream.device} for tensors on {t.device}")
+    return t.device
+
+
+def _stride(t):
+    """Elements between rows; a single row (or none) has no stride of its own."""
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
+
+
+def _size(query, *args) -> int:
+    b = ctypes.c_size_t()
+    _check(query(*args, ctypes.byref(b)))
+    return b.value
+
+
+def _seqs(seq_offsets, device):
+    import torch
+
+    if seq_offsets is None:
+        return 1
+    if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2:
+        _refuse("seq_offsets must hold at least two boundaries")
+    _tensor("seq_offsets", seq_offsets, torch.int32, (seq_offsets.shape[0],), device)
+    return seq_offsets.shape[0] - 1
+
+
+def router_loss_query(d: LayerDims, num_tokens: int, num_seqs: int = 1) -> int:
+    return _size(lib().moe_router_loss_query, ctypes.byref(d.c()), num_tokens, num_seqs)
+
+
+def router_loss(d: LayerDims, logits, ids, losses, counts, mean_probs, seq_tokens, workspace,
+                seq_offsets=None, token_mask=None, stream=None):
+    """Balance loss, z-loss and per-expert counts.  logits: float32 cuda [T, E];
+    ids: int32 [T, k]; seq_offsets: int32 [S + 1] (None: one sequence);
+    token_mask: uint8 [T], 0 for padding; outputs losses float32 [2], counts
+    int32 [S, E], mean_probs float32 [S, E], seq_tokens int32 [S + 2];
+    workspace: uint8 of router_loss_query bytes."""
+    import torch
+
+    dev = _current(logits, stream)
+    T, E = logits.shape[0], d.num_experts
+    S, k = _seqs(seq_offsets, dev), ids.shape[-1]
+    _tensor("logits", logits, torch.float32, (T, E), dev)
+    _tensor("ids", ids, torch.int32, (T, k), dev)
+    _tensor("token_mask", token_mask, torch.uint8, (T,), dev)
+    _tensor("losses", losses, torch.float32, (2,), dev)
+    _tensor("counts", counts, torch.int32, (S, E), dev)
+    _tensor("mean_probs", mean_probs, torch.float32, (S, E), dev)
+    _tensor("seq_tokens", seq_tokens, torch.int32, (S + 2,), dev)
+    _check(lib().moe_router_loss(
+        ctypes.byref(d.c()), _ptr(logits), _ptr(ids), T, k, _ptr(seq_offsets), S, _ptr(token_mask),
+        _ptr(losses), _ptr(counts), _ptr(mean_probs), _ptr(seq_tokens), _ptr(workspace),
+        _buffer("workspace", workspace, dev), _stream(stream)))
+
+
+def router_backward(d: LayerDims, logits, ids, dlogits, weights=None, dweights=None, dlosses=None,
+                    counts=None, seq_tokens=None, seq_offsets=None, token_mask=None, stream=None):
+    """dlogits float32 [T, E] from the routing weights' gradient (weights and
+    dweights float32 [T, k]) and the losses' (dlosses float32 [2], with the
+    counts and seq_tokens of router_loss)."""
+    import torch
+
+    dev = _current(logits, stream)
+    T, E = logits.shape[0], d.num_experts
+    S, k = _seqs(seq_offsets, dev), ids.shape[-1]
+    f32 = torch.float32
+    _tensor("logits", logits, f32, (T, E), dev)
+    _tensor("ids", ids, torch.int32, (T, k), dev)
+    _tensor("dlogits", dlogits, f32, (T, E), dev)
+    _tensor("weights", weights, f32, (T, k), dev)
+    _tensor("dweights", dweights, f32, (T, k), dev)
+    _tensor("dlosses", dlosses, f32, (2,), dev)
+    _tensor("counts", counts, torch.int32, (S, E), dev)
+    _tensor("seq_tokens", seq_tokens, torch.int32, (S + 2,), dev)
+    _tensor("token_mask", token_mask, torch.uint8, (T,), dev)
+    _check(lib().moe_router_backward(
+        ctypes.byref(d.c()), _ptr(logits), _ptr(ids), T, k, _ptr(seq_offsets), S, _ptr(token_mask),
+        _ptr(weights), _ptr(dweights), _ptr(dlosses), _ptr(counts), _ptr(seq_tokens), _ptr(dlogits),
+        _stream(stream)))
+
+
+def finalize_backward(d: LayerDims, dout, weights, y2, slot_row, dweights, dy2=None, stream=None):
+    """Gradient of the weighted sum.  dout: bf16 (or int16 bits) [T, H]; weights
+    float32 [T, k]; y2 float32 [T*k, H]; slot_row int32 [T, k]; outputs dweights
+    float32 [T, k] and dy2 [T*k, H], float32 or bf16 (int16 bits), or None."""
+    import torch
+
+    dev = _current(dout, stream)
+    T, H, k = dout.shape[0], d.hidden, weights.shape[-1]
+    bits = (torch.bfloat16, torch.int16)
+    _tensor("dout", dout, bits, (T, H), dev)
+    _tensor("weights", weights, torch.float32, (T, k), dev)
+    _tensor("y2", y2, torch.float32, (T * k, H), dev)
+    _tensor("slot_row", slot_row, torch.int32, (T, k), dev)
+    _tensor("dweights", dweights, torch.float32, (T, k), dev)
+    _tensor("dy2", dy2, bits + (torch.float32,), (T * k, H), dev)
+    kind = T_F32 if dy2 is not None and dy2.dtype == torch.float32 else T_BF16
+    _check(lib().moe_finalize_backward(
+        ctypes.byref(d.c()), _ptr(dout), T, k, _ptr(weights), _ptr(y2), _ptr(slot_row),
+        _ptr(dweights), _ptr(dy2), kind, _stream(stream)))
+
+
+@dataclass(frozen=True)
+class AdapterDims:
+    """num_adapters factors A bf16 [rank, in_features] and B bf16 [rank,
+    out_features]; out_type: "bf16" or "f32" (base, out and dout)."""
+
+    num_adapters: int
+    rank: int
+    in_features: int
+    out_features: int
+    out_type: str = "bf16"
+
+    def c(self) -> CAdapterDims:
+        return CAdapterDims(self.num_adapters, self.rank, self.in_features, self.out_features,
+                            OUT_TYPE[self.out_type])
+
+    def _torch_out(self):
+        import torch
+
+        return torch.float32 if self.out_type == "f32" else (torch.bfloat16, torch.int16)
+
+
+def adapter_plan_query(num_adapters: int, num_tokens: int) -> int:
+    return _size(lib().moe_adapter_plan_query, num_adapters, num_tokens)
+
+
+def adapter_plan(num_adapters: int, adapter_ids, plan, stream=None):
+    """Groups the tokens of a batch by adapter.  adapter_ids: int32 cuda [T], ids
+    outside [0, num_adapters) mean no adapter; plan: uint8 of
+    adapter_plan_query bytes."""
+    import torch
+
+    dev = _current(adapter_ids, stream)
+    T = adapter_ids.shape[0]
+    _tensor("adapter_ids", adapter_ids, torch.int32, (T,), dev)
+    _check(lib().moe_adapter_plan(num_adapters, _ptr(adapter_ids), T, _ptr(plan),
+                                  _buffer("plan", plan, dev), _stream(stream)))
+
+
+def adapter_workspace_query(d: AdapterDims, num_tokens: int) -> int:
+    return _size(lib().moe_adapter_workspace_query, ctypes.byref(d.c()), num_tokens)
+
+
+def adapter_saved_query(d: AdapterDims, num_tokens: int) -> int:
+    return _size(lib().moe_adapter_saved_query, ctypes.byref(d.c()), num_tokens)
+
+
+def _adapter_factors(d: AdapterDims, a, b, scale, dev):
+    import torch
+
+    bits = (torch.bfloat16, torch.int16)
+    _tensor("a", a, bits, (d.num_adapters, d.rank, d.in_features), dev)
+    _tensor("b", b, bits, (d.num_adapters, d.rank, d.out_features), dev)
+    _tensor("scale", scale, torch.float32, (d.num_adapters,), dev)
+    return bits
+
+
+def adapter_apply(d: AdapterDims, x, plan, a, b, scale, base, out, workspace, saved=None,
+                  stream=None):
+    """out = base + scale * (x A^T) B of each token's adapter.  x: bf16 cuda
+    [T, K]; a bf16 [L, R, K]; b bf16 [L, R, N]; scale float32 [L]; base (or None)
+    and out [T, N] of the dims' type; x, base and out may have a row stride;
+    saved: uint8 of adapter_saved_query bytes for adapter_backward."""
+    dev = _current(x, stream)
+    T = x.shape[0]
+    bits = _adapter_factors(d, a, b, scale, dev)
+    _tensor("x", x, bits, (T, d.in_features), dev, rows=True)
+    _tensor("base", base, d._torch_out(), (T, d.out_features), dev, rows=True)
+    _tensor("out", out, d._torch_out(), (T, d.out_features), dev, rows=True)
+    _check(lib().moe_adapter_apply(
+        ctypes.byref(d.c()), _ptr(x), _stride(x), T, _ptr(plan), _buffer("plan", plan, dev),
+        _ptr(a), _ptr(b), _ptr(scale), _ptr(base), _stride(out if base is None else base),
+        _ptr(out), _stride(out), _ptr(saved), _buffer("saved", saved, dev), _ptr(workspace),
+        _buffer("workspace", workspace, dev), _stream(stream)))
+
+
+def adapter_backward(d: AdapterDims, dout, x, plan, a, b, scale, saved, da, db, workspace, dx=None,
+                     dx_base=None, stream=None):
+    """Gradients of adapter_apply: da, db float32 of the factors' shapes (or both
+    None) and dx = dx_base + ... bf16 [T, K] (or None).  saved: as
+    adapter_apply left it for the same plan."""
+    import torch
+
+    dev = _current(dout, stream)
+    T = dout.shape[0]
+    bits = _adapter_factors(d, a, b, scale, dev)
+    K, N = d.in_features, d.out_features
+    _tensor("dout", dout, d._torch_out(), (T, N), dev, rows=True)
+    _tensor("x", x, bits, (T, K), dev, rows=True)
+    _tensor("dx", dx, bits, (T, K), dev, rows=True)
+    _tensor("dx_base", dx_base, bits, (T, K), dev, rows=True)
+    _tensor("da", da, torch.float32, (d.num_adapters, d.rank, K), dev)
+    _tensor("db", db, torch.float32, (d.num_adapters, d.rank, N), dev)
+    stride = lambda t, n: n if t is None else _stride(t)  # noqa: E731
+    _check(lib().moe_adapter_backward(
+        ctypes.byref(d.c()), _ptr(dout), _stride(dout), _ptr(x), stride(x, K), T, _ptr(plan),
+        _buffer("plan", plan, dev), _ptr(a), _ptr(b), _ptr(scale), _ptr(saved),
+        _buffer("saved", saved, dev), _ptr(da), _ptr(db), _ptr(dx_base), stride(dx_base, K),
+        _ptr(dx), stride(dx, K), _ptr(workspace), _buffer("workspace", workspace, dev),
+        _stream(stream)))

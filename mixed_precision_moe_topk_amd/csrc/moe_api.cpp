@@ -25,6 +25,7 @@
 
 #include "../../include/moe.h"
 #include "moe_common.h"
+#include "moe_host.h"
 
 namespace {
 
@@ -618,8 +619,25 @@ moe_status run_ws_untraced(const moe_dims* dims, const void* hidden, int64_t num
   return run_checked(dims, hidden, num_tokens, router_logits, weights, scales, top_k, out,
                      workspace, workspace_bytes, stream, -1, false);
 }
-// Records a failure of the calling thread for moe_last_error.
+// The helpers of moe_host.h.
 moe_status set_error(moe_status st, const char* msg) { return fail(st, "%s", msg); }
+moe_status set_errorf(moe_status st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return fail(st, "%s", buf);
+}
+moe_status set_ok() { return ok(); }
+moe_status check_hip(hipError_t e, const char* what, hipStream_t st) {
+  return hip_check(e, what, st);
+}
+moe_status check_gfx950() { return check_device(); }
+moe_status check_layer(const moe_dims* dims, int64_t num_tokens, int32_t top_k) {
+  moe_ws_layout L;
+  return layout_of(dims, num_tokens, top_k, &L);
+}
 }  // namespace moe
 
 extern "C" {

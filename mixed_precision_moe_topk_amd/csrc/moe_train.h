@@ -1,0 +1,163 @@
+// Launch parameters of the training and adapter operators beside the layer:
+// the router's losses and gradients, the gradient of the weighted sum, and
+// low-rank adapters.
+#pragma once
+
+#include "moe_common.h"
+
+namespace moe {
+
+// ---------------------------------------------------------------- router
+constexpr int kLossRun = 16;    // consecutive tokens one wave sums
+constexpr int kLossWaves = 4;   // waves (runs) per block of the loss kernel
+constexpr int kLossBlock = kLossRun * kLossWaves;
+
+struct RouterLossParams {
+  const float* logits;         // [T, E]
+  const int32_t* ids;          // [T, k]
+  const int32_t* seq_offsets;  // [S + 1], or null: one sequence of all tokens
+  const uint8_t* mask;         // [T], or null: every token counts
+  int64_t tokens;
+  int32_t experts;
+  int32_t top_k;
+  int32_t seqs;
+  // one slot per (run of tokens, sequence): probability sums [E], selections
+  // [E], the sum of squared log-sum-exps and the tokens (see slot_words)
+  float* slots;
+  float* seq_part;   // [S, ceil(E/64)] balance terms, then [S] z sums
+  int32_t* counter;  // [1] blocks of the second kernel that have finished
+  float* losses;       // [2]
+  int32_t* counts;     // [S, E]
+  float* mean_probs;   // [S, E]
+  int32_t* seq_tokens; // [S + 2]
+};
+// Words of one slot: E probability sums, E selections, z sum, token count.
+__host__ __device__ constexpr int64_t slot_words(int64_t experts) { return 2 * experts + 2; }
+
+struct RouterGradParams {
+  const float* logits;
+  const int32_t* ids;
+  const float* weights;    // [T, k], with dweights
+  const float* dweights;   // [T, k] or null
+  const int32_t* seq_offsets;
+  const uint8_t* mask;
+  const int32_t* counts;      // [S, E], with dlosses
+  const int32_t* seq_tokens;  // [S + 2], with dlosses
+  const float* dlosses;       // [2] or null
+  int64_t tokens;
+  int32_t experts;
+  int32_t top_k;
+  int32_t seqs;
+  float* dlogits;  // [T, E]
+};
+
+hipError_t launch_router_loss(const RouterLossParams& p, hipStream_t st);
+hipError_t launch_router_grad(const RouterGradParams& p, hipStream_t st);
+
+// ---------------------------------------------------------------- weighted sum
+// dweights [T, k], dy2 [T*k, H] (bf16 bits or float32; null: not wanted).
+hipError_t launch_finalize_grad(const uint16_t* dout, const float* weights, const float* y2,
+                                const int32_t* slot_row, int64_t T, int32_t k, int32_t H,
+                                float* dweights, void* dy2, bool dy2_f32, hipStream_t st);
+
+// ---------------------------------------------------------------- adapters
+constexpr int kMaxAdapters = 1023;   // one more group holds the tokens without one
+constexpr int kMaxRank = 128;
+constexpr int kAdapterTile = 64;     // rows of a tile
+constexpr int kAdapterPad = 16;      // an adapter's rows start at a multiple of this
+constexpr int kPlanChunk = 64;       // tokens per wave of the plan kernels
+constexpr int kPlanGroup = 1024;     // tokens per block of the plan kernels
+
+// Plan of a batch: its tokens grouped by adapter.  Int32 words:
+//   head [4]: tiles, padded rows
+//   first [L + 2]: first row of each group (multiples of kAdapterPad); group L
+//                  holds the tokens without an adapter
+//   rows [max_rows]: token of each row, -1 in the padding behind a group
+//   tiles [max_tiles][4]: group, first row, rows, unused
+//   counts [nblocks, L + 1]: scratch of the plan kernels
+struct PlanLayout {
+  int64_t first, rows, tiles, counts, total;  // offsets in words
+  int64_t max_rows, max_tiles, nblocks;
+  PlanLayout(int32_t adapters, int64_t tokens) {
+    const int64_t g = adapters + 1, used = tokens < g ? tokens : g;
+    max_rows = (tokens + used * (kAdapterPad - 1) + 31) / 32 * 32;
+    max_tiles = tokens / kAdapterTile + used;
+    nblocks = (tokens + kPlanGroup - 1) / kPlanGroup;
+    const auto up = [](int64_t w) { return (w + 63) / 64 * 64; };
+    first = 64;
+    rows = first + up(g + 1);
+    tiles = rows + up(max_rows);
+    counts = tiles + up(4 * max_tiles);
+    total = counts + up(nblocks * g);
+  }
+};
+
+struct PlanParams {
+  const int32_t* adapter_ids;  // [T]
+  int64_t tokens;
+  int32_t adapters;
+  int32_t* plan;
+};
+hipError_t launch_adapter_plan(const PlanParams& p, const PlanLayout& l, hipStream_t st);
+
+struct PlanView {
+  const int32_t* head;
+  const int32_t* first;
+  const int32_t* rows;
+  const Tile* tiles;
+  int64_t tokens, max_rows, max_tiles;
+  int32_t adapters;
+};
+
+// part[s][row][Rp] = X[token(row)] . W[adapter]^T over the s-th part of K.
+struct ShrinkParams {
+  PlanView plan;
+  const void* x;
+  int64_t x_stride;    // elements
+  const uint16_t* w;   // [L, R, K] bf16
+  int32_t rank, rank_pad, K;
+  int32_t splits, split_k;
+  float* part;
+};
+// out[t] = base[t] + scale * sum_s part[s][row(t)] . W[adapter]
+struct ExpandParams {
+  PlanView plan;
+  const float* part;
+  int32_t splits;
+  const float* scale;  // [L]
+  const uint16_t* w;   // [L, R, N] bf16
+  int32_t rank, rank_pad, N;
+  const void* base;    // or null: 0
+  int64_t base_stride;
+  void* out;
+  int64_t out_stride;
+};
+// saved[0 / 1][r][row] = high / low bf16 halves of scale * sum_s part[s][row][r]
+struct JoinParams {
+  PlanView plan;
+  const float* part;
+  int32_t splits;
+  const float* scale;
+  int32_t rank_pad;
+  uint16_t* saved;
+};
+// grad[adapter][r][c] = sum over the adapter's rows of saved[r][row] * X[token(row)][c]
+struct OuterSide {
+  const uint16_t* saved;
+  const void* x;
+  int64_t x_stride;
+  int32_t C;
+  float* grad;
+};
+struct OuterParams {
+  PlanView plan;
+  OuterSide side[2];  // [0] bf16 x; [1] dout (bf16 or float32)
+  int32_t rank, rank_pad;
+  int32_t blocks0;    // column blocks of side 0
+};
+hipError_t launch_adapter_shrink(const ShrinkParams& p, bool x_f32, hipStream_t st);
+hipError_t launch_adapter_expand(const ExpandParams& p, bool out_f32, hipStream_t st);
+hipError_t launch_adapter_join(const JoinParams& p, hipStream_t st);
+hipError_t launch_adapter_outer(const OuterParams& p, bool dout_f32, hipStream_t st);
+
+}  // namespace moe
