@@ -534,7 +534,8 @@ moe_status moe_adapter_saved_query(const moe_adapter_dims* dims, int64_t num_tok
  *   workspace: device buffer of moe_adapter_workspace_query bytes, needs no
  *          initialisation; calls that may run at the same time need their own
  * The low-rank rows are float32; where they enter the second product they are
- * split into two bf16 halves (relative error at most 2^-17).
+ * split into bf16 parts (two for a bf16 out, relative error at most 2^-17; three
+ * for a float out, 2^-24).
  * num_tokens = 0 returns MOE_OK without launching.  Errors as moe_run_ws. */
 moe_status moe_adapter_apply(const moe_adapter_dims* dims, const void* x, int64_t x_stride,
                              int64_t num_tokens, const void* plan, size_t plan_bytes,

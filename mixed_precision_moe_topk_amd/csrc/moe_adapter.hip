@@ -14,10 +14,13 @@
 // (8 rows x 8 columns a lane, one byte permute for two elements), so nothing
 // passes through LDS but the low-rank rows and the waves' partial sums.
 //
-// x and the factors are bf16, u and v float32.  Where u and v enter a matrix
-// instruction they are split into a high and a low bf16 half (relative error
-// at most 2^-18), which fill the two halves of a 32-long contraction: a bf16 u
-// would cost the float32 outputs 2^-9.  Float32 dout is split likewise.
+// x and the factors are bf16, u and v float32.  Where float32 values enter a
+// matrix instruction they are split into bf16 parts, v = v0 + v1 (+ v2): two
+// parts hold v to 2^-18 and serve bf16 results, three hold all of a float32 and
+// serve float32 results (the factors' gradients, float32 out).  A single bf16
+// part would cost 2^-9.
+#include <type_traits>
+
 #include "moe_train.h"
 
 namespace moe {
@@ -187,37 +190,64 @@ __device__ __forceinline__ int64_t plan_token(const PlanView& v, int64_t row) {
   return t < v.tokens ? t : -1;
 }
 
-__device__ __forceinline__ v8bf as_bf16x8(const uint4& u) { return __builtin_bit_cast(v8bf, u); }
-
-// v = hi + lo up to 2^-18 |v|; an infinite hi takes lo = 0.
-__device__ __forceinline__ void split_bf16(float v, __bf16* hi, __bf16* lo) {
-  const __bf16 h = (__bf16)v;
-  const float r = v - (float)h;
-  *hi = h;
-  *lo = (__bf16)(__builtin_isinf((float)h) ? 0.0f : r);
+// v as a sum of N bf16 parts; an infinite first part leaves the others 0.
+template <int N>
+__device__ __forceinline__ void split_bf16(float v, __bf16 (&part)[N]) {
+  part[0] = (__bf16)v;
+  const bool inf = __builtin_isinf((float)part[0]);
+#pragma unroll
+  for (int i = 1; i < N; ++i) {
+    v = inf ? 0.0f : v - (float)part[i - 1];
+    part[i] = (__bf16)v;
+  }
 }
-__device__ __forceinline__ void split8(const float4& a, const float4& b, v8bf* hi, v8bf* lo) {
-  const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+template <int N>
+__device__ __forceinline__ void split8(const float (&v)[8], v8bf (&part)[N]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    __bf16 h, l;
-    split_bf16(v[i], &h, &l);
-    (*hi)[i] = h;
-    (*lo)[i] = l;
+    __bf16 q[N];
+    split_bf16<N>(v[i], q);
+#pragma unroll
+    for (int n = 0; n < N; ++n) part[n][i] = q[n];
   }
 }
 
-// 8 rows x 8 columns of bf16 (row i in raw[i]) -> per column its 8 rows.
-__device__ __forceinline__ void transpose8(const uint4 (&raw)[8], v8bf (&col)[8]) {
-  const auto word = [&](int i, int c) { return c == 0 ? raw[i].x : c == 1 ? raw[i].y : c == 2 ? raw[i].z : raw[i].w; };
+// 8 rows x 2 W columns of bf16, row i in raw[i][0 .. W) -> per column its 8
+// rows: one byte permute for two elements.
+template <int W>
+__device__ __forceinline__ void transpose8(const uint32_t (&raw)[8][W], v8bf (&col)[2 * W]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < 2 * W; ++j) {
     v4u q;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      q[i] = __builtin_amdgcn_perm(word(2 * i + 1, j / 2), word(2 * i, j / 2),
+      q[i] = __builtin_amdgcn_perm(raw[2 * i + 1][j / 2], raw[2 * i][j / 2],
                                    j & 1 ? 0x07060302u : 0x05040100u);
     col[j] = __builtin_bit_cast(v8bf, q);
+  }
+}
+
+template <int W>
+__device__ __forceinline__ void load_words(const void* p, bool in, uint32_t (&w)[W]) {
+  typedef uint32_t vec __attribute__((ext_vector_type(W)));
+  vec v = {};
+  if (in) v = *static_cast<const vec*>(p);
+#pragma unroll
+  for (int i = 0; i < W; ++i) w[i] = v[i];
+}
+__device__ __forceinline__ v8bf load_bf16x8(const void* p, bool in) {
+  uint32_t w[4];
+  load_words<4>(p, in, w);
+  return __builtin_bit_cast(v8bf, v4u{w[0], w[1], w[2], w[3]});
+}
+__device__ __forceinline__ void load_f32x8(const float* p, bool in, float (&v)[8]) {
+  uint32_t a[4], b[4];
+  load_words<4>(p, in, a);
+  load_words<4>(p + 4, in, b);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = __uint_as_float(a[i]);
+    v[4 + i] = __uint_as_float(b[i]);
   }
 }
 
@@ -225,77 +255,136 @@ __device__ __forceinline__ v4f mfma_bf16(const v8bf& a, const v8bf& b, const v4f
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// Sums the accumulators of a block's four waves into wave 0's, in the order
-// (0 + 2) + (1 + 3).  red holds 2 N 64 float4.
-template <int N>
+// Sums the accumulators of a block's WAVES waves into wave 0's: the upper half
+// of the waves hands its sums to the lower half until one is left.  red holds
+// WAVES / 2 x N x 64 entries.
+template <int WAVES, int N>
 __device__ __forceinline__ void join_waves(v4f (&acc)[N], v4f* red) {
   const int w = threadIdx.x / kWave, lane = lane_id();
-  if (w >= 2) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) red[((w - 2) * N + i) * kWave + lane] = acc[i];
+  for (int h = WAVES / 2; h > 0; h /= 2) {
+    if (w >= h && w < 2 * h) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) red[((w - h) * N + i) * kWave + lane] = acc[i];
+    }
+    __syncthreads();
+    if (w < h) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[i] += red[(w * N + i) * kWave + lane];
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  if (w < 2) {
+}
+
+// ---------------------------------------------------------------- low-rank rows
+// Where the low-rank rows go.  frag: operands of expand, per 16 rows and 32
+// ranks one 1-KB block for each part, lane (l16, g) holding ranks [8 g, 8 g + 8)
+// of row l16.  saved: operands of outer, part n of rank r and row i at
+// saved[(n rank_pad + r) max_rows + i].  Both optional.
+__device__ __forceinline__ int64_t frag_block(int64_t row16, int rank_pad32, int r32, int parts, int n) {
+  return ((row16 * (rank_pad32 / 32) + r32) * parts + n) * 512;
+}
+
+// Ranks [16 r + 4 g, + 4) of row row0 + l16 (row0 a multiple of 16), scaled; 0
+// behind the adapter's last row and rank.
+template <int PARTS>
+__device__ __forceinline__ void put_low(const LowRows& o, int64_t row0, int r, const v4f& v) {
+  typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
+  const int l16 = lane_id() & 15, g = lane_id() >> 4;
+  v4bf part[3];
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] += red[(w * N + i) * kWave + lane];
+  for (int i = 0; i < 4; ++i) {
+    __bf16 q[3];
+    split_bf16<3>(v[i], q);
+#pragma unroll
+    for (int n = 0; n < 3; ++n) part[n][i] = q[n];
   }
-  __syncthreads();
-  if (w == 1) {
+  if (o.frag) {
+    const int at = (l16 + 16 * (2 * (r & 1) + (g >> 1))) * 8 + 4 * (g & 1);
 #pragma unroll
-    for (int i = 0; i < N; ++i) red[i * kWave + lane] = acc[i];
+    for (int n = 0; n < PARTS; ++n) {
+      __bf16* dst = reinterpret_cast<__bf16*>(o.frag) + frag_block(row0 / 16, o.rank_pad32, r / 2, PARTS, n);
+      *reinterpret_cast<v4bf*>(dst + at) = part[n];
+      if (16 * (r + 1) == o.rank_pad && o.rank_pad != o.rank_pad32)  // no rank in the block's other half
+        *reinterpret_cast<v4bf*>(dst + at + 256) = v4bf{};
+    }
   }
-  __syncthreads();
-  if (w == 0) {
+  if (o.saved) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] += red[i * kWave + lane];
+    for (int n = 0; n < 3; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        reinterpret_cast<__bf16*>(o.saved)[((int64_t)n * o.rank_pad + 16 * r + 4 * g + i) * o.max_rows + row0 + l16] =
+            part[n][i];
   }
 }
 
 // ---------------------------------------------------------------- shrink
-// One 64-wide step of K: lane (l16, g) holds elements [8 g, 8 g + 8) of each
-// 32-wide half, of W row l16 of a rank block and of X row l16 of a row block.
-template <int MT, int RT, bool F32, bool GUARD>
-__device__ __forceinline__ void shrink_step(const char* const (&xp)[MT], const uint16_t* const (&wp)[RT],
-                                            int k0, int ke, v4f (&acc)[MT * RT]) {
-  const int g = lane_id() / 16;
+// Operands of one 64-wide step of K: lane (l16, g) holds elements [8 g, 8 g +
+// 8) of each 32-wide half, of W row l16 of a rank block and of X row l16 of a
+// row block.
+template <int MT, int RT>
+struct ShrinkStep {
+  v8bf a[2][RT], x[2][MT];
+  template <bool GUARD>
+  __device__ __forceinline__ void load(const uint16_t* const (&xp)[MT], const uint16_t* const (&wp)[RT], int k0,
+                                       int ke) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = k0 + 32 * h + 8 * (lane_id() / 16);
+      const bool in = !GUARD || k < ke;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) x[h][m] = load_bf16x8(xp[m] + k, in);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) a[h][r] = load_bf16x8(wp[r] + k, in);
+    }
+  }
+  __device__ __forceinline__ void add(v4f (&acc)[MT * RT]) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) acc[m * RT + r] = mfma_bf16(a[h][r], x[h][m], acc[m * RT + r]);
+  }
+};
+
+// The same step with float32 X, in three parts.
+template <int MT, int RT, bool GUARD>
+__device__ __forceinline__ void shrink_f32(const float* const (&xp)[MT], const uint16_t* const (&wp)[RT], int k0,
+                                           int ke, v4f (&acc)[MT * RT]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int k = k0 + 32 * h + 8 * g;
+    const int k = k0 + 32 * h + 8 * (lane_id() / 16);
     const bool in = !GUARD || k < ke;
     v8bf a[RT];
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
-      a[r] = as_bf16x8(in ? *reinterpret_cast<const uint4*>(wp[r] + k) : make_uint4(0, 0, 0, 0));
+    for (int r = 0; r < RT; ++r) a[r] = load_bf16x8(wp[r] + k, in);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      if constexpr (F32) {
-        const float4* s = reinterpret_cast<const float4*>(xp[m] + (int64_t)k * 4);
-        v8bf hi, lo;
-        split8(in ? s[0] : make_float4(0.f, 0.f, 0.f, 0.f), in ? s[1] : make_float4(0.f, 0.f, 0.f, 0.f), &hi, &lo);
+      float v[8];
+      v8bf x[3];
+      load_f32x8(xp[m] + k, in, v);
+      split8<3>(v, x);
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          acc[m * RT + r] = mfma_bf16(a[r], lo, acc[m * RT + r]);
-          acc[m * RT + r] = mfma_bf16(a[r], hi, acc[m * RT + r]);
-        }
-      } else {
-        const v8bf b = as_bf16x8(in ? *reinterpret_cast<const uint4*>(xp[m] + (int64_t)k * 2) : make_uint4(0, 0, 0, 0));
+      for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int r = 0; r < RT; ++r) acc[m * RT + r] = mfma_bf16(a[r], b, acc[m * RT + r]);
-      }
+        for (int q = 2; q >= 0; --q) acc[m * RT + r] = mfma_bf16(a[r], x[q], acc[m * RT + r]);
     }
   }
 }
 
 template <int MT, int RT, bool F32>
 __device__ __forceinline__ void shrink_tile(const ShrinkParams& p, const Tile& tile, int split, v4f* red) {
+  typedef std::conditional_t<F32, float, uint16_t> X;
   const int lane = lane_id(), w = threadIdx.x / kWave;
   const int l16 = lane & 15, g = lane >> 4;
-  const char* xp[MT];
+  const X* xp[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    // rows behind the tile's last repeat it; nothing reads their sums
+    // rows behind the tile's last repeat it; their sums are put as 0
     const int64_t t = plan_token(p.plan, tile.row0 + min(16 * m + l16, tile.nrows - 1));
-    xp[m] = static_cast<const char*>(p.x) + (t < 0 ? 0 : t) * p.x_stride * (F32 ? 4 : 2);
+    xp[m] = static_cast<const X*>(p.x) + (t < 0 ? 0 : t) * p.x_stride;
   }
   const uint16_t* wp[RT];
 #pragma unroll
@@ -306,25 +395,57 @@ __device__ __forceinline__ void shrink_tile(const ShrinkParams& p, const Tile& t
   for (int i = 0; i < MT * RT; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
   const int kb = split * p.split_k, ke = min(p.K, kb + p.split_k);
   int k = kb + 64 * w;
-  for (; k + 64 <= ke; k += 256) shrink_step<MT, RT, F32, false>(xp, wp, k, ke, acc);
-  if (k < ke) shrink_step<MT, RT, F32, true>(xp, wp, k, ke, acc);
-  join_waves(acc, red);
+  if constexpr (F32) {
+    for (; k + 64 <= ke; k += 256) shrink_f32<MT, RT, false>(xp, wp, k, ke, acc);
+    if (k < ke) shrink_f32<MT, RT, true>(xp, wp, k, ke, acc);
+  } else {
+    // the next step's loads run under this one's products
+    ShrinkStep<MT, RT> s;
+    if (k + 64 <= ke) {
+      s.template load<false>(xp, wp, k, ke);
+      for (k += 256; k + 64 <= ke; k += 256) {
+        ShrinkStep<MT, RT> next;
+        next.template load<false>(xp, wp, k, ke);
+        s.add(acc);
+        s = next;
+      }
+      s.add(acc);
+    }
+    if (k < ke) {
+      s.template load<true>(xp, wp, k, ke);
+      s.add(acc);
+    }
+  }
+  join_waves<4>(acc, red);
   if (w != 0) return;
   // lane: row l16 of a row block, ranks [4 g, 4 g + 4) of a rank block
   float* part = p.part + (int64_t)split * p.plan.max_rows * p.rank_pad;
-  const int rows = (tile.nrows + kAdapterPad - 1) / kAdapterPad * kAdapterPad;
+  const float scale = p.low.frag || p.low.saved ? p.scale[tile.expert] : 1.0f;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    if (16 * m >= rows) break;
+    if (16 * m >= tile.nrows) break;
+    const bool live = 16 * m + l16 < tile.nrows;
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
+      if (16 * r >= p.rank_pad) break;
       v4f v = acc[m * RT + r];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = 16 * r + 4 * g + i < p.rank ? v[i] : 0.0f;
-      if (16 * r < p.rank_pad)
+      for (int i = 0; i < 4; ++i) v[i] = live && 16 * r + 4 * g + i < p.rank ? v[i] * scale : 0.0f;
+      if (p.part)
         *reinterpret_cast<v4f*>(part + (int64_t)(tile.row0 + 16 * m + l16) * p.rank_pad + 16 * r + 4 * g) = v;
+      else if (p.low.parts == 3)
+        put_low<3>(p.low, tile.row0 + 16 * m, r, v);
+      else
+        put_low<2>(p.low, tile.row0 + 16 * m, r, v);
     }
   }
+}
+
+// Tile of block b: neighbouring tiles, mostly of one adapter, on one of the 8
+// XCDs (block b runs on XCD b % 8), so that its L2 holds their factor.
+__device__ __forceinline__ int64_t xcd_tile(const PlanView& v, int64_t b) {
+  const int64_t each = (v.head[0] + 7) / 8;
+  return b / 8 < each ? b % 8 * each + b / 8 : v.max_tiles;
 }
 
 // Block (tile, split): the four waves take the split's 64-wide steps of K in
@@ -333,14 +454,15 @@ template <int RT, bool F32>
 __global__ __launch_bounds__(256) void k_adapter_shrink(ShrinkParams p) {
   __shared__ v4f red[2 * 4 * RT * kWave];
   Tile tile;
-  if (!plan_tile(p.plan, blockIdx.x, &tile) || tile.expert == p.plan.adapters) return;
+  if (!plan_tile(p.plan, xcd_tile(p.plan, blockIdx.x), &tile) || tile.expert == p.plan.adapters) return;
   if (tile.nrows <= 16) shrink_tile<1, RT, F32>(p, tile, blockIdx.y, red);
+  else if (tile.nrows <= 32) shrink_tile<2, RT, F32>(p, tile, blockIdx.y, red);
   else shrink_tile<4, RT, F32>(p, tile, blockIdx.y, red);
 }
 
 template <bool F32>
 static void launch_shrink(const ShrinkParams& p, hipStream_t st) {
-  const dim3 grid((unsigned)p.plan.max_tiles, (unsigned)p.splits);
+  const dim3 grid((unsigned)((p.plan.max_tiles + 7) / 8 * 8), (unsigned)p.splits);
   if (p.rank_pad <= 16) k_adapter_shrink<1, F32><<<grid, 256, 0, st>>>(p);
   else if (p.rank_pad <= 32) k_adapter_shrink<2, F32><<<grid, 256, 0, st>>>(p);
   else if (p.rank_pad <= 64) k_adapter_shrink<4, F32><<<grid, 256, 0, st>>>(p);
@@ -352,266 +474,260 @@ hipError_t launch_adapter_shrink(const ShrinkParams& p, bool x_f32, hipStream_t 
   return hipGetLastError();
 }
 
-// ---------------------------------------------------------------- expand
-constexpr int kExpandCols = 128;  // columns of a wave
-
-__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    v[2 * j] = __uint_as_float(w[j] << 16);
-    v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-  }
-}
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
-  v8bf o;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) o[j] = (__bf16)v[j];
-  *reinterpret_cast<v8bf*>(p) = o;
-}
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-
-// Base (or 0) plus add for 8 columns of one token.
-template <typename T>
-__device__ __forceinline__ void emit8(const ExpandParams& p, int64_t t, int n, const float (&add)[8]) {
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (p.base) load8(static_cast<const T*>(p.base) + t * p.base_stride + n, v);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] += add[j];
-  store8(static_cast<T*>(p.out) + t * p.out_stride + n, v);
-}
-
-// u of the tile's rows as matrix operands in LDS: per row block and rank block
-// a lane's 8 elements, the high halves of ranks [8 g, 8 g + 8) in lane groups
-// 0 and 1, the low halves in groups 2 and 3.
-template <int MT>
-__device__ __forceinline__ void expand_rows(const ExpandParams& p, const Tile& tile, v8bf* frag) {
-  const int rb = p.rank_pad / 16;
-  const float scale = p.scale[tile.expert];
-  const int64_t step = p.plan.max_rows * (int64_t)p.rank_pad;
-  for (int i = threadIdx.x; i < MT * rb * 32; i += blockDim.x) {
-    const int l = i & 31, m = i / 32 / rb, r = i / 32 % rb;
-    const int row = min(16 * m + (l & 15), tile.nrows - 1);
-    const float* s = p.part + (int64_t)(tile.row0 + row) * p.rank_pad + 16 * r + 8 * (l >> 4);
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-    for (int q = 0; q < p.splits; ++q, s += step) {
-      const float4 x = reinterpret_cast<const float4*>(s)[0], y = reinterpret_cast<const float4*>(s)[1];
-      a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
-      b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
-    }
-    a.x *= scale; a.y *= scale; a.z *= scale; a.w *= scale;
-    b.x *= scale; b.y *= scale; b.z *= scale; b.w *= scale;
-    v8bf hi, lo;
-    split8(a, b, &hi, &lo);
-    frag[(m * rb + r) * kWave + l] = hi;
-    frag[(m * rb + r) * kWave + l + 32] = lo;
-  }
-}
-
-// A wave's 128 columns of a tile: lane (l16, g) holds columns 8 l16 + j, which
-// are column l16 of matrix j, and rows 4 g + i of a row block, so that it
-// reads and writes 8 consecutive elements of a row.
-template <int MT, typename T>
-__device__ __forceinline__ void expand_tile(const ExpandParams& p, const Tile& tile, int n0, const v8bf* frag) {
-  const int lane = lane_id(), l16 = lane & 15, g = lane >> 4;
-  const int n = n0 + 8 * l16, rb = p.rank_pad / 16;
-  const bool in = n < p.N;
-  v4f acc[MT][8];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) acc[m][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  for (int r = 0; r < rb; ++r) {
-    uint4 raw[8];
-    v8bf b[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int q = 16 * r + 8 * (g & 1) + i;
-      raw[i] = in && q < p.rank
-                   ? *reinterpret_cast<const uint4*>(p.w + ((int64_t)tile.expert * p.rank + q) * p.N + n)
-                   : make_uint4(0, 0, 0, 0);
-    }
-    transpose8(raw, b);
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const v8bf a = frag[(m * rb + r) * kWave + lane];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) acc[m][j] = mfma_bf16(a, b[j], acc[m][j]);
-    }
-  }
-  if (!in) return;
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = 16 * m + 4 * g + i;
-      if (row >= tile.nrows) continue;
-      const int64_t t = plan_token(p.plan, tile.row0 + row);
-      if (t < 0) continue;
-      float add[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) add[j] = acc[m][j][i];
-      emit8<T>(p, t, n, add);
-    }
-}
-
-// Block (tile, columns): 128 columns a wave.
-template <typename T>
-__global__ __launch_bounds__(256) void k_adapter_expand(ExpandParams p) {
-  __shared__ v8bf frag[(kAdapterTile / 16) * (kMaxRank / 16) * kWave];
-  Tile tile;
-  if (!plan_tile(p.plan, blockIdx.x, &tile)) return;
-  const int n0 = (blockIdx.y * (blockDim.x / kWave) + threadIdx.x / kWave) * kExpandCols;
-  if (tile.expert == p.plan.adapters) {  // no adapter: the base as it is
-    if (p.base == p.out && p.base) return;
-    const int lane = lane_id(), n = n0 + 8 * (lane & 15);
-    const float none[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int row = lane >> 4; row < tile.nrows; row += 4) {
-      const int64_t t = plan_token(p.plan, tile.row0 + row);
-      if (n < p.N && t >= 0) emit8<T>(p, t, n, none);
-    }
-    return;
-  }
-  if (tile.nrows <= 16) expand_rows<1>(p, tile, frag);
-  else expand_rows<4>(p, tile, frag);
-  __syncthreads();
-  if (n0 >= p.N) return;
-  if (tile.nrows <= 16) expand_tile<1, T>(p, tile, n0, frag);
-  else expand_tile<4, T>(p, tile, n0, frag);
-}
-
-hipError_t launch_adapter_expand(const ExpandParams& p, bool out_f32, hipStream_t st) {
-  // four waves a block, one where few tiles leave CUs without work
-  const int64_t cols = (p.N + kExpandCols - 1) / kExpandCols;
-  const int waves = p.plan.max_tiles * cols >= 2048 ? 4 : 1;
-  const dim3 grid((unsigned)p.plan.max_tiles, (unsigned)((cols + waves - 1) / waves));
-  if (out_f32) k_adapter_expand<float><<<grid, waves * kWave, 0, st>>>(p);
-  else k_adapter_expand<uint16_t><<<grid, waves * kWave, 0, st>>>(p);
-  return hipGetLastError();
-}
-
 // ---------------------------------------------------------------- join
-// One block per tile: thread (rank r, 8 rows) writes 16 bytes of each half.
+// The splits' sums of a tile, scaled, into frag and saved: a wave for 16 rows
+// and 16 ranks.
 __global__ __launch_bounds__(256) void k_adapter_join(JoinParams p) {
   Tile tile;
   if (!plan_tile(p.plan, blockIdx.x, &tile) || tile.expert == p.plan.adapters) return;
-  const int Rp = p.rank_pad;
-  const int rows = (tile.nrows + kAdapterPad - 1) / kAdapterPad * kAdapterPad;
-  const int64_t step = p.plan.max_rows * (int64_t)Rp;
+  const int lane = lane_id(), l16 = lane & 15, g = lane >> 4, ranks = p.rank_pad / 16;
+  const int64_t step = p.plan.max_rows * (int64_t)p.rank_pad;
   const float scale = p.scale[tile.expert];
-  for (int i = threadIdx.x; i < rows / 8 * Rp; i += 256) {
-    const int r = i % Rp, c = i / Rp * 8;
-    v8bf hi, lo;
+  const int blocks = (tile.nrows + 15) / 16 * ranks;
+  for (int i = blockIdx.y * 4 + threadIdx.x / kWave; i < blocks; i += 4 * gridDim.y) {
+    const int64_t row0 = tile.row0 + 16 * (i / ranks);
+    const int r = i % ranks;
+    const float* s = p.part + (row0 + l16) * p.rank_pad + 16 * r + 4 * g;
+    v4f v = {0.f, 0.f, 0.f, 0.f};
+    for (int q0 = 0; q0 < p.splits; q0 += 4) {
+      v4f x[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float v = 0.0f;
-      if (c + j < tile.nrows) {
-        const float* s = p.part + (int64_t)(tile.row0 + c + j) * Rp + r;
-        for (int q = 0; q < p.splits; ++q, s += step) v += *s;
-        v *= scale;
-      }
-      __bf16 h, l;
-      split_bf16(v, &h, &l);
-      hi[j] = h;
-      lo[j] = l;
+      for (int q = 0; q < 4; ++q)
+        x[q] = q0 + q < p.splits ? *reinterpret_cast<const v4f*>(s + (q0 + q) * step) : v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v += x[q];
     }
-    uint16_t* dst = p.saved + (int64_t)r * p.plan.max_rows + tile.row0 + c;
-    *reinterpret_cast<v8bf*>(dst) = hi;
-    *reinterpret_cast<v8bf*>(dst + step) = lo;
+    v *= scale;
+    if (p.low.parts == 3) put_low<3>(p.low, row0, r, v);
+    else put_low<2>(p.low, row0, r, v);
   }
 }
 
 hipError_t launch_adapter_join(const JoinParams& p, hipStream_t st) {
-  k_adapter_join<<<(unsigned)p.plan.max_tiles, 256, 0, st>>>(p);
+  k_adapter_join<<<dim3((unsigned)p.plan.max_tiles, (unsigned)((p.rank_pad + 31) / 32)), 256, 0, st>>>(p);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- expand
+constexpr int kExpandCols = 64;  // columns of a wave
+
+__device__ __forceinline__ void load4(const uint16_t* p, float (&v)[4]) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  v[0] = __uint_as_float(u.x << 16);
+  v[1] = __uint_as_float(u.x & 0xFFFF0000u);
+  v[2] = __uint_as_float(u.y << 16);
+  v[3] = __uint_as_float(u.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+}
+__device__ __forceinline__ void store4(uint16_t* p, const float (&v)[4]) {
+  typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
+  *reinterpret_cast<v4bf*>(p) = v4bf{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+}
+__device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+
+// A wave's 64 columns of a tile.  The factor's columns stay in registers, as
+// matrix operands of all its ranks, while the tile's row blocks pass: lane
+// (l16, g) holds columns 4 l16 + j, which are column l16 of matrix j, and of
+// the sums rows 4 g + i, so it reads and writes 4 consecutive elements of a row
+// and a lane group 128 bytes (bf16).  RT: blocks of 32 ranks.  JOINED: the
+// low-rank rows come as operands (frag); else as the splits' float32 sums, which
+// every wave adds up for itself: less time than a launch that does it once,
+// where there are few rows.
+template <int RT, typename T, bool JOINED>
+__global__ __launch_bounds__(256) void k_adapter_expand(ExpandParams p) {
+  constexpr int PARTS = sizeof(T) == 4 ? 3 : 2;
+  Tile tile;
+  if (!plan_tile(p.plan, blockIdx.y, &tile)) return;
+  const int n0 = (blockIdx.x * (blockDim.x / kWave) + threadIdx.x / kWave) * kExpandCols;
+  const int lane = lane_id(), l16 = lane & 15, g = lane >> 4;
+  const int n = n0 + 4 * l16;
+  const bool in = n < p.N;
+  if (n0 >= p.N) return;
+  const T* base = static_cast<const T*>(p.base);
+  T* out = static_cast<T*>(p.out);
+  const bool low = tile.expert != p.plan.adapters;
+  if (!low && p.base == p.out && p.base) return;  // no adapter, and the base is in place
+
+  v8bf b[RT][4];
+  if (low) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      uint32_t raw[8][2];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int q = 32 * r + 8 * g + i;
+        load_words<2>(p.w + ((int64_t)tile.expert * p.rank + q) * p.N + n, in && q < p.rank, raw[i]);
+      }
+      transpose8<2>(raw, b[r]);
+    }
+  }
+  const int64_t step = p.plan.max_rows * (int64_t)p.rank_pad;
+  const float scale = low && !JOINED ? p.scale[tile.expert] : 0.0f;
+  for (int m = 0; 16 * m < tile.nrows; ++m) {
+    int64_t t[4];
+    float v[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 16 * m + 4 * g + i;
+      t[i] = in && row < tile.nrows ? plan_token(p.plan, tile.row0 + row) : -1;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[i][j] = 0.0f;
+      if (base && t[i] >= 0) load4(base + t[i] * p.base_stride + n, v[i]);
+    }
+    if (low) {
+      v4f acc[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        if (32 * r >= p.rank_pad) break;
+        v8bf a[PARTS];
+        if constexpr (JOINED) {
+#pragma unroll
+          for (int q = 0; q < PARTS; ++q)
+            a[q] = load_bf16x8(p.frag + frag_block(tile.row0 / 16 + m, p.rank_pad32, r, PARTS, q) + lane * 8, true);
+        } else {
+          const int row = min(16 * m + l16, tile.nrows - 1);
+          const float* s = p.part + (int64_t)(tile.row0 + row) * p.rank_pad + 32 * r + 8 * g;
+          const bool some = 32 * r + 8 * g < p.rank_pad;
+          float u[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) u[i] = 0.0f;
+          for (int q0 = 0; q0 < p.splits; q0 += 4) {
+            float x[4][8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) load_f32x8(s + (q0 + q) * step, some && q0 + q < p.splits, x[q]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) u[i] += x[q][i];
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) u[i] *= scale;
+          split8<PARTS>(u, a);
+        }
+#pragma unroll
+        for (int q = PARTS - 1; q >= 0; --q)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[j] = mfma_bf16(a[q], b[r][j], acc[j]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i][j] += acc[j][i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (t[i] >= 0) store4(out + t[i] * p.out_stride + n, v[i]);
+  }
+}
+
+template <typename T, bool JOINED>
+static void launch_expand(const ExpandParams& p, hipStream_t st) {
+  const int64_t cols = (p.N + kExpandCols - 1) / kExpandCols;
+  const int waves = cols >= 4 ? 4 : (int)cols;
+  // columns first: the blocks that run together cover whole rows
+  const dim3 grid((unsigned)((cols + waves - 1) / waves), (unsigned)p.plan.max_tiles), block(waves * kWave);
+  if (p.rank_pad <= 32) k_adapter_expand<1, T, JOINED><<<grid, block, 0, st>>>(p);
+  else if (p.rank_pad <= 64) k_adapter_expand<2, T, JOINED><<<grid, block, 0, st>>>(p);
+  else k_adapter_expand<4, T, JOINED><<<grid, block, 0, st>>>(p);
+}
+hipError_t launch_adapter_expand(const ExpandParams& p, bool out_f32, hipStream_t st) {
+  if (out_f32 && p.frag) launch_expand<float, true>(p, st);
+  else if (out_f32) launch_expand<float, false>(p, st);
+  else if (p.frag) launch_expand<uint16_t, true>(p, st);
+  else launch_expand<uint16_t, false>(p, st);
   return hipGetLastError();
 }
 
 // ---------------------------------------------------------------- outer
+constexpr int kOuterWaves = 8;
+
 // 32 rows of an adapter a step: lane (l16, g) holds rows [8 g, 8 g + 8) of
-// columns [8 l16, 8 l16 + 8) of X, and of rank l16 of a rank block of saved.
-template <int RT, bool F32>
+// columns [CT l16, CT l16 + CT) of X, and of rank l16 of a rank block of saved.
+// F32: X is float32, split like the saved values; the products of parts whose
+// sizes lie 2^-27 apart or more are left out.
+template <int RT, int CT, bool F32>
 __device__ __forceinline__ void outer_sum(const OuterParams& p, const OuterSide& s, int a, int r0, int c0,
-                                          v4f (&acc)[RT * 8]) {
-  const int lane = lane_id(), w = threadIdx.x / kWave, l16 = lane & 15, g = lane >> 4;
-  const int c = c0 + 8 * l16;
-  const int64_t M = p.plan.max_rows;
+                                          v4f (&acc)[RT * CT]) {
   if (p.plan.tokens == 0) return;
+  const int lane = lane_id(), w = threadIdx.x / kWave, l16 = lane & 15, g = lane >> 4;
+  const int c = c0 + CT * l16;
+  const int64_t M = p.plan.max_rows, plane = M * p.rank_pad;
   int64_t b = p.plan.first[a], e = p.plan.first[a + 1];
   b = b < 0 ? 0 : b / kAdapterPad * kAdapterPad;
   e = e > M ? M : e;
-  for (int64_t row = b + 32 * w + 8 * g; row - 8 * g < e; row += 128) {
+  for (int64_t row = b + 32 * w + 8 * g; row - 8 * g < e; row += 32 * kOuterWaves) {
     const bool live = row < e;
-    v8bf hi[RT], lo[RT];
+    v8bf u[RT][3];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
       const uint16_t* src = s.saved + (int64_t)(r0 + 16 * r + l16) * M + row;
       const bool in = live && r0 + 16 * r < p.rank_pad;
-      hi[r] = as_bf16x8(in ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0));
-      lo[r] = as_bf16x8(in ? *reinterpret_cast<const uint4*>(src + M * p.rank_pad) : make_uint4(0, 0, 0, 0));
+#pragma unroll
+      for (int n = 0; n < 3; ++n) u[r][n] = load_bf16x8(src + n * plane, in);
     }
-    uint4 raw[8], low[8];
+    int64_t t[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t t = live ? plan_token(p.plan, row + i) : -1;
-      raw[i] = low[i] = make_uint4(0, 0, 0, 0);
-      if (t >= 0 && c < s.C) {
-        if constexpr (F32) {
-          const float4* x = reinterpret_cast<const float4*>(static_cast<const float*>(s.x) + t * s.x_stride + c);
-          v8bf h, l;
-          split8(x[0], x[1], &h, &l);
-          raw[i] = __builtin_bit_cast(uint4, h);
-          low[i] = __builtin_bit_cast(uint4, l);
-        } else {
-          raw[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(s.x) + t * s.x_stride + c);
-        }
-      }
-    }
-    v8bf x[8];
-    transpose8(raw, x);
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        acc[r * 8 + j] = mfma_bf16(lo[r], x[j], acc[r * 8 + j]);
-        acc[r * 8 + j] = mfma_bf16(hi[r], x[j], acc[r * 8 + j]);
-      }
+    for (int i = 0; i < 8; ++i) t[i] = live && c < s.C ? plan_token(p.plan, row + i) : -1;
     if constexpr (F32) {
-      transpose8(low, x);
+      static_assert(CT == 4, "");
+      float x[8][4];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint32_t q[4];
+        load_words<4>(static_cast<const float*>(s.x) + t[i] * s.x_stride + c, t[i] >= 0, q);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[i][j] = __uint_as_float(q[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float col[8] = {x[0][j], x[1][j], x[2][j], x[3][j], x[4][j], x[5][j], x[6][j], x[7][j]};
+        v8bf q[3];
+        split8<3>(col, q);
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int n = 2; n >= 0; --n)
+#pragma unroll
+            for (int m = 2 - n; m >= 0; --m) acc[r * CT + j] = mfma_bf16(u[r][n], q[m], acc[r * CT + j]);
+      }
+    } else {
+      uint32_t raw[8][CT / 2];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        load_words<CT / 2>(static_cast<const uint16_t*>(s.x) + t[i] * s.x_stride + c, t[i] >= 0, raw[i]);
+      v8bf x[CT];
+      transpose8<CT / 2>(raw, x);
 #pragma unroll
       for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[r * 8 + j] = mfma_bf16(hi[r], x[j], acc[r * 8 + j]);
+        for (int j = 0; j < CT; ++j)
+#pragma unroll
+          for (int n = 2; n >= 0; --n) acc[r * CT + j] = mfma_bf16(u[r][n], x[j], acc[r * CT + j]);
     }
   }
 }
 
-// Block (128 columns of either side, adapter, 64 ranks): the four waves take
-// the adapter's rows in turn.  An adapter without tokens gets zeros.
-template <int RT, bool F32>
-__global__ __launch_bounds__(256) void k_adapter_outer(OuterParams p) {
-  __shared__ v4f red[2 * RT * 8 * kWave];
-  const bool second = (int)blockIdx.x >= p.blocks0;
-  const OuterSide& s = p.side[second ? 1 : 0];
-  const int c0 = ((int)blockIdx.x - (second ? p.blocks0 : 0)) * kExpandCols;
-  const int a = blockIdx.y, r0 = blockIdx.z * 16 * RT;
-  v4f acc[RT * 8];
+// Block (16 CT columns, adapter, 16 RT ranks): the waves take the adapter's
+// rows in turn and join their sums.  An adapter without tokens gets zeros.
+template <int RT, int CT, bool F32>
+__global__ __launch_bounds__(kOuterWaves* kWave) void k_adapter_outer(OuterParams p, OuterSide s) {
+  __shared__ v4f red[kOuterWaves / 2 * RT * CT * kWave];
+  const int c0 = blockIdx.x * 16 * CT, a = blockIdx.y, r0 = blockIdx.z * 16 * RT;
+  v4f acc[RT * CT];
 #pragma unroll
-  for (int i = 0; i < RT * 8; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
-  if (F32 && second) outer_sum<RT, true>(p, s, a, r0, c0, acc);
-  else outer_sum<RT, false>(p, s, a, r0, c0, acc);
-  join_waves(acc, red);
+  for (int i = 0; i < RT * CT; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
+  outer_sum<RT, CT, F32>(p, s, a, r0, c0, acc);
+  join_waves<kOuterWaves>(acc, red);
   if (threadIdx.x >= kWave) return;
   const int l16 = threadIdx.x & 15, g = threadIdx.x >> 4;
-  const int c = c0 + 8 * l16;
+  const int c = c0 + CT * l16;
   if (c >= s.C) return;
 #pragma unroll
   for (int r = 0; r < RT; ++r)
@@ -619,25 +735,31 @@ __global__ __launch_bounds__(256) void k_adapter_outer(OuterParams p) {
     for (int i = 0; i < 4; ++i) {
       const int q = r0 + 16 * r + 4 * g + i;
       if (q >= p.rank) continue;
-      float v[8];
+      float* dst = s.grad + ((int64_t)a * p.rank + q) * s.C + c;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = acc[r * 8 + j][i];
-      store8(s.grad + ((int64_t)a * p.rank + q) * s.C + c, v);
+      for (int j = 0; j < CT; j += 4) {
+        const float v[4] = {acc[r * CT + j][i], acc[r * CT + j + 1][i], acc[r * CT + j + 2][i], acc[r * CT + j + 3][i]};
+        store4(dst + j, v);
+      }
     }
 }
 
-template <bool F32>
-static void launch_outer(const OuterParams& p, hipStream_t st) {
-  const int64_t cb = p.blocks0 + (p.side[1].C + kExpandCols - 1) / kExpandCols;
-  const unsigned z = p.rank_pad > 64 ? 2 : 1;
-  const dim3 grid((unsigned)cb, (unsigned)p.plan.adapters, z);
-  if (p.rank_pad <= 16) k_adapter_outer<1, F32><<<grid, 256, 0, st>>>(p);
-  else if (p.rank_pad <= 32) k_adapter_outer<2, F32><<<grid, 256, 0, st>>>(p);
-  else k_adapter_outer<4, F32><<<grid, 256, 0, st>>>(p);
+template <int RT, int CT, bool F32>
+static void launch_outer(const OuterParams& p, const OuterSide& s, hipStream_t st) {
+  const dim3 grid((unsigned)((s.C + 16 * CT - 1) / (16 * CT)), (unsigned)p.plan.adapters,
+                  (unsigned)((p.rank_pad + 16 * RT - 1) / (16 * RT)));
+  k_adapter_outer<RT, CT, F32><<<grid, kOuterWaves * kWave, 0, st>>>(p, s);
 }
-hipError_t launch_adapter_outer(const OuterParams& p, bool dout_f32, hipStream_t st) {
-  if (dout_f32) launch_outer<true>(p, st);
-  else launch_outer<false>(p, st);
+hipError_t launch_adapter_outer(const OuterParams& p, const OuterSide& s, bool x_f32, hipStream_t st) {
+  if (x_f32) {
+    if (p.rank_pad <= 16) launch_outer<1, 4, true>(p, s, st);
+    else if (p.rank_pad <= 32) launch_outer<2, 4, true>(p, s, st);
+    else launch_outer<4, 4, true>(p, s, st);
+  } else {
+    if (p.rank_pad <= 16) launch_outer<1, 8, false>(p, s, st);
+    else if (p.rank_pad <= 32) launch_outer<2, 8, false>(p, s, st);
+    else launch_outer<4, 4, false>(p, s, st);
+  }
   return hipGetLastError();
 }
 

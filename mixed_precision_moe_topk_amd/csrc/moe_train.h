@@ -109,37 +109,50 @@ struct PlanView {
   int32_t adapters;
 };
 
-// part[s][row][Rp] = X[token(row)] . W[adapter]^T over the s-th part of K.
+// Scaled low-rank rows as operands of expand (frag) and of outer (saved), in
+// bf16 parts (layouts in moe_adapter.hip); either may be null.
+struct LowRows {
+  uint16_t* frag;
+  uint16_t* saved;
+  int32_t parts;  // of frag: 2, or 3 for float32 results
+  int32_t rank_pad, rank_pad32;
+  int64_t max_rows;
+};
+// X[token(row)] . W[adapter]^T over the s-th part of K: unscaled float32 sums
+// part[s][row][rank_pad], or (part null, one part) the scaled rows.
 struct ShrinkParams {
   PlanView plan;
   const void* x;
   int64_t x_stride;    // elements
   const uint16_t* w;   // [L, R, K] bf16
+  const float* scale;  // [L]
   int32_t rank, rank_pad, K;
   int32_t splits, split_k;
   float* part;
+  LowRows low;
 };
-// out[t] = base[t] + scale * sum_s part[s][row(t)] . W[adapter]
-struct ExpandParams {
-  PlanView plan;
-  const float* part;
-  int32_t splits;
-  const float* scale;  // [L]
-  const uint16_t* w;   // [L, R, N] bf16
-  int32_t rank, rank_pad, N;
-  const void* base;    // or null: 0
-  int64_t base_stride;
-  void* out;
-  int64_t out_stride;
-};
-// saved[0 / 1][r][row] = high / low bf16 halves of scale * sum_s part[s][row][r]
+// The scaled rows from the sums of the parts.
 struct JoinParams {
   PlanView plan;
   const float* part;
   int32_t splits;
   const float* scale;
   int32_t rank_pad;
-  uint16_t* saved;
+  LowRows low;
+};
+// out[t] = base[t] + row(t) . W[adapter], the rows from frag or (null) part.
+struct ExpandParams {
+  PlanView plan;
+  const uint16_t* frag;
+  const float* part;
+  int32_t splits;
+  const float* scale;  // [L]
+  const uint16_t* w;   // [L, R, N] bf16
+  int32_t rank, rank_pad, rank_pad32, N;
+  const void* base;    // or null: 0
+  int64_t base_stride;
+  void* out;
+  int64_t out_stride;
 };
 // grad[adapter][r][c] = sum over the adapter's rows of saved[r][row] * X[token(row)][c]
 struct OuterSide {
@@ -151,13 +164,11 @@ struct OuterSide {
 };
 struct OuterParams {
   PlanView plan;
-  OuterSide side[2];  // [0] bf16 x; [1] dout (bf16 or float32)
   int32_t rank, rank_pad;
-  int32_t blocks0;    // column blocks of side 0
 };
 hipError_t launch_adapter_shrink(const ShrinkParams& p, bool x_f32, hipStream_t st);
 hipError_t launch_adapter_expand(const ExpandParams& p, bool out_f32, hipStream_t st);
 hipError_t launch_adapter_join(const JoinParams& p, hipStream_t st);
-hipError_t launch_adapter_outer(const OuterParams& p, bool dout_f32, hipStream_t st);
+hipError_t launch_adapter_outer(const OuterParams& p, const OuterSide& s, bool x_f32, hipStream_t st);
 
 }  // namespace moe

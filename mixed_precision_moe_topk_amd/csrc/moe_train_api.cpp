@@ -94,29 +94,34 @@ moe_status check_stride(int64_t stride, int64_t features) {
 
 int32_t rank_pad(const moe_adapter_dims* d) { return (d->rank + 15) / 16 * 16; }
 
-// Parts of a contraction over `features`: enough blocks for the GPU's 256 CUs
-// where the tiles alone are few, 256 elements a part at least.
+// Parts of a contraction over `features`: about one block (tile and part) for
+// each of the 256 CUs, 256 elements a part at least.
 int32_t splits_of(int64_t max_tiles, int64_t features) {
-  const int64_t want = ceil_div(1024, std::max<int64_t>(1, max_tiles));
-  return (int32_t)std::max<int64_t>(1, std::min<int64_t>({want, ceil_div(features, 256), 32}));
+  const int64_t want = ceil_div(256, std::max<int64_t>(1, max_tiles));
+  return (int32_t)std::max<int64_t>(1, std::min<int64_t>({want, ceil_div(features, 256), 8}));
 }
 int32_t split_width(int64_t features, int32_t splits) {
   return (int32_t)(ceil_div(ceil_div(features, splits), 64) * 64);
 }
 
+// Up to so many tokens expand adds up the parts for itself.
+constexpr int64_t kFewTokens = 128;
+
+// Workspace: the parts of the larger contraction, expand's operands, and the
+// backward pass's v as outer's operands.
 struct AdapterLayout {
   moe::PlanLayout plan;
-  int32_t rp, splits_x, splits_d;
-  size_t part_bytes;   // the larger direction's partial sums
-  size_t saved_bytes;  // u or v as bf16 halves
+  int32_t rp, rp32, splits_x, splits_d;
+  size_t part_bytes, frag_bytes, saved_bytes;
   AdapterLayout(const moe_adapter_dims* d, int64_t tokens)
-      : plan(d->num_adapters, tokens), rp(rank_pad(d)) {
+      : plan(d->num_adapters, tokens), rp(rank_pad(d)), rp32((d->rank + 31) / 32 * 32) {
     splits_x = splits_of(plan.max_tiles, d->in_features);
     splits_d = splits_of(plan.max_tiles, d->out_features);
     part_bytes = align256((size_t)std::max(splits_x, splits_d) * plan.max_rows * rp * 4);
-    saved_bytes = align256((size_t)plan.max_rows * rp * 4);
+    frag_bytes = align256((size_t)plan.max_rows * rp32 * 6);
+    saved_bytes = align256((size_t)plan.max_rows * rp * 6);
   }
-  size_t workspace() const { return part_bytes + saved_bytes; }
+  size_t workspace() const { return part_bytes + frag_bytes + saved_bytes; }
 };
 
 moe::PlanView plan_view(const void* plan, const moe::PlanLayout& l, int32_t adapters,
@@ -134,51 +139,61 @@ moe::PlanView plan_view(const void* plan, const moe::PlanLayout& l, int32_t adap
   return v;
 }
 
-moe::ShrinkParams shrink_params(const moe::PlanView& v, const AdapterLayout& l, int32_t rank,
-                                const void* x, int64_t stride, const void* w, int32_t features,
-                                int32_t splits, void* workspace) {
+// One product with a factor on each side: shrink of x with w, then (out not
+// null) expand with w2; `saved` (or null) takes the low-rank rows.
+struct Product {
+  const void* x;
+  int64_t x_stride;
+  const void* w;
+  int32_t features, splits;
+  bool x_f32;
+  const void* w2;
+  int32_t features2;
+  const void* base;
+  int64_t base_stride;
+  void* out;
+  int64_t out_stride;
+  bool out_f32;
+  void* saved;
+};
+
+moe_status run_product(const Product& q, const moe::PlanView& v, const AdapterLayout& l,
+                       int32_t rank, const float* scale, void* workspace, hipStream_t stream) {
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  float* part = reinterpret_cast<float*>(ws);
+  const bool few = v.tokens <= kFewTokens;  // expand takes the parts themselves
+  moe::LowRows low;
+  low.frag = few || !q.out ? nullptr : reinterpret_cast<uint16_t*>(ws + l.part_bytes);
+  low.saved = static_cast<uint16_t*>(q.saved);
+  low.parts = q.out_f32 ? 3 : 2;
+  low.rank_pad = l.rp;
+  low.rank_pad32 = l.rp32;
+  low.max_rows = l.plan.max_rows;
   moe::ShrinkParams s;
   s.plan = v;
-  s.x = x;
-  s.x_stride = stride;
-  s.w = static_cast<const uint16_t*>(w);
+  s.x = q.x;
+  s.x_stride = q.x_stride;
+  s.w = static_cast<const uint16_t*>(q.w);
+  s.scale = scale;
   s.rank = rank;
   s.rank_pad = l.rp;
-  s.K = features;
-  s.split_k = split_width(features, splits);
-  s.splits = (int32_t)ceil_div(features, s.split_k);
-  s.part = static_cast<float*>(workspace);
-  return s;
-}
-
-moe::ExpandParams expand_params(const moe::ShrinkParams& s, const float* scale, const void* w,
-                                int32_t features, const void* base, int64_t base_stride, void* out,
-                                int64_t out_stride) {
-  moe::ExpandParams e;
-  e.plan = s.plan;
-  e.part = s.part;
-  e.splits = s.splits;
-  e.scale = scale;
-  e.w = static_cast<const uint16_t*>(w);
-  e.rank = s.rank;
-  e.rank_pad = s.rank_pad;
-  e.N = features;
-  e.base = base;
-  e.base_stride = base_stride;
-  e.out = out;
-  e.out_stride = out_stride;
-  return e;
-}
-
-moe::JoinParams join_params(const moe::ShrinkParams& s, const float* scale, void* saved) {
-  moe::JoinParams j;
-  j.plan = s.plan;
-  j.part = s.part;
-  j.splits = s.splits;
-  j.scale = scale;
-  j.rank_pad = s.rank_pad;
-  j.saved = static_cast<uint16_t*>(saved);
-  return j;
+  s.K = q.features;
+  s.split_k = split_width(q.features, q.splits);
+  s.splits = (int32_t)ceil_div(q.features, s.split_k);
+  const bool direct = s.splits == 1 && !few;  // shrink writes the rows itself
+  s.part = direct ? nullptr : part;
+  s.low = low;
+  if (!direct) s.low.frag = s.low.saved = nullptr;
+  MOE_RETURN_IF(moe::check_hip(moe::launch_adapter_shrink(s, q.x_f32, stream), "adapter shrink", stream));
+  if (!direct && (low.frag || low.saved)) {
+    const moe::JoinParams j = {v, part, s.splits, scale, l.rp, low};
+    MOE_RETURN_IF(moe::check_hip(moe::launch_adapter_join(j, stream), "adapter join", stream));
+  }
+  if (!q.out) return MOE_OK;
+  const moe::ExpandParams e = {v, low.frag, part, s.splits, scale, static_cast<const uint16_t*>(q.w2),
+                               rank, l.rp, l.rp32, q.features2, q.base, q.base_stride, q.out,
+                               q.out_stride};
+  return moe::check_hip(moe::launch_adapter_expand(e, q.out_f32, stream), "adapter expand", stream);
 }
 
 }  // namespace
@@ -347,17 +362,9 @@ moe_status moe_adapter_apply(const moe_adapter_dims* dims, const void* x, int64_
   if (saved) MOE_RETURN_IF(check_room(saved_bytes, l.saved_bytes, "saved"));
   MOE_RETURN_IF(moe::check_gfx950());
   const moe::PlanView v = plan_view(plan, l.plan, dims->num_adapters, num_tokens);
-  const moe::ShrinkParams s = shrink_params(v, l, dims->rank, x, x_stride, a, dims->in_features,
-                                            l.splits_x, workspace);
-  MOE_RETURN_IF(moe::check_hip(moe::launch_adapter_shrink(s, false, stream), "adapter shrink", stream));
-  if (saved)
-    MOE_RETURN_IF(moe::check_hip(moe::launch_adapter_join(join_params(s, scale, saved), stream),
-                                 "adapter join", stream));
-  MOE_RETURN_IF(moe::check_hip(
-      moe::launch_adapter_expand(expand_params(s, scale, b, dims->out_features, base, base_stride,
-                                               out, out_stride),
-                                 dims->out_type == MOE_T_F32, stream),
-      "adapter expand", stream));
+  const Product q = {x, x_stride, a, dims->in_features, l.splits_x, false, b, dims->out_features,
+                     base, base_stride, out, out_stride, dims->out_type == MOE_T_F32, saved};
+  MOE_RETURN_IF(run_product(q, v, l, dims->rank, scale, workspace, stream));
   return moe::set_ok();
 }
 
@@ -396,30 +403,20 @@ moe_status moe_adapter_backward(const moe_adapter_dims* dims, const void* dout,
   MOE_RETURN_IF(moe::check_gfx950());
   const moe::PlanView v = plan_view(plan, l.plan, dims->num_adapters, num_tokens);
   const bool f32 = dims->out_type == MOE_T_F32;
-  uint8_t* vt = static_cast<uint8_t*>(workspace) + l.part_bytes;
+  void* vt = num_tokens > 0 ? static_cast<uint8_t*>(workspace) + l.part_bytes + l.frag_bytes : nullptr;
   if (num_tokens > 0) {
-    const moe::ShrinkParams s = shrink_params(v, l, dims->rank, dout, dout_stride, b,
-                                              dims->out_features, l.splits_d, workspace);
-    MOE_RETURN_IF(moe::check_hip(moe::launch_adapter_shrink(s, f32, stream), "adapter shrink", stream));
-    if (dx)
-      MOE_RETURN_IF(moe::check_hip(
-          moe::launch_adapter_expand(expand_params(s, scale, a, dims->in_features, dx_base,
-                                                   dx_base_stride, dx, dx_stride),
-                                     false, stream),
-          "adapter expand", stream));
-    if (da)
-      MOE_RETURN_IF(moe::check_hip(moe::launch_adapter_join(join_params(s, scale, vt), stream),
-                                   "adapter join", stream));
+    const Product q = {dout, dout_stride, b, dims->out_features, l.splits_d, f32, a,
+                       dims->in_features, dx_base, dx_base_stride, dx, dx_stride, false,
+                       da ? vt : nullptr};
+    MOE_RETURN_IF(run_product(q, v, l, dims->rank, scale, workspace, stream));
   }
   if (!da) return moe::set_ok();
-  moe::OuterParams o;
-  o.plan = v;
-  o.rank = dims->rank;
-  o.rank_pad = l.rp;
-  o.blocks0 = (int32_t)ceil_div(dims->in_features, 128);
-  o.side[0] = {reinterpret_cast<const uint16_t*>(vt), x, x_stride, dims->in_features, da};
-  o.side[1] = {static_cast<const uint16_t*>(saved), dout, dout_stride, dims->out_features, db};
-  MOE_RETURN_IF(moe::check_hip(moe::launch_adapter_outer(o, f32, stream), "adapter gradients", stream));
+  const moe::OuterParams o = {v, dims->rank, l.rp};
+  const moe::OuterSide sa = {static_cast<const uint16_t*>(vt), x, x_stride, dims->in_features, da};
+  const moe::OuterSide sb = {static_cast<const uint16_t*>(saved), dout, dout_stride,
+                             dims->out_features, db};
+  MOE_RETURN_IF(moe::check_hip(moe::launch_adapter_outer(o, sa, false, stream), "adapter da", stream));
+  MOE_RETURN_IF(moe::check_hip(moe::launch_adapter_outer(o, sb, f32, stream), "adapter db", stream));
   return moe::set_ok();
 }
 
