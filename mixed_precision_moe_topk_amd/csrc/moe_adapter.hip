@@ -99,10 +99,11 @@ __device__ int32_t plan_scan(const PlanParams& p, const PlanLayout& l, int32_t n
       t.pad = 0;
       tiles[tile0 + i] = t;
     }
-    if (e == G - 1) {
+    if (e == G - 1) {  // the group without an adapter comes last
       p.plan[l.first + G] = row0 + pad;
       p.plan[0] = tile0 + nt;
       p.plan[1] = row0 + pad;
+      p.plan[2] = tile0;
     }
   }
   return row0;
@@ -320,153 +321,190 @@ __device__ __forceinline__ void put_low(const LowRows& o, int64_t row0, int r, c
 }
 
 // ---------------------------------------------------------------- shrink
-// Operands of one 64-wide step of K: lane (l16, g) holds elements [8 g, 8 g +
-// 8) of each 32-wide half, of W row l16 of a rank block and of X row l16 of a
-// row block.
-template <int MT, int RT>
-struct ShrinkStep {
-  v8bf a[2][RT], x[2][MT];
-  template <bool GUARD>
-  __device__ __forceinline__ void load(const uint16_t* const (&xp)[MT], const uint16_t* const (&wp)[RT], int k0,
-                                       int ke) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = k0 + 32 * h + 8 * (lane_id() / 16);
-      const bool in = !GUARD || k < ke;
-#pragma unroll
-      for (int m = 0; m < MT; ++m) x[h][m] = load_bf16x8(xp[m] + k, in);
-#pragma unroll
-      for (int r = 0; r < RT; ++r) a[h][r] = load_bf16x8(wp[r] + k, in);
-    }
-  }
-  __device__ __forceinline__ void add(v4f (&acc)[MT * RT]) const {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int r = 0; r < RT; ++r) acc[m * RT + r] = mfma_bf16(a[h][r], x[h][m], acc[m * RT + r]);
-  }
+// The work is cut into units, kShrinkK elements of K of one tile, and every
+// block takes an equal run of them, which ends inside a tile: as many tiles as
+// CUs, or a few more, would leave most CUs waiting for those with two.  A tile
+// is then summed by several blocks (`slots`, at most kMaxSlots), whose float32
+// sums meet in the join or in expand.
+struct ShrinkRuns {
+  int32_t units;  // of a tile
+  int32_t run;    // units of a block
+  int64_t total;
 };
-
-// The same step with float32 X, in three parts.
-template <int MT, int RT, bool GUARD>
-__device__ __forceinline__ void shrink_f32(const float* const (&xp)[MT], const uint16_t* const (&wp)[RT], int k0,
-                                           int ke, v4f (&acc)[MT * RT]) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int k = k0 + 32 * h + 8 * (lane_id() / 16);
-    const bool in = !GUARD || k < ke;
-    v8bf a[RT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) a[r] = load_bf16x8(wp[r] + k, in);
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      float v[8];
-      v8bf x[3];
-      load_f32x8(xp[m] + k, in, v);
-      split8<3>(v, x);
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int q = 2; q >= 0; --q) acc[m * RT + r] = mfma_bf16(a[r], x[q], acc[m * RT + r]);
-    }
-  }
+__device__ __forceinline__ ShrinkRuns shrink_runs(const PlanView& v, const ShrinkShape& s) {
+  ShrinkRuns r;
+  r.units = s.units;
+  const int64_t tiles = max(0, min(v.head[2], (int32_t)v.max_tiles));
+  r.total = tiles * s.units;
+  const int64_t each = (r.total + kShrinkBlocks - 1) / kShrinkBlocks;
+  r.run = (int32_t)max((int64_t)s.min_run, each);
+  return r;
+}
+// First of the blocks that sum tile i, and how many they are.
+__device__ __forceinline__ int shrink_first(const ShrinkRuns& r, int64_t i) { return (int)(i * r.units / r.run); }
+__device__ __forceinline__ int shrink_slots(const ShrinkRuns& r, int64_t i) {
+  return (int)((i * r.units + r.units - 1) / r.run) - shrink_first(r, i) + 1;
 }
 
-template <int MT, int RT, bool F32>
-__device__ __forceinline__ void shrink_tile(const ShrinkParams& p, const Tile& tile, int split, v4f* red) {
+template <int RT>
+struct ShrinkLds {
+  static constexpr int KC = RT <= 4 ? 128 : 64;  // elements of K staged at once
+  static constexpr int P = KC + 8;               // row pitch: 16-byte reads of 16 rows meet all banks
+  static constexpr int kWords = 2 * (kAdapterTile + 16 * RT) * P;
+};
+
+// Rows that fill less than two matrix row blocks: operands straight from
+// memory, the waves taking the 64-wide steps of [k0, ke) in turn (FEW; their
+// sums are joined), or all of them for 16 rows each.
+template <int RT, bool F32, bool FEW>
+__device__ __forceinline__ void shrink_direct(const ShrinkParams& p, const Tile& tile, int k0, int ke, v4f (&acc)[RT],
+                                              v4f* red) {
   typedef std::conditional_t<F32, float, uint16_t> X;
-  const int lane = lane_id(), w = threadIdx.x / kWave;
-  const int l16 = lane & 15, g = lane >> 4;
-  const X* xp[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    // rows behind the tile's last repeat it; their sums are put as 0
-    const int64_t t = plan_token(p.plan, tile.row0 + min(16 * m + l16, tile.nrows - 1));
-    xp[m] = static_cast<const X*>(p.x) + (t < 0 ? 0 : t) * p.x_stride;
-  }
+  const int lane = lane_id(), w = threadIdx.x / kWave, l16 = lane & 15, g = lane >> 4;
+  // rows behind the tile's last repeat it; their sums are dropped
+  const int64_t t = plan_token(p.plan, tile.row0 + min((FEW ? 0 : 16 * w) + l16, tile.nrows - 1));
+  const X* xp = static_cast<const X*>(p.x) + (t < 0 ? 0 : t) * p.x_stride + 8 * g;
   const uint16_t* wp[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r)
-    wp[r] = p.w + ((int64_t)tile.expert * p.rank + min(16 * r + l16, p.rank - 1)) * p.K;
-  v4f acc[MT * RT];
+    wp[r] = p.w + ((int64_t)tile.expert * p.rank + min(16 * r + l16, p.rank - 1)) * p.K + 8 * g;
+  for (int k = k0 + (FEW ? 64 * w : 0); k < ke; k += FEW ? 256 : 64) {
+    v8bf a[2][RT], x[2][F32 ? 3 : 1];
 #pragma unroll
-  for (int i = 0; i < MT * RT; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
-  const int kb = split * p.split_k, ke = min(p.K, kb + p.split_k);
-  int k = kb + 64 * w;
-  if constexpr (F32) {
-    for (; k + 64 <= ke; k += 256) shrink_f32<MT, RT, false>(xp, wp, k, ke, acc);
-    if (k < ke) shrink_f32<MT, RT, true>(xp, wp, k, ke, acc);
-  } else {
-    // the next step's loads run under this one's products
-    ShrinkStep<MT, RT> s;
-    if (k + 64 <= ke) {
-      s.template load<false>(xp, wp, k, ke);
-      for (k += 256; k + 64 <= ke; k += 256) {
-        ShrinkStep<MT, RT> next;
-        next.template load<false>(xp, wp, k, ke);
-        s.add(acc);
-        s = next;
+    for (int h = 0; h < 2; ++h) {
+      const bool in = k + 32 * h + 8 * g < ke;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) a[h][r] = load_bf16x8(wp[r] + k + 32 * h, in);
+      if constexpr (F32) {
+        float v[8];
+        load_f32x8(xp + k + 32 * h, in, v);
+        split8<3>(v, x[h]);
+      } else {
+        x[h][0] = load_bf16x8(xp + k + 32 * h, in);
       }
-      s.add(acc);
     }
-    if (k < ke) {
-      s.template load<true>(xp, wp, k, ke);
-      s.add(acc);
-    }
-  }
-  join_waves<4>(acc, red);
-  if (w != 0) return;
-  // lane: row l16 of a row block, ranks [4 g, 4 g + 4) of a rank block
-  float* part = p.part + (int64_t)split * p.plan.max_rows * p.rank_pad;
-  const float scale = p.low.frag || p.low.saved ? p.scale[tile.expert] : 1.0f;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    if (16 * m >= tile.nrows) break;
-    const bool live = 16 * m + l16 < tile.nrows;
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int q = F32 ? 2 : 0; q >= 0; --q) acc[r] = mfma_bf16(a[h][r], x[h][q], acc[r]);
+  }
+  if constexpr (FEW) join_waves<4>(acc, red);
+}
+
+// A whole tile: KC elements of K of its rows and of the factor pass through
+// LDS, read from memory in whole row pieces (256 bytes at RT <= 4; 16 rows of 64
+// bytes, as the matrix operands lie, ran at two thirds of the speed), the next
+// piece under this one's products.  Wave w sums rows [16 w, 16 w + 16).
+template <int RT>
+__device__ __forceinline__ void shrink_staged(const ShrinkParams& p, const Tile& tile, int k0, int ke, v4f (&acc)[RT],
+                                              uint16_t* lds) {
+  constexpr int KC = ShrinkLds<RT>::KC, P = ShrinkLds<RT>::P;
+  constexpr int VR = KC / 8, ROWS = 256 / VR;               // vectors of a row, rows a pass
+  constexpr int NX = kAdapterTile / ROWS, NA = (16 * RT + ROWS - 1) / ROWS;
+  const int lane = lane_id(), w = threadIdx.x / kWave, l16 = lane & 15, g = lane >> 4;
+  const int row = threadIdx.x / VR, col = threadIdx.x % VR * 8;
+  uint16_t* sx = lds;
+  uint16_t* sa = lds + 2 * kAdapterTile * P;
+  const uint16_t *xp[NX], *wp[NA];
+#pragma unroll
+  for (int i = 0; i < NX; ++i) {
+    const int64_t t = plan_token(p.plan, tile.row0 + min(i * ROWS + row, tile.nrows - 1));
+    xp[i] = static_cast<const uint16_t*>(p.x) + (t < 0 ? 0 : t) * p.x_stride + col;
+  }
+#pragma unroll
+  for (int i = 0; i < NA; ++i)
+    wp[i] = p.w + ((int64_t)tile.expert * p.rank + min(i * ROWS + row, p.rank - 1)) * p.K + col;
+  v4u rx[NX], ra[NA];
+  const auto load = [&](int k) {
+    const bool in = k + col < ke;
+#pragma unroll
+    for (int i = 0; i < NX; ++i)
+      rx[i] = in ? __builtin_nontemporal_load(reinterpret_cast<const v4u*>(xp[i] + k)) : v4u{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < NA; ++i) ra[i] = in ? *reinterpret_cast<const v4u*>(wp[i] + k) : v4u{0, 0, 0, 0};
+  };
+  const auto put = [&](int b) {
+#pragma unroll
+    for (int i = 0; i < NX; ++i)
+      *reinterpret_cast<v4u*>(sx + (b * kAdapterTile + i * ROWS + row) * P + col) = rx[i];
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (NA * ROWS == 16 * RT || i * ROWS + row < 16 * RT)
+        *reinterpret_cast<v4u*>(sa + (b * 16 * RT + i * ROWS + row) * P + col) = ra[i];
+  };
+  load(k0);
+  put(0);
+  __syncthreads();
+  int b = 0;
+  for (int k = k0; k < ke; k += KC, b ^= 1) {
+    const bool more = k + KC < ke;
+    if (more) load(k + KC);
+    const uint16_t* x = sx + (b * kAdapterTile + 16 * w + l16) * P + 8 * g;
+    const uint16_t* a = sa + (b * 16 * RT + l16) * P + 8 * g;
+#pragma unroll
+    for (int s = 0; s < KC; s += 32) {
+      const v8bf xs = *reinterpret_cast<const v8bf*>(x + s);
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+        acc[r] = mfma_bf16(*reinterpret_cast<const v8bf*>(a + 16 * r * P + s), xs, acc[r]);
+    }
+    if (more) put(b ^ 1);
+    __syncthreads();
+  }
+}
+
+// kShrinkBlocks blocks, two a CU; block b runs on XCD b % 8, and neighbouring
+// runs, mostly of one adapter, go to one XCD, whose L2 then holds its factor.
+template <int RT, bool F32>
+__global__ __launch_bounds__(256) void k_adapter_shrink(ShrinkParams p) {
+  constexpr int kLds = F32 ? 16 : ShrinkLds<RT>::kWords;
+  __shared__ uint4 lds[(kLds * 2 > 2 * RT * kWave * 16 ? kLds * 2 : 2 * RT * kWave * 16) / 16];
+  const int lane = lane_id(), w = threadIdx.x / kWave, l16 = lane & 15, g = lane >> 4;
+  const ShrinkRuns runs = shrink_runs(p.plan, p.shape);
+  const int me = (int)(blockIdx.x % 8 * (kShrinkBlocks / 8) + blockIdx.x / 8);
+  int64_t u = (int64_t)me * runs.run;
+  const int64_t end = min(u + runs.run, runs.total);
+  while (u < end) {
+    const int64_t i = u / runs.units;
+    const int c0 = (int)(u - i * runs.units), c1 = (int)min((int64_t)runs.units, c0 + end - u);
+    u += c1 - c0;
+    Tile tile;
+    if (!plan_tile(p.plan, i, &tile) || tile.expert == p.plan.adapters) return;
+    const int k0 = c0 * kShrinkK, ke = min(p.K, c1 * kShrinkK);
+    const bool few = tile.nrows <= 16;
+    v4f acc[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[r] = v4f{0.f, 0.f, 0.f, 0.f};
+    if (few) shrink_direct<RT, F32, true>(p, tile, k0, ke, acc, reinterpret_cast<v4f*>(lds));
+    else if constexpr (F32) {
+      if (16 * w < tile.nrows) shrink_direct<RT, F32, false>(p, tile, k0, ke, acc, nullptr);
+    } else {
+      shrink_staged<RT>(p, tile, k0, ke, acc, reinterpret_cast<uint16_t*>(lds));
+    }
+    // lane: row l16 of the wave's 16, ranks [4 g, 4 g + 4) of a rank block
+    const int row = (few ? 0 : 16 * w) + l16;
+    if ((few && w > 0) || (!few && 16 * w >= tile.nrows)) continue;
+    float* part = p.part + (me - shrink_first(runs, i)) * p.plan.max_rows * p.rank_pad +
+                  (tile.row0 + row) * (int64_t)p.rank_pad + 4 * g;
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
       if (16 * r >= p.rank_pad) break;
-      v4f v = acc[m * RT + r];
+      v4f v = acc[r];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = live && 16 * r + 4 * g + i < p.rank ? v[i] * scale : 0.0f;
-      if (p.part)
-        *reinterpret_cast<v4f*>(part + (int64_t)(tile.row0 + 16 * m + l16) * p.rank_pad + 16 * r + 4 * g) = v;
-      else if (p.low.parts == 3)
-        put_low<3>(p.low, tile.row0 + 16 * m, r, v);
-      else
-        put_low<2>(p.low, tile.row0 + 16 * m, r, v);
+      for (int q = 0; q < 4; ++q) v[q] = row < tile.nrows && 16 * r + 4 * g + q < p.rank ? v[q] : 0.0f;
+      *reinterpret_cast<v4f*>(part + 16 * r) = v;
     }
   }
-}
-
-// Tile of block b: neighbouring tiles, mostly of one adapter, on one of the 8
-// XCDs (block b runs on XCD b % 8), so that its L2 holds their factor.
-__device__ __forceinline__ int64_t xcd_tile(const PlanView& v, int64_t b) {
-  const int64_t each = (v.head[0] + 7) / 8;
-  return b / 8 < each ? b % 8 * each + b / 8 : v.max_tiles;
-}
-
-// Block (tile, split): the four waves take the split's 64-wide steps of K in
-// turn and join their sums.
-template <int RT, bool F32>
-__global__ __launch_bounds__(256) void k_adapter_shrink(ShrinkParams p) {
-  __shared__ v4f red[2 * 4 * RT * kWave];
-  Tile tile;
-  if (!plan_tile(p.plan, xcd_tile(p.plan, blockIdx.x), &tile) || tile.expert == p.plan.adapters) return;
-  if (tile.nrows <= 16) shrink_tile<1, RT, F32>(p, tile, blockIdx.y, red);
-  else if (tile.nrows <= 32) shrink_tile<2, RT, F32>(p, tile, blockIdx.y, red);
-  else shrink_tile<4, RT, F32>(p, tile, blockIdx.y, red);
 }
 
 template <bool F32>
 static void launch_shrink(const ShrinkParams& p, hipStream_t st) {
-  const dim3 grid((unsigned)((p.plan.max_tiles + 7) / 8 * 8), (unsigned)p.splits);
-  if (p.rank_pad <= 16) k_adapter_shrink<1, F32><<<grid, 256, 0, st>>>(p);
-  else if (p.rank_pad <= 32) k_adapter_shrink<2, F32><<<grid, 256, 0, st>>>(p);
-  else if (p.rank_pad <= 64) k_adapter_shrink<4, F32><<<grid, 256, 0, st>>>(p);
-  else k_adapter_shrink<8, F32><<<grid, 256, 0, st>>>(p);
+  if (p.rank_pad <= 16) k_adapter_shrink<1, F32><<<kShrinkBlocks, 256, 0, st>>>(p);
+  else if (p.rank_pad <= 32) k_adapter_shrink<2, F32><<<kShrinkBlocks, 256, 0, st>>>(p);
+  else if (p.rank_pad <= 64) k_adapter_shrink<4, F32><<<kShrinkBlocks, 256, 0, st>>>(p);
+  else k_adapter_shrink<8, F32><<<kShrinkBlocks, 256, 0, st>>>(p);
 }
 hipError_t launch_adapter_shrink(const ShrinkParams& p, bool x_f32, hipStream_t st) {
   if (x_f32) launch_shrink<true>(p, st);
@@ -475,7 +513,7 @@ hipError_t launch_adapter_shrink(const ShrinkParams& p, bool x_f32, hipStream_t 
 }
 
 // ---------------------------------------------------------------- join
-// The splits' sums of a tile, scaled, into frag and saved: a wave for 16 rows
+// The blocks' sums of a tile, scaled, into frag and saved: a wave for 16 rows
 // and 16 ranks.
 __global__ __launch_bounds__(256) void k_adapter_join(JoinParams p) {
   Tile tile;
@@ -483,20 +521,18 @@ __global__ __launch_bounds__(256) void k_adapter_join(JoinParams p) {
   const int lane = lane_id(), l16 = lane & 15, g = lane >> 4, ranks = p.rank_pad / 16;
   const int64_t step = p.plan.max_rows * (int64_t)p.rank_pad;
   const float scale = p.scale[tile.expert];
+  const int slots = min(shrink_slots(shrink_runs(p.plan, p.shape), blockIdx.x), kMaxSlots);
   const int blocks = (tile.nrows + 15) / 16 * ranks;
   for (int i = blockIdx.y * 4 + threadIdx.x / kWave; i < blocks; i += 4 * gridDim.y) {
     const int64_t row0 = tile.row0 + 16 * (i / ranks);
     const int r = i % ranks;
     const float* s = p.part + (row0 + l16) * p.rank_pad + 16 * r + 4 * g;
-    v4f v = {0.f, 0.f, 0.f, 0.f};
-    for (int q0 = 0; q0 < p.splits; q0 += 4) {
-      v4f x[4];
+    v4f x[kMaxSlots], v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        x[q] = q0 + q < p.splits ? *reinterpret_cast<const v4f*>(s + (q0 + q) * step) : v4f{0.f, 0.f, 0.f, 0.f};
+    for (int q = 0; q < kMaxSlots; ++q)
+      x[q] = q < slots ? *reinterpret_cast<const v4f*>(s + q * step) : v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v += x[q];
-    }
+    for (int q = 0; q < kMaxSlots; ++q) v += x[q];
     v *= scale;
     if (p.low.parts == 3) put_low<3>(p.low, row0, r, v);
     else put_low<2>(p.low, row0, r, v);
@@ -509,104 +545,123 @@ hipError_t launch_adapter_join(const JoinParams& p, hipStream_t st) {
 }
 
 // ---------------------------------------------------------------- expand
-constexpr int kExpandCols = 64;  // columns of a wave
+constexpr int kExpandCols = 128;  // columns of a wave
 
-__device__ __forceinline__ void load4(const uint16_t* p, float (&v)[4]) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  v[0] = __uint_as_float(u.x << 16);
-  v[1] = __uint_as_float(u.x & 0xFFFF0000u);
-  v[2] = __uint_as_float(u.y << 16);
-  v[3] = __uint_as_float(u.y & 0xFFFF0000u);
-}
-__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
-  const float4 a = *reinterpret_cast<const float4*>(p);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-}
-__device__ __forceinline__ void store4(uint16_t* p, const float (&v)[4]) {
-  typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
-  *reinterpret_cast<v4bf*>(p) = v4bf{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-}
-__device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-}
+// 8 elements of a row; read once and written once, so past the caches.
+struct Row8Bf16 {
+  v4u w;
+  __device__ __forceinline__ void load(const uint16_t* p) {
+    w = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(p));
+  }
+  __device__ __forceinline__ float get(int j) const {
+    return __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+  }
+  __device__ __forceinline__ static void store(uint16_t* p, const float (&v)[8]) {
+    v8bf o;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = (__bf16)v[j];
+    __builtin_nontemporal_store(__builtin_bit_cast(v4u, o), reinterpret_cast<v4u*>(p));
+  }
+};
+struct Row8F32 {
+  v4f w[2];
+  __device__ __forceinline__ void load(const float* p) {
+    w[0] = __builtin_nontemporal_load(reinterpret_cast<const v4f*>(p));
+    w[1] = __builtin_nontemporal_load(reinterpret_cast<const v4f*>(p) + 1);
+  }
+  __device__ __forceinline__ float get(int j) const { return w[j / 4][j % 4]; }
+  __device__ __forceinline__ static void store(float* p, const float (&v)[8]) {
+    __builtin_nontemporal_store(v4f{v[0], v[1], v[2], v[3]}, reinterpret_cast<v4f*>(p));
+    __builtin_nontemporal_store(v4f{v[4], v[5], v[6], v[7]}, reinterpret_cast<v4f*>(p) + 1);
+  }
+};
 
-// A wave's 64 columns of a tile.  The factor's columns stay in registers, as
+// A wave's 128 columns of a tile.  The factor's columns stay in registers, as
 // matrix operands of all its ranks, while the tile's row blocks pass: lane
-// (l16, g) holds columns 4 l16 + j, which are column l16 of matrix j, and of
-// the sums rows 4 g + i, so it reads and writes 4 consecutive elements of a row
-// and a lane group 128 bytes (bf16).  RT: blocks of 32 ranks.  JOINED: the
-// low-rank rows come as operands (frag); else as the splits' float32 sums, which
-// every wave adds up for itself: less time than a launch that does it once,
-// where there are few rows.
+// (l16, g) holds columns 8 l16 + j, which are column l16 of matrix j, and of
+// the sums rows 4 g + i, so it reads and writes 8 consecutive elements of a
+// row.  RT: blocks of 32 ranks.  JOINED: the low-rank rows come as operands
+// (frag); else as the float32 sums of shrink's blocks, which every wave adds up
+// for itself: less time than a launch that does it once, where rows are few.
 template <int RT, typename T, bool JOINED>
 __global__ __launch_bounds__(256) void k_adapter_expand(ExpandParams p) {
   constexpr int PARTS = sizeof(T) == 4 ? 3 : 2;
+  typedef std::conditional_t<sizeof(T) == 4, Row8F32, Row8Bf16> Row8;
+  // neighbouring blocks on one XCD (block b runs on XCD b % 8), columns first:
+  // its blocks cover whole rows of one tile and share a factor
+  const int64_t total = (int64_t)min(p.plan.head[0], (int32_t)p.plan.max_tiles) * p.col_blocks;
+  const int64_t each = (total + 7) / 8, id = blockIdx.x % 8 * each + blockIdx.x / 8;
+  if (blockIdx.x / 8 >= each || id >= total) return;
   Tile tile;
-  if (!plan_tile(p.plan, blockIdx.y, &tile)) return;
-  const int n0 = (blockIdx.x * (blockDim.x / kWave) + threadIdx.x / kWave) * kExpandCols;
-  const int lane = lane_id(), l16 = lane & 15, g = lane >> 4;
-  const int n = n0 + 4 * l16;
-  const bool in = n < p.N;
+  if (!plan_tile(p.plan, id / p.col_blocks, &tile)) return;
+  const int n0 = (int)((id % p.col_blocks) * (blockDim.x / kWave) + threadIdx.x / kWave) * kExpandCols;
   if (n0 >= p.N) return;
+  const int lane = lane_id(), l16 = lane & 15, g = lane >> 4;
+  const bool in = n0 + 8 * l16 < p.N;
+  const int n = in ? n0 + 8 * l16 : 0;  // columns behind the last read the first and store nothing
   const T* base = static_cast<const T*>(p.base);
   T* out = static_cast<T*>(p.out);
   const bool low = tile.expert != p.plan.adapters;
   if (!low && p.base == p.out && p.base) return;  // no adapter, and the base is in place
 
-  v8bf b[RT][4];
+  v8bf b[RT][8];
   if (low) {
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      uint32_t raw[8][2];
+      uint32_t raw[8][4];
+      const uint16_t* w = p.w + ((int64_t)tile.expert * p.rank + 32 * r + 8 * g) * p.N + n;
+      const int left = p.rank - 32 * r - 8 * g;  // ranks of this lane's 8
+      if (32 * (r + 1) <= p.rank) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int q = 32 * r + 8 * g + i;
-        load_words<2>(p.w + ((int64_t)tile.expert * p.rank + q) * p.N + n, in && q < p.rank, raw[i]);
+        for (int i = 0; i < 8; ++i) load_words<4>(w + (int64_t)i * p.N, true, raw[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) load_words<4>(w + (int64_t)i * p.N, i < left, raw[i]);
       }
-      transpose8<2>(raw, b[r]);
+      transpose8<4>(raw, b[r]);
     }
   }
   const int64_t step = p.plan.max_rows * (int64_t)p.rank_pad;
   const float scale = low && !JOINED ? p.scale[tile.expert] : 0.0f;
+  const int slots = low && !JOINED
+                        ? min(shrink_slots(shrink_runs(p.plan, p.shape), id / p.col_blocks), kMaxSlots) : 0;
+#pragma unroll 1
   for (int m = 0; 16 * m < tile.nrows; ++m) {
     int64_t t[4];
-    float v[4][4];
+    Row8 v[4];
+    // a row behind the last reads the last one's base and stores nothing
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = 16 * m + 4 * g + i;
-      t[i] = in && row < tile.nrows ? plan_token(p.plan, tile.row0 + row) : -1;
+    for (int i = 0; i < 4; ++i)
+      t[i] = max((int64_t)0, plan_token(p.plan, tile.row0 + min(16 * m + 4 * g + i, tile.nrows - 1)));
+    if (base) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[i][j] = 0.0f;
-      if (base && t[i] >= 0) load4(base + t[i] * p.base_stride + n, v[i]);
+      for (int i = 0; i < 4; ++i) v[i].load(base + t[i] * p.base_stride + n);
     }
-    if (low) {
-      v4f acc[4];
+    v4f acc[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < 8; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
+    if (low) {
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         if (32 * r >= p.rank_pad) break;
         v8bf a[PARTS];
         if constexpr (JOINED) {
+          const uint16_t* f = p.frag + frag_block(tile.row0 / 16 + m, p.rank_pad32, r, PARTS, 0) + lane * 8;
 #pragma unroll
-          for (int q = 0; q < PARTS; ++q)
-            a[q] = load_bf16x8(p.frag + frag_block(tile.row0 / 16 + m, p.rank_pad32, r, PARTS, q) + lane * 8, true);
+          for (int q = 0; q < PARTS; ++q) a[q] = load_bf16x8(f + 512 * q, true);
         } else {
           const int row = min(16 * m + l16, tile.nrows - 1);
           const float* s = p.part + (int64_t)(tile.row0 + row) * p.rank_pad + 32 * r + 8 * g;
           const bool some = 32 * r + 8 * g < p.rank_pad;
-          float u[8];
+          float u[8], x[kMaxSlots][8];
+#pragma unroll
+          for (int q = 0; q < kMaxSlots; ++q) load_f32x8(s + q * step, some && q < slots, x[q]);
 #pragma unroll
           for (int i = 0; i < 8; ++i) u[i] = 0.0f;
-          for (int q0 = 0; q0 < p.splits; q0 += 4) {
-            float x[4][8];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) load_f32x8(s + (q0 + q) * step, some && q0 + q < p.splits, x[q]);
+          for (int q = 0; q < kMaxSlots; ++q)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-              for (int i = 0; i < 8; ++i) u[i] += x[q][i];
-          }
+            for (int i = 0; i < 8; ++i) u[i] += x[q][i];
 #pragma unroll
           for (int i = 0; i < 8; ++i) u[i] *= scale;
           split8<PARTS>(u, a);
@@ -614,25 +669,25 @@ __global__ __launch_bounds__(256) void k_adapter_expand(ExpandParams p) {
 #pragma unroll
         for (int q = PARTS - 1; q >= 0; --q)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[j] = mfma_bf16(a[q], b[r][j], acc[j]);
+          for (int j = 0; j < 8; ++j) acc[j] = mfma_bf16(a[q], b[r][j], acc[j]);
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[i][j] += acc[j][i];
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (t[i] >= 0) store4(out + t[i] * p.out_stride + n, v[i]);
+    for (int i = 0; i < 4; ++i) {
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = base ? v[i].get(j) + acc[j][i] : acc[j][i];
+      if (in && 16 * m + 4 * g + i < tile.nrows) Row8::store(out + t[i] * p.out_stride + n, o);
+    }
   }
 }
 
 template <typename T, bool JOINED>
-static void launch_expand(const ExpandParams& p, hipStream_t st) {
+static void launch_expand(ExpandParams p, hipStream_t st) {
   const int64_t cols = (p.N + kExpandCols - 1) / kExpandCols;
   const int waves = cols >= 4 ? 4 : (int)cols;
-  // columns first: the blocks that run together cover whole rows
-  const dim3 grid((unsigned)((cols + waves - 1) / waves), (unsigned)p.plan.max_tiles), block(waves * kWave);
+  p.col_blocks = (int32_t)((cols + waves - 1) / waves);
+  const unsigned grid = (unsigned)((p.plan.max_tiles * p.col_blocks + 7) / 8 * 8), block = waves * kWave;
   if (p.rank_pad <= 32) k_adapter_expand<1, T, JOINED><<<grid, block, 0, st>>>(p);
   else if (p.rank_pad <= 64) k_adapter_expand<2, T, JOINED><<<grid, block, 0, st>>>(p);
   else k_adapter_expand<4, T, JOINED><<<grid, block, 0, st>>>(p);
@@ -737,10 +792,9 @@ __global__ __launch_bounds__(kOuterWaves* kWave) void k_adapter_outer(OuterParam
       if (q >= p.rank) continue;
       float* dst = s.grad + ((int64_t)a * p.rank + q) * s.C + c;
 #pragma unroll
-      for (int j = 0; j < CT; j += 4) {
-        const float v[4] = {acc[r * CT + j][i], acc[r * CT + j + 1][i], acc[r * CT + j + 2][i], acc[r * CT + j + 3][i]};
-        store4(dst + j, v);
-      }
+      for (int j = 0; j < CT; j += 4)
+        *reinterpret_cast<v4f*>(dst + j) =
+            v4f{acc[r * CT + j][i], acc[r * CT + j + 1][i], acc[r * CT + j + 2][i], acc[r * CT + j + 3][i]};
     }
 }
 

@@ -69,7 +69,7 @@ constexpr int kPlanChunk = 64;       // tokens per wave of the plan kernels
 constexpr int kPlanGroup = 1024;     // tokens per block of the plan kernels
 
 // Plan of a batch: its tokens grouped by adapter.  Int32 words:
-//   head [4]: tiles, padded rows
+//   head [4]: tiles, padded rows, tiles of tokens with an adapter (the first)
 //   first [L + 2]: first row of each group (multiples of kAdapterPad); group L
 //                  holds the tokens without an adapter
 //   rows [max_rows]: token of each row, -1 in the padding behind a group
@@ -118,24 +118,29 @@ struct LowRows {
   int32_t rank_pad, rank_pad32;
   int64_t max_rows;
 };
-// X[token(row)] . W[adapter]^T over the s-th part of K: unscaled float32 sums
-// part[s][row][rank_pad], or (part null, one part) the scaled rows.
+constexpr int kShrinkK = 128;       // elements of K in a unit of shrink's work
+constexpr int kShrinkBlocks = 512;  // blocks of shrink
+constexpr int kMaxSlots = 8;        // blocks that may share a tile
+// How shrink cuts its work: units of a tile, and the fewest units of a block.
+struct ShrinkShape {
+  int32_t units, min_run;
+};
+// X[token(row)] . W[adapter]^T in float32, unscaled: part[slot][row][rank_pad],
+// a slot for each block that takes part in the row's tile.
 struct ShrinkParams {
   PlanView plan;
+  ShrinkShape shape;
   const void* x;
   int64_t x_stride;    // elements
   const uint16_t* w;   // [L, R, K] bf16
-  const float* scale;  // [L]
   int32_t rank, rank_pad, K;
-  int32_t splits, split_k;
   float* part;
-  LowRows low;
 };
-// The scaled rows from the sums of the parts.
+// The scaled rows from the slots' sums.
 struct JoinParams {
   PlanView plan;
+  ShrinkShape shape;
   const float* part;
-  int32_t splits;
   const float* scale;
   int32_t rank_pad;
   LowRows low;
@@ -143,9 +148,9 @@ struct JoinParams {
 // out[t] = base[t] + row(t) . W[adapter], the rows from frag or (null) part.
 struct ExpandParams {
   PlanView plan;
+  ShrinkShape shape;
   const uint16_t* frag;
   const float* part;
-  int32_t splits;
   const float* scale;  // [L]
   const uint16_t* w;   // [L, R, N] bf16
   int32_t rank, rank_pad, rank_pad32, N;
@@ -153,6 +158,7 @@ struct ExpandParams {
   int64_t base_stride;
   void* out;
   int64_t out_stride;
+  int32_t col_blocks;  // set by the launcher
 };
 // grad[adapter][r][c] = sum over the adapter's rows of saved[r][row] * X[token(row)][c]
 struct OuterSide {

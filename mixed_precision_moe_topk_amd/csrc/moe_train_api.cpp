@@ -94,15 +94,14 @@ moe_status check_stride(int64_t stride, int64_t features) {
 
 int32_t rank_pad(const moe_adapter_dims* d) { return (d->rank + 15) / 16 * 16; }
 
-// Parts of a contraction over `features`: about one block (tile and part) for
-// each of the 256 CUs, 256 elements a part at least.
-int32_t splits_of(int64_t max_tiles, int64_t features) {
-  const int64_t want = ceil_div(256, std::max<int64_t>(1, max_tiles));
-  return (int32_t)std::max<int64_t>(1, std::min<int64_t>({want, ceil_div(features, 256), 8}));
+// How shrink cuts a contraction over `features`: a block takes at least a
+// seventh of a tile, so that at most 8 blocks share one; from 32768 tokens on a
+// whole tile, which keeps the sums' room at two rows a token.
+moe::ShrinkShape shrink_shape(int64_t tokens, int64_t features) {
+  const int32_t units = (int32_t)ceil_div(features, moe::kShrinkK);
+  return {units, tokens >= 32768 ? units : (int32_t)ceil_div(units, 7)};
 }
-int32_t split_width(int64_t features, int32_t splits) {
-  return (int32_t)(ceil_div(ceil_div(features, splits), 64) * 64);
-}
+int32_t max_slots(const moe::ShrinkShape& s) { return (s.units - 1) / s.min_run + 2; }
 
 // Up to so many tokens expand adds up the parts for itself.
 constexpr int64_t kFewTokens = 128;
@@ -111,13 +110,14 @@ constexpr int64_t kFewTokens = 128;
 // backward pass's v as outer's operands.
 struct AdapterLayout {
   moe::PlanLayout plan;
-  int32_t rp, rp32, splits_x, splits_d;
+  int32_t rp, rp32;
+  moe::ShrinkShape shape_x, shape_d;
   size_t part_bytes, frag_bytes, saved_bytes;
   AdapterLayout(const moe_adapter_dims* d, int64_t tokens)
       : plan(d->num_adapters, tokens), rp(rank_pad(d)), rp32((d->rank + 31) / 32 * 32) {
-    splits_x = splits_of(plan.max_tiles, d->in_features);
-    splits_d = splits_of(plan.max_tiles, d->out_features);
-    part_bytes = align256((size_t)std::max(splits_x, splits_d) * plan.max_rows * rp * 4);
+    shape_x = shrink_shape(tokens, d->in_features);
+    shape_d = shrink_shape(tokens, d->out_features);
+    part_bytes = align256((size_t)std::max(max_slots(shape_x), max_slots(shape_d)) * plan.max_rows * rp * 4);
     frag_bytes = align256((size_t)plan.max_rows * rp32 * 6);
     saved_bytes = align256((size_t)plan.max_rows * rp * 6);
   }
@@ -145,7 +145,8 @@ struct Product {
   const void* x;
   int64_t x_stride;
   const void* w;
-  int32_t features, splits;
+  int32_t features;
+  moe::ShrinkShape shape;
   bool x_f32;
   const void* w2;
   int32_t features2;
@@ -169,30 +170,17 @@ moe_status run_product(const Product& q, const moe::PlanView& v, const AdapterLa
   low.rank_pad = l.rp;
   low.rank_pad32 = l.rp32;
   low.max_rows = l.plan.max_rows;
-  moe::ShrinkParams s;
-  s.plan = v;
-  s.x = q.x;
-  s.x_stride = q.x_stride;
-  s.w = static_cast<const uint16_t*>(q.w);
-  s.scale = scale;
-  s.rank = rank;
-  s.rank_pad = l.rp;
-  s.K = q.features;
-  s.split_k = split_width(q.features, q.splits);
-  s.splits = (int32_t)ceil_div(q.features, s.split_k);
-  const bool direct = s.splits == 1 && !few;  // shrink writes the rows itself
-  s.part = direct ? nullptr : part;
-  s.low = low;
-  if (!direct) s.low.frag = s.low.saved = nullptr;
+  const moe::ShrinkParams s = {v, q.shape, q.x, q.x_stride, static_cast<const uint16_t*>(q.w),
+                               rank, l.rp, q.features, part};
   MOE_RETURN_IF(moe::check_hip(moe::launch_adapter_shrink(s, q.x_f32, stream), "adapter shrink", stream));
-  if (!direct && (low.frag || low.saved)) {
-    const moe::JoinParams j = {v, part, s.splits, scale, l.rp, low};
+  if (low.frag || low.saved) {
+    const moe::JoinParams j = {v, q.shape, part, scale, l.rp, low};
     MOE_RETURN_IF(moe::check_hip(moe::launch_adapter_join(j, stream), "adapter join", stream));
   }
   if (!q.out) return MOE_OK;
-  const moe::ExpandParams e = {v, low.frag, part, s.splits, scale, static_cast<const uint16_t*>(q.w2),
+  const moe::ExpandParams e = {v, q.shape, low.frag, part, scale, static_cast<const uint16_t*>(q.w2),
                                rank, l.rp, l.rp32, q.features2, q.base, q.base_stride, q.out,
-                               q.out_stride};
+                               q.out_stride, 0};
   return moe::check_hip(moe::launch_adapter_expand(e, q.out_f32, stream), "adapter expand", stream);
 }
 
@@ -362,7 +350,7 @@ moe_status moe_adapter_apply(const moe_adapter_dims* dims, const void* x, int64_
   if (saved) MOE_RETURN_IF(check_room(saved_bytes, l.saved_bytes, "saved"));
   MOE_RETURN_IF(moe::check_gfx950());
   const moe::PlanView v = plan_view(plan, l.plan, dims->num_adapters, num_tokens);
-  const Product q = {x, x_stride, a, dims->in_features, l.splits_x, false, b, dims->out_features,
+  const Product q = {x, x_stride, a, dims->in_features, l.shape_x, false, b, dims->out_features,
                      base, base_stride, out, out_stride, dims->out_type == MOE_T_F32, saved};
   MOE_RETURN_IF(run_product(q, v, l, dims->rank, scale, workspace, stream));
   return moe::set_ok();
@@ -405,7 +393,7 @@ moe_status moe_adapter_backward(const moe_adapter_dims* dims, const void* dout,
   const bool f32 = dims->out_type == MOE_T_F32;
   void* vt = num_tokens > 0 ? static_cast<uint8_t*>(workspace) + l.part_bytes + l.frag_bytes : nullptr;
   if (num_tokens > 0) {
-    const Product q = {dout, dout_stride, b, dims->out_features, l.splits_d, f32, a,
+    const Product q = {dout, dout_stride, b, dims->out_features, l.shape_d, f32, a,
                        dims->in_features, dx_base, dx_base_stride, dx, dx_stride, false,
                        da ? vt : nullptr};
     MOE_RETURN_IF(run_product(q, v, l, dims->rank, scale, workspace, stream));
