@@ -8,6 +8,7 @@ ABI is declared in include/moe.h.  If the library is missing every call raises
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -149,6 +150,10 @@ class LayerDims:
 
     def c(self) -> Dims:
         return Dims(self.num_experts, self.hidden, self.inter, WFMT[self.wfmt], AFMT[self.afmt])
+
+    @functools.cache
+    def ref(self):
+        return ctypes.byref(self.c())
 
 
 def abi_version() -> int:
@@ -298,49 +303,73 @@ def set_fc2_fused(enable: bool):
 # ---------------------------------------------------------------- training and adapters
 # These calls check their tensors before the library sees a pointer: a wrong
 # element type, shape, stride or device raises MoeError (MOE_ERR_INVALID_ARG).
+# They are short calls in a decode step's loop, so the checks pass one tensor
+# in a few attribute reads and spell out what is wrong only when something is.
 
 def _refuse(msg: str):
     raise MoeError(1, msg)
 
 
-def _tensor(name, t, dtype, shape, device, rows=False):
-    """Checks tensor t (None passes); rows: 2-d with any row stride, else
-    contiguous.  dtype: the one, or a tuple of those that share the bits."""
+def _tensor(name, t, dtypes, shape, index, rows=False):
+    """Address of tensor t, None for None; t has to have one of the dtypes, the
+    shape and the device index; rows: any stride between rows, else contiguous."""
     if t is None:
-        return
-    if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
-        _refuse(f"{name} is {t.dtype}, {dtype} is needed")
-    if tuple(t.shape) != shape:
+        return None
+    if (t.dtype in dtypes and t.shape == shape and t.get_device() == index
+            and (t.is_contiguous() or (rows and (shape[1] == 1 or t.stride(1) == 1)))):
+        return t.data_ptr()
+    if t.dtype not in dtypes:
+        _refuse(f"{name} is {t.dtype}, {' or '.join(map(str, dtypes))} is needed")
+    if t.shape != shape:
         _refuse(f"{name} has shape {tuple(t.shape)}, {shape} is needed")
-    if t.device != device:
-        _refuse(f"{name} is on {t.device}, the call runs on {device}")
-    if not t.is_contiguous() and not (rows and (shape[1] == 1 or t.stride(1) == 1)):
-        _refuse(f"{name} is not contiguous")
+    if t.get_device() != index:
+        _refuse(f"{name} is on {t.device}, the call runs on cuda:{index}")
+    _refuse(f"{name} is not contiguous")
 
 
-def _buffer(name, t, device):
+def _buffer(name, t, index):
+    """(address, bytes) of a workspace; (None, 0) for None."""
     if t is None:
-        return 0
-    if t.device != device or not t.is_contiguous():
-        _refuse(f"{name} must be a contiguous buffer on {device}")
-    return t.numel() * t.element_size()
+        return None, 0
+    if t.get_device() != index or not t.is_contiguous():
+        _refuse(f"{name} must be a contiguous buffer on cuda:{index}")
+    return t.data_ptr(), t.nbytes
+
+
+def _types():
+    """Element types by name (torch is imported when first needed)."""
+    global _dtypes
+    if _dtypes is None:
+        import torch
+
+        _dtypes = dict(f32=(torch.float32,), i32=(torch.int32,), u8=(torch.uint8,),
+                       bf16=(torch.bfloat16, torch.int16),
+                       row=(torch.float32, torch.bfloat16, torch.int16))
+    return _dtypes
+
+
+_dtypes = None
 
 
 def _current(t, stream):
-    """The device of tensor t, which has to be the current one (the library
-    launches on it) and the stream's."""
+    """(index of tensor t's device, stream handle): the device has to be the
+    current one (the library launches on it) and the stream's."""
     import torch
 
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+    index = t.get_device()
+    if index < 0 or index != torch.cuda.current_device():
         _refuse(f"tensors on {t.device}, but the current device is another one")
-    if stream is not None and stream.device != t.device:
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    elif stream.device_index != index:
         _refuse(f"stream of {stream.device} for tensors on {t.device}")
-    return t.device
+    return index, stream.cuda_stream
 
 
-def _stride(t):
-    """Elements between rows; a single row (or none) has no stride of its own."""
-    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
+def _stride(t, features):
+    """Elements between rows; a single row (or none, or no tensor) has no stride
+    of its own."""
+    return t.stride(0) if t is not None and t.shape[0] > 1 else (features + 7) // 8 * 8
 
 
 def _size(query, *args) -> int:
@@ -349,19 +378,18 @@ def _size(query, *args) -> int:
     return b.value
 
 
-def _seqs(seq_offsets, device):
-    import torch
-
+def _seqs(seq_offsets, index):
+    """(sequences, address of their boundaries)."""
     if seq_offsets is None:
-        return 1
+        return 1, None
     if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2:
         _refuse("seq_offsets must hold at least two boundaries")
-    _tensor("seq_offsets", seq_offsets, torch.int32, (seq_offsets.shape[0],), device)
-    return seq_offsets.shape[0] - 1
+    n = seq_offsets.shape[0]
+    return n - 1, _tensor("seq_offsets", seq_offsets, _types()["i32"], (n,), index)
 
 
 def router_loss_query(d: LayerDims, num_tokens: int, num_seqs: int = 1) -> int:
-    return _size(lib().moe_router_loss_query, ctypes.byref(d.c()), num_tokens, num_seqs)
+    return _size(lib().moe_router_loss_query, d.ref(), num_tokens, num_seqs)
 
 
 def router_loss(d: LayerDims, logits, ids, losses, counts, mean_probs, seq_tokens, workspace,
@@ -371,22 +399,18 @@ def router_loss(d: LayerDims, logits, ids, losses, counts, mean_probs, seq_token
     token_mask: uint8 [T], 0 for padding; outputs losses float32 [2], counts
     int32 [S, E], mean_probs float32 [S, E], seq_tokens int32 [S + 2];
     workspace: uint8 of router_loss_query bytes."""
-    import torch
-
-    dev = _current(logits, stream)
-    T, E = logits.shape[0], d.num_experts
-    S, k = _seqs(seq_offsets, dev), ids.shape[-1]
-    _tensor("logits", logits, torch.float32, (T, E), dev)
-    _tensor("ids", ids, torch.int32, (T, k), dev)
-    _tensor("token_mask", token_mask, torch.uint8, (T,), dev)
-    _tensor("losses", losses, torch.float32, (2,), dev)
-    _tensor("counts", counts, torch.int32, (S, E), dev)
-    _tensor("mean_probs", mean_probs, torch.float32, (S, E), dev)
-    _tensor("seq_tokens", seq_tokens, torch.int32, (S + 2,), dev)
+    dev, st = _current(logits, stream)
+    ty = _types()
+    f32, i32 = ty["f32"], ty["i32"]
+    T, E, k = logits.shape[0], d.num_experts, ids.shape[-1]
+    S, offs = _seqs(seq_offsets, dev)
+    ws, room = _buffer("workspace", workspace, dev)
     _check(lib().moe_router_loss(
-        ctypes.byref(d.c()), _ptr(logits), _ptr(ids), T, k, _ptr(seq_offsets), S, _ptr(token_mask),
-        _ptr(losses), _ptr(counts), _ptr(mean_probs), _ptr(seq_tokens), _ptr(workspace),
-        _buffer("workspace", workspace, dev), _stream(stream)))
+        d.ref(), _tensor("logits", logits, f32, (T, E), dev), _tensor("ids", ids, i32, (T, k), dev),
+        T, k, offs, S, _tensor("token_mask", token_mask, ty["u8"], (T,), dev),
+        _tensor("losses", losses, f32, (2,), dev), _tensor("counts", counts, i32, (S, E), dev),
+        _tensor("mean_probs", mean_probs, f32, (S, E), dev),
+        _tensor("seq_tokens", seq_tokens, i32, (S + 2,), dev), ws, room, st))
 
 
 def router_backward(d: LayerDims, logits, ids, dlogits, weights=None, dweights=None, dlosses=None,
@@ -394,46 +418,36 @@ def router_backward(d: LayerDims, logits, ids, dlogits, weights=None, dweights=N
     """dlogits float32 [T, E] from the routing weights' gradient (weights and
     dweights float32 [T, k]) and the losses' (dlosses float32 [2], with the
     counts and seq_tokens of router_loss)."""
-    import torch
-
-    dev = _current(logits, stream)
-    T, E = logits.shape[0], d.num_experts
-    S, k = _seqs(seq_offsets, dev), ids.shape[-1]
-    f32 = torch.float32
-    _tensor("logits", logits, f32, (T, E), dev)
-    _tensor("ids", ids, torch.int32, (T, k), dev)
-    _tensor("dlogits", dlogits, f32, (T, E), dev)
-    _tensor("weights", weights, f32, (T, k), dev)
-    _tensor("dweights", dweights, f32, (T, k), dev)
-    _tensor("dlosses", dlosses, f32, (2,), dev)
-    _tensor("counts", counts, torch.int32, (S, E), dev)
-    _tensor("seq_tokens", seq_tokens, torch.int32, (S + 2,), dev)
-    _tensor("token_mask", token_mask, torch.uint8, (T,), dev)
+    dev, st = _current(logits, stream)
+    ty = _types()
+    f32, i32 = ty["f32"], ty["i32"]
+    T, E, k = logits.shape[0], d.num_experts, ids.shape[-1]
+    S, offs = _seqs(seq_offsets, dev)
     _check(lib().moe_router_backward(
-        ctypes.byref(d.c()), _ptr(logits), _ptr(ids), T, k, _ptr(seq_offsets), S, _ptr(token_mask),
-        _ptr(weights), _ptr(dweights), _ptr(dlosses), _ptr(counts), _ptr(seq_tokens), _ptr(dlogits),
-        _stream(stream)))
+        d.ref(), _tensor("logits", logits, f32, (T, E), dev), _tensor("ids", ids, i32, (T, k), dev),
+        T, k, offs, S, _tensor("token_mask", token_mask, ty["u8"], (T,), dev),
+        _tensor("weights", weights, f32, (T, k), dev),
+        _tensor("dweights", dweights, f32, (T, k), dev), _tensor("dlosses", dlosses, f32, (2,), dev),
+        _tensor("counts", counts, i32, (S, E), dev),
+        _tensor("seq_tokens", seq_tokens, i32, (S + 2,), dev),
+        _tensor("dlogits", dlogits, f32, (T, E), dev), st))
 
 
 def finalize_backward(d: LayerDims, dout, weights, y2, slot_row, dweights, dy2=None, stream=None):
     """Gradient of the weighted sum.  dout: bf16 (or int16 bits) [T, H]; weights
     float32 [T, k]; y2 float32 [T*k, H]; slot_row int32 [T, k]; outputs dweights
     float32 [T, k] and dy2 [T*k, H], float32 or bf16 (int16 bits), or None."""
-    import torch
-
-    dev = _current(dout, stream)
+    dev, st = _current(dout, stream)
+    ty = _types()
+    f32 = ty["f32"]
     T, H, k = dout.shape[0], d.hidden, weights.shape[-1]
-    bits = (torch.bfloat16, torch.int16)
-    _tensor("dout", dout, bits, (T, H), dev)
-    _tensor("weights", weights, torch.float32, (T, k), dev)
-    _tensor("y2", y2, torch.float32, (T * k, H), dev)
-    _tensor("slot_row", slot_row, torch.int32, (T, k), dev)
-    _tensor("dweights", dweights, torch.float32, (T, k), dev)
-    _tensor("dy2", dy2, bits + (torch.float32,), (T * k, H), dev)
-    kind = T_F32 if dy2 is not None and dy2.dtype == torch.float32 else T_BF16
+    kind = T_F32 if dy2 is not None and dy2.dtype in f32 else T_BF16
     _check(lib().moe_finalize_backward(
-        ctypes.byref(d.c()), _ptr(dout), T, k, _ptr(weights), _ptr(y2), _ptr(slot_row),
-        _ptr(dweights), _ptr(dy2), kind, _stream(stream)))
+        d.ref(), _tensor("dout", dout, ty["bf16"], (T, H), dev), T, k,
+        _tensor("weights", weights, f32, (T, k), dev), _tensor("y2", y2, f32, (T * k, H), dev),
+        _tensor("slot_row", slot_row, ty["i32"], (T, k), dev),
+        _tensor("dweights", dweights, f32, (T, k), dev),
+        _tensor("dy2", dy2, ty["row"], (T * k, H), dev), kind, st))
 
 
 @dataclass(frozen=True)
@@ -451,10 +465,9 @@ class AdapterDims:
         return CAdapterDims(self.num_adapters, self.rank, self.in_features, self.out_features,
                             OUT_TYPE[self.out_type])
 
-    def _torch_out(self):
-        import torch
-
-        return torch.float32 if self.out_type == "f32" else (torch.bfloat16, torch.int16)
+    @functools.cache
+    def ref(self):
+        return ctypes.byref(self.c())
 
 
 def adapter_plan_query(num_adapters: int, num_tokens: int) -> int:
@@ -465,31 +478,28 @@ def adapter_plan(num_adapters: int, adapter_ids, plan, stream=None):
     """Groups the tokens of a batch by adapter.  adapter_ids: int32 cuda [T], ids
     outside [0, num_adapters) mean no adapter; plan: uint8 of
     adapter_plan_query bytes."""
-    import torch
-
-    dev = _current(adapter_ids, stream)
+    dev, st = _current(adapter_ids, stream)
     T = adapter_ids.shape[0]
-    _tensor("adapter_ids", adapter_ids, torch.int32, (T,), dev)
-    _check(lib().moe_adapter_plan(num_adapters, _ptr(adapter_ids), T, _ptr(plan),
-                                  _buffer("plan", plan, dev), _stream(stream)))
+    pl, room = _buffer("plan", plan, dev)
+    _check(lib().moe_adapter_plan(
+        num_adapters, _tensor("adapter_ids", adapter_ids, _types()["i32"], (T,), dev), T, pl, room,
+        st))
 
 
 def adapter_workspace_query(d: AdapterDims, num_tokens: int) -> int:
-    return _size(lib().moe_adapter_workspace_query, ctypes.byref(d.c()), num_tokens)
+    return _size(lib().moe_adapter_workspace_query, d.ref(), num_tokens)
 
 
 def adapter_saved_query(d: AdapterDims, num_tokens: int) -> int:
-    return _size(lib().moe_adapter_saved_query, ctypes.byref(d.c()), num_tokens)
+    return _size(lib().moe_adapter_saved_query, d.ref(), num_tokens)
 
 
-def _adapter_factors(d: AdapterDims, a, b, scale, dev):
-    import torch
-
-    bits = (torch.bfloat16, torch.int16)
-    _tensor("a", a, bits, (d.num_adapters, d.rank, d.in_features), dev)
-    _tensor("b", b, bits, (d.num_adapters, d.rank, d.out_features), dev)
-    _tensor("scale", scale, torch.float32, (d.num_adapters,), dev)
-    return bits
+def _factors(d: AdapterDims, a, b, scale, dev, ty):
+    """Addresses of the adapters' factors and scales."""
+    L, R = d.num_adapters, d.rank
+    return (_tensor("a", a, ty["bf16"], (L, R, d.in_features), dev),
+            _tensor("b", b, ty["bf16"], (L, R, d.out_features), dev),
+            _tensor("scale", scale, ty["f32"], (L,), dev))
 
 
 def adapter_apply(d: AdapterDims, x, plan, a, b, scale, base, out, workspace, saved=None,
@@ -498,17 +508,18 @@ def adapter_apply(d: AdapterDims, x, plan, a, b, scale, base, out, workspace, sa
     [T, K]; a bf16 [L, R, K]; b bf16 [L, R, N]; scale float32 [L]; base (or None)
     and out [T, N] of the dims' type; x, base and out may have a row stride;
     saved: uint8 of adapter_saved_query bytes for adapter_backward."""
-    dev = _current(x, stream)
-    T = x.shape[0]
-    bits = _adapter_factors(d, a, b, scale, dev)
-    _tensor("x", x, bits, (T, d.in_features), dev, rows=True)
-    _tensor("base", base, d._torch_out(), (T, d.out_features), dev, rows=True)
-    _tensor("out", out, d._torch_out(), (T, d.out_features), dev, rows=True)
+    dev, st = _current(x, stream)
+    ty = _types()
+    T, K, N = x.shape[0], d.in_features, d.out_features
+    ot = ty[d.out_type]
+    pl, plan_room = _buffer("plan", plan, dev)
+    sv, saved_room = _buffer("saved", saved, dev)
+    ws, room = _buffer("workspace", workspace, dev)
     _check(lib().moe_adapter_apply(
-        ctypes.byref(d.c()), _ptr(x), _stride(x), T, _ptr(plan), _buffer("plan", plan, dev),
-        _ptr(a), _ptr(b), _ptr(scale), _ptr(base), _stride(out if base is None else base),
-        _ptr(out), _stride(out), _ptr(saved), _buffer("saved", saved, dev), _ptr(workspace),
-        _buffer("workspace", workspace, dev), _stream(stream)))
+        d.ref(), _tensor("x", x, ty["bf16"], (T, K), dev, True), _stride(x, K), T, pl, plan_room,
+        *_factors(d, a, b, scale, dev, ty), _tensor("base", base, ot, (T, N), dev, True),
+        _stride(base, N), _tensor("out", out, ot, (T, N), dev, True), _stride(out, N), sv,
+        saved_room, ws, room, st))
 
 
 def adapter_backward(d: AdapterDims, dout, x, plan, a, b, scale, saved, da, db, workspace, dx=None,
@@ -516,22 +527,18 @@ def adapter_backward(d: AdapterDims, dout, x, plan, a, b, scale, saved, da, db, 
     """Gradients of adapter_apply: da, db float32 of the factors' shapes (or both
     None) and dx = dx_base + ... bf16 [T, K] (or None).  saved: as
     adapter_apply left it for the same plan."""
-    import torch
-
-    dev = _current(dout, stream)
-    T = dout.shape[0]
-    bits = _adapter_factors(d, a, b, scale, dev)
-    K, N = d.in_features, d.out_features
-    _tensor("dout", dout, d._torch_out(), (T, N), dev, rows=True)
-    _tensor("x", x, bits, (T, K), dev, rows=True)
-    _tensor("dx", dx, bits, (T, K), dev, rows=True)
-    _tensor("dx_base", dx_base, bits, (T, K), dev, rows=True)
-    _tensor("da", da, torch.float32, (d.num_adapters, d.rank, K), dev)
-    _tensor("db", db, torch.float32, (d.num_adapters, d.rank, N), dev)
-    stride = lambda t, n: n if t is None else _stride(t)  # noqa: E731
+    dev, st = _current(dout, stream)
+    ty = _types()
+    bits = ty["bf16"]
+    T, K, N = dout.shape[0], d.in_features, d.out_features
+    L, R = d.num_adapters, d.rank
+    pl, plan_room = _buffer("plan", plan, dev)
+    sv, saved_room = _buffer("saved", saved, dev)
+    ws, room = _buffer("workspace", workspace, dev)
     _check(lib().moe_adapter_backward(
-        ctypes.byref(d.c()), _ptr(dout), _stride(dout), _ptr(x), stride(x, K), T, _ptr(plan),
-        _buffer("plan", plan, dev), _ptr(a), _ptr(b), _ptr(scale), _ptr(saved),
-        _buffer("saved", saved, dev), _ptr(da), _ptr(db), _ptr(dx_base), stride(dx_base, K),
-        _ptr(dx), stride(dx, K), _ptr(workspace), _buffer("workspace", workspace, dev),
-        _stream(stream)))
+        d.ref(), _tensor("dout", dout, ty[d.out_type], (T, N), dev, True), _stride(dout, N),
+        _tensor("x", x, bits, (T, K), dev, True), _stride(x, K), T, pl, plan_room,
+        *_factors(d, a, b, scale, dev, ty), sv, saved_room,
+        _tensor("da", da, ty["f32"], (L, R, K), dev), _tensor("db", db, ty["f32"], (L, R, N), dev),
+        _tensor("dx_base", dx_base, bits, (T, K), dev, True), _stride(dx_base, K),
+        _tensor("dx", dx, bits, (T, K), dev, True), _stride(dx, K), ws, room, st))

@@ -8,8 +8,8 @@
 namespace moe {
 
 // ---------------------------------------------------------------- router
-constexpr int kLossRun = 16;    // consecutive tokens one wave sums
-constexpr int kLossWaves = 4;   // waves (runs) per block of the loss kernel
+constexpr int kLossRun = 8;     // consecutive tokens one wave sums
+constexpr int kLossWaves = 8;   // waves (runs) per block of the loss kernel
 constexpr int kLossBlock = kLossRun * kLossWaves;
 
 struct RouterLossParams {
