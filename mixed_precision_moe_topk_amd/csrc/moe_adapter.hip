@@ -60,9 +60,10 @@ __device__ __forceinline__ int plan_rank(const uint64_t (*mask)[kMaxAdapters + 1
 }
 
 // Thread e holds the tokens n of group e: first rows, padding and tiles.
-// Returns the first row of group e.
+// Returns the first row of group e; the block that has to write fills the
+// plan's lists.
 __device__ int32_t plan_scan(const PlanParams& p, const PlanLayout& l, int32_t n,
-                             int32_t (*wsum)[16]) {
+                             int32_t (*wsum)[16], bool write) {
   const int G = p.adapters + 1, e = threadIdx.x;
   const int lane = lane_id(), w = threadIdx.x / kWave;
   const int32_t pad = (n + kAdapterPad - 1) / kAdapterPad * kAdapterPad;
@@ -87,7 +88,7 @@ __device__ int32_t plan_scan(const PlanParams& p, const PlanLayout& l, int32_t n
     pb += wsum[1][i];
   }
   const int32_t row0 = pa + a - pad, tile0 = pb + b - nt;
-  if (e < G) {
+  if (e < G && write) {
     p.plan[l.first + e] = row0;
     for (int32_t i = n; i < pad; ++i) p.plan[l.rows + row0 + i] = -1;
     Tile* tiles = reinterpret_cast<Tile*>(p.plan + l.tiles);
@@ -109,19 +110,54 @@ __device__ int32_t plan_scan(const PlanParams& p, const PlanLayout& l, int32_t n
   return row0;
 }
 
-// A batch of at most 1024 tokens in one launch.
-__global__ __launch_bounds__(kPlanGroup) void k_plan_small(PlanParams p, PlanLayout l) {
+// Adds a wave's tokens to counters in LDS: the first groups met with one add
+// each (prompts hold few), the lanes that are left one by one.
+__device__ __forceinline__ void plan_add(int32_t* count, int g) {
+  uint64_t left = __ballot(g >= 0);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    if (left == 0) return;
+    const int first = __ffsll((unsigned long long)left) - 1;
+    const int lead = __builtin_amdgcn_readlane(g, first);
+    const uint64_t same = __ballot(g == lead);
+    if (lane_id() == first) atomicAdd(&count[lead], (int32_t)__popcll(same));
+    left &= ~same;
+  }
+  if (left >> lane_id() & 1) atomicAdd(&count[g], 1);
+}
+
+// A batch of up to kPlanOne tokens in one launch: every block counts all the
+// tokens for itself (integer counts in LDS), those before its own apart, and so
+// knows where its rows go; block 0 writes the rest of the plan.  4096 tokens: 7.4
+// us against 13.4 in three launches; 16384: 16.6 against 13.9.
+__global__ __launch_bounds__(kPlanGroup) void k_plan_one(PlanParams p, PlanLayout l) {
   __shared__ uint64_t mask[kPlanChunks][kMaxAdapters + 1];
-  __shared__ int32_t first[kMaxAdapters + 1];
+  __shared__ int32_t before[kMaxAdapters + 1], after[kMaxAdapters + 1];
   __shared__ int32_t wsum[2][16];
-  const int g = plan_masks(p, 0, mask);
-  int32_t n = 0;
-  if ((int)threadIdx.x <= p.adapters)
-    for (int u = 0; u < kPlanChunks; ++u) n += __popcll(mask[u][threadIdx.x]);
-  const int32_t row0 = plan_scan(p, l, n, wsum);
-  if ((int)threadIdx.x <= p.adapters) first[threadIdx.x] = row0;
+  const int G = p.adapters + 1, e = threadIdx.x;
+  if (e < G) before[e] = after[e] = 0;
+  const int g = plan_masks(p, blockIdx.x, mask);  // (its barriers cover the counters)
+  constexpr int kB = 8;  // reads in flight
+  for (int64_t b0 = 0; b0 < l.nblocks; b0 += kB) {
+    int o[kB];
+#pragma unroll
+    for (int u = 0; u < kB; ++u) {
+      const int64_t t = (b0 + u) * kPlanGroup + threadIdx.x;
+      o[u] = b0 + u != blockIdx.x && t < p.tokens ? plan_group(p, t) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kB; ++u) plan_add(b0 + u < blockIdx.x ? before : after, o[u]);
+  }
   __syncthreads();
-  if (g >= 0) p.plan[l.rows + first[g] + plan_rank(mask, g)] = (int32_t)threadIdx.x;
+  int32_t n = 0;
+  if (e < G) {
+    for (int u = 0; u < kPlanChunks; ++u) n += __popcll(mask[u][e]);
+    n += before[e] + after[e];
+  }
+  const int32_t row0 = plan_scan(p, l, n, wsum, blockIdx.x == 0);
+  if (e < G) before[e] += row0;
+  __syncthreads();
+  if (g >= 0) p.plan[l.rows + before[g] + plan_rank(mask, g)] = (int32_t)(blockIdx.x * kPlanGroup + threadIdx.x);
 }
 
 __global__ __launch_bounds__(kPlanGroup) void k_plan_count(PlanParams p, PlanLayout l) {
@@ -151,7 +187,7 @@ __global__ __launch_bounds__(kPlanGroup) void k_plan_scan(PlanParams p, PlanLayo
       }
     }
   }
-  plan_scan(p, l, n, wsum);
+  plan_scan(p, l, n, wsum, true);
 }
 
 __global__ __launch_bounds__(kPlanGroup) void k_plan_scatter(PlanParams p, PlanLayout l) {
@@ -165,8 +201,8 @@ __global__ __launch_bounds__(kPlanGroup) void k_plan_scatter(PlanParams p, PlanL
 }
 
 hipError_t launch_adapter_plan(const PlanParams& p, const PlanLayout& l, hipStream_t st) {
-  if (p.tokens <= kPlanGroup) {
-    k_plan_small<<<1, kPlanGroup, 0, st>>>(p, l);
+  if (p.tokens <= kPlanOne) {
+    k_plan_one<<<(unsigned)l.nblocks, kPlanGroup, 0, st>>>(p, l);
     return hipGetLastError();
   }
   k_plan_count<<<(unsigned)l.nblocks, kPlanGroup, 0, st>>>(p, l);
@@ -589,11 +625,14 @@ __global__ __launch_bounds__(256) void k_adapter_expand(ExpandParams p) {
   typedef std::conditional_t<sizeof(T) == 4, Row8F32, Row8Bf16> Row8;
   // neighbouring blocks on one XCD (block b runs on XCD b % 8), columns first:
   // its blocks cover whole rows of one tile and share a factor
-  const int64_t total = (int64_t)min(p.plan.head[0], (int32_t)p.plan.max_tiles) * p.col_blocks;
+  const int32_t per_tile = p.col_blocks * p.row_blocks;
+  const int64_t total = (int64_t)min(p.plan.head[0], (int32_t)p.plan.max_tiles) * per_tile;
   const int64_t each = (total + 7) / 8, id = blockIdx.x % 8 * each + blockIdx.x / 8;
   if (blockIdx.x / 8 >= each || id >= total) return;
   Tile tile;
-  if (!plan_tile(p.plan, id / p.col_blocks, &tile)) return;
+  if (!plan_tile(p.plan, id / per_tile, &tile)) return;
+  const int m0 = (int)(id % per_tile / p.col_blocks);
+  if (16 * m0 >= tile.nrows) return;
   const int n0 = (int)((id % p.col_blocks) * (blockDim.x / kWave) + threadIdx.x / kWave) * kExpandCols;
   if (n0 >= p.N) return;
   const int lane = lane_id(), l16 = lane & 15, g = lane >> 4;
@@ -624,9 +663,9 @@ __global__ __launch_bounds__(256) void k_adapter_expand(ExpandParams p) {
   const int64_t step = p.plan.max_rows * (int64_t)p.rank_pad;
   const float scale = low && !JOINED ? p.scale[tile.expert] : 0.0f;
   const int slots = low && !JOINED
-                        ? min(shrink_slots(shrink_runs(p.plan, p.shape), id / p.col_blocks), kMaxSlots) : 0;
+                        ? min(shrink_slots(shrink_runs(p.plan, p.shape), id / per_tile), kMaxSlots) : 0;
 #pragma unroll 1
-  for (int m = 0; 16 * m < tile.nrows; ++m) {
+  for (int m = m0; 16 * m < tile.nrows; m += p.row_blocks) {
     int64_t t[4];
     Row8 v[4];
     // a row behind the last reads the last one's base and stores nothing
@@ -687,7 +726,11 @@ static void launch_expand(ExpandParams p, hipStream_t st) {
   const int64_t cols = (p.N + kExpandCols - 1) / kExpandCols;
   const int waves = cols >= 4 ? 4 : (int)cols;
   p.col_blocks = (int32_t)((cols + waves - 1) / waves);
-  const unsigned grid = (unsigned)((p.plan.max_tiles * p.col_blocks + 7) / 8 * 8), block = waves * kWave;
+  // few waves (a narrow result): a block for each 16 rows of a tile, else the
+  // waves take them one after another and read their columns once
+  p.row_blocks = p.plan.max_tiles * cols < 2048 && p.plan.tokens > p.plan.max_tiles ? kAdapterTile / 16 : 1;
+  const unsigned grid = (unsigned)((p.plan.max_tiles * p.col_blocks * p.row_blocks + 7) / 8 * 8);
+  const unsigned block = waves * kWave;
   if (p.rank_pad <= 32) k_adapter_expand<1, T, JOINED><<<grid, block, 0, st>>>(p);
   else if (p.rank_pad <= 64) k_adapter_expand<2, T, JOINED><<<grid, block, 0, st>>>(p);
   else k_adapter_expand<4, T, JOINED><<<grid, block, 0, st>>>(p);
@@ -701,119 +744,270 @@ hipError_t launch_adapter_expand(const ExpandParams& p, bool out_f32, hipStream_
 }
 
 // ---------------------------------------------------------------- outer
-constexpr int kOuterWaves = 8;
+constexpr int kOuterRows = 64;  // rows of an adapter staged at once
 
-// 32 rows of an adapter a step: lane (l16, g) holds rows [8 g, 8 g + 8) of
-// columns [CT l16, CT l16 + CT) of X, and of rank l16 of a rank block of saved.
-// F32: X is float32, split like the saved values; the products of parts whose
-// sizes lie 2^-27 apart or more are left out.
-template <int RT, int CT, bool F32>
-__device__ __forceinline__ void outer_sum(const OuterParams& p, const OuterSide& s, int a, int r0, int c0,
-                                          v4f (&acc)[RT * CT]) {
-  if (p.plan.tokens == 0) return;
-  const int lane = lane_id(), w = threadIdx.x / kWave, l16 = lane & 15, g = lane >> 4;
-  const int c = c0 + CT * l16;
-  const int64_t M = p.plan.max_rows, plane = M * p.rank_pad;
-  int64_t b = p.plan.first[a], e = p.plan.first[a + 1];
-  b = b < 0 ? 0 : b / kAdapterPad * kAdapterPad;
-  e = e > M ? M : e;
-  for (int64_t row = b + 32 * w + 8 * g; row - 8 * g < e; row += 32 * kOuterWaves) {
-    const bool live = row < e;
-    v8bf u[RT][3];
+// A staged line holds 64 rows of one column (or rank) as 8 pieces of 8 rows;
+// piece i lies at place i ^ swizzle, so that the 16 lines a matrix operand
+// reads, and the lines a wave writes, meet all banks.
+__device__ __forceinline__ int outer_at(int line, int piece) {
+  return line * kOuterRows + (piece ^ ((line >> 2 ^ (line >> 1 & 1) << 2) & 7)) * 8;
+}
+
+// An adapter of n rows is summed in m = max(1, ceil(n / p.chunk)) segments of
+// equal length, so that few adapters, or one that has most tokens, still fill
+// the CUs, in one round of blocks: a block's steps follow one another at the
+// memory's latency, and the longest segment sets the time.  Segments are
+// numbered along the adapters.  A single one is summed into the gradient at
+// once, several into partial sums (slots, numbered among themselves), which
+// k_adapter_outer_join adds up.
+struct OuterSegment {
+  int a, m;
+  int64_t row, end;  // its rows
+  int64_t slot;      // of the partial sums; -1: the gradient itself
+};
+// Segment j, or (JOIN) the j-th adapter of several segments, with its first
+// slot; false behind the last.  By the whole wave, 64 adapters at a time.
+template <bool JOIN>
+__device__ __forceinline__ bool outer_segment(const OuterParams& p, int64_t j, OuterSegment* s) {
+  const int L = p.plan.adapters;
+  if (p.plan.tokens == 0) {
+    *s = {(int)j, 1, 0, 0, -1};
+    return !JOIN && j < L;
+  }
+  const int64_t M = p.plan.max_rows;
+  int64_t segs = 0, slots = 0, several = 0;  // of the adapters before
+  for (int a0 = 0; a0 < L; a0 += kWave) {
+    const int a = a0 + lane_id();
+    const int64_t b = min(max((int64_t)p.plan.first[min(a, L)], (int64_t)0), M) / kAdapterPad * kAdapterPad;
+    const int64_t e = min(max((int64_t)p.plan.first[min(a + 1, L)], b), M) / kAdapterPad * kAdapterPad;
+    const int m = a < L ? max(1, (int)((e - b + p.chunk - 1) / p.chunk)) : 0;
+    const int q = m > 1 ? m : 0;
+    int sm = m, sq = q;
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const uint16_t* src = s.saved + (int64_t)(r0 + 16 * r + l16) * M + row;
-      const bool in = live && r0 + 16 * r < p.rank_pad;
-#pragma unroll
-      for (int n = 0; n < 3; ++n) u[r][n] = load_bf16x8(src + n * plane, in);
-    }
-    int64_t t[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = live && c < s.C ? plan_token(p.plan, row + i) : -1;
-    if constexpr (F32) {
-      static_assert(CT == 4, "");
-      float x[8][4];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint32_t q[4];
-        load_words<4>(static_cast<const float*>(s.x) + t[i] * s.x_stride + c, t[i] >= 0, q);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[i][j] = __uint_as_float(q[j]);
+    for (int o = 1; o < kWave; o <<= 1) {
+      const int ym = __shfl_up(sm, o), yq = __shfl_up(sq, o);
+      if (lane_id() >= o) {
+        sm += ym;
+        sq += yq;
       }
+    }
+    const uint64_t many = __ballot(m > 1);
+    const uint64_t hit = JOIN ? __ballot(m > 1 && several + __popcll(many & ((1ull << lane_id()) - 1ull)) == j)
+                              : __ballot(a < L && segs + sm > j);
+    if (hit) {
+      const int f = __ffsll((unsigned long long)hit) - 1;
+      const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, f); };
+      const int64_t row = of((int)b), end = of((int)e);
+      s->a = a0 + f;
+      s->m = of(m);
+      const int64_t k = JOIN ? 0 : j - (segs + of(sm) - s->m);
+      const int64_t len = ((end - row + s->m - 1) / s->m + kOuterRows - 1) / kOuterRows * kOuterRows;
+      s->row = row + k * len;
+      s->end = min(end, s->row + len);
+      s->slot = s->m > 1 ? slots + of(sq) - s->m + k : -1;
+      return s->slot < 2 * (int64_t)p.chunks;  // a plan of these sizes has no more
+    }
+    segs += __builtin_amdgcn_readlane(sm, kWave - 1);
+    slots += __builtin_amdgcn_readlane(sq, kWave - 1);
+    several += __popcll(many);
+  }
+  return false;
+}
+
+// Sums of one block's columns [c0, c0 + CB) of a factor.  Each thread reads 8
+// rows x 8 bytes (a wave two whole 256-byte row pieces), turns them in
+// registers into lines of 8 rows, and hands them to the block through LDS; the
+// saved values already lie so.  The four waves then sum a quarter of the
+// columns each, over all rows: no partial sums to join.  F32: X is float32,
+// three bf16 parts like the saved values; products of parts whose sizes lie
+// 2^-27 or more apart are left out.
+template <int RT, bool F32>
+__device__ __forceinline__ void outer_block(const OuterParams& p, const OuterSide& s, const OuterSegment& seg, int c0,
+                                            __bf16* lds) {
+  constexpr int XP = F32 ? 3 : 1;       // parts of X
+  constexpr int CB = F32 ? 64 : 128;    // columns of a block
+  constexpr int TW = CB / 64;           // matrix columns blocks of a wave
+  constexpr int W = F32 ? 2 : 4;        // columns of a thread
+  constexpr int NV = (3 * 16 * RT * 8 + 255) / 256;
+  typedef std::conditional_t<F32, float, uint16_t> X;
+  __bf16* xs = lds;
+  __bf16* vs = lds + XP * CB * kOuterRows;
+  const int lane = lane_id(), w = threadIdx.x / kWave, l16 = lane & 15, g = lane >> 4;
+  const int piece = threadIdx.x / 32, col = threadIdx.x % 32 * W;
+  const bool in = c0 + col < s.C;
+  const X* x = static_cast<const X*>(s.x) + c0 + col;
+  const int64_t M = p.plan.max_rows;
+  int64_t row = seg.row;
+  const int64_t end = seg.end;
+  // The next step's tokens, as they lie in the plan: read without a condition
+  // and looked at when they are used (a test at the read would wait for it, and
+  // for all reads before it).
+  int4 tok[2];
+  uint32_t raw[8][2];
+  v4u rv[NV];
+  const auto tokens = [&](int64_t r) {
+    const int4* t = reinterpret_cast<const int4*>(p.plan.rows + min(r + 8 * piece, M - 8));
+    tok[0] = t[0];
+    tok[1] = t[1];
+  };
+  const auto load = [&](int64_t r) {
+    const int32_t t[8] = {tok[0].x, tok[0].y, tok[0].z, tok[0].w, tok[1].x, tok[1].y, tok[1].z, tok[1].w};
+    const bool live = in && r + 8 * piece < end;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float col[8] = {x[0][j], x[1][j], x[2][j], x[3][j], x[4][j], x[5][j], x[6][j], x[7][j]};
+    for (int i = 0; i < 8; ++i) {
+      const bool ok = live && t[i] >= 0 && t[i] < p.plan.tokens;
+      load_words<2>(x + (ok ? t[i] : 0) * s.x_stride, ok, raw[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = i * 256 + threadIdx.x, line = v / 8;  // line: part, then rank
+      const int rank = line % (16 * RT), part = line / (16 * RT);
+      const bool ok = line < 3 * 16 * RT && rank < p.rank_pad && r + 8 * (v % 8) < end;
+      rv[i] = ok ? *reinterpret_cast<const v4u*>(s.saved + ((int64_t)part * p.rank_pad + rank) * M + r + 8 * (v % 8))
+                 : v4u{0, 0, 0, 0};
+    }
+  };
+  const auto put = [&]() {
+    if constexpr (F32) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float v[8];
         v8bf q[3];
-        split8<3>(col, q);
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(raw[i][j]);
+        split8<3>(v, q);
 #pragma unroll
-          for (int n = 2; n >= 0; --n)
-#pragma unroll
-            for (int m = 2 - n; m >= 0; --m) acc[r * CT + j] = mfma_bf16(u[r][n], q[m], acc[r * CT + j]);
+        for (int n = 0; n < 3; ++n)
+          *reinterpret_cast<v8bf*>(xs + n * CB * kOuterRows + outer_at(col + j, piece)) = q[n];
       }
     } else {
-      uint32_t raw[8][CT / 2];
+      v8bf q[4];
+      transpose8<2>(raw, q);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        load_words<CT / 2>(static_cast<const uint16_t*>(s.x) + t[i] * s.x_stride + c, t[i] >= 0, raw[i]);
-      v8bf x[CT];
-      transpose8<CT / 2>(raw, x);
+      for (int j = 0; j < 4; ++j) *reinterpret_cast<v8bf*>(xs + outer_at(col + j, piece)) = q[j];
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = i * 256 + threadIdx.x;
+      if (3 * 16 * RT * 8 % 256 == 0 || v < 3 * 16 * RT * 8)
+        *reinterpret_cast<v4u*>(vs + outer_at(v / 8, v % 8)) = rv[i];
+    }
+  };
+  v4f acc[TW][RT];
+#pragma unroll
+  for (int t = 0; t < TW; ++t)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[t][r] = v4f{0.f, 0.f, 0.f, 0.f};
+  if (row < end) {
+    tokens(row);
+    load(row);
+    tokens(row + kOuterRows);
+  }
+  for (; row < end; row += kOuterRows) {
+    put();
+    __syncthreads();
+    if (row + kOuterRows < end) {  // under this step's products
+      load(row + kOuterRows);
+      tokens(row + 2 * kOuterRows);
+    }
+#pragma unroll
+    for (int k = 0; k < kOuterRows / 32; ++k) {
+      v8bf u[RT][3];
 #pragma unroll
       for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int j = 0; j < CT; ++j)
+        for (int n = 0; n < 3; ++n)
+          u[r][n] = *reinterpret_cast<const v8bf*>(vs + outer_at((n * RT + r) * 16 + l16, 4 * k + g));
 #pragma unroll
-          for (int n = 2; n >= 0; --n) acc[r * CT + j] = mfma_bf16(u[r][n], x[j], acc[r * CT + j]);
+      for (int t = 0; t < TW; ++t)
+#pragma unroll
+        for (int m = XP - 1; m >= 0; --m) {
+          const v8bf q = *reinterpret_cast<const v8bf*>(
+              xs + m * CB * kOuterRows + outer_at((w * TW + t) * 16 + l16, 4 * k + g));
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int n = 2 - m; n >= 0; --n) acc[t][r] = mfma_bf16(q, u[r][n], acc[t][r]);
+        }
     }
+    __syncthreads();
   }
-}
-
-// Block (16 CT columns, adapter, 16 RT ranks): the waves take the adapter's
-// rows in turn and join their sums.  An adapter without tokens gets zeros.
-template <int RT, int CT, bool F32>
-__global__ __launch_bounds__(kOuterWaves* kWave) void k_adapter_outer(OuterParams p, OuterSide s) {
-  __shared__ v4f red[kOuterWaves / 2 * RT * CT * kWave];
-  const int c0 = blockIdx.x * 16 * CT, a = blockIdx.y, r0 = blockIdx.z * 16 * RT;
-  v4f acc[RT * CT];
+  float* grad = seg.slot < 0 ? s.grad + (int64_t)seg.a * p.rank * s.C
+                             : p.part + (seg.slot * (p.x.C + p.dout.C) + s.part_at) * p.rank;
+  // lane: rank l16 of a rank block, columns 4 g .. 4 g + 3 of a column block
 #pragma unroll
-  for (int i = 0; i < RT * CT; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
-  outer_sum<RT, CT, F32>(p, s, a, r0, c0, acc);
-  join_waves<kOuterWaves>(acc, red);
-  if (threadIdx.x >= kWave) return;
-  const int l16 = threadIdx.x & 15, g = threadIdx.x >> 4;
-  const int c = c0 + CT * l16;
-  if (c >= s.C) return;
+  for (int t = 0; t < TW; ++t)
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int q = r0 + 16 * r + 4 * g + i;
-      if (q >= p.rank) continue;
-      float* dst = s.grad + ((int64_t)a * p.rank + q) * s.C + c;
-#pragma unroll
-      for (int j = 0; j < CT; j += 4)
-        *reinterpret_cast<v4f*>(dst + j) =
-            v4f{acc[r * CT + j][i], acc[r * CT + j + 1][i], acc[r * CT + j + 2][i], acc[r * CT + j + 3][i]};
+    for (int r = 0; r < RT; ++r) {
+      const int c = c0 + (w * TW + t) * 16 + 4 * g, q = 16 * r + l16;
+      if (q < p.rank && c < s.C)
+        *reinterpret_cast<v4f*>(grad + (int64_t)q * s.C + c) = acc[t][r];
     }
 }
 
-template <int RT, int CT, bool F32>
-static void launch_outer(const OuterParams& p, const OuterSide& s, hipStream_t st) {
-  const dim3 grid((unsigned)((s.C + 16 * CT - 1) / (16 * CT)), (unsigned)p.plan.adapters,
-                  (unsigned)((p.rank_pad + 16 * RT - 1) / (16 * RT)));
-  k_adapter_outer<RT, CT, F32><<<grid, kOuterWaves * kWave, 0, st>>>(p, s);
+// Block (columns of either factor, segment).  Both factors in one launch: the
+// second's blocks fill the CUs the first leaves.
+template <int RT, bool F32>
+__global__ __launch_bounds__(256) void k_adapter_outer(OuterParams p) {
+  constexpr int kLds = (F32 ? 3 * 64 : 128) * kOuterRows + 3 * 16 * RT * kOuterRows;
+  __shared__ __align__(16) __bf16 lds[kLds];
+  // columns first, over all XCDs: segments differ in length, and a run of them on
+  // one XCD (its L2 would hold their saved values) left others idle
+  const int64_t id = blockIdx.x;
+  OuterSegment seg;
+  if (!outer_segment<false>(p, id / p.cols, &seg)) return;
+  const int col = (int)(id % p.cols), second = col - p.cols0;
+  if (second < 0) outer_block<RT, false>(p, p.x, seg, col * 128, lds);
+  else outer_block<RT, F32>(p, p.dout, seg, second * (F32 ? 64 : 128), lds);
 }
-hipError_t launch_adapter_outer(const OuterParams& p, const OuterSide& s, bool x_f32, hipStream_t st) {
-  if (x_f32) {
-    if (p.rank_pad <= 16) launch_outer<1, 4, true>(p, s, st);
-    else if (p.rank_pad <= 32) launch_outer<2, 4, true>(p, s, st);
-    else launch_outer<4, 4, true>(p, s, st);
+
+// Block (elements, j): the partial sums of the j-th adapter of several
+// segments, added in the rows' order.
+__global__ __launch_bounds__(256) void k_adapter_outer_join(OuterParams p) {
+  OuterSegment seg;
+  if (!outer_segment<true>(p, blockIdx.y, &seg)) return;
+  const int64_t CA = (int64_t)p.x.C * p.rank, both = CA + (int64_t)p.dout.C * p.rank;
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= both) return;
+  const int64_t step = both / 4, last = min((int64_t)seg.m, 2 * (int64_t)p.chunks - seg.slot);
+  const v4f* src = reinterpret_cast<const v4f*>(p.part + i) + seg.slot * step;
+  v4f v = {0.f, 0.f, 0.f, 0.f};
+  for (int64_t k = 0; k < last; k += 4) {  // four segments' reads together
+    v4f x[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) x[q] = k + q < last ? src[(k + q) * step] : v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v += x[q];
+  }
+  float* dst = i < CA ? p.x.grad + seg.a * CA + i : p.dout.grad + (int64_t)seg.a * (both - CA) + (i - CA);
+  *reinterpret_cast<v4f*>(dst) = v;
+}
+
+template <int RT, bool F32>
+static void launch_outer(OuterParams p, hipStream_t st) {
+  const int cols = F32 ? 64 : 128;
+  p.cols0 = (p.x.C + 127) / 128;
+  p.cols = p.cols0 + (p.dout.C + cols - 1) / cols;
+  // at most one segment an adapter and one a chunk
+  k_adapter_outer<RT, F32><<<(unsigned)(p.cols * ((int64_t)p.plan.adapters + p.chunks)), 256, 0, st>>>(p);
+}
+hipError_t launch_adapter_outer(const OuterParams& p, bool dout_f32, hipStream_t st) {
+  const int rt = p.rank_pad / 16;
+  if (dout_f32) {
+    if (rt <= 1) launch_outer<1, true>(p, st);
+    else if (rt <= 2) launch_outer<2, true>(p, st);
+    else if (rt <= 4) launch_outer<4, true>(p, st);
+    else launch_outer<8, true>(p, st);
   } else {
-    if (p.rank_pad <= 16) launch_outer<1, 8, false>(p, s, st);
-    else if (p.rank_pad <= 32) launch_outer<2, 8, false>(p, s, st);
-    else launch_outer<4, 4, false>(p, s, st);
+    if (rt <= 1) launch_outer<1, false>(p, st);
+    else if (rt <= 2) launch_outer<2, false>(p, st);
+    else if (rt <= 4) launch_outer<4, false>(p, st);
+    else launch_outer<8, false>(p, st);
   }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.chunks <= 1) return e;
+  const int64_t both = (int64_t)p.rank * (p.x.C + p.dout.C);
+  k_adapter_outer_join<<<dim3((unsigned)((both + 1023) / 1024), (unsigned)min(p.chunks, p.plan.adapters)), 256, 0, st>>>(p);
   return hipGetLastError();
 }
 

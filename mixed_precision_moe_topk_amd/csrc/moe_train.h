@@ -67,6 +67,7 @@ constexpr int kAdapterTile = 64;     // rows of a tile
 constexpr int kAdapterPad = 16;      // an adapter's rows start at a multiple of this
 constexpr int kPlanChunk = 64;       // tokens per wave of the plan kernels
 constexpr int kPlanGroup = 1024;     // tokens per block of the plan kernels
+constexpr int kPlanOne = 8 * kPlanGroup;  // tokens planned in one launch
 
 // Plan of a batch: its tokens grouped by adapter.  Int32 words:
 //   head [4]: tiles, padded rows, tiles of tokens with an adapter (the first)
@@ -158,7 +159,7 @@ struct ExpandParams {
   int64_t base_stride;
   void* out;
   int64_t out_stride;
-  int32_t col_blocks;  // set by the launcher
+  int32_t col_blocks, row_blocks;  // of a tile, set by the launcher
 };
 // grad[adapter][r][c] = sum over the adapter's rows of saved[r][row] * X[token(row)][c]
 struct OuterSide {
@@ -167,14 +168,20 @@ struct OuterSide {
   int64_t x_stride;
   int32_t C;
   float* grad;
+  int64_t part_at;  // columns before its own in a slot of the partial sums
 };
 struct OuterParams {
   PlanView plan;
+  OuterSide x, dout;  // dout bf16 or float32
   int32_t rank, rank_pad;
+  int64_t chunk;      // most rows of a segment (a multiple of 64)
+  int32_t chunks;     // chunks of all rows
+  float* part;        // [2 chunks][rank (x.C + dout.C)]
+  int32_t cols0, cols;  // column blocks of x and of both, set by the launcher
 };
 hipError_t launch_adapter_shrink(const ShrinkParams& p, bool x_f32, hipStream_t st);
 hipError_t launch_adapter_expand(const ExpandParams& p, bool out_f32, hipStream_t st);
 hipError_t launch_adapter_join(const JoinParams& p, hipStream_t st);
-hipError_t launch_adapter_outer(const OuterParams& p, const OuterSide& s, bool x_f32, hipStream_t st);
+hipError_t launch_adapter_outer(const OuterParams& p, bool dout_f32, hipStream_t st);
 
 }  // namespace moe

@@ -106,13 +106,15 @@ int32_t max_slots(const moe::ShrinkShape& s) { return (s.units - 1) / s.min_run 
 // Up to so many tokens expand adds up the parts for itself.
 constexpr int64_t kFewTokens = 128;
 
-// Workspace: the parts of the larger contraction, expand's operands, and the
-// backward pass's v as outer's operands.
+// Workspace: the sums of the larger contraction, expand's operands, the backward
+// pass's v as outer's operands, and the factors' gradients of the segments.
 struct AdapterLayout {
   moe::PlanLayout plan;
   int32_t rp, rp32;
   moe::ShrinkShape shape_x, shape_d;
-  size_t part_bytes, frag_bytes, saved_bytes;
+  size_t part_bytes, frag_bytes, saved_bytes, outer_bytes;
+  int64_t chunk;  // rows of a segment of the factors' gradients
+  int32_t chunks;
   AdapterLayout(const moe_adapter_dims* d, int64_t tokens)
       : plan(d->num_adapters, tokens), rp(rank_pad(d)), rp32((d->rank + 31) / 32 * 32) {
     shape_x = shrink_shape(tokens, d->in_features);
@@ -120,8 +122,20 @@ struct AdapterLayout {
     part_bytes = align256((size_t)std::max(max_slots(shape_x), max_slots(shape_d)) * plan.max_rows * rp * 4);
     frag_bytes = align256((size_t)plan.max_rows * rp32 * 6);
     saved_bytes = align256((size_t)plan.max_rows * rp * 6);
+    // segments of all adapters for as many blocks as run at once (registers
+    // allow 4, 2 or 1 a CU by the rank), 256 rows a segment at least: rows are
+    // cut into what is left when every adapter has one, or into half as many
+    const int64_t cols = ceil_div(d->in_features, 128) +
+                         ceil_div(d->out_features, d->out_type == MOE_T_F32 ? 64 : 128);
+    const int64_t segments = std::max<int64_t>(1, (rp <= 32 ? 1024 : rp <= 64 ? 512 : 256) / cols);
+    const int64_t cuts = std::max({(int64_t)1, segments / 2, segments - d->num_adapters});
+    chunk = std::max<int64_t>(256, ceil_div(ceil_div(plan.max_rows, cuts), 64) * 64);
+    chunks = (int32_t)std::max<int64_t>(1, ceil_div(plan.max_rows, chunk));
+    outer_bytes = chunks > 1 ? align256((size_t)chunks * 2 * d->rank *
+                                        ((size_t)d->in_features + d->out_features) * 4) : 0;
   }
-  size_t workspace() const { return part_bytes + frag_bytes + saved_bytes; }
+  size_t outer_at() const { return part_bytes + frag_bytes + saved_bytes; }
+  size_t workspace() const { return outer_at() + outer_bytes; }
 };
 
 moe::PlanView plan_view(const void* plan, const moe::PlanLayout& l, int32_t adapters,
@@ -180,7 +194,7 @@ moe_status run_product(const Product& q, const moe::PlanView& v, const AdapterLa
   if (!q.out) return MOE_OK;
   const moe::ExpandParams e = {v, q.shape, low.frag, part, scale, static_cast<const uint16_t*>(q.w2),
                                rank, l.rp, l.rp32, q.features2, q.base, q.base_stride, q.out,
-                               q.out_stride, 0};
+                               q.out_stride, 0, 0};
   return moe::check_hip(moe::launch_adapter_expand(e, q.out_f32, stream), "adapter expand", stream);
 }
 
@@ -399,12 +413,17 @@ moe_status moe_adapter_backward(const moe_adapter_dims* dims, const void* dout,
     MOE_RETURN_IF(run_product(q, v, l, dims->rank, scale, workspace, stream));
   }
   if (!da) return moe::set_ok();
-  const moe::OuterParams o = {v, dims->rank, l.rp};
-  const moe::OuterSide sa = {static_cast<const uint16_t*>(vt), x, x_stride, dims->in_features, da};
-  const moe::OuterSide sb = {static_cast<const uint16_t*>(saved), dout, dout_stride,
-                             dims->out_features, db};
-  MOE_RETURN_IF(moe::check_hip(moe::launch_adapter_outer(o, sa, false, stream), "adapter da", stream));
-  MOE_RETURN_IF(moe::check_hip(moe::launch_adapter_outer(o, sb, f32, stream), "adapter db", stream));
+  moe::OuterParams o = {};
+  o.plan = v;
+  o.x = {static_cast<const uint16_t*>(vt), x, x_stride, dims->in_features, da, 0};
+  o.dout = {static_cast<const uint16_t*>(saved), dout, dout_stride, dims->out_features, db,
+            dims->in_features};
+  o.rank = dims->rank;
+  o.rank_pad = l.rp;
+  o.chunk = l.chunk;
+  o.chunks = l.chunks;
+  o.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + l.outer_at());
+  MOE_RETURN_IF(moe::check_hip(moe::launch_adapter_outer(o, f32, stream), "adapter gradients", stream));
   return moe::set_ok();
 }
 

@@ -130,6 +130,10 @@ def one(rng, T, L):
     return np.full(T, L - 1)
 
 
+def few_of_many(rng, T, L):
+    return np.sort(rng.choice([2, 3, 17, 30, -1], T, p=[0.5, 0.01, 0.4, 0.05, 0.04]))
+
+
 def nobody(rng, T, L):
     return np.full(T, -1)
 
@@ -159,6 +163,12 @@ CASES = [  # tokens, adapters, rank, K, N, out, ids
     (1025, 9, 24, 256, 384, "bf16", some_without),    # past the single-block plan
     (2500, 5, 32, 128, 256, "bf16", runs),
     (40, 3, 16, 128, 128, "bf16", nobody),
+    (32, 40, 8, 64, 64, "bf16", each),                # a padded row count without slack, then idle adapters
+    (1500, 40, 16, 128, 256, "bf16", few_of_many),    # segments of adapters with idle ones between
+    (1500, 40, 70, 136, 64, "f32", few_of_many),
+    (2100, 1, 16, 256, 136, "bf16", one),             # one adapter's rows in several segments
+    (1100, 1, 128, 128, 128, "f32", one),
+    (9000, 3, 8, 64, 64, "bf16", scattered),          # past the plan of one launch
 ]
 
 
