@@ -494,7 +494,7 @@ __device__ __forceinline__ void shrink_staged(const ShrinkParams& p, const Tile&
 // kShrinkBlocks blocks, two a CU; block b runs on XCD b % 8, and neighbouring
 // runs, mostly of one adapter, go to one XCD, whose L2 then holds its factor.
 template <int RT, bool F32>
-__global__ __launch_bounds__(256) void k_adapter_shrink(ShrinkParams p) {
+__global__ __launch_bounds__(256, 2) void k_adapter_shrink(ShrinkParams p) {
   constexpr int kLds = F32 ? 16 : ShrinkLds<RT>::kWords;
   __shared__ uint4 lds[(kLds * 2 > 2 * RT * kWave * 16 ? kLds * 2 : 2 * RT * kWave * 16) / 16];
   const int lane = lane_id(), w = threadIdx.x / kWave, l16 = lane & 15, g = lane >> 4;
@@ -620,7 +620,7 @@ struct Row8F32 {
 // (frag); else as the float32 sums of shrink's blocks, which every wave adds up
 // for itself: less time than a launch that does it once, where rows are few.
 template <int RT, typename T, bool JOINED>
-__global__ __launch_bounds__(256) void k_adapter_expand(ExpandParams p) {
+__global__ __launch_bounds__(256, JOINED ? (RT == 1 && sizeof(T) == 2 ? 4 : RT <= 2 ? 3 : 2) : 1) void k_adapter_expand(ExpandParams p) {
   constexpr int PARTS = sizeof(T) == 4 ? 3 : 2;
   typedef std::conditional_t<sizeof(T) == 4, Row8F32, Row8Bf16> Row8;
   // neighbouring blocks on one XCD (block b runs on XCD b % 8), columns first:
@@ -835,7 +835,7 @@ __device__ __forceinline__ void outer_block(const OuterParams& p, const OuterSid
   const int lane = lane_id(), w = threadIdx.x / kWave, l16 = lane & 15, g = lane >> 4;
   const int piece = threadIdx.x / 32, col = threadIdx.x % 32 * W;
   const bool in = c0 + col < s.C;
-  const X* x = static_cast<const X*>(s.x) + c0 + col;
+  const X* x = static_cast<const X*>(s.x) + (in ? c0 + col : 0);
   const int64_t M = p.plan.max_rows;
   int64_t row = seg.row;
   const int64_t end = seg.end;
@@ -850,24 +850,29 @@ __device__ __forceinline__ void outer_block(const OuterParams& p, const OuterSid
     tok[0] = t[0];
     tok[1] = t[1];
   };
+  uint32_t keep;  // bit i: row i of this thread's 8 counts (padding and rows behind the end do not)
   const auto load = [&](int64_t r) {
     const int32_t t[8] = {tok[0].x, tok[0].y, tok[0].z, tok[0].w, tok[1].x, tok[1].y, tok[1].z, tok[1].w};
-    const bool live = in && r + 8 * piece < end;
+    keep = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const bool ok = live && t[i] >= 0 && t[i] < p.plan.tokens;
-      load_words<2>(x + (ok ? t[i] : 0) * s.x_stride, ok, raw[i]);
+      const bool ok = (uint32_t)t[i] < (uint32_t)p.plan.tokens;
+      keep |= ok && in && r + 8 * piece < end ? 1u << i : 0;
+      load_words<2>(x + (ok ? t[i] : 0) * s.x_stride, true, raw[i]);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = i * 256 + threadIdx.x, line = v / 8;  // line: part, then rank
-      const int rank = line % (16 * RT), part = line / (16 * RT);
-      const bool ok = line < 3 * 16 * RT && rank < p.rank_pad && r + 8 * (v % 8) < end;
-      rv[i] = ok ? *reinterpret_cast<const v4u*>(s.saved + ((int64_t)part * p.rank_pad + rank) * M + r + 8 * (v % 8))
-                 : v4u{0, 0, 0, 0};
+      const int v = i * 256 + threadIdx.x, line = min(v / 8, 3 * 16 * RT - 1);  // line: part, then rank
+      const int rank = min(line % (16 * RT), p.rank_pad - 1), part = line / (16 * RT);
+      rv[i] = *reinterpret_cast<const v4u*>(s.saved + ((int64_t)part * p.rank_pad + rank) * M +
+                                            min(r + 8 * (v % 8), M - 8));
     }
   };
-  const auto put = [&]() {
+  const auto put = [&](int64_t r) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) raw[i][j] = keep >> i & 1 ? raw[i][j] : 0;
     if constexpr (F32) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -889,8 +894,9 @@ __device__ __forceinline__ void outer_block(const OuterParams& p, const OuterSid
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = i * 256 + threadIdx.x;
+      const bool ok = r + 8 * (v % 8) < end;  // (ranks behind the last repeat it, and are not stored)
       if (3 * 16 * RT * 8 % 256 == 0 || v < 3 * 16 * RT * 8)
-        *reinterpret_cast<v4u*>(vs + outer_at(v / 8, v % 8)) = rv[i];
+        *reinterpret_cast<v4u*>(vs + outer_at(v / 8, v % 8)) = ok ? rv[i] : v4u{0, 0, 0, 0};
     }
   };
   v4f acc[TW][RT];
@@ -904,7 +910,7 @@ __device__ __forceinline__ void outer_block(const OuterParams& p, const OuterSid
     tokens(row + kOuterRows);
   }
   for (; row < end; row += kOuterRows) {
-    put();
+    put(row);
     __syncthreads();
     if (row + kOuterRows < end) {  // under this step's products
       load(row + kOuterRows);
@@ -948,7 +954,7 @@ __device__ __forceinline__ void outer_block(const OuterParams& p, const OuterSid
 // Block (columns of either factor, segment).  Both factors in one launch: the
 // second's blocks fill the CUs the first leaves.
 template <int RT, bool F32>
-__global__ __launch_bounds__(256) void k_adapter_outer(OuterParams p) {
+__global__ __launch_bounds__(256, RT <= 2 ? 4 : RT == 4 ? 2 : 1) void k_adapter_outer(OuterParams p) {
   constexpr int kLds = (F32 ? 3 * 64 : 128) * kOuterRows + 3 * 16 * RT * kOuterRows;
   __shared__ __align__(16) __bf16 lds[kLds];
   // columns first, over all XCDs: segments differ in length, and a run of them on

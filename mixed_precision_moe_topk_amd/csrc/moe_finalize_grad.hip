@@ -42,13 +42,18 @@ __global__ __launch_bounds__(256) void k_finalize_grad(const uint16_t* __restric
   __shared__ float red[4][KC];
   const int64_t t = blockIdx.x;
   const int j0 = blockIdx.y * KC;
+  // a slot past the last, or a row outside the batch, reads row 0 and stores
+  // nothing (no branch around a read: the reads of a column group go together)
   int64_t row[KC];
+  bool ok[KC];
   float w[KC], acc[KC];
 #pragma unroll
   for (int j = 0; j < KC; ++j) {
-    const int64_t r = j0 + j < k ? slot_row[t * k + j0 + j] : -1;
-    row[j] = r >= 0 && r < rows ? r : -1;  // a slot past the last, or no row of the batch
-    w[j] = row[j] >= 0 ? weights[t * k + j0 + j] : 0.0f;
+    const int s = j0 + j < k ? j0 + j : k - 1;
+    const int64_t r = slot_row[t * k + s];
+    ok[j] = j0 + j < k && r >= 0 && r < rows;
+    row[j] = ok[j] ? r : 0;
+    w[j] = weights[t * k + s];
     acc[j] = 0.0f;
   }
   const int nv = H / 8;
@@ -57,19 +62,16 @@ __global__ __launch_bounds__(256) void k_finalize_grad(const uint16_t* __restric
     bf16x8_to_f32(reinterpret_cast<const uint4*>(dout + t * H)[i], d);
     float4 y[KC][2];
 #pragma unroll
-    for (int j = 0; j < KC; ++j)
-      if (row[j] >= 0) {
-        const float4* src = reinterpret_cast<const float4*>(y2 + row[j] * H) + 2 * i;
-        y[j][0] = load_stream(src);
-        y[j][1] = load_stream(src + 1);
-      } else {
-        y[j][0] = y[j][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
+    for (int j = 0; j < KC; ++j) {
+      const float4* src = reinterpret_cast<const float4*>(y2 + row[j] * H) + 2 * i;
+      y[j][0] = load_stream(src);
+      y[j][1] = load_stream(src + 1);
+    }
 #pragma unroll
     for (int j = 0; j < KC; ++j) {
       acc[j] += d[0] * y[j][0].x + d[1] * y[j][0].y + d[2] * y[j][0].z + d[3] * y[j][0].w +
                 d[4] * y[j][1].x + d[5] * y[j][1].y + d[6] * y[j][1].z + d[7] * y[j][1].w;
-      if (ROWS != kNoRows && row[j] >= 0) {
+      if (ROWS != kNoRows && ok[j]) {
         float g[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) g[c] = w[j] * d[c];
@@ -94,8 +96,11 @@ __global__ __launch_bounds__(256) void k_finalize_grad(const uint16_t* __restric
   }
   __syncthreads();
   const int j = threadIdx.x;
+  bool mine = false;
+#pragma unroll
+  for (int q = 0; q < KC; ++q) mine |= q == j && ok[q];
   if (j < KC && j0 + j < k)
-    dweights[t * k + j0 + j] = (red[0][j] + red[1][j]) + (red[2][j] + red[3][j]);
+    dweights[t * k + j0 + j] = mine ? (red[0][j] + red[1][j]) + (red[2][j] + red[3][j]) : 0.0f;
 }
 
 template <int KC>
