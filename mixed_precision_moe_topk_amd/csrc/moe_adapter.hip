@@ -583,7 +583,8 @@ hipError_t launch_adapter_join(const JoinParams& p, hipStream_t st) {
 // ---------------------------------------------------------------- expand
 constexpr int kExpandCols = 128;  // columns of a wave
 
-// 8 elements of a row; read once and written once, so past the caches.
+// 8 elements of a row.  bf16 rows pass the caches by (read once, written once);
+// float32 ones take two accesses to a line, which must not leave in between.
 struct Row8Bf16 {
   v4u w;
   __device__ __forceinline__ void load(const uint16_t* p) {
@@ -602,13 +603,13 @@ struct Row8Bf16 {
 struct Row8F32 {
   v4f w[2];
   __device__ __forceinline__ void load(const float* p) {
-    w[0] = __builtin_nontemporal_load(reinterpret_cast<const v4f*>(p));
-    w[1] = __builtin_nontemporal_load(reinterpret_cast<const v4f*>(p) + 1);
+    w[0] = reinterpret_cast<const v4f*>(p)[0];
+    w[1] = reinterpret_cast<const v4f*>(p)[1];
   }
   __device__ __forceinline__ float get(int j) const { return w[j / 4][j % 4]; }
   __device__ __forceinline__ static void store(float* p, const float (&v)[8]) {
-    __builtin_nontemporal_store(v4f{v[0], v[1], v[2], v[3]}, reinterpret_cast<v4f*>(p));
-    __builtin_nontemporal_store(v4f{v[4], v[5], v[6], v[7]}, reinterpret_cast<v4f*>(p) + 1);
+    reinterpret_cast<v4f*>(p)[0] = v4f{v[0], v[1], v[2], v[3]};
+    reinterpret_cast<v4f*>(p)[1] = v4f{v[4], v[5], v[6], v[7]};
   }
 };
 

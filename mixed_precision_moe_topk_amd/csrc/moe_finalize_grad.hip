@@ -10,13 +10,11 @@ extern "C" __device__ __attribute__((const)) float __ockl_wfred_add_f32(float);
 
 namespace moe {
 
-__device__ __forceinline__ void bf16x8_to_f32(const uint4& u, float (&v)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    v[2 * j] = __uint_as_float(w[j] << 16);
-    v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-  }
+__device__ __forceinline__ void bf16x4_to_f32(const uint2& u, float (&v)[4]) {
+  v[0] = __uint_as_float(u.x << 16);
+  v[1] = __uint_as_float(u.x & 0xFFFF0000u);
+  v[2] = __uint_as_float(u.y << 16);
+  v[3] = __uint_as_float(u.y & 0xFFFF0000u);
 }
 
 // Rounds to bf16 to nearest even; NaN stays NaN (bf16_bits takes finite
@@ -25,21 +23,23 @@ __device__ __forceinline__ uint32_t bf16_bits_any(float v) {
   return v == v ? bf16_bits(v) : 0x7FC0u | (__float_as_uint(v) >> 16 & 0x8000u);
 }
 
+constexpr int kGradThreads = 512;  // at most; see grad_threads
+
 enum RowGrad : int { kNoRows = 0, kRowsBf16 = 1, kRowsF32 = 2 };
 
-// One block of 256 threads per (token, KC slots from slot blockIdx.y * KC).
-// Thread i holds columns [8 i, 8 i + 8), + 2048, ...; the KC rows of a column
-// group are read together.  dy2 may be y2: a thread writes an element after it
+// One block per (token, KC slots from slot blockIdx.y * KC).  Thread i holds
+// columns [4 i, 4 i + 4), then those a block's width further, ...; the KC rows
+// of a column group are read together, each wave a whole kilobyte of a row.  dy2 may be y2: a thread writes an element after it
 // has read it.
 template <int KC, int ROWS>
-__global__ __launch_bounds__(256) void k_finalize_grad(const uint16_t* __restrict__ dout,
+__global__ __launch_bounds__(kGradThreads) void k_finalize_grad(const uint16_t* __restrict__ dout,
                                                        const float* __restrict__ weights,
                                                        const float* y2,
                                                        const int32_t* __restrict__ slot_row,
                                                        int32_t k, int32_t H, int64_t rows,
                                                        float* __restrict__ dweights,
                                                        void* dy2) {
-  __shared__ float red[4][KC];
+  __shared__ float red[kGradThreads / kWave][KC];
   const int64_t t = blockIdx.x;
   const int j0 = blockIdx.y * KC;
   // a slot past the last, or a row outside the batch, reads row 0 and stores
@@ -56,34 +56,27 @@ __global__ __launch_bounds__(256) void k_finalize_grad(const uint16_t* __restric
     w[j] = weights[t * k + s];
     acc[j] = 0.0f;
   }
-  const int nv = H / 8;
-  for (int i = threadIdx.x; i < nv; i += 256) {
-    float d[8];
-    bf16x8_to_f32(reinterpret_cast<const uint4*>(dout + t * H)[i], d);
-    float4 y[KC][2];
+  const int nv = H / 4;
+  for (int i = threadIdx.x; i < nv; i += blockDim.x) {
+    float d[4];
+    bf16x4_to_f32(reinterpret_cast<const uint2*>(dout + t * H)[i], d);
+    float4 y[KC];
 #pragma unroll
     for (int j = 0; j < KC; ++j) {
-      const float4* src = reinterpret_cast<const float4*>(y2 + row[j] * H) + 2 * i;
-      y[j][0] = load_stream(src);
-      y[j][1] = load_stream(src + 1);
+      const float4* src = reinterpret_cast<const float4*>(y2 + row[j] * H) + i;
+      y[j] = KC == 1 ? *src : load_stream(src);
     }
 #pragma unroll
     for (int j = 0; j < KC; ++j) {
-      acc[j] += d[0] * y[j][0].x + d[1] * y[j][0].y + d[2] * y[j][0].z + d[3] * y[j][0].w +
-                d[4] * y[j][1].x + d[5] * y[j][1].y + d[6] * y[j][1].z + d[7] * y[j][1].w;
+      acc[j] += d[0] * y[j].x + d[1] * y[j].y + d[2] * y[j].z + d[3] * y[j].w;
       if (ROWS != kNoRows && ok[j]) {
-        float g[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) g[c] = w[j] * d[c];
+        const v4f g = {w[j] * d[0], w[j] * d[1], w[j] * d[2], w[j] * d[3]};
         if (ROWS == kRowsF32) {
-          v4f* dst = reinterpret_cast<v4f*>(static_cast<float*>(dy2) + row[j] * H) + 2 * i;
-          __builtin_nontemporal_store(v4f{g[0], g[1], g[2], g[3]}, dst);
-          __builtin_nontemporal_store(v4f{g[4], g[5], g[6], g[7]}, dst + 1);
+          __builtin_nontemporal_store(g, reinterpret_cast<v4f*>(static_cast<float*>(dy2) + row[j] * H) + i);
         } else {
-          v4u o;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) o[c] = bf16_bits_any(g[2 * c]) | bf16_bits_any(g[2 * c + 1]) << 16;
-          __builtin_nontemporal_store(o, reinterpret_cast<v4u*>(static_cast<uint16_t*>(dy2) + row[j] * H) + i);
+          typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+          const v2u o = {bf16_bits_any(g[0]) | bf16_bits_any(g[1]) << 16, bf16_bits_any(g[2]) | bf16_bits_any(g[3]) << 16};
+          __builtin_nontemporal_store(o, reinterpret_cast<v2u*>(static_cast<uint16_t*>(dy2) + row[j] * H) + i);
         }
       }
     }
@@ -99,8 +92,18 @@ __global__ __launch_bounds__(256) void k_finalize_grad(const uint16_t* __restric
   bool mine = false;
 #pragma unroll
   for (int q = 0; q < KC; ++q) mine |= q == j && ok[q];
+  float sum = 0.0f;
+  if (j < KC)
+    for (unsigned i = 0; i < blockDim.x / kWave; ++i) sum += red[i][j];
   if (j < KC && j0 + j < k)
-    dweights[t * k + j0 + j] = mine ? (red[0][j] + red[1][j]) + (red[2][j] + red[3][j]) : 0.0f;
+    dweights[t * k + j0 + j] = mine ? sum : 0.0f;
+}
+
+// Threads of a block: the row's 16-byte pieces in as few rounds as blocks of
+// kGradThreads need, all rounds full (H = 7168: four of 448).
+static unsigned grad_threads(int32_t H) {
+  const int nv = H / 4, rounds = (nv + kGradThreads - 1) / kGradThreads;
+  return (unsigned)((nv + rounds * kWave - 1) / (rounds * kWave) * kWave);
 }
 
 template <int KC>
@@ -109,9 +112,10 @@ static void launch_kc(const uint16_t* dout, const float* weights, const float* y
                       void* dy2, bool f32, hipStream_t st) {
   const dim3 grid((unsigned)T, (unsigned)((k + KC - 1) / KC));
   const int64_t rows = T * k;
-  if (!dy2) k_finalize_grad<KC, kNoRows><<<grid, 256, 0, st>>>(dout, weights, y2, slot_row, k, H, rows, dweights, dy2);
-  else if (f32) k_finalize_grad<KC, kRowsF32><<<grid, 256, 0, st>>>(dout, weights, y2, slot_row, k, H, rows, dweights, dy2);
-  else k_finalize_grad<KC, kRowsBf16><<<grid, 256, 0, st>>>(dout, weights, y2, slot_row, k, H, rows, dweights, dy2);
+  const unsigned threads = grad_threads(H);
+  if (!dy2) k_finalize_grad<KC, kNoRows><<<grid, threads, 0, st>>>(dout, weights, y2, slot_row, k, H, rows, dweights, dy2);
+  else if (f32) k_finalize_grad<KC, kRowsF32><<<grid, threads, 0, st>>>(dout, weights, y2, slot_row, k, H, rows, dweights, dy2);
+  else k_finalize_grad<KC, kRowsBf16><<<grid, threads, 0, st>>>(dout, weights, y2, slot_row, k, H, rows, dweights, dy2);
 }
 
 hipError_t launch_finalize_grad(const uint16_t* dout, const float* weights, const float* y2,
