@@ -138,7 +138,7 @@ __global__ __launch_bounds__(kPlanGroup) void k_plan_one(PlanParams p, PlanLayou
   if (e < G) before[e] = after[e] = 0;
   const int g = plan_masks(p, blockIdx.x, mask);  // (its barriers cover the counters)
   constexpr int kB = 8;  // reads in flight
-  for (int64_t b0 = 0; b0 < l.nblocks; b0 += kB) {
+  for (int64_t b0 = 0; l.nblocks > 1 && b0 < l.nblocks; b0 += kB) {
     int o[kB];
 #pragma unroll
     for (int u = 0; u < kB; ++u) {
@@ -362,6 +362,10 @@ __device__ __forceinline__ void put_low(const LowRows& o, int64_t row0, int r, c
 // CUs, or a few more, would leave most CUs waiting for those with two.  A tile
 // is then summed by several blocks (`slots`, at most kMaxSlots), whose float32
 // sums meet in the join or in expand.
+__device__ __forceinline__ int64_t quotient(int64_t a, int32_t b) {  // a >= 0, b > 0
+  // the usual sizes fit the 32-bit division, a fraction of the 64-bit one's steps
+  return a >> 32 == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
 struct ShrinkRuns {
   int32_t units;  // of a tile
   int32_t run;    // units of a block
@@ -377,9 +381,9 @@ __device__ __forceinline__ ShrinkRuns shrink_runs(const PlanView& v, const Shrin
   return r;
 }
 // First of the blocks that sum tile i, and how many they are.
-__device__ __forceinline__ int shrink_first(const ShrinkRuns& r, int64_t i) { return (int)(i * r.units / r.run); }
+__device__ __forceinline__ int shrink_first(const ShrinkRuns& r, int64_t i) { return (int)quotient(i * r.units, r.run); }
 __device__ __forceinline__ int shrink_slots(const ShrinkRuns& r, int64_t i) {
-  return (int)((i * r.units + r.units - 1) / r.run) - shrink_first(r, i) + 1;
+  return (int)quotient(i * r.units + r.units - 1, r.run) - shrink_first(r, i) + 1;
 }
 
 template <int RT>
@@ -404,27 +408,43 @@ __device__ __forceinline__ void shrink_direct(const ShrinkParams& p, const Tile&
 #pragma unroll
   for (int r = 0; r < RT; ++r)
     wp[r] = p.w + ((int64_t)tile.expert * p.rank + min(16 * r + l16, p.rank - 1)) * p.K + 8 * g;
-  for (int k = k0 + (FEW ? 64 * w : 0); k < ke; k += FEW ? 256 : 64) {
-    v8bf a[2][RT], x[2][F32 ? 3 : 1];
+  // U steps' reads at once, without a branch around any (a step behind the end
+  // repeats the last 8 elements and counts as 0): with so few rows a block's life
+  // is the memory's latency, a few times over
+  constexpr int U = FEW && !F32 && RT <= 2 ? 4 : FEW && !F32 && RT <= 4 ? 2 : 1;
+  constexpr int STEP = FEW ? 256 : 64;
+  for (int k = k0 + (FEW ? 64 * w : 0); k < ke; k += U * STEP) {
+    v8bf a[U][2][RT], x[U][2][F32 ? 3 : 1];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const bool in = k + 32 * h + 8 * g < ke;
+    for (int q = 0; q < U; ++q)
 #pragma unroll
-      for (int r = 0; r < RT; ++r) a[h][r] = load_bf16x8(wp[r] + k + 32 * h, in);
-      if constexpr (F32) {
-        float v[8];
-        load_f32x8(xp + k + 32 * h, in, v);
-        split8<3>(v, x[h]);
-      } else {
-        x[h][0] = load_bf16x8(xp + k + 32 * h, in);
+      for (int h = 0; h < 2; ++h) {
+        const int at = k + q * STEP + 32 * h;  // (x and w point at the lane's 8 elements)
+        const bool in = at + 8 * g < ke;
+        const int from = in ? at : ke - 8 - 8 * g;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          a[q][h][r] = load_bf16x8(wp[r] + from, true);
+          a[q][h][r] = in ? a[q][h][r] : v8bf{};
+        }
+        if constexpr (F32) {
+          float v[8];
+          load_f32x8(xp + from, true, v);
+          split8<3>(v, x[q][h]);
+        } else {
+          x[q][h][0] = load_bf16x8(xp + from, true);
+        }
+#pragma unroll
+        for (int n = 0; n < (F32 ? 3 : 1); ++n) x[q][h][n] = in ? x[q][h][n] : v8bf{};
       }
-    }
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int q = 0; q < U; ++q)
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int q = F32 ? 2 : 0; q >= 0; --q) acc[r] = mfma_bf16(a[h][r], x[h][q], acc[r]);
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int n = F32 ? 2 : 0; n >= 0; --n) acc[r] = mfma_bf16(a[q][h][r], x[q][h][n], acc[r]);
   }
   if constexpr (FEW) join_waves<4>(acc, red);
 }
@@ -503,7 +523,7 @@ __global__ __launch_bounds__(256, 2) void k_adapter_shrink(ShrinkParams p) {
   int64_t u = (int64_t)me * runs.run;
   const int64_t end = min(u + runs.run, runs.total);
   while (u < end) {
-    const int64_t i = u / runs.units;
+    const int64_t i = quotient(u, runs.units);
     const int c0 = (int)(u - i * runs.units), c1 = (int)min((int64_t)runs.units, c0 + end - u);
     u += c1 - c0;
     Tile tile;
@@ -627,14 +647,15 @@ __global__ __launch_bounds__(256, JOINED ? (RT == 1 && sizeof(T) == 2 ? 4 : RT <
   // neighbouring blocks on one XCD (block b runs on XCD b % 8), columns first:
   // its blocks cover whole rows of one tile and share a factor
   const int32_t per_tile = p.col_blocks * p.row_blocks;
-  const int64_t total = (int64_t)min(p.plan.head[0], (int32_t)p.plan.max_tiles) * per_tile;
-  const int64_t each = (total + 7) / 8, id = blockIdx.x % 8 * each + blockIdx.x / 8;
+  const uint32_t total = (uint32_t)max(0, min(p.plan.head[0], (int32_t)p.plan.max_tiles)) * per_tile;  // <= the grid
+  const uint32_t each = (total + 7) / 8, id = blockIdx.x % 8 * each + blockIdx.x / 8;
   if (blockIdx.x / 8 >= each || id >= total) return;
+  const uint32_t ti = id / (uint32_t)per_tile, at = id - ti * per_tile;
   Tile tile;
-  if (!plan_tile(p.plan, id / per_tile, &tile)) return;
-  const int m0 = (int)(id % per_tile / p.col_blocks);
+  if (!plan_tile(p.plan, ti, &tile)) return;
+  const int m0 = (int)(at / (uint32_t)p.col_blocks);
   if (16 * m0 >= tile.nrows) return;
-  const int n0 = (int)((id % p.col_blocks) * (blockDim.x / kWave) + threadIdx.x / kWave) * kExpandCols;
+  const int n0 = (int)((at - m0 * p.col_blocks) * (blockDim.x / kWave) + threadIdx.x / kWave) * kExpandCols;
   if (n0 >= p.N) return;
   const int lane = lane_id(), l16 = lane & 15, g = lane >> 4;
   const bool in = n0 + 8 * l16 < p.N;
@@ -664,7 +685,7 @@ __global__ __launch_bounds__(256, JOINED ? (RT == 1 && sizeof(T) == 2 ? 4 : RT <
   const int64_t step = p.plan.max_rows * (int64_t)p.rank_pad;
   const float scale = low && !JOINED ? p.scale[tile.expert] : 0.0f;
   const int slots = low && !JOINED
-                        ? min(shrink_slots(shrink_runs(p.plan, p.shape), id / per_tile), kMaxSlots) : 0;
+                        ? min(shrink_slots(shrink_runs(p.plan, p.shape), ti), kMaxSlots) : 0;
 #pragma unroll 1
   for (int m = m0; 16 * m < tile.nrows; m += p.row_blocks) {
     int64_t t[4];
@@ -960,10 +981,10 @@ __global__ __launch_bounds__(256, RT <= 2 ? 4 : RT == 4 ? 2 : 1) void k_adapter_
   __shared__ __align__(16) __bf16 lds[kLds];
   // columns first, over all XCDs: segments differ in length, and a run of them on
   // one XCD (its L2 would hold their saved values) left others idle
-  const int64_t id = blockIdx.x;
+  const uint32_t at = blockIdx.x / (uint32_t)p.cols;
   OuterSegment seg;
-  if (!outer_segment<false>(p, id / p.cols, &seg)) return;
-  const int col = (int)(id % p.cols), second = col - p.cols0;
+  if (!outer_segment<false>(p, at, &seg)) return;
+  const int col = (int)(blockIdx.x - at * p.cols), second = col - p.cols0;
   if (second < 0) outer_block<RT, false>(p, p.x, seg, col * 128, lds);
   else outer_block<RT, F32>(p, p.dout, seg, second * (F32 ? 64 : 128), lds);
 }
