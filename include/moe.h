@@ -431,7 +431,8 @@ moe_status moe_router_loss_query(const moe_dims* dims, int64_t num_tokens, int32
  *   seq_tokens:    device int32 [num_seqs + 2] out: n_s, then all tokens, then
  *                  the sequences that have tokens
  *   workspace:     device buffer of moe_router_loss_query bytes; needs no
- *                  initialisation
+ *                  initialisation; calls that may run at the same time need
+ *                  their own
  * NaN logits rank as -inf as in moe_route; a token with no logit above -inf
  * has p = 0 and lse = 0; a logit of +inf makes the losses NaN.  num_tokens = 0
  * writes zeros.  Errors as moe_run_ws. */
@@ -475,7 +476,9 @@ moe_status moe_router_backward(const moe_dims* dims, const float* router_logits,
  *   dy2:      device out [num_tokens * top_k, hidden], float or bf16 bits by
  *             dy2_type (moe_type; rounded once, to nearest even), or null when
  *             not wanted; float dy2 may be y2
- * num_tokens = 0 returns MOE_OK without launching.  Errors as moe_run_ws. */
+ * num_tokens = 0 returns MOE_OK without launching.  Errors as moe_run_ws, and
+ * MOE_ERR_INVALID_ARG when num_tokens * hidden / 4 reaches about 2^32 (one
+ * launch holds fewer threads). */
 moe_status moe_finalize_backward(const moe_dims* dims, const void* dout, int64_t num_tokens,
                                  int32_t top_k, const float* weights, const float* y2,
                                  const int32_t* slot_row, float* dweights, void* dy2,
@@ -493,7 +496,7 @@ moe_status moe_finalize_backward(const moe_dims* dims, const void* dout, int64_t
  * A plan groups a batch's tokens by adapter.  It depends on the adapter ids
  * alone, so one plan serves every projection of every layer, and the backward
  * pass.  1 <= num_adapters <= 1023, 1 <= rank <= 128, features multiples of 8
- * up to 2^20, num_tokens up to 2^26. */
+ * up to 2^18, num_tokens up to 2^26. */
 typedef struct {
   int32_t num_adapters;
   int32_t rank;

@@ -128,8 +128,8 @@ __device__ __forceinline__ void plan_add(int32_t* count, int g) {
 
 // A batch of up to kPlanOne tokens in one launch: every block counts all the
 // tokens for itself (integer counts in LDS), those before its own apart, and so
-// knows where its rows go; block 0 writes the rest of the plan.  4096 tokens: 7.4
-// us against 13.4 in three launches; 16384: 16.6 against 13.9.
+// knows where its rows go; block 0 writes the rest of the plan.  4096 tokens: 7.3
+// us against 13.4 in three launches; 16384: 16.6 against 11 in two.
 __global__ __launch_bounds__(kPlanGroup) void k_plan_one(PlanParams p, PlanLayout l) {
   __shared__ uint64_t mask[kPlanChunks][kMaxAdapters + 1];
   __shared__ int32_t before[kMaxAdapters + 1], after[kMaxAdapters + 1];
@@ -161,41 +161,64 @@ __global__ __launch_bounds__(kPlanGroup) void k_plan_one(PlanParams p, PlanLayou
 }
 
 __global__ __launch_bounds__(kPlanGroup) void k_plan_count(PlanParams p, PlanLayout l) {
-  __shared__ uint64_t mask[kPlanChunks][kMaxAdapters + 1];
-  plan_masks(p, blockIdx.x, mask);
+  __shared__ int32_t count[kMaxAdapters + 1];
+  const int G = p.adapters + 1, e = threadIdx.x;
+  const int64_t t = (int64_t)blockIdx.x * kPlanGroup + threadIdx.x;
+  const int g = t < p.tokens ? plan_group(p, t) : -1;
+  if (e < G) count[e] = 0;
+  __syncthreads();
+  plan_add(count, g);
+  __syncthreads();
+  if (e < G) p.plan[l.counts + (int64_t)blockIdx.x * G + e] = count[e];
+}
+
+// Tokens of group e in all blocks, and (before) in the first `upto`; `store`
+// puts the prefixes in the counts' place.
+__device__ __forceinline__ int32_t plan_total(const PlanParams& p, const PlanLayout& l, int e, int64_t upto,
+                                              int32_t* before, bool store) {
   const int G = p.adapters + 1;
-  if ((int)threadIdx.x >= G) return;
   int32_t n = 0;
-  for (int u = 0; u < kPlanChunks; ++u) n += __popcll(mask[u][threadIdx.x]);
-  p.plan[l.counts + (int64_t)blockIdx.x * G + threadIdx.x] = n;
+  constexpr int kB = 16;  // independent loads in flight
+  for (int64_t b0 = 0; b0 < l.nblocks; b0 += kB) {
+    int32_t v[kB];
+#pragma unroll
+    for (int u = 0; u < kB; ++u) v[u] = b0 + u < l.nblocks ? p.plan[l.counts + (b0 + u) * G + e] : 0;
+#pragma unroll
+    for (int u = 0; u < kB; ++u) {
+      if (store && b0 + u < l.nblocks) p.plan[l.counts + (b0 + u) * G + e] = n;
+      if (b0 + u == upto) *before = n;
+      n += v[u];
+    }
+  }
+  return n;
 }
 
 __global__ __launch_bounds__(kPlanGroup) void k_plan_scan(PlanParams p, PlanLayout l) {
   __shared__ int32_t wsum[2][16];
-  const int G = p.adapters + 1, e = threadIdx.x;
-  int32_t n = 0;
-  if (e < G) {
-    constexpr int kB = 16;  // independent loads in flight
-    for (int64_t b0 = 0; b0 < l.nblocks; b0 += kB) {
-      int32_t v[kB];
-#pragma unroll
-      for (int u = 0; u < kB; ++u) v[u] = b0 + u < l.nblocks ? p.plan[l.counts + (b0 + u) * G + e] : 0;
-#pragma unroll
-      for (int u = 0; u < kB; ++u) {
-        if (b0 + u < l.nblocks) p.plan[l.counts + (b0 + u) * G + e] = n;
-        n += v[u];
-      }
-    }
-  }
+  const int e = threadIdx.x;
+  int32_t n = 0, before;
+  if (e <= p.adapters) n = plan_total(p, l, e, -1, &before, true);
   plan_scan(p, l, n, wsum, true);
 }
 
+// SCAN: every block adds up the counts for itself, which saves the scan's launch
+// while they are few.
+template <bool SCAN>
 __global__ __launch_bounds__(kPlanGroup) void k_plan_scatter(PlanParams p, PlanLayout l) {
   __shared__ uint64_t mask[kPlanChunks][kMaxAdapters + 1];
+  __shared__ int32_t first[kMaxAdapters + 1];
+  __shared__ int32_t wsum[2][16];
+  const int G = p.adapters + 1, e = threadIdx.x;
   const int g = plan_masks(p, blockIdx.x, mask);
+  if (SCAN) {
+    int32_t n = 0, before = 0;
+    if (e < G) n = plan_total(p, l, e, blockIdx.x, &before, false);
+    const int32_t row0 = plan_scan(p, l, n, wsum, blockIdx.x == 0);
+    if (e < G) first[e] = row0 + before;
+    __syncthreads();
+  }
   if (g < 0) return;
-  const int G = p.adapters + 1;
-  const int32_t row = p.plan[l.first + g] + p.plan[l.counts + (int64_t)blockIdx.x * G + g] +
+  const int32_t row = (SCAN ? first[g] : p.plan[l.first + g] + p.plan[l.counts + (int64_t)blockIdx.x * G + g]) +
                       plan_rank(mask, g);
   p.plan[l.rows + row] = (int32_t)(blockIdx.x * (int64_t)kPlanGroup + threadIdx.x);
 }
@@ -206,8 +229,12 @@ hipError_t launch_adapter_plan(const PlanParams& p, const PlanLayout& l, hipStre
     return hipGetLastError();
   }
   k_plan_count<<<(unsigned)l.nblocks, kPlanGroup, 0, st>>>(p, l);
-  k_plan_scan<<<1, kPlanGroup, 0, st>>>(p, l);
-  k_plan_scatter<<<(unsigned)l.nblocks, kPlanGroup, 0, st>>>(p, l);
+  if (l.nblocks <= 64) {
+    k_plan_scatter<true><<<(unsigned)l.nblocks, kPlanGroup, 0, st>>>(p, l);
+  } else {
+    k_plan_scan<<<1, kPlanGroup, 0, st>>>(p, l);
+    k_plan_scatter<false><<<(unsigned)l.nblocks, kPlanGroup, 0, st>>>(p, l);
+  }
   return hipGetLastError();
 }
 
@@ -844,12 +871,15 @@ __device__ __forceinline__ bool outer_segment(const OuterParams& p, int64_t j, O
 // three bf16 parts like the saved values; products of parts whose sizes lie
 // 2^-27 or more apart are left out.
 template <int RT, bool F32>
+constexpr int outer_cols() { return F32 ? 64 : RT <= 2 ? 256 : 128; }  // columns of a block
+template <int RT, bool F32>
 __device__ __forceinline__ void outer_block(const OuterParams& p, const OuterSide& s, const OuterSegment& seg, int c0,
                                             __bf16* lds) {
   constexpr int XP = F32 ? 3 : 1;       // parts of X
-  constexpr int CB = F32 ? 64 : 128;    // columns of a block
-  constexpr int TW = CB / 64;           // matrix columns blocks of a wave
-  constexpr int W = F32 ? 2 : 4;        // columns of a thread
+  constexpr int CB = outer_cols<RT, F32>();
+  constexpr int TW = CB / 64;           // matrix column blocks of a wave
+  constexpr int W = CB / 32;            // columns of a thread
+  constexpr int WORDS = F32 ? W : W / 2;
   constexpr int NV = (3 * 16 * RT * 8 + 255) / 256;
   typedef std::conditional_t<F32, float, uint16_t> X;
   __bf16* xs = lds;
@@ -865,7 +895,7 @@ __device__ __forceinline__ void outer_block(const OuterParams& p, const OuterSid
   // and looked at when they are used (a test at the read would wait for it, and
   // for all reads before it).
   int4 tok[2];
-  uint32_t raw[8][2];
+  uint32_t raw[8][WORDS];
   v4u rv[NV];
   const auto tokens = [&](int64_t r) {
     const int4* t = reinterpret_cast<const int4*>(p.plan.rows + min(r + 8 * piece, M - 8));
@@ -880,7 +910,7 @@ __device__ __forceinline__ void outer_block(const OuterParams& p, const OuterSid
     for (int i = 0; i < 8; ++i) {
       const bool ok = (uint32_t)t[i] < (uint32_t)p.plan.tokens;
       keep |= ok && in && r + 8 * piece < end ? 1u << i : 0;
-      load_words<2>(x + (ok ? t[i] : 0) * s.x_stride, true, raw[i]);
+      load_words<WORDS>(x + (ok ? t[i] : 0) * s.x_stride, true, raw[i]);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -894,10 +924,10 @@ __device__ __forceinline__ void outer_block(const OuterParams& p, const OuterSid
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) raw[i][j] = keep >> i & 1 ? raw[i][j] : 0;
+      for (int j = 0; j < WORDS; ++j) raw[i][j] = keep >> i & 1 ? raw[i][j] : 0;
     if constexpr (F32) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < W; ++j) {
         float v[8];
         v8bf q[3];
 #pragma unroll
@@ -908,10 +938,10 @@ __device__ __forceinline__ void outer_block(const OuterParams& p, const OuterSid
           *reinterpret_cast<v8bf*>(xs + n * CB * kOuterRows + outer_at(col + j, piece)) = q[n];
       }
     } else {
-      v8bf q[4];
-      transpose8<2>(raw, q);
+      v8bf q[W];
+      transpose8<WORDS>(raw, q);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) *reinterpret_cast<v8bf*>(xs + outer_at(col + j, piece)) = q[j];
+      for (int j = 0; j < W; ++j) *reinterpret_cast<v8bf*>(xs + outer_at(col + j, piece)) = q[j];
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -976,8 +1006,9 @@ __device__ __forceinline__ void outer_block(const OuterParams& p, const OuterSid
 // Block (columns of either factor, segment).  Both factors in one launch: the
 // second's blocks fill the CUs the first leaves.
 template <int RT, bool F32>
-__global__ __launch_bounds__(256, RT <= 2 ? 4 : RT == 4 ? 2 : 1) void k_adapter_outer(OuterParams p) {
-  constexpr int kLds = (F32 ? 3 * 64 : 128) * kOuterRows + 3 * 16 * RT * kOuterRows;
+__global__ __launch_bounds__(256, RT <= 2 ? 3 : RT == 4 ? 2 : 1) void k_adapter_outer(OuterParams p) {
+  constexpr int kX = outer_cols<RT, false>();
+  constexpr int kLds = (F32 && 3 * 64 > kX ? 3 * 64 : kX) * kOuterRows + 3 * 16 * RT * kOuterRows;
   __shared__ __align__(16) __bf16 lds[kLds];
   // columns first, over all XCDs: segments differ in length, and a run of them on
   // one XCD (its L2 would hold their saved values) left others idle
@@ -985,8 +1016,8 @@ __global__ __launch_bounds__(256, RT <= 2 ? 4 : RT == 4 ? 2 : 1) void k_adapter_
   OuterSegment seg;
   if (!outer_segment<false>(p, at, &seg)) return;
   const int col = (int)(blockIdx.x - at * p.cols), second = col - p.cols0;
-  if (second < 0) outer_block<RT, false>(p, p.x, seg, col * 128, lds);
-  else outer_block<RT, F32>(p, p.dout, seg, second * (F32 ? 64 : 128), lds);
+  if (second < 0) outer_block<RT, false>(p, p.x, seg, col * kX, lds);
+  else outer_block<RT, F32>(p, p.dout, seg, second * outer_cols<RT, F32>(), lds);
 }
 
 // Block (elements, j): the partial sums of the j-th adapter of several
@@ -1013,9 +1044,9 @@ __global__ __launch_bounds__(256) void k_adapter_outer_join(OuterParams p) {
 
 template <int RT, bool F32>
 static void launch_outer(OuterParams p, hipStream_t st) {
-  const int cols = F32 ? 64 : 128;
-  p.cols0 = (p.x.C + 127) / 128;
-  p.cols = p.cols0 + (p.dout.C + cols - 1) / cols;
+  constexpr int X = outer_cols<RT, false>(), D = outer_cols<RT, F32>();
+  p.cols0 = (p.x.C + X - 1) / X;
+  p.cols = p.cols0 + (p.dout.C + D - 1) / D;
   // at most one segment an adapter and one a chunk
   k_adapter_outer<RT, F32><<<(unsigned)(p.cols * ((int64_t)p.plan.adapters + p.chunks)), 256, 0, st>>>(p);
 }

@@ -23,7 +23,7 @@ __device__ __forceinline__ uint32_t bf16_bits_any(float v) {
   return v == v ? bf16_bits(v) : 0x7FC0u | (__float_as_uint(v) >> 16 & 0x8000u);
 }
 
-constexpr int kGradThreads = 512;  // at most; see grad_threads
+constexpr int kGradThreads = 512;  // at most; see finalize_grad_threads
 
 enum RowGrad : int { kNoRows = 0, kRowsBf16 = 1, kRowsF32 = 2 };
 
@@ -101,7 +101,7 @@ __global__ __launch_bounds__(kGradThreads) void k_finalize_grad(const uint16_t* 
 
 // Threads of a block: the row's 16-byte pieces in as few rounds as blocks of
 // kGradThreads need, all rounds full (H = 7168: four of 448).
-static unsigned grad_threads(int32_t H) {
+unsigned finalize_grad_threads(int32_t H) {
   const int nv = H / 4, rounds = (nv + kGradThreads - 1) / kGradThreads;
   return (unsigned)((nv + rounds * kWave - 1) / (rounds * kWave) * kWave);
 }
@@ -112,7 +112,7 @@ static void launch_kc(const uint16_t* dout, const float* weights, const float* y
                       void* dy2, bool f32, hipStream_t st) {
   const dim3 grid((unsigned)T, (unsigned)((k + KC - 1) / KC));
   const int64_t rows = T * k;
-  const unsigned threads = grad_threads(H);
+  const unsigned threads = finalize_grad_threads(H);
   if (!dy2) k_finalize_grad<KC, kNoRows><<<grid, threads, 0, st>>>(dout, weights, y2, slot_row, k, H, rows, dweights, dy2);
   else if (f32) k_finalize_grad<KC, kRowsF32><<<grid, threads, 0, st>>>(dout, weights, y2, slot_row, k, H, rows, dweights, dy2);
   else k_finalize_grad<KC, kRowsBf16><<<grid, threads, 0, st>>>(dout, weights, y2, slot_row, k, H, rows, dweights, dy2);

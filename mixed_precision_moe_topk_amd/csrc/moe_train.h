@@ -56,6 +56,7 @@ hipError_t launch_router_grad(const RouterGradParams& p, hipStream_t st);
 
 // ---------------------------------------------------------------- weighted sum
 // dweights [T, k], dy2 [T*k, H] (bf16 bits or float32; null: not wanted).
+unsigned finalize_grad_threads(int32_t H);  // threads of a token's block
 hipError_t launch_finalize_grad(const uint16_t* dout, const float* weights, const float* y2,
                                 const int32_t* slot_row, int64_t T, int32_t k, int32_t H,
                                 float* dweights, void* dy2, bool dy2_f32, hipStream_t st);

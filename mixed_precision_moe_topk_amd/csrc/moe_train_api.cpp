@@ -76,8 +76,8 @@ moe_status check_adapter(const moe_adapter_dims* d, int64_t num_tokens) {
   if (d->rank < 1 || d->rank > moe::kMaxRank)
     return set_errorf(MOE_ERR_INVALID_ARG, "rank %d outside [1, %d]", d->rank, moe::kMaxRank);
   for (const int32_t n : {d->in_features, d->out_features})
-    if (n < 8 || n % 8 != 0 || n > (1 << 20))
-      return set_errorf(MOE_ERR_INVALID_ARG, "%d features: a multiple of 8 in [8, 2^20] is needed", n);
+    if (n < 8 || n % 8 != 0 || n > (1 << 18))
+      return set_errorf(MOE_ERR_INVALID_ARG, "%d features: a multiple of 8 in [8, 2^18] is needed", n);
   if (d->out_type != MOE_T_BF16 && d->out_type != MOE_T_F32)
     return set_errorf(MOE_ERR_INVALID_ARG, "unknown output type %d", d->out_type);
   return MOE_OK;
@@ -123,11 +123,12 @@ struct AdapterLayout {
     frag_bytes = align256((size_t)plan.max_rows * rp32 * 6);
     saved_bytes = align256((size_t)plan.max_rows * rp * 6);
     // segments of all adapters for as many blocks as run at once (registers
-    // allow 4, 2 or 1 a CU by the rank), 256 rows a segment at least: rows are
+    // allow 3, 2 or 1 a CU by the rank), 256 rows a segment at least: rows are
     // cut into what is left when every adapter has one, or into half as many
-    const int64_t cols = ceil_div(d->in_features, 128) +
-                         ceil_div(d->out_features, d->out_type == MOE_T_F32 ? 64 : 128);
-    const int64_t segments = std::max<int64_t>(1, (rp <= 32 ? 1024 : rp <= 64 ? 512 : 256) / cols);
+    const int64_t wide = rp <= 32 ? 256 : 128;  // columns of a block
+    const int64_t cols = ceil_div(d->in_features, wide) +
+                         ceil_div(d->out_features, d->out_type == MOE_T_F32 ? 64 : wide);
+    const int64_t segments = std::max<int64_t>(1, (rp <= 32 ? 768 : rp <= 64 ? 512 : 256) / cols);
     const int64_t cuts = std::max({(int64_t)1, segments / 2, segments - d->num_adapters});
     chunk = std::max<int64_t>(256, ceil_div(ceil_div(plan.max_rows, cuts), 64) * 64);
     chunks = (int32_t)std::max<int64_t>(1, ceil_div(plan.max_rows, chunk));
@@ -291,6 +292,9 @@ moe_status moe_finalize_backward(const moe_dims* dims, const void* dout, int64_t
   if (dy2_type != MOE_T_BF16 && dy2_type != MOE_T_F32)
     return set_errorf(MOE_ERR_INVALID_ARG, "unknown dy2 type %d", dy2_type);
   if (num_tokens == 0) return moe::set_ok();
+  if (num_tokens * moe::finalize_grad_threads(dims->hidden) >= (int64_t)1 << 32)
+    return set_errorf(MOE_ERR_INVALID_ARG, "num_tokens %lld with hidden %d: more than 2^32 threads",
+                      (long long)num_tokens, dims->hidden);
   MOE_RETURN_IF(check_pointers({dout, weights, y2, slot_row, dweights}));
   MOE_RETURN_IF(check_optional(dy2));
   MOE_RETURN_IF(moe::check_gfx950());

@@ -169,6 +169,10 @@ CASES = [  # tokens, adapters, rank, K, N, out, ids
     (2100, 1, 16, 256, 136, "bf16", one),             # one adapter's rows in several segments
     (1100, 1, 128, 128, 128, "f32", one),
     (9000, 3, 8, 64, 64, "bf16", scattered),          # past the plan of one launch
+    (33000, 5, 8, 64, 72, "f32", some_without),       # whole tiles for shrink's blocks
+    (66000, 2, 4, 16, 8, "bf16", runs),               # a plan of three launches
+    (128, 3, 32, 264, 200, "bf16", scattered),        # the most tokens whose rows expand adds up itself
+    (129, 3, 32, 264, 200, "f32", scattered),
 ]
 
 

@@ -213,6 +213,25 @@ def test_ids_out_of_range_and_repeated_ids():
     assert np.all(x[1] == 0)
 
 
+def test_gradient_in_place_of_the_logits():
+    import mixed_precision_moe_topk_amd as M
+
+    T, E, k = 203, 130, 5
+    logits, ids, w = _routing(71, T, E, k)
+    b = Buffers(T, E, 2)
+    offs = _dev(np.array([0, 101, 203], np.int32))
+    z, i = _dev(logits), _dev(ids)
+    b.run(z, i, offs, None)
+    kw = dict(weights=_dev(w), dweights=_dev(w), dlosses=_dev(np.array([1.0, 1.0], np.float32)), counts=b.counts,
+              seq_tokens=b.tokens, seq_offsets=offs)
+    import torch
+
+    out = torch.empty_like(z)
+    M.router_backward(b.d, z, i, out, **kw)
+    M.router_backward(b.d, z, i, z, **kw)
+    assert torch.equal(out, z)
+
+
 def test_no_tokens():
     import mixed_precision_moe_topk_amd as M
     import torch

@@ -73,6 +73,7 @@ def test_finalize_backward_refuses(L):
     for name in ("dout", "w", "y2", "rows", "dw"):
         assert f(**{name: None}) == 1 and f(**{name: BAD}) == 1, name
     assert f(dy2=BAD) == 1 and f(kind=2) == 1 and f(k=9) == 1 and f(T=-1) == 1
+    assert f(T=1 << 26) == 1 and b"threads" in L.moe_last_error()  # 64 threads a token
 
 
 def test_adapter_queries(L):
@@ -84,7 +85,7 @@ def test_adapter_queries(L):
     assert M.adapter_workspace_query(d, 100) >= 2 * 100 * 32 * 4
     assert M.adapter_saved_query(d, 100) >= 100 * 32 * 4
     for bad in (dict(rank=0), dict(rank=129), dict(in_features=12), dict(out_features=0), dict(num_adapters=0),
-                dict(in_features=(1 << 20) + 8)):
+                dict(in_features=(1 << 18) + 8)):
         kw = dict(num_adapters=4, rank=20, in_features=256, out_features=512)
         kw.update(bad)
         assert _status(M.adapter_workspace_query, M.AdapterDims(**kw), 4) == 1, bad
