@@ -557,7 +557,8 @@ moe_status moe_adapter_apply(const moe_adapter_dims* dims, const void* x, int64_
  *   da, db: device float [num_adapters, rank, in_features] and [num_adapters,
  *           rank, out_features] out, fully overwritten (zeros for an adapter
  *           without tokens); both null when the factors are not trained
- *   dx:     device bf16 [num_tokens, in_features] out, or null
+ *   dx:     device bf16 [num_tokens, in_features] out, or null; not x or dout
+ *           when da and db are wanted
  *   dx_base: device bf16 [num_tokens, in_features]; may be dx (with the same
  *           stride); null: 0
  * num_tokens = 0 writes zeros into da and db.  Errors as moe_run_ws, and

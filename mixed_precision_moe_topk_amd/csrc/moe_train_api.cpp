@@ -297,6 +297,8 @@ moe_status moe_finalize_backward(const moe_dims* dims, const void* dout, int64_t
                       (long long)num_tokens, dims->hidden);
   MOE_RETURN_IF(check_pointers({dout, weights, y2, slot_row, dweights}));
   MOE_RETURN_IF(check_optional(dy2));
+  if (dy2 == y2 && dy2_type != MOE_T_F32)
+    return set_error(MOE_ERR_INVALID_ARG, "only a float dy2 may be y2");
   MOE_RETURN_IF(moe::check_gfx950());
   MOE_RETURN_IF(moe::check_hip(
       moe::launch_finalize_grad(static_cast<const uint16_t*>(dout), weights, y2, slot_row,
@@ -404,6 +406,9 @@ moe_status moe_adapter_backward(const moe_adapter_dims* dims, const void* dout,
     MOE_RETURN_IF(check_room(plan_bytes, (size_t)l.plan.total * 4, "plan"));
     MOE_RETURN_IF(check_room(workspace_bytes, l.workspace(), "workspace"));
     if (da) MOE_RETURN_IF(check_room(saved_bytes, l.saved_bytes, "saved"));
+    // dx is written before the factors' gradients read x and dout
+    if (da && dx && (dx == x || dx == dout))
+      return set_error(MOE_ERR_INVALID_ARG, "dx must not be x or dout");
   }
   if (num_tokens == 0 && !da) return moe::set_ok();
   MOE_RETURN_IF(moe::check_gfx950());

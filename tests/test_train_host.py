@@ -152,3 +152,21 @@ def test_binding_refuses_cpu_tensors(L):
     a = M.AdapterDims(4, 8, 8, 8)
     assert _status(M.adapter_apply, a, z, z, z, z, z, z, z, z) == 1
     assert _status(M.adapter_backward, a, z, z, z, z, z, z, z, z, z, z) == 1
+
+
+def test_outputs_over_inputs_that_are_still_read_are_refused(L):
+    """bf16 row gradients over the float rows they come from; dx over what the
+    factors' gradients read after it."""
+    X = [ctypes.c_void_p(0x10000 * i) for i in range(1, 16)]
+
+    assert L.moe_finalize_backward(_d(), X[0], 4, 2, X[1], X[4], X[2], X[3], X[4], M.T_BF16, None) == 1
+    assert b"y2" in L.moe_last_error()
+
+    dims = M.AdapterDims(4, 20, 256, 256).c()
+
+    def back(dx, da=X[9], db=X[10]):
+        return L.moe_adapter_backward(ctypes.byref(dims), X[0], 256, X[1], 256, 4, X[2], BIG, X[3], X[4], X[5], X[6],
+                                      BIG, da, db, None, 256, dx, 256, X[8], BIG, None)
+
+    for dx in (X[0], X[1]):
+        assert back(dx) == 1 and b"dx" in L.moe_last_error()
