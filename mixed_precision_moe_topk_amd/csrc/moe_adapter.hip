@@ -640,11 +640,14 @@ struct Row8Bf16 {
   __device__ __forceinline__ float get(int j) const {
     return __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
   }
-  __device__ __forceinline__ static void store(uint16_t* p, const float (&v)[8]) {
+  __device__ __forceinline__ void set(const float (&v)[8]) {
     v8bf o;
 #pragma unroll
     for (int j = 0; j < 8; ++j) o[j] = (__bf16)v[j];
-    __builtin_nontemporal_store(__builtin_bit_cast(v4u, o), reinterpret_cast<v4u*>(p));
+    w = __builtin_bit_cast(v4u, o);
+  }
+  __device__ __forceinline__ void store(uint16_t* p) const {
+    __builtin_nontemporal_store(w, reinterpret_cast<v4u*>(p));
   }
 };
 struct Row8F32 {
@@ -654,9 +657,13 @@ struct Row8F32 {
     w[1] = reinterpret_cast<const v4f*>(p)[1];
   }
   __device__ __forceinline__ float get(int j) const { return w[j / 4][j % 4]; }
-  __device__ __forceinline__ static void store(float* p, const float (&v)[8]) {
-    reinterpret_cast<v4f*>(p)[0] = v4f{v[0], v[1], v[2], v[3]};
-    reinterpret_cast<v4f*>(p)[1] = v4f{v[4], v[5], v[6], v[7]};
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+    w[0] = v4f{v[0], v[1], v[2], v[3]};
+    w[1] = v4f{v[4], v[5], v[6], v[7]};
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    reinterpret_cast<v4f*>(p)[0] = w[0];
+    reinterpret_cast<v4f*>(p)[1] = w[1];
   }
 };
 
@@ -692,6 +699,38 @@ __global__ __launch_bounds__(256, JOINED ? (RT == 1 && sizeof(T) == 2 ? 4 : RT <
   const bool low = tile.expert != p.plan.adapters;
   if (!low && p.base == p.out && p.base) return;  // no adapter, and the base is in place
 
+  // Row 16 m + 4 g + i of the tile is the lane's i-th of step m; rows behind the
+  // last read the last one's base and store nothing.
+  const int tok = max(0, (int)plan_token(p.plan, tile.row0 + min(lane, tile.nrows - 1)));
+  int t[4], tn[4];  // of this step and of the rows in v
+  Row8 v[4];
+  const auto load_base = [&](int m) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tn[i] = __shfl(tok, 16 * m + 4 * g + i);
+    if (base) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i].load(base + tn[i] * (int64_t)p.base_stride + n);
+    }
+  };
+  v8bf a[RT][PARTS];  // the rows as operands
+  const auto load_rows = [&](int m, int r) {
+    const uint16_t* f =
+        p.frag + frag_block(tile.row0 / 16 + m, p.rank_pad32, 32 * r < p.rank_pad ? r : 0, PARTS, 0) + lane * 8;
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q) a[r][q] = load_bf16x8(f + 512 * q, true);
+  };
+  // AHEAD: a step's reads go out before the last one's stores, and the first
+  // under the factor's (float32 rows do not leave the registers for it)
+  constexpr bool AHEAD = JOINED && sizeof(T) == 2;
+  const auto ahead = [&](int m) {
+    if (!low) return;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) load_rows(m, r);
+  };
+  if (AHEAD) {
+    ahead(m0);
+    load_base(m0);
+  }
   v8bf b[RT][8];
   if (low) {
 #pragma unroll
@@ -715,16 +754,7 @@ __global__ __launch_bounds__(256, JOINED ? (RT == 1 && sizeof(T) == 2 ? 4 : RT <
                         ? min(shrink_slots(shrink_runs(p.plan, p.shape), ti), kMaxSlots) : 0;
 #pragma unroll 1
   for (int m = m0; 16 * m < tile.nrows; m += p.row_blocks) {
-    int64_t t[4];
-    Row8 v[4];
-    // a row behind the last reads the last one's base and stores nothing
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      t[i] = max((int64_t)0, plan_token(p.plan, tile.row0 + min(16 * m + 4 * g + i, tile.nrows - 1)));
-    if (base) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i].load(base + t[i] * p.base_stride + n);
-    }
+    if (!AHEAD) load_base(m);
     v4f acc[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
@@ -732,12 +762,8 @@ __global__ __launch_bounds__(256, JOINED ? (RT == 1 && sizeof(T) == 2 ? 4 : RT <
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         if (32 * r >= p.rank_pad) break;
-        v8bf a[PARTS];
-        if constexpr (JOINED) {
-          const uint16_t* f = p.frag + frag_block(tile.row0 / 16 + m, p.rank_pad32, r, PARTS, 0) + lane * 8;
-#pragma unroll
-          for (int q = 0; q < PARTS; ++q) a[q] = load_bf16x8(f + 512 * q, true);
-        } else {
+        if constexpr (JOINED && !AHEAD) load_rows(m, r);
+        if constexpr (!JOINED) {
           const int row = min(16 * m + l16, tile.nrows - 1);
           const float* s = p.part + (int64_t)(tile.row0 + row) * p.rank_pad + 32 * r + 8 * g;
           const bool some = 32 * r + 8 * g < p.rank_pad;
@@ -752,21 +778,31 @@ __global__ __launch_bounds__(256, JOINED ? (RT == 1 && sizeof(T) == 2 ? 4 : RT <
             for (int i = 0; i < 8; ++i) u[i] += x[q][i];
 #pragma unroll
           for (int i = 0; i < 8; ++i) u[i] *= scale;
-          split8<PARTS>(u, a);
+          split8<PARTS>(u, a[r]);
         }
 #pragma unroll
         for (int q = PARTS - 1; q >= 0; --q)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) acc[j] = mfma_bf16(a[q], b[r][j], acc[j]);
+          for (int j = 0; j < 8; ++j) acc[j] = mfma_bf16(a[r][q], b[r][j], acc[j]);
       }
     }
+    const int next = m + p.row_blocks;
+    const bool more = AHEAD && 16 * next < tile.nrows;
+    if (more) ahead(next);
+    Row8 o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float o[8];
+      float f[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = base ? v[i].get(j) + acc[j][i] : acc[j][i];
-      if (in && 16 * m + 4 * g + i < tile.nrows) Row8::store(out + t[i] * p.out_stride + n, o);
+      for (int j = 0; j < 8; ++j) f[j] = base ? v[i].get(j) + acc[j][i] : acc[j][i];
+      o[i].set(f);
+      t[i] = tn[i];
     }
+    // (a wait for reads waits for the stores issued before them as well)
+    if (more) load_base(next);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (in && 16 * m + 4 * g + i < tile.nrows) o[i].store(out + t[i] * (int64_t)p.out_stride + n);
   }
 }
 
