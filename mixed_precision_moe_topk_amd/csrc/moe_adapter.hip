@@ -623,7 +623,7 @@ __global__ __launch_bounds__(256) void k_adapter_join(JoinParams p) {
 }
 
 hipError_t launch_adapter_join(const JoinParams& p, hipStream_t st) {
-  k_adapter_join<<<dim3((unsigned)p.plan.max_tiles, (unsigned)((p.rank_pad + 31) / 32)), 256, 0, st>>>(p);
+  k_adapter_join<<<dim3((unsigned)p.plan.max_tiles, (unsigned)(p.rank_pad / 16)), 256, 0, st>>>(p);
   return hipGetLastError();
 }
 
