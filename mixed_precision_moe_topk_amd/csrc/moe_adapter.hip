@@ -26,8 +26,10 @@
 namespace moe {
 
 // ---------------------------------------------------------------- plan
-__device__ __forceinline__ int plan_group(const PlanParams& p, int64_t t) {
-  const int32_t id = p.adapter_ids[t];
+__device__ __forceinline__ int32_t plan_id(const PlanParams& p, int64_t t) {
+  return p.adapter_ids[min(t, p.tokens - 1)];
+}
+__device__ __forceinline__ int plan_group(const PlanParams& p, int32_t id) {
   return (uint32_t)id < (uint32_t)p.adapters ? id : p.adapters;
 }
 
@@ -40,11 +42,12 @@ __device__ __forceinline__ int plan_masks(const PlanParams& p, int64_t block,
   const int G = p.adapters + 1;
   const int lane = lane_id(), w = threadIdx.x / kWave;
   const int64_t t = block * kPlanGroup + threadIdx.x;
+  const int32_t id = plan_id(p, t);  // under the masks' clearing
   for (int e = lane; e < G; e += kWave) mask[w][e] = 0;
   __syncthreads();
   int g = -1;
   if (t < p.tokens) {
-    g = plan_group(p, t);
+    g = plan_group(p, id);
     atomicOr(reinterpret_cast<unsigned long long*>(&mask[w][g]), 1ull << lane);
   }
   __syncthreads();
@@ -128,25 +131,27 @@ __device__ __forceinline__ void plan_add(int32_t* count, int g) {
 
 // A batch of up to kPlanOne tokens in one launch: every block counts all the
 // tokens for itself (integer counts in LDS), those before its own apart, and so
-// knows where its rows go; block 0 writes the rest of the plan.  4096 tokens: 7.3
+// knows where its rows go; block 0 writes the rest of the plan.  4096 tokens: 6.3
 // us against 13.4 in three launches; 16384: 16.6 against 11 in two.
 __global__ __launch_bounds__(kPlanGroup) void k_plan_one(PlanParams p, PlanLayout l) {
   __shared__ uint64_t mask[kPlanChunks][kMaxAdapters + 1];
   __shared__ int32_t before[kMaxAdapters + 1], after[kMaxAdapters + 1];
   __shared__ int32_t wsum[2][16];
   const int G = p.adapters + 1, e = threadIdx.x;
+  constexpr int kB = kPlanOne / kPlanGroup;
+  int32_t id[kB];  // of all blocks' tokens, read at once
+  if (l.nblocks > 1) {
+#pragma unroll
+    for (int u = 0; u < kB; ++u) id[u] = plan_id(p, (int64_t)u * kPlanGroup + threadIdx.x);
+  }
   if (e < G) before[e] = after[e] = 0;
   const int g = plan_masks(p, blockIdx.x, mask);  // (its barriers cover the counters)
-  constexpr int kB = 8;  // reads in flight
-  for (int64_t b0 = 0; l.nblocks > 1 && b0 < l.nblocks; b0 += kB) {
-    int o[kB];
+  if (l.nblocks > 1) {
 #pragma unroll
     for (int u = 0; u < kB; ++u) {
-      const int64_t t = (b0 + u) * kPlanGroup + threadIdx.x;
-      o[u] = b0 + u != blockIdx.x && t < p.tokens ? plan_group(p, t) : -1;
+      const bool other = u != (int)blockIdx.x && u * kPlanGroup + (int)threadIdx.x < p.tokens;
+      plan_add(u < (int)blockIdx.x ? before : after, other ? plan_group(p, id[u]) : -1);
     }
-#pragma unroll
-    for (int u = 0; u < kB; ++u) plan_add(b0 + u < blockIdx.x ? before : after, o[u]);
   }
   __syncthreads();
   int32_t n = 0;
@@ -164,7 +169,7 @@ __global__ __launch_bounds__(kPlanGroup) void k_plan_count(PlanParams p, PlanLay
   __shared__ int32_t count[kMaxAdapters + 1];
   const int G = p.adapters + 1, e = threadIdx.x;
   const int64_t t = (int64_t)blockIdx.x * kPlanGroup + threadIdx.x;
-  const int g = t < p.tokens ? plan_group(p, t) : -1;
+  const int g = t < p.tokens ? plan_group(p, plan_id(p, t)) : -1;
   if (e < G) count[e] = 0;
   __syncthreads();
   plan_add(count, g);
