@@ -15,9 +15,10 @@
 // (S' sequences with tokens, n tokens).  NaN logits rank as -inf, as in the
 // router; a token with no logit above -inf has p = 0, lse = 0 and no gradient.
 //
-// Both passes read the logits once and are bound by that read (and the
-// gradient's write).  Everything is summed in float32, in an order that only
-// the sizes and the sequences decide.
+// Both passes read the logits once.  Long batches are bound by that read (and
+// the gradient's write), short ones by the chain of a token's reductions and the
+// launches.  Everything is summed in float32, in an order that only the sizes and
+// the sequences decide.
 #include <type_traits>
 #include <utility>
 
@@ -161,6 +162,10 @@ __device__ __forceinline__ float balance_term(const RouterLossParams& p, int32_t
   return (float)c * ((float)p.experts * per / (float)p.top_k) * mean;
 }
 
+// Measured: 16 tokens 4.6 us (SINGLE); 4096 x 256 experts 7.6 us; 16384 x 384 in
+// 37 sequences 12 us (25 MB of logits, 2.1 TB/s: half of its time is a wave's
+// chain from the first read to the last reduction).
+//
 // Sums over runs of kLossRun tokens, one wave each, a batch of tokens at a
 // time (the chain of a token's reductions is a microsecond long): probabilities
 // in registers, selections in LDS counters.  A wave writes what it has when
@@ -351,6 +356,9 @@ __device__ __forceinline__ V get_shared(const V* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+// 6.0 us for 4096 tokens and 256 experts, 7.2 for 16384, 384 and 37 sequences:
+// latency (boundaries, slots, the joins in LDS, the counter).
+//
 // Block (x, s): experts [64 x, 64 x + 64) of sequence s.  Its 16 waves take
 // the sequence's slots in turn; then f, P and the block's part of the balance
 // loss.  The last block to finish sums the sequences' parts in order.
@@ -558,6 +566,8 @@ __device__ __forceinline__ float row_same(float v, int32_t key, std::integer_seq
 // numbers give, then what the sequence and the selections give; with a wave for
 // so few tokens their latency is most of its life.  A batch that enters
 // another sequence reads that one's factors again.
+// Measured: 64 tokens x 256 experts 5.9 us; 16384 x 384 15.9 us (51 MB read and
+// written, 3.2 TB/s).
 template <int PER>
 __global__ __launch_bounds__(256) void k_router_grad(RouterGradParams p) {
   constexpr int B = batch_of<PER>();
