@@ -954,6 +954,7 @@ __device__ __forceinline__ void outer_block(const OuterParams& p, const OuterSid
   const bool in = c0 + col < s.C;
   const X* x = static_cast<const X*>(s.x) + (in ? c0 + col : 0);
   const int64_t M = p.plan.max_rows;
+  const uint32_t last = (uint32_t)max((int64_t)1, p.plan.tokens) - 1;
   int64_t row = seg.row;
   const int64_t end = seg.end;
   // The next step's tokens, as they lie in the plan: read without a condition
@@ -967,16 +968,16 @@ __device__ __forceinline__ void outer_block(const OuterParams& p, const OuterSid
     tok[0] = t[0];
     tok[1] = t[1];
   };
-  uint32_t keep;  // bit i: row i of this thread's 8 counts (padding and rows behind the end do not)
+  uint32_t drop;  // bit 7 - i: row i of this thread's 8 is padding, or behind the end
   const auto load = [&](int64_t r) {
     const int32_t t[8] = {tok[0].x, tok[0].y, tok[0].z, tok[0].w, tok[1].x, tok[1].y, tok[1].z, tok[1].w};
-    keep = 0;
+    drop = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const bool ok = (uint32_t)t[i] < (uint32_t)p.plan.tokens;
-      keep |= ok && in && r + 8 * piece < end ? 1u << i : 0;
-      load_words<WORDS>(x + (ok ? t[i] : 0) * s.x_stride, true, raw[i]);
+      drop = __builtin_amdgcn_alignbit(drop, (uint32_t)t[i], 31);  // drop << 1 | sign of t
+      load_words<WORDS>(x + (int64_t)min((uint32_t)t[i], last) * s.x_stride, true, raw[i]);
     }
+    drop = in && r + 8 * piece < end ? drop : 0xFF;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = i * 256 + threadIdx.x, line = min(v / 8, 3 * 16 * RT - 1);  // line: part, then rank
@@ -986,10 +987,12 @@ __device__ __forceinline__ void outer_block(const OuterParams& p, const OuterSid
     }
   };
   const auto put = [&](int64_t r) {
+    if (__any((int)drop)) {  // mostly none is
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int j = 0; j < WORDS; ++j) raw[i][j] = keep >> i & 1 ? raw[i][j] : 0;
+        for (int j = 0; j < WORDS; ++j) raw[i][j] = drop >> (7 - i) & 1 ? 0 : raw[i][j];
+    }
     if constexpr (F32) {
 #pragma unroll
       for (int j = 0; j < W; ++j) {
