@@ -862,6 +862,14 @@ __device__ __forceinline__ int outer_at(int line, int piece) {
   return line * kOuterRows + (piece ^ ((line >> 2 ^ (line >> 1 & 1) << 2) & 7)) * 8;
 }
 
+// Line of column c in a block whose waves take TW matrix blocks each: column l16
+// of a wave's block t is its column TW l16 + t, so that a lane ends with TW
+// neighbouring columns and a wave stores whole 256-byte pieces at TW = 4.
+template <int TW>
+__device__ __forceinline__ int outer_line(int c) {
+  return c / (16 * TW) * (16 * TW) + c % TW * 16 + c / TW % 16;
+}
+
 // An adapter of n rows is summed in m = max(1, ceil(n / p.chunk)) segments of
 // equal length, so that few adapters, or one that has most tokens, still fill
 // the CUs, in one round of blocks: a block's steps follow one another at the
@@ -1003,13 +1011,13 @@ __device__ __forceinline__ void outer_block(const OuterParams& p, const OuterSid
         split8<3>(v, q);
 #pragma unroll
         for (int n = 0; n < 3; ++n)
-          *reinterpret_cast<v8bf*>(xs + n * CB * kOuterRows + outer_at(col + j, piece)) = q[n];
+          *reinterpret_cast<v8bf*>(xs + n * CB * kOuterRows + outer_at(outer_line<TW>(col + j), piece)) = q[n];
       }
     } else {
       v8bf q[W];
       transpose8<WORDS>(raw, q);
 #pragma unroll
-      for (int j = 0; j < W; ++j) *reinterpret_cast<v8bf*>(xs + outer_at(col + j, piece)) = q[j];
+      for (int j = 0; j < W; ++j) *reinterpret_cast<v8bf*>(xs + outer_at(outer_line<TW>(col + j), piece)) = q[j];
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -1053,21 +1061,26 @@ __device__ __forceinline__ void outer_block(const OuterParams& p, const OuterSid
 #pragma unroll
           for (int r = 0; r < RT; ++r)
 #pragma unroll
-            for (int n = 2 - m; n >= 0; --n) acc[t][r] = mfma_bf16(q, u[r][n], acc[t][r]);
+            for (int n = 2 - m; n >= 0; --n) acc[t][r] = mfma_bf16(u[r][n], q, acc[t][r]);
         }
     }
     __syncthreads();
   }
   float* grad = seg.slot < 0 ? s.grad + (int64_t)seg.a * p.rank * s.C
                              : p.part + (seg.slot * (p.x.C + p.dout.C) + s.part_at) * p.rank;
-  // lane: rank l16 of a rank block, columns 4 g .. 4 g + 3 of a column block
+  // lane: TW columns of ranks 4 g .. 4 g + 3 of a rank block
+  typedef float vec __attribute__((ext_vector_type(TW)));
+  const int c = c0 + (w * 16 + l16) * TW;
+  if (c >= s.C) return;
 #pragma unroll
-  for (int t = 0; t < TW; ++t)
+  for (int r = 0; r < RT; ++r)
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const int c = c0 + (w * TW + t) * 16 + 4 * g, q = 16 * r + l16;
-      if (q < p.rank && c < s.C)
-        *reinterpret_cast<v4f*>(grad + (int64_t)q * s.C + c) = acc[t][r];
+    for (int i = 0; i < 4; ++i) {
+      const int q = 16 * r + 4 * g + i;
+      vec v;
+#pragma unroll
+      for (int t = 0; t < TW; ++t) v[t] = acc[t][r][i];
+      if (q < p.rank) *reinterpret_cast<vec*>(grad + (int64_t)q * s.C + c) = v;
     }
 }
 
