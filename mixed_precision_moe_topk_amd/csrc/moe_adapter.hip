@@ -267,9 +267,12 @@ __device__ __forceinline__ int64_t plan_token(const PlanView& v, int64_t row) {
   return t < v.tokens ? t : -1;
 }
 
-// v as a sum of N bf16 parts; an infinite first part leaves the others 0.
+// v as a sum of N bf16 parts; an infinite first part leaves the others 0.  No
+// product is fused into the differences: the parts are those of the rounded v
+// wherever they are made.
 template <int N>
 __device__ __forceinline__ void split_bf16(float v, __bf16 (&part)[N]) {
+#pragma clang fp contract(off)
   part[0] = (__bf16)v;
   const bool inf = __builtin_isinf((float)part[0]);
 #pragma unroll
@@ -687,13 +690,27 @@ struct Row8F32 {
   }
 };
 
+// Ranks [r0, r0 + 8) of a tile's row as operands of outer, 0 behind the last row.
+__device__ __forceinline__ void put_saved(const ExpandParams& p, const Tile& tile, int row, int r0, const float (&u)[8]) {
+  const int64_t M = p.plan.max_rows, part = (int64_t)p.rank_pad * M;
+  __bf16* dst = reinterpret_cast<__bf16*>(p.saved) + r0 * M + tile.row0 + row;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    __bf16 q[3];
+    split_bf16<3>(row < tile.nrows ? u[i] : 0.0f, q);
+#pragma unroll
+    for (int n = 0; n < 3; ++n) dst[n * part + i * M] = q[n];
+  }
+}
+
 // A wave's 128 columns of a tile.  The factor's columns stay in registers, as
 // matrix operands of all its ranks, while the tile's row blocks pass: lane
 // (l16, g) holds columns 8 l16 + j, which are column l16 of matrix j, and of
 // the sums rows 4 g + i, so it reads and writes 8 consecutive elements of a
 // row.  RT: blocks of 32 ranks.  JOINED: the low-rank rows come as operands
 // (frag); else as the float32 sums of shrink's blocks, which every wave adds up
-// for itself: less time than a launch that does it once, where rows are few.
+// for itself, and the first columns' writes to `saved` when it is wanted: less
+// time than a launch that does it once, where rows are few.
 // Measured: 4096 tokens, rank 32: 27 us (117 MB of base and out, 4.3 TB/s);
 // 16384, rank 64: 97 us (470 MB, 4.85 TB/s; 109 us with each step's reads behind
 // the last one's stores); 64 tokens of 64 adapters, rank 32: 7.6 us (32 MB), one
@@ -802,6 +819,7 @@ __global__ __launch_bounds__(256, JOINED ? (RT == 1 && sizeof(T) == 2 ? 4 : RT <
             for (int i = 0; i < 8; ++i) u[i] += x[q][i];
 #pragma unroll
           for (int i = 0; i < 8; ++i) u[i] *= scale;
+          if (p.saved && n0 == 0 && some) put_saved(p, tile, 16 * m + l16, 32 * r + 8 * g, u);
           split8<PARTS>(u, a[r]);
         }
 #pragma unroll
@@ -871,12 +889,12 @@ __device__ __forceinline__ int outer_line(int c) {
 }
 
 // An adapter of n rows is summed in m = max(1, ceil(n / p.chunk)) segments of
-// equal length, so that few adapters, or one that has most tokens, still fill
-// the CUs, in one round of blocks: a block's steps follow one another at the
-// memory's latency, and the longest segment sets the time.  Segments are
-// numbered along the adapters.  A single one is summed into the gradient at
-// once, several into partial sums (slots, numbered among themselves), which
-// k_adapter_outer_join adds up.
+// equal length (one where p.chunks is 1), so that few adapters, or one that has
+// most tokens, still fill the CUs, in one round of blocks: a block's steps follow
+// one another at the memory's latency, and the longest segment sets the time.
+// Segments are numbered along the adapters.  A single one is summed into the
+// gradient at once, several into partial sums (slots, numbered among themselves),
+// which k_adapter_outer_join adds up.
 struct OuterSegment {
   int a, m;
   int64_t row, end;  // its rows
@@ -897,7 +915,7 @@ __device__ __forceinline__ bool outer_segment(const OuterParams& p, int64_t j, O
     const int a = a0 + lane_id();
     const int64_t b = min(max((int64_t)p.plan.first[min(a, L)], (int64_t)0), M) / kAdapterPad * kAdapterPad;
     const int64_t e = min(max((int64_t)p.plan.first[min(a + 1, L)], b), M) / kAdapterPad * kAdapterPad;
-    const int m = a < L ? max(1, (int)((e - b + p.chunk - 1) / p.chunk)) : 0;
+    const int m = a < L ? p.chunks > 1 ? max(1, (int)((e - b + p.chunk - 1) / p.chunk)) : 1 : 0;
     const int q = m > 1 ? m : 0;
     int sm = m, sq = q;
 #pragma unroll

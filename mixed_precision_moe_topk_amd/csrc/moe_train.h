@@ -160,6 +160,7 @@ struct ExpandParams {
   int64_t base_stride;
   void* out;
   int64_t out_stride;
+  uint16_t* saved;  // with part: where the rows go as operands of outer, or null
   int32_t col_blocks, row_blocks;  // of a tile, set by the launcher
 };
 // grad[adapter][r][c] = sum over the adapter's rows of saved[r][row] * X[token(row)][c]

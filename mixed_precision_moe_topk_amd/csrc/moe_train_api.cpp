@@ -131,7 +131,8 @@ struct AdapterLayout {
     const int64_t segments = std::max<int64_t>(1, (rp <= 32 ? 768 : rp <= 64 ? 512 : 256) / cols);
     const int64_t cuts = std::max({(int64_t)1, segments / 2, segments - d->num_adapters});
     chunk = std::max<int64_t>(256, ceil_div(ceil_div(plan.max_rows, cuts), 64) * 64);
-    chunks = (int32_t)std::max<int64_t>(1, ceil_div(plan.max_rows, chunk));
+    // (one where no adapter can have more rows than a segment)
+    chunks = tokens <= chunk ? 1 : (int32_t)ceil_div(plan.max_rows, chunk);
     outer_bytes = chunks > 1 ? align256((size_t)chunks * 2 * d->rank *
                                         ((size_t)d->in_features + d->out_features) * 4) : 0;
   }
@@ -188,14 +189,14 @@ moe_status run_product(const Product& q, const moe::PlanView& v, const AdapterLa
   const moe::ShrinkParams s = {v, q.shape, q.x, q.x_stride, static_cast<const uint16_t*>(q.w),
                                rank, l.rp, q.features, part};
   MOE_RETURN_IF(moe::check_hip(moe::launch_adapter_shrink(s, q.x_f32, stream), "adapter shrink", stream));
-  if (low.frag || low.saved) {
+  if (low.frag || (low.saved && !q.out)) {
     const moe::JoinParams j = {v, q.shape, part, scale, l.rp, low};
     MOE_RETURN_IF(moe::check_hip(moe::launch_adapter_join(j, stream), "adapter join", stream));
   }
   if (!q.out) return MOE_OK;
   const moe::ExpandParams e = {v, q.shape, low.frag, part, scale, static_cast<const uint16_t*>(q.w2),
                                rank, l.rp, l.rp32, q.features2, q.base, q.base_stride, q.out,
-                               q.out_stride, 0, 0};
+                               q.out_stride, few ? low.saved : nullptr, 0, 0};
   return moe::check_hip(moe::launch_adapter_expand(e, q.out_f32, stream), "adapter expand", stream);
 }
 
