@@ -103,8 +103,12 @@ moe::ShrinkShape shrink_shape(int64_t tokens, int64_t features) {
 }
 int32_t max_slots(const moe::ShrinkShape& s) { return (s.units - 1) / s.min_run + 2; }
 
-// Up to so many tokens expand adds up the parts for itself.
-constexpr int64_t kFewTokens = 128;
+// Up to so many sums (tokens x ranks) expand adds up the parts for itself: every
+// wave of 128 columns reads them again, which costs less than the join's launch
+// while they are few.  7168 x 7168 features, us a call without and with the join:
+// 400 tokens, rank 16: 22.0, 24.3; 800, 16: 27.5, 27.2; 400, 64: 31.3, 30.8; 400,
+// 128: 62, 51.  1024 x 2048, 400, 16: 16.8, 20.3.
+constexpr int64_t kFewSums = 16384;
 
 // Workspace: the sums of the larger contraction, expand's operands, the backward
 // pass's v as outer's operands, and the factors' gradients of the segments.
@@ -178,7 +182,7 @@ moe_status run_product(const Product& q, const moe::PlanView& v, const AdapterLa
                        int32_t rank, const float* scale, void* workspace, hipStream_t stream) {
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   float* part = reinterpret_cast<float*>(ws);
-  const bool few = v.tokens <= kFewTokens;  // expand takes the parts themselves
+  const bool few = v.tokens * l.rp <= kFewSums;  // expand takes the parts themselves
   moe::LowRows low;
   low.frag = few || !q.out ? nullptr : reinterpret_cast<uint16_t*>(ws + l.part_bytes);
   low.saved = static_cast<uint16_t*>(q.saved);

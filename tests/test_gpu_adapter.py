@@ -171,8 +171,13 @@ CASES = [  # tokens, adapters, rank, K, N, out, ids
     (9000, 3, 8, 64, 64, "bf16", scattered),          # past the plan of one launch
     (33000, 5, 8, 64, 72, "f32", some_without),       # whole tiles for shrink's blocks
     (66000, 2, 4, 16, 8, "bf16", runs),               # a plan of three launches
-    (128, 3, 32, 264, 200, "bf16", scattered),        # the most tokens whose rows expand adds up itself
+    (128, 3, 32, 264, 200, "bf16", scattered),
     (129, 3, 32, 264, 200, "f32", scattered),
+    (512, 3, 32, 264, 200, "f32", scattered),         # the most sums that expand adds up itself
+    (513, 3, 32, 264, 200, "bf16", scattered),
+    (1024, 5, 15, 520, 136, "bf16", runs),
+    (1030, 5, 16, 520, 136, "f32", runs),
+    (128, 9, 128, 136, 264, "f32", each),
 ]
 
 
