@@ -961,6 +961,9 @@ __device__ __forceinline__ bool outer_segment(const OuterParams& p, int64_t j, O
 // memory and, not fully under it, LDS and the saved values' reads from L2.  Four
 // waves that split the rows and transpose straight into operands, without LDS,
 // took 36 us: each reads the saved values for 128 columns in place of 256.
+// RT > 4: eight waves, two for each quarter, half of the ranks each.
+template <int RT>
+constexpr int outer_threads() { return RT <= 4 ? 256 : 512; }
 template <int RT, bool F32>
 constexpr int outer_cols() { return F32 ? 64 : RT <= 2 ? 256 : 128; }  // columns of a block
 template <int RT, bool F32>
@@ -969,14 +972,17 @@ __device__ __forceinline__ void outer_block(const OuterParams& p, const OuterSid
   constexpr int XP = F32 ? 3 : 1;       // parts of X
   constexpr int CB = outer_cols<RT, F32>();
   constexpr int TW = CB / 64;           // matrix column blocks of a wave
-  constexpr int W = CB / 32;            // columns of a thread
+  constexpr int NT = outer_threads<RT>(), PT = NT / 8;  // threads, and those of 8 rows
+  constexpr int RW = RT * 256 / NT;     // rank blocks of a wave
+  constexpr int W = CB / PT;            // columns of a thread
   constexpr int WORDS = F32 ? W : W / 2;
-  constexpr int NV = (3 * 16 * RT * 8 + 255) / 256;
+  constexpr int NV = (3 * 16 * RT * 8 + NT - 1) / NT;
   typedef std::conditional_t<F32, float, uint16_t> X;
   __bf16* xs = lds;
   __bf16* vs = lds + XP * CB * kOuterRows;
-  const int lane = lane_id(), w = threadIdx.x / kWave, l16 = lane & 15, g = lane >> 4;
-  const int piece = threadIdx.x / 32, col = threadIdx.x % 32 * W;
+  const int lane = lane_id(), l16 = lane & 15, g = lane >> 4;
+  const int w = threadIdx.x / kWave % 4, r0 = threadIdx.x / 256 * RW;  // the wave's columns and rank blocks
+  const int piece = threadIdx.x / PT, col = threadIdx.x % PT * W;
   const bool in = c0 + col < s.C;
   const X* x = static_cast<const X*>(s.x) + (in ? c0 + col : 0);
   const int64_t M = p.plan.max_rows;
@@ -1006,7 +1012,7 @@ __device__ __forceinline__ void outer_block(const OuterParams& p, const OuterSid
     drop = in && r + 8 * piece < end ? drop : 0xFF;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = i * 256 + threadIdx.x, line = min(v / 8, 3 * 16 * RT - 1);  // line: part, then rank
+      const int v = i * NT + threadIdx.x, line = min(v / 8, 3 * 16 * RT - 1);  // line: part, then rank
       const int rank = min(line % (16 * RT), p.rank_pad - 1), part = line / (16 * RT);
       rv[i] = *reinterpret_cast<const v4u*>(s.saved + ((int64_t)part * p.rank_pad + rank) * M +
                                             min(r + 8 * (v % 8), M - 8));
@@ -1039,17 +1045,17 @@ __device__ __forceinline__ void outer_block(const OuterParams& p, const OuterSid
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = i * 256 + threadIdx.x;
+      const int v = i * NT + threadIdx.x;
       const bool ok = r + 8 * (v % 8) < end;  // (ranks behind the last repeat it, and are not stored)
-      if (3 * 16 * RT * 8 % 256 == 0 || v < 3 * 16 * RT * 8)
+      if (3 * 16 * RT * 8 % NT == 0 || v < 3 * 16 * RT * 8)
         *reinterpret_cast<v4u*>(vs + outer_at(v / 8, v % 8)) = ok ? rv[i] : v4u{0, 0, 0, 0};
     }
   };
-  v4f acc[TW][RT];
+  v4f acc[TW][RW];
 #pragma unroll
   for (int t = 0; t < TW; ++t)
 #pragma unroll
-    for (int r = 0; r < RT; ++r) acc[t][r] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int r = 0; r < RW; ++r) acc[t][r] = v4f{0.f, 0.f, 0.f, 0.f};
   if (row < end) {
     tokens(row);
     load(row);
@@ -1064,22 +1070,23 @@ __device__ __forceinline__ void outer_block(const OuterParams& p, const OuterSid
     }
 #pragma unroll
     for (int k = 0; k < kOuterRows / 32; ++k) {
-      v8bf u[RT][3];
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int n = 0; n < 3; ++n)
-          u[r][n] = *reinterpret_cast<const v8bf*>(vs + outer_at((n * RT + r) * 16 + l16, 4 * k + g));
+      v8bf q[TW][XP];
 #pragma unroll
       for (int t = 0; t < TW; ++t)
 #pragma unroll
-        for (int m = XP - 1; m >= 0; --m) {
-          const v8bf q = *reinterpret_cast<const v8bf*>(
+        for (int m = 0; m < XP; ++m)
+          q[t][m] = *reinterpret_cast<const v8bf*>(
               xs + m * CB * kOuterRows + outer_at((w * TW + t) * 16 + l16, 4 * k + g));
 #pragma unroll
-          for (int r = 0; r < RT; ++r)
+      for (int n = 2; n >= 0; --n)
 #pragma unroll
-            for (int n = 2 - m; n >= 0; --n) acc[t][r] = mfma_bf16(u[r][n], q, acc[t][r]);
+        for (int r = 0; r < RW; ++r) {
+          const v8bf u =
+              *reinterpret_cast<const v8bf*>(vs + outer_at((n * RT + r0 + r) * 16 + l16, 4 * k + g));
+#pragma unroll
+          for (int m = min(XP - 1, 2 - n); m >= 0; --m)
+#pragma unroll
+            for (int t = 0; t < TW; ++t) acc[t][r] = mfma_bf16(u, q[t][m], acc[t][r]);
         }
     }
     __syncthreads();
@@ -1091,10 +1098,10 @@ __device__ __forceinline__ void outer_block(const OuterParams& p, const OuterSid
   const int c = c0 + (w * 16 + l16) * TW;
   if (c >= s.C) return;
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
+  for (int r = 0; r < RW; ++r)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int q = 16 * r + 4 * g + i;
+      const int q = 16 * (r0 + r) + 4 * g + i;
       vec v;
 #pragma unroll
       for (int t = 0; t < TW; ++t) v[t] = acc[t][r][i];
@@ -1105,7 +1112,7 @@ __device__ __forceinline__ void outer_block(const OuterParams& p, const OuterSid
 // Block (columns of either factor, segment).  Both factors in one launch: the
 // second's blocks fill the CUs the first leaves.
 template <int RT, bool F32>
-__global__ __launch_bounds__(256, RT <= 2 ? 3 : RT == 4 ? 2 : 1) void k_adapter_outer(OuterParams p) {
+__global__ __launch_bounds__(outer_threads<RT>(), RT <= 4 ? 3 : 4) void k_adapter_outer(OuterParams p) {
   constexpr int kX = outer_cols<RT, false>();
   constexpr int kLds = (F32 && 3 * 64 > kX ? 3 * 64 : kX) * kOuterRows + 3 * 16 * RT * kOuterRows;
   __shared__ __align__(16) __bf16 lds[kLds];
@@ -1147,7 +1154,7 @@ static void launch_outer(OuterParams p, hipStream_t st) {
   p.cols0 = (p.x.C + X - 1) / X;
   p.cols = p.cols0 + (p.dout.C + D - 1) / D;
   // at most one segment an adapter and one a chunk
-  k_adapter_outer<RT, F32><<<(unsigned)(p.cols * ((int64_t)p.plan.adapters + p.chunks)), 256, 0, st>>>(p);
+  k_adapter_outer<RT, F32><<<(unsigned)(p.cols * ((int64_t)p.plan.adapters + p.chunks)), outer_threads<RT>(), 0, st>>>(p);
 }
 hipError_t launch_adapter_outer(const OuterParams& p, bool dout_f32, hipStream_t st) {
   const int rt = p.rank_pad / 16;

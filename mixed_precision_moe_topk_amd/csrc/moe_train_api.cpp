@@ -127,12 +127,12 @@ struct AdapterLayout {
     frag_bytes = align256((size_t)plan.max_rows * rp32 * 6);
     saved_bytes = align256((size_t)plan.max_rows * rp * 6);
     // segments of all adapters for as many blocks as run at once (registers
-    // allow 3, 2 or 1 a CU by the rank), 256 rows a segment at least: rows are
+    // allow 3 or 2 a CU by the rank), 256 rows a segment at least: rows are
     // cut into what is left when every adapter has one, or into half as many
     const int64_t wide = rp <= 32 ? 256 : 128;  // columns of a block
     const int64_t cols = ceil_div(d->in_features, wide) +
                          ceil_div(d->out_features, d->out_type == MOE_T_F32 ? 64 : wide);
-    const int64_t segments = std::max<int64_t>(1, (rp <= 32 ? 768 : rp <= 64 ? 512 : 256) / cols);
+    const int64_t segments = std::max<int64_t>(1, (rp <= 64 ? 768 : 512) / cols);
     const int64_t cuts = std::max({(int64_t)1, segments / 2, segments - d->num_adapters});
     chunk = std::max<int64_t>(256, ceil_div(ceil_div(plan.max_rows, cuts), 64) * 64);
     // (one where no adapter can have more rows than a segment)
