@@ -949,18 +949,20 @@ __device__ __forceinline__ bool outer_segment(const OuterParams& p, int64_t j, O
   return false;
 }
 
-// Sums of one block's columns [c0, c0 + CB) of a factor.  Each thread reads 8
-// rows x 8 bytes (a wave two whole 256-byte row pieces), turns them in
+// Sums of one block's columns [c0, c0 + CB) of a factor.  Each thread reads W
+// columns of 8 rows (a wave whole row pieces of 256 or 512 bytes), turns them in
 // registers into lines of 8 rows, and hands them to the block through LDS; the
-// saved values already lie so.  The four waves then sum a quarter of the
-// columns each, over all rows: no partial sums to join.  F32: X is float32,
+// saved values already lie so.  The waves then sum a quarter of the columns
+// each, over all rows: no partial sums to join.  F32: X is float32,
 // three bf16 parts like the saved values; products of parts whose sizes lie
 // 2^-27 or more apart are left out.
-// Measured: 4096 tokens, rank 32, both factors: 34 us (117 MB of x and dout, 3.4
-// TB/s), beside the router (7168 and 256 float32 columns, rank 12) 20 us.  Bound by
-// memory and, not fully under it, LDS and the saved values' reads from L2.  Four
-// waves that split the rows and transpose straight into operands, without LDS,
-// took 36 us: each reads the saved values for 128 columns in place of 256.
+// Measured: 4096 tokens, rank 32, both factors: 32 us (117 MB of x and dout, 3.7
+// TB/s; rank 64: 45, 128: 72 us), beside the router (7168 and 256 float32
+// columns, rank 12) 19.5 us.  Bound by memory: without the products 3 us less, without
+// the sums' stores 3.7, a launch without rows 6.5.  Four waves that split the rows
+// and transpose straight into operands, without LDS, took 36 us: each reads the
+// saved values for 128 columns in place of 256.  Rank 64 by eight waves, 256
+// columns: 49 us.
 // RT > 4: eight waves, two for each quarter, half of the ranks each.
 template <int RT>
 constexpr int outer_threads() { return RT <= 4 ? 256 : 512; }
