@@ -201,6 +201,54 @@ def test_strided_rows_and_places(out):
         c.check(c.run(base="in place", dx="in place"))
 
 
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_strided_rows_and_places_of_long_batches(out):
+    """The same where the low-rank rows are joined before expand."""
+    c = Case(700, 4, 36, 264, 200, out, some_without, 12, (8, 16, 24))
+    c.check(c.run())
+    c.check(c.run(base="none", dx="none"), base="none", dx="none")
+    c.check(c.run(base="in place", dx="in place"))
+
+
+def test_frozen_factors_and_input_alone_of_long_batches():
+    """dx alone, and the factors' gradients alone, where rows are joined."""
+    import torch
+
+    import mixed_precision_moe_topk_amd as M
+
+    c = Case(1100, 3, 44, 136, 264, "bf16", some_without, 42)
+    r = c.run(dx="none")
+    T, L, R, K, N = c.shape
+    d = M.AdapterDims(L, R, K, N)
+    buf = lambda n: torch.empty(n, dtype=torch.uint8, device="cuda")  # noqa: E731
+    plan, ws, saved = (buf(n) for n in (M.adapter_plan_query(L, T), M.adapter_workspace_query(d, T),
+                                        M.adapter_saved_query(d, T)))
+    x, a, b, dout = (c.dev(v, True) for v in (c.x, c.a, c.b, c.dout))
+    scale = c.dev(c.scale, False)
+    M.adapter_plan(L, c.dev(c.ids, False), plan)
+    dx = torch.empty_like(x)
+    M.adapter_backward(d, dout, None, plan, a, b, scale, None, None, None, ws, dx=dx)
+    assert np.array_equal(dx.float().cpu().numpy(), r["dx"])
+    M.adapter_apply(d, x, plan, a, b, scale, None, torch.empty_like(dout), ws, saved=saved)
+    da, db = torch.empty(L, R, K, device="cuda"), torch.empty(L, R, N, device="cuda")
+    M.adapter_backward(d, dout, x, plan, a, b, scale, saved, da, db, ws)
+    assert np.array_equal(da.cpu().numpy(), r["da"]) and np.array_equal(db.cpu().numpy(), r["db"])
+
+
+def test_infinities_pass_as_the_formula_has_them():
+    """One infinite element of x: the same infinities and NaN as in float64, and
+    no NaN from ranks that only pad, on both ways of the low-rank rows."""
+    for T in (40, 700):
+        c = Case(T, 2, 1, 64, 136, "bf16", each, 33)
+        c.x[4, 9] = np.inf
+        r = c.run()
+        f = lambda v: v.astype(np.float64)  # noqa: E731
+        with np.errstate(invalid="ignore"):
+            ref = OT.adapter_apply(f(c.x), c.ids, f(c.a), f(c.b), f(c.scale), f(c.base))
+        assert np.isinf(ref[4]).all() and np.isfinite(np.delete(ref, 4, 0)).all()
+        assert np.array_equal(r["out"][4], ref[4]) and np.isfinite(np.delete(r["out"], 4, 0)).all()
+
+
 def test_long_rows_and_many_tokens():
     """The layer's own width; contractions split over several blocks, and an
     adapter with thousands of tokens."""
