@@ -406,7 +406,7 @@ __device__ __forceinline__ void put_low(const LowRows& o, int64_t row0, int r, c
 // is then summed by several blocks (`slots`, at most kMaxSlots), whose float32
 // sums meet in the join or in expand.
 // Measured: 4096 tokens, rank 32: 13.7 us (58.7 MB of x, 4.3 TB/s); 16384,
-// rank 64: 57 us (4.1 TB/s: every 64 rows of x read as many of the factor, from
+// rank 64: 55 us (4.3 TB/s: every 64 rows of x read as many of the factor, from
 // L2); 64 tokens of 64 adapters, rank 32: 8.8 us (29 MB of factors, 3.3 TB/s, of
 // which 3.8 us are the launch's, as one token takes).
 // Blocks a CU: two with two LDS buffers; four with one buffer took 22 and 62 us.
@@ -500,7 +500,11 @@ __device__ __forceinline__ void shrink_direct(const ShrinkParams& p, const Tile&
 // A whole tile: KC elements of K of its rows and of the factor pass through
 // LDS, read from memory in whole row pieces (256 bytes at RT <= 4; 16 rows of 64
 // bytes, as the matrix operands lie, ran at two thirds of the speed), the next
-// piece under this one's products.  Wave w sums rows [16 w, 16 w + 16).
+// piece under this one's products.  Wave w sums rows [16 w, 16 w + 16), or from
+// rank 64 on 32 rows and half of the ranks (acc: rows, then ranks), which reads a
+// fifth (rank 64) or a third less from LDS.
+template <int RT>
+constexpr int shrink_row_blocks() { return RT >= 4 ? 2 : 1; }  // of a wave
 template <int RT>
 __device__ __forceinline__ void shrink_staged(const ShrinkParams& p, const Tile& tile, int k0, int ke, v4f (&acc)[RT],
                                               uint16_t* lds) {
@@ -509,6 +513,8 @@ __device__ __forceinline__ void shrink_staged(const ShrinkParams& p, const Tile&
   constexpr int NX = kAdapterTile / ROWS, NA = (16 * RT + ROWS - 1) / ROWS;
   const int lane = lane_id(), w = threadIdx.x / kWave, l16 = lane & 15, g = lane >> 4;
   const int row = threadIdx.x / VR, col = threadIdx.x % VR * 8;
+  constexpr int RB = shrink_row_blocks<RT>(), RW = RT / RB;
+  const int m0 = RB * (w % (4 / RB)), r0 = RW * (w / (4 / RB));  // the wave's row and rank blocks
   uint16_t* sx = lds;
   uint16_t* sa = lds + 2 * kAdapterTile * P;
   const uint16_t *xp[NX], *wp[NA];
@@ -545,14 +551,19 @@ __device__ __forceinline__ void shrink_staged(const ShrinkParams& p, const Tile&
   for (int k = k0; k < ke; k += KC, b ^= 1) {
     const bool more = k + KC < ke;
     if (more) load(k + KC);
-    const uint16_t* x = sx + (b * kAdapterTile + 16 * w + l16) * P + 8 * g;
-    const uint16_t* a = sa + (b * 16 * RT + l16) * P + 8 * g;
+    const uint16_t* x = sx + (b * kAdapterTile + 16 * m0 + l16) * P + 8 * g;
+    const uint16_t* a = sa + (b * 16 * RT + 16 * r0 + l16) * P + 8 * g;
 #pragma unroll
     for (int s = 0; s < KC; s += 32) {
-      const v8bf xs = *reinterpret_cast<const v8bf*>(x + s);
+      v8bf xs[RB];
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
-        acc[r] = mfma_bf16(*reinterpret_cast<const v8bf*>(a + 16 * r * P + s), xs, acc[r]);
+      for (int m = 0; m < RB; ++m) xs[m] = *reinterpret_cast<const v8bf*>(x + 16 * m * P + s);
+#pragma unroll
+      for (int r = 0; r < RW; ++r) {
+        const v8bf as = *reinterpret_cast<const v8bf*>(a + 16 * r * P + s);
+#pragma unroll
+        for (int m = 0; m < RB; ++m) acc[m * RW + r] = mfma_bf16(as, xs[m], acc[m * RW + r]);
+      }
     }
     if (more) put(b ^ 1);
     __syncthreads();
@@ -587,18 +598,22 @@ __global__ __launch_bounds__(256, 2) void k_adapter_shrink(ShrinkParams p) {
     } else {
       shrink_staged<RT>(p, tile, k0, ke, acc, reinterpret_cast<uint16_t*>(lds));
     }
-    // lane: row l16 of the wave's 16, ranks [4 g, 4 g + 4) of a rank block
-    const int row = (few ? 0 : 16 * w) + l16;
-    if ((few && w > 0) || (!few && 16 * w >= tile.nrows)) continue;
+    if (few && w > 0) continue;
+    // lane: row l16 of a row block, ranks [4 g, 4 g + 4) of a rank block
+    constexpr int RB = F32 ? 1 : shrink_row_blocks<RT>(), RW = RT / RB;
     float* part = p.part + (me - shrink_first(runs, i)) * p.plan.max_rows * p.rank_pad +
-                  (tile.row0 + row) * (int64_t)p.rank_pad + 4 * g;
+                  tile.row0 * (int64_t)p.rank_pad + 4 * g;
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      if (16 * r >= p.rank_pad) break;
-      v4f v = acc[r];
+    for (int q = 0; q < RT; ++q) {
+      // acc[q]: its row and rank block
+      const int m = few ? 0 : RB * (w % (4 / RB)) + q / RW;
+      const int r = few ? q : RW * (w / (4 / RB)) + q % RW;
+      const int row = 16 * m + l16;
+      if (16 * m >= tile.nrows || 16 * r >= p.rank_pad) continue;
+      v4f v = acc[q];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] = row < tile.nrows && 16 * r + 4 * g + q < p.rank ? v[q] : 0.0f;
-      *reinterpret_cast<v4f*>(part + 16 * r) = v;
+      for (int c = 0; c < 4; ++c) v[c] = row < tile.nrows && 16 * r + 4 * g + c < p.rank ? v[c] : 0.0f;
+      *reinterpret_cast<v4f*>(part + row * (int64_t)p.rank_pad + 16 * r) = v;
     }
   }
 }
