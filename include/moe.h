@@ -561,8 +561,9 @@ moe_status moe_adapter_apply(const moe_adapter_dims* dims, const void* x, int64_
  *           when da and db are wanted
  *   dx_base: device bf16 [num_tokens, in_features]; may be dx (with the same
  *           stride); null: 0
- * num_tokens = 0 writes zeros into da and db.  Errors as moe_run_ws, and
- * MOE_ERR_INVALID_ARG when no gradient is wanted. */
+ * num_tokens = 0 writes zeros into da and db, or returns MOE_OK without
+ * launching when they are null.  Errors as moe_run_ws, and
+ * MOE_ERR_INVALID_ARG when no gradient of some tokens is wanted. */
 moe_status moe_adapter_backward(const moe_adapter_dims* dims, const void* dout,
                                 int64_t dout_stride, const void* x, int64_t x_stride,
                                 int64_t num_tokens, const void* plan, size_t plan_bytes,

@@ -392,7 +392,9 @@ moe_status moe_adapter_backward(const moe_adapter_dims* dims, const void* dout,
   MOE_RETURN_IF(check_adapter(dims, num_tokens));
   if ((da == nullptr) != (db == nullptr))
     return set_error(MOE_ERR_INVALID_ARG, "da and db are wanted together or not at all");
-  if (!da && !dx) return set_error(MOE_ERR_INVALID_ARG, "neither dx nor da and db: no gradient");
+  // (dx of no tokens has no address)
+  if (!da && !dx && num_tokens > 0)
+    return set_error(MOE_ERR_INVALID_ARG, "neither dx nor da and db: no gradient");
   if (da) MOE_RETURN_IF(check_pointers({da, db}));
   MOE_RETURN_IF(check_optional(dx));
   MOE_RETURN_IF(check_optional(dx_base));

@@ -429,3 +429,20 @@ def test_binding_refuses_wrong_tensors():
     with pytest.raises(M.MoeError):
         M.adapter_plan(L, e(T, t=torch.int64), plan)
     torch.cuda.synchronize()
+
+
+def test_no_tokens_and_frozen_factors():
+    """An empty batch asked for dx alone, as a rank without tokens has it."""
+    import torch
+
+    import mixed_precision_moe_topk_amd as M
+
+    d = M.AdapterDims(3, 8, 64, 128)
+    e = lambda *s: torch.empty(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    plan, ws = (torch.empty(n, dtype=torch.uint8, device="cuda")
+                for n in (M.adapter_plan_query(3, 0), M.adapter_workspace_query(d, 0)))
+    M.adapter_backward(d, e(0, 128), e(0, 64), plan, e(3, 8, 64), e(3, 8, 128), torch.ones(3, device="cuda"), None,
+                       None, None, ws, dx=e(0, 64))
+    M.adapter_backward(d, e(0, 128), None, plan, e(3, 8, 64), e(3, 8, 128), torch.ones(3, device="cuda"), None,
+                       None, None, ws, dx=e(0, 64), dx_base=e(0, 64))
+    torch.cuda.synchronize()

@@ -170,3 +170,19 @@ def test_outputs_over_inputs_that_are_still_read_are_refused(L):
 
     for dx in (X[0], X[1]):
         assert back(dx) == 1 and b"dx" in L.moe_last_error()
+
+
+def test_an_empty_batch_with_frozen_factors_is_accepted(L):
+    """No token and no factors' gradients: nothing to write, whatever dx is (an
+    empty tensor has no address)."""
+    import torch
+
+    dims = M.AdapterDims(4, 20, 256, 512).c()
+    for dx in (None, OK):
+        assert L.moe_adapter_backward(ctypes.byref(dims), None, 512, None, 256, 0, None, 0, None, None, None, None, 0,
+                                      None, None, None, 256, dx, 256, None, 0, None) == 0
+    # one factor without the other stays refused, and so does no gradient of some tokens
+    for da, db, tokens in ((OK, None, 0), (None, OK, 0), (None, None, 4)):
+        assert L.moe_adapter_backward(ctypes.byref(dims), OK, 512, OK, 256, tokens, OK, BIG, OK, OK, OK, OK, BIG, da,
+                                      db, None, 256, None, 256, OK, BIG, None) == 1
+    assert torch.empty(0, 256).data_ptr() == 0
