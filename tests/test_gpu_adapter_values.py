@@ -1,0 +1,74 @@
+"""Low-rank adapters on the GPU at values where the bf16 parts of a float32 could
+show: full mantissas."""
+import numpy as np
+import pytest
+
+from oracle import formats as F
+from tests.test_gpu_adapter import Case, each
+
+pytestmark = pytest.mark.gpu
+
+PATHS = [24, 1032]  # tokens: expand adds up the blocks' sums itself, or takes joined rows (rank 16 at most)
+
+
+def rest_of_two(v):
+    """What two bf16 parts leave of v, relative."""
+    v = np.asarray(v, np.float32)
+    p = [F.bf16_to_f32(F.bf16_rne(v))]
+    p.append(F.bf16_to_f32(F.bf16_rne((v - p[0]).astype(np.float32))))
+    return np.abs(v.astype(np.float64) - p[0] - p[1]) / np.abs(v)
+
+
+def full(rng, n):
+    """n floats in +-[1, 2) of which two bf16 parts leave 2^-19 or more."""
+    v = (1 + rng.random(64 * n)).astype(np.float32)
+    v = v[rest_of_two(v) >= 2.0 ** -19][:n]
+    assert len(v) == n
+    return v * rng.choice([-1, 1], n).astype(np.float32)
+
+
+class Diagonal(Case):
+    """Rank 1, x = 1 and A = 1: u = scale of the adapter; dout a diagonal.  One
+    term in every sum, so that the float32 result is the term."""
+
+    def __init__(self, T, out, scale, diagonal):
+        super().__init__(T, len(scale), 1, T, T, out, each, T)
+        self.x = np.eye(T, dtype=np.float32)
+        self.a = np.ones((len(scale), 1, T), np.float32)
+        n = np.arange(T)
+        self.b = np.broadcast_to((np.where(n % 2, -1, 1) * 2.0 ** (n % 5 - 2)).astype(np.float32),
+                                 (len(scale), 1, T)).copy()
+        self.scale = np.asarray(scale, np.float32)
+        self.dout = np.diag(np.asarray(diagonal, np.float32))
+        self.dxb = np.zeros((T, T), np.float32)
+
+    def wants(self):
+        """u B, the diagonal's part of dA and of dB; zero elsewhere."""
+        T = self.shape[0]
+        t = np.arange(T)
+        s, b, d = self.scale.astype(np.float64)[self.ids], self.b[0, 0].astype(np.float64), np.diag(self.dout).astype(np.float64)
+        da, db = np.zeros(self.a.shape), np.zeros(self.b.shape)
+        da[self.ids, 0, t] = s * d * b
+        db[self.ids, 0, t] = s * d
+        return s[:, None] * b, da, db
+
+
+@pytest.mark.parametrize("T", PATHS)
+@pytest.mark.parametrize("which,out", [("rows", "bf16"), ("rows", "f32"), ("dout", "f32"), ("both", "f32")])
+def test_float32_results_keep_24_bits(T, which, out):
+    """Three bf16 parts of the low-rank rows, and of a float32 dout, hold the
+    float32 value.  With one of them a power of two every product and every sum
+    of parts fits 24 bits: one step (2^-23) is granted.  With both full, v is
+    rounded once, the products of parts that are left out are two of 2^-25 and
+    one of 2^-34, and six additions are off by a step each: 8 steps, 2^-20.  Two
+    parts would leave 2^-19 or more of the values used here."""
+    rng = np.random.default_rng(T)
+    scale = np.float32([2.0, -0.5, 4.0]) if which == "dout" else full(rng, 3)
+    c = Diagonal(T, out, scale, np.ones(T) if which == "rows" else full(rng, T))
+    r = c.run(base="none", dx="none")
+    o, da, db = c.wants()
+    tol = 8 * 2.0 ** -23 if which == "both" else 2.0 ** -23
+    if out == "f32":
+        assert np.all(np.abs(r["out"] - o) <= 2.0 ** -23 * np.abs(o))
+    assert np.all(np.abs(r["da"] - da) <= tol * np.abs(da))
+    assert np.all(np.abs(r["db"] - db) <= tol * np.abs(db))

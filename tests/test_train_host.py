@@ -186,3 +186,13 @@ def test_an_empty_batch_with_frozen_factors_is_accepted(L):
         assert L.moe_adapter_backward(ctypes.byref(dims), OK, 512, OK, 256, tokens, OK, BIG, OK, OK, OK, OK, BIG, da,
                                       db, None, 256, None, 256, OK, BIG, None) == 1
     assert torch.empty(0, 256).data_ptr() == 0
+
+
+def test_router_loss_workspace_holds_every_slot(L):
+    """2 E + 2 words for each run of 8 tokens (whole blocks of 8 runs) and for each
+    sequence, then the sequences' parts."""
+    for experts, tokens, seqs in ((8, 64, 1), (8, 65, 1), (8, 4096, 9), (384, 16384, 37), (1024, 1, 65535)):
+        runs = -(-tokens // 64) * 8
+        parts = seqs * (-(-experts // 64) + 1)
+        need = 4 * ((runs + seqs) * (2 * experts + 2) + parts)
+        assert need < M.router_loss_query(M.LayerDims(experts, 256, 512), tokens, seqs) <= need + 1024
