@@ -454,6 +454,8 @@ moe_status moe_router_loss(const moe_dims* dims, const float* router_logits, con
  *   dlogits:       device float [num_tokens, num_experts] out.  Zero for
  *                  masked tokens and for tokens with no logit above -inf; the
  *                  rows of tokens in no sequence are left as they were
+ * An expert that a token selects more than once gets its slots' terms of the
+ * weights, summed in the slots' order.
  * dlogits may be router_logits.  num_tokens = 0 returns MOE_OK without
  * launching.  Errors as moe_run_ws, and MOE_ERR_INVALID_ARG when both
  * gradients are null. */

@@ -547,18 +547,24 @@ __device__ __forceinline__ float row_sum(float v) {
   v += row_ror<2>(v);
   return v + row_ror<1>(v);
 }
-// Sum of v over the lanes of the row that hold this lane's key.
+// v of the lane N places before in the row where it holds this lane's key, else
+// 0; first: cleared where that lane stands before this one in the row.
 template <int N>
-__device__ __forceinline__ float row_other(float v, int32_t key) {
+__device__ __forceinline__ float row_other(float v, int32_t key, bool& first) {
   // both moves with all lanes on: a lane that is off gives nothing
   const float other = row_ror<N>(v);
-  const int32_t k = row_ror<N>(key);
-  return k == key ? other : 0.0f;
+  const bool same = row_ror<N>(key) == key;
+  if (same && N <= lane_id() % 16) first = false;
+  return same ? other : 0.0f;
 }
+// In the first lane of the row that holds a key (first true): v summed over all
+// lanes that hold it, in their order.  The values are added as they are rounded.
 template <int... N>
-__device__ __forceinline__ float row_same(float v, int32_t key, std::integer_sequence<int, N...>) {
+__device__ __forceinline__ float row_same(float v, int32_t key, bool& first, std::integer_sequence<int, N...>) {
+#pragma clang fp contract(off)
   float r = v;
-  ((r += row_other<N + 1>(v, key)), ...);
+  first = true;
+  ((r += row_other<15 - N>(v, key, first)), ...);  // the next lane's comes from 15 places before
   return r;
 }
 
@@ -621,12 +627,14 @@ __global__ __launch_bounds__(256) void k_router_grad(RouterGradParams p) {
   for (int i = 0; i < PER; ++i) f[i] = 0.0f;
   if (losses && seq.s >= 0) factors();
   // the selections' part: w (dw - sum w dw) of each, summed over a token's
-  // selections of one expert (they differ, but for a caller's own ids)
+  // selections of one expert (they differ, but for a caller's own ids), which its
+  // first one stores
   float sel = 0.0f;
+  bool first = true;
   if (chosen) {
     wj = slot ? wj : 0.0f;
     dj = slot ? dj : 0.0f;
-    sel = row_same(wj * (dj - row_sum(wj * dj)), id, std::make_integer_sequence<int, 15>());
+    sel = row_same(wj * (dj - row_sum(wj * dj)), id, first, std::make_integer_sequence<int, 15>());
   }
   exponentials<PER, B>(x, m, sum);
   float inv[B], lz[B], dots[B];  // dots: sum of p f with the factors of the token's sequence
@@ -671,7 +679,7 @@ __global__ __launch_bounds__(256) void k_router_grad(RouterGradParams p) {
     store_row<PER>(out, E, g);
     // the selected experts again, with both parts (the wave's stores to an
     // address keep their order)
-    if (live_row && chosen && lane / 16 == b && id >= 0)
+    if (live_row && chosen && lane / 16 == b && id >= 0 && first)
       out[id] = (losses ? __expf(xj - m[b]) * inv[b] * ((fj - dots[b]) + lz[b]) : 0.0f) + sel;
   }
 }

@@ -385,3 +385,35 @@ def test_captured_training_step_replays():
             assert np.array_equal(x, y)
         step()  # eager work between replays
     del graph
+
+
+@pytest.mark.parametrize("E,k", [(16, 6), (300, 16), (1024, 3)])
+def test_repeated_ids_are_summed_in_slot_order(E, k):
+    """A token that selects one expert in several slots: their terms, added in the
+    slots' order, bit for bit.  A slot's term is what it gives with other ids."""
+    import torch
+
+    import mixed_precision_moe_topk_amd as M
+
+    T = 203
+    rng = np.random.default_rng(E)
+    logits, ids, w = _routing(81, T, E, k)
+    dw = rng.standard_normal((T, k)).astype(np.float32)
+    d = M.LayerDims(E, 256, 512)
+
+    def grad(ids):
+        out = torch.full((T, E), np.nan, device="cuda")
+        M.router_backward(d, _dev(logits), _dev(ids), out, weights=_dev(w), dweights=_dev(dw))
+        return out.cpu().numpy()
+
+    term = np.take_along_axis(grad(ids), ids, axis=1)
+    same = rng.integers(0, 3, (T, k)).astype(np.int32) * 5 % E
+    want = np.zeros((T, E), np.float32)
+    for t in range(T):
+        for e in set(same[t].tolist()):
+            slots = np.nonzero(same[t] == e)[0]
+            want[t, e] = term[t, slots[0]]
+            for j in slots[1:]:
+                want[t, e] = np.float32(want[t, e] + term[t, j])
+    other = grad(same) != want
+    assert not other.any(), int(other.sum())
