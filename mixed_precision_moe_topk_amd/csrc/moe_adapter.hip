@@ -853,6 +853,7 @@ __global__ __launch_bounds__(256, JOINED ? (RT == 1 && sizeof(T) == 2 ? 4 : RT <
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = base ? v[i].get(j) + acc[j][i] : acc[j][i];
       o[i].set(f);
+      if (!low && base) o[i] = v[i];  // as it is: -0 + 0 would be 0
       t[i] = tn[i];
     }
     // (a wait for reads waits for the stores issued before them as well)

@@ -1,5 +1,5 @@
 """Low-rank adapters on the GPU at values where the bf16 parts of a float32 could
-show: full mantissas."""
+show: full mantissas, signed zeros."""
 import numpy as np
 import pytest
 
@@ -72,3 +72,26 @@ def test_float32_results_keep_24_bits(T, which, out):
         assert np.all(np.abs(r["out"] - o) <= 2.0 ** -23 * np.abs(o))
     assert np.all(np.abs(r["da"] - da) <= tol * np.abs(da))
     assert np.all(np.abs(r["db"] - db) <= tol * np.abs(db))
+
+
+@pytest.mark.parametrize("T", PATHS)
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_rows_without_an_adapter_are_their_base(T, out):
+    """The same bits: negative zeros, the smallest numbers, infinities; NaN stays
+    NaN; 0 without a base."""
+    K, N = 72, 136
+    c = Case(T, 2, 3, K, N, out, lambda rng, T, L: np.where(np.arange(T) % 3 == 1, -1, np.arange(T) % 2), 5)
+    tiny = np.float32(2.0 ** -133)  # the smallest bf16
+    special = np.float32([-0.0, 0.0, tiny, -tiny, np.inf, -np.inf, np.nan, np.finfo(np.float32).tiny])
+    off = c.ids < 0
+    c.base[off, :8] = special
+    c.dxb[off, 8:16] = special
+    for place in ("given", "in place"):
+        r = c.run(base=place, dx="base" if place == "given" else place)
+        for got, want in ((r["out"][off], c.base[off]), (r["dx"][off], c.dxb[off])):
+            nan = np.isnan(want)
+            assert np.all(np.isnan(got[nan])) and nan.any()
+            other = got[~nan].view(np.uint32) != want[~nan].view(np.uint32)
+            assert not other.any(), int(other.sum())
+    r = c.run(base="none", dx="none")
+    assert not r["out"][off].view(np.uint32).any() and not r["dx"][off].view(np.uint32).any()
