@@ -529,8 +529,8 @@ moe_status moe_adapter_saved_query(const moe_adapter_dims* dims, int64_t num_tok
  *   x:     device bf16 [num_tokens, in_features], x_stride elements between
  *          rows (all strides: multiples of 8, at least the features)
  *   plan:  of the same num_adapters and num_tokens.  (With a buffer that holds
- *          another plan the results are undefined, but no access leaves the
- *          given buffers.)
+ *          another plan, or anything else, the results are undefined, but no
+ *          access leaves the given buffers.)
  *   scale: device float [num_adapters]
  *   base:  device [num_tokens, out_features] of out_type; may be out (with the
  *          same stride); null: 0

@@ -252,14 +252,12 @@ hipError_t launch_adapter_plan(const PlanParams& p, const PlanLayout& l, hipStre
 }
 
 // ---------------------------------------------------------------- operands
-// Tile i of the plan; false behind the last one, and for an entry that a plan
-// of these sizes cannot hold (a buffer that was never planned).
+// Tile i of the plan; false behind the last one, and for one that the plan
+// cannot hold.
 __device__ __forceinline__ bool plan_tile(const PlanView& v, int64_t i, Tile* t) {
   if (i >= v.max_tiles || i >= v.head[0]) return false;
   *t = v.tiles[i];
-  return (uint32_t)t->expert <= (uint32_t)v.adapters && t->nrows >= 1 &&
-         t->nrows <= kAdapterTile && t->row0 >= 0 && t->row0 % kAdapterPad == 0 &&
-         t->row0 + (t->nrows + kAdapterPad - 1) / kAdapterPad * kAdapterPad <= v.max_rows;
+  return plan_tile_fits(*t, v.adapters, v.max_rows);
 }
 // Token of a row, -1 for padding.
 __device__ __forceinline__ int64_t plan_token(const PlanView& v, int64_t row) {

@@ -94,6 +94,14 @@ struct PlanLayout {
   }
 };
 
+// Whether a plan of these sizes can hold the tile: a buffer that was never
+// planned, or for another batch, may hold any words.
+__host__ __device__ inline bool plan_tile_fits(const Tile& t, int32_t adapters, int64_t max_rows) {
+  return t.expert >= 0 && t.expert <= adapters && t.nrows >= 1 && t.nrows <= kAdapterTile &&
+         t.row0 >= 0 && t.row0 % kAdapterPad == 0 &&
+         (int64_t)t.row0 + (t.nrows + kAdapterPad - 1) / kAdapterPad * kAdapterPad <= max_rows;
+}
+
 struct PlanParams {
   const int32_t* adapter_ids;  // [T]
   int64_t tokens;
