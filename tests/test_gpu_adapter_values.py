@@ -1,5 +1,6 @@
 """Low-rank adapters on the GPU at values where the bf16 parts of a float32 could
-show: full mantissas, signed zeros."""
+show: full mantissas, the largest floats, signed
+zeros."""
 import numpy as np
 import pytest
 
@@ -95,3 +96,26 @@ def test_rows_without_an_adapter_are_their_base(T, out):
             assert not other.any(), int(other.sum())
     r = c.run(base="none", dx="none")
     assert not r["out"][off].view(np.uint32).any() and not r["dx"][off].view(np.uint32).any()
+
+
+@pytest.mark.parametrize("T", PATHS)
+def test_the_largest_floats_stay_finite(T):
+    """Values that round up to an infinite bf16 (from 511 / 512 of 2^128 on): as a
+    scale, hence a low-rank row, and as elements of dout."""
+    top = np.finfo(np.float32).max
+    c = Diagonal(T, "f32", [top, -top, np.float32(3.397e38)], np.ones(T))
+    c.b *= np.float32(2.0 ** -30)
+    r = c.run(base="none", dx="none")
+    o, da, db = c.wants()
+    assert np.all(np.abs(r["out"] - o) <= 2.0 ** -23 * np.abs(o))
+    assert np.all(np.abs(r["da"] - da) <= 2.0 ** -23 * np.abs(da))
+    assert np.all(np.abs(r["db"] - db) <= 2.0 ** -23 * np.abs(db))
+    c = Diagonal(T, "f32", [0.25, -0.25, 0.125], np.where(np.arange(T) % 2, top, -top))
+    c.b *= np.float32(0.25)
+    r = c.run(base="none", dx="none")
+    o, da, db = c.wants()
+    assert np.all(np.abs(r["da"] - da) <= 2.0 ** -23 * np.abs(da))
+    assert np.all(np.abs(r["db"] - db) <= 2.0 ** -23 * np.abs(db))
+    dx = np.zeros((T, T))
+    dx += (c.scale.astype(np.float64)[c.ids] * np.diag(c.dout).astype(np.float64) * c.b[0, 0])[:, None]
+    assert np.all(np.abs(r["dx"] - dx) <= (2.0 ** -8 + 2.0 ** -16) * np.abs(dx))
