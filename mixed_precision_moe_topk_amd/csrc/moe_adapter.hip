@@ -24,6 +24,15 @@
 // parts hold v to 2^-18 and serve bf16 results, three hold all of a float32 and
 // serve float32 results (the factors' gradients, float32 out).  A single bf16
 // part would cost 2^-9.
+//
+// An infinity in the operand opposite the parts would meet parts of both signs
+// and zeros, whose sum is NaN where v times the infinity is infinite.  The first
+// part alone has v's sign and zeros (but for v below 2^-126, which counts as 0
+// there).  So where a wave's sums are not all finite they are taken again: expand
+// lets only the first parts meet a factor's infinities, shrink of float32 rows
+// and outer take the sums of the first parts alone where both are not finite.
+// Looking at the sums costs at most 1 us of a launch; a batch trained on an
+// infinity or on NaN throughout takes two to four times as long.
 #include <type_traits>
 
 #include "moe_train.h"
@@ -336,6 +345,29 @@ __device__ __forceinline__ v4f mfma_bf16(const v8bf& a, const v8bf& b, const v4f
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
+// Infinities and NaN as 0.
+__device__ __forceinline__ v8bf clear_infinite(const v8bf& v) {
+  v4u w = __builtin_bit_cast(v4u, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)  // an exponent of ones carries into the sign's place
+    w[i] &= ~(((w[i] & 0x7F807F80u) + 0x00800080u >> 15 & 0x00010001u) * 0xFFFFu);
+  return __builtin_bit_cast(v8bf, w);
+}
+
+// Whether any of this lane's sums is infinite or NaN (or their total is beyond
+// the floats: then a second look finds nothing).
+template <int N>
+__device__ __forceinline__ bool any_infinite(const v4f (&acc)[N]) {
+  v4f t = acc[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) t += acc[i];
+  return !__builtin_isfinite(t[0] + t[1] + (t[2] + t[3]));
+}
+// A sum of all parts' products, given that of the first parts'.
+__device__ __forceinline__ float or_first(float all, float first) {
+  return __builtin_isfinite(all) || __builtin_isfinite(first) ? all : first;
+}
+
 // Sums the accumulators of a block's WAVES waves into wave 0's: the upper half
 // of the waves hands its sums to the lower half until one is left.  red holds
 // WAVES / 2 x N x 64 entries.
@@ -462,38 +494,54 @@ __device__ __forceinline__ void shrink_direct(const ShrinkParams& p, const Tile&
   // is the memory's latency, a few times over
   constexpr int U = FEW && !F32 && RT <= 2 ? 4 : FEW && !F32 && RT <= 4 ? 2 : 1;
   constexpr int STEP = FEW ? 256 : 64;
-  for (int k = k0 + (FEW ? 64 * w : 0); k < ke; k += U * STEP) {
-    v8bf a[U][2][RT], x[U][2][F32 ? 3 : 1];
+  const auto add = [&](auto parts, v4f (&sum)[RT]) {
+    constexpr int PARTS = decltype(parts)::value;
+    for (int k = k0 + (FEW ? 64 * w : 0); k < ke; k += U * STEP) {
+      v8bf a[U][2][RT], x[U][2][PARTS];
 #pragma unroll
-    for (int q = 0; q < U; ++q)
+      for (int q = 0; q < U; ++q)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int at = k + q * STEP + 32 * h;  // (x and w point at the lane's 8 elements)
-        const bool in = at + 8 * g < ke;
-        const int from = in ? at : ke - 8 - 8 * g;
+        for (int h = 0; h < 2; ++h) {
+          const int at = k + q * STEP + 32 * h;  // (x and w point at the lane's 8 elements)
+          const bool in = at + 8 * g < ke;
+          const int from = in ? at : ke - 8 - 8 * g;
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          a[q][h][r] = load_bf16x8(wp[r] + from, true);
-          a[q][h][r] = in ? a[q][h][r] : v8bf{};
+          for (int r = 0; r < RT; ++r) {
+            a[q][h][r] = load_bf16x8(wp[r] + from, true);
+            a[q][h][r] = in ? a[q][h][r] : v8bf{};
+          }
+          if constexpr (F32) {
+            float v[8];
+            load_f32x8(xp + from, true, v);
+            split8<PARTS>(v, x[q][h]);
+          } else {
+            x[q][h][0] = load_bf16x8(xp + from, true);
+          }
+#pragma unroll
+          for (int n = 0; n < PARTS; ++n) x[q][h][n] = in ? x[q][h][n] : v8bf{};
         }
-        if constexpr (F32) {
-          float v[8];
-          load_f32x8(xp + from, true, v);
-          split8<3>(v, x[q][h]);
-        } else {
-          x[q][h][0] = load_bf16x8(xp + from, true);
-        }
 #pragma unroll
-        for (int n = 0; n < (F32 ? 3 : 1); ++n) x[q][h][n] = in ? x[q][h][n] : v8bf{};
-      }
+      for (int q = 0; q < U; ++q)
 #pragma unroll
-    for (int q = 0; q < U; ++q)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+          for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
+            for (int n = PARTS - 1; n >= 0; --n) sum[r] = mfma_bf16(a[q][h][r], x[q][h][n], sum[r]);
+    }
+  };
+  add(std::integral_constant<int, F32 ? 3 : 1>(), acc);
+  if constexpr (F32) {
+    if (__any(any_infinite(acc))) {
+      v4f first[RT];
 #pragma unroll
-          for (int n = F32 ? 2 : 0; n >= 0; --n) acc[r] = mfma_bf16(a[q][h][r], x[q][h][n], acc[r]);
+      for (int r = 0; r < RT; ++r) first[r] = v4f{0.f, 0.f, 0.f, 0.f};
+      add(std::integral_constant<int, 1>(), first);
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[r][c] = or_first(acc[r][c], first[r][c]);
+    }
   }
   if constexpr (FEW) join_waves<4>(acc, red);
 }
@@ -719,6 +767,72 @@ __device__ __forceinline__ void put_saved(const ExpandParams& p, const Tile& til
   }
 }
 
+// The steps of a wave's columns whose sums are not finite (bits of steps): as in
+// expand, but only the first parts of the rows meet a factor's infinities.  It
+// reads everything anew: rarely run, it must not hold registers where it is not.
+template <typename T, bool JOINED, typename Row8, int PARTS>
+__device__ __forceinline__ void expand_again(const ExpandParams& p, const Tile& tile, uint32_t steps, int n0, int slots,
+                                             float scale) {
+  int lane = lane_id();
+  asm volatile("" : "+v"(lane));  // nothing of this is computed ahead
+  const int l16 = lane & 15, g = lane >> 4;
+  const bool in = n0 + 8 * l16 < p.N;
+  const int n = in ? n0 + 8 * l16 : 0;
+#pragma unroll 1
+  for (int m = 0; m < kAdapterTile / 16; ++m) {
+    if (!(steps >> m & 1)) continue;
+    v4f acc[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int r = 0; 32 * r < p.rank_pad; ++r) {
+      const int rank = 32 * r + 8 * g;
+      v8bf row[PARTS], col[8];
+      if constexpr (JOINED) {
+        const uint16_t* f = p.frag + frag_block(tile.row0 / 16 + m, p.rank_pad32, r, PARTS, 0) + lane * 8;
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) row[q] = load_bf16x8(f + 512 * q, true);
+      } else {
+        const float* s = p.part + (int64_t)(tile.row0 + min(16 * m + l16, tile.nrows - 1)) * p.rank_pad + rank;
+        float u[8] = {}, x[8];
+#pragma unroll 1
+        for (int q = 0; q < slots; ++q) {
+          load_f32x8(s + q * (p.plan.max_rows * p.rank_pad), rank < p.rank_pad, x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) u[i] += x[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] *= scale;
+        split8<PARTS>(u, row);
+      }
+      uint32_t raw[8][4];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        load_words<4>(p.w + ((int64_t)tile.expert * p.rank + rank + i) * p.N + n, rank + i < p.rank, raw[i]);
+      transpose8<4>(raw, col);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const v8bf rest = clear_infinite(col[j]);
+#pragma unroll
+        for (int q = PARTS - 1; q >= 0; --q) acc[j] = mfma_bf16(row[q], q > 0 ? rest : col[j], acc[j]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = 16 * m + 4 * g + i;
+      if (!in || at >= tile.nrows) continue;
+      const int64_t t = max((int64_t)0, plan_token(p.plan, tile.row0 + at));
+      float f[8];
+      Row8 v;
+      if (p.base) v.load(static_cast<const T*>(p.base) + t * p.base_stride + n);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = p.base ? v.get(j) + acc[j][i] : acc[j][i];
+      v.set(f);
+      v.store(static_cast<T*>(p.out) + t * p.out_stride + n);
+    }
+  }
+}
+
 // A wave's 128 columns of a tile.  The factor's columns stay in registers, as
 // matrix operands of all its ranks, while the tile's row blocks pass: lane
 // (l16, g) holds columns 8 l16 + j, which are column l16 of matrix j, and of
@@ -732,7 +846,7 @@ __device__ __forceinline__ void put_saved(const ExpandParams& p, const Tile& til
 // the last one's stores); 64 tokens of 64 adapters, rank 32: 7.6 us (32 MB), one
 // token 5.1.
 template <int RT, typename T, bool JOINED>
-__global__ __launch_bounds__(256, JOINED ? (RT == 1 && sizeof(T) == 2 ? 4 : RT <= 2 ? 3 : 2) : 1) void k_adapter_expand(ExpandParams p) {
+__global__ __launch_bounds__(256, JOINED ? (RT == 1 && sizeof(T) == 2 ? 4 : RT <= 2 ? 3 : 2) : RT == 1 && sizeof(T) == 2 ? 3 : 1) void k_adapter_expand(ExpandParams p) {
   constexpr int PARTS = sizeof(T) == 4 ? 3 : 2;
   typedef std::conditional_t<sizeof(T) == 4, Row8F32, Row8Bf16> Row8;
   // neighbouring blocks on one XCD (block b runs on XCD b % 8), columns first:
@@ -809,6 +923,7 @@ __global__ __launch_bounds__(256, JOINED ? (RT == 1 && sizeof(T) == 2 ? 4 : RT <
   const float scale = low && !JOINED ? p.scale[tile.expert] : 0.0f;
   const int slots = low && !JOINED
                         ? min(shrink_slots(shrink_runs(p.plan, p.shape), ti), kMaxSlots) : 0;
+  uint32_t again = 0;  // bit m: a step with sums that are not finite, which is left for expand_again
 #pragma unroll 1
   for (int m = m0; 16 * m < tile.nrows; m += p.row_blocks) {
     if (!AHEAD) load_base(m);
@@ -844,6 +959,8 @@ __global__ __launch_bounds__(256, JOINED ? (RT == 1 && sizeof(T) == 2 ? 4 : RT <
           for (int j = 0; j < 8; ++j) acc[j] = mfma_bf16(a[r][q], b[r][j], acc[j]);
       }
     }
+    const bool odd = low && __any(any_infinite(acc));
+    again |= odd << m;
     const int next = m + p.row_blocks;
     const bool more = AHEAD && 16 * next < tile.nrows;
     if (more) ahead(next);
@@ -861,8 +978,9 @@ __global__ __launch_bounds__(256, JOINED ? (RT == 1 && sizeof(T) == 2 ? 4 : RT <
     if (more) load_base(next);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (in && 16 * m + 4 * g + i < tile.nrows) o[i].store(out + t[i] * (int64_t)p.out_stride + n);
+      if (in && !odd && 16 * m + 4 * g + i < tile.nrows) o[i].store(out + t[i] * (int64_t)p.out_stride + n);
   }
+  if (again) expand_again<T, JOINED, Row8, PARTS>(p, tile, again, n0, slots, scale);
 }
 
 template <typename T, bool JOINED>
@@ -964,6 +1082,55 @@ __device__ __forceinline__ bool outer_segment(const OuterParams& p, int64_t j, O
     several += __popcll(many);
   }
   return false;
+}
+
+// A wave's sums again, from the first parts alone and straight from memory: where
+// neither is finite the first parts' takes the stored one's place.
+template <bool F32, int TW, int RW>
+__device__ __forceinline__ void outer_again(const OuterParams& p, const OuterSide& s, const OuterSegment& seg, float* grad,
+                                            int c0) {
+  typedef std::conditional_t<F32, float, uint16_t> X;
+  int thread = threadIdx.x;
+  asm volatile("" : "+v"(thread));  // nothing of this is computed ahead, where it would hold registers
+  const int l16 = thread & 15, g = thread / 16 % 4, r0 = thread / 256 * RW;
+  c0 += thread / kWave % 4 * 16 * TW;
+  const int64_t M = p.plan.max_rows;
+#pragma unroll 1
+  for (int i = 0; i < TW * RW; ++i) {
+    const int c = c0 + l16 * TW + i % TW, r = 16 * (r0 + i / TW);
+    float all[4];
+    bool odd = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int rank = r + 4 * g + k;
+      all[k] = c < s.C && rank < p.rank ? grad[(int64_t)rank * s.C + c] : 0.0f;
+      odd |= !__builtin_isfinite(all[k]);
+    }
+    if (!__any(odd)) continue;
+    const X* x = static_cast<const X*>(s.x) + min(c, s.C - 1);
+    const uint16_t* saved = s.saved + min(r + l16, p.rank_pad - 1) * M;
+    v4f first = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int64_t row = seg.row + 8 * g; row - 8 * g < seg.end; row += 32) {
+      const bool in = row < seg.end;  // (segments are whole pieces of 16 rows)
+      v8bf q;
+      int64_t t[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) t[k] = in ? plan_token(p.plan, row + k) : -1;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const X v = x[max(t[k], (int64_t)0) * s.x_stride];
+        __bf16 part[1];
+        if constexpr (F32) split_bf16<1>(v, part);
+        else part[0] = __builtin_bit_cast(__bf16, v);
+        q[k] = t[k] < 0 ? (__bf16)0.0f : part[0];
+      }
+      first = mfma_bf16(load_bf16x8(saved + row, in), q, first);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (!__builtin_isfinite(all[k])) grad[(int64_t)(r + 4 * g + k) * s.C + c] = or_first(all[k], first[k]);
+  }
 }
 
 // Sums of one block's columns [c0, c0 + CB) of a factor.  Each thread reads W
@@ -1115,17 +1282,22 @@ __device__ __forceinline__ void outer_block(const OuterParams& p, const OuterSid
   // lane: TW columns of ranks 4 g .. 4 g + 3 of a rank block
   typedef float vec __attribute__((ext_vector_type(TW)));
   const int c = c0 + (w * 16 + l16) * TW;
-  if (c >= s.C) return;
+  if (c < s.C) {
 #pragma unroll
-  for (int r = 0; r < RW; ++r)
+    for (int r = 0; r < RW; ++r)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int q = 16 * (r0 + r) + 4 * g + i;
-      vec v;
+      for (int i = 0; i < 4; ++i) {
+        const int q = 16 * (r0 + r) + 4 * g + i;
+        vec v;
 #pragma unroll
-      for (int t = 0; t < TW; ++t) v[t] = acc[t][r][i];
-      if (q < p.rank) *reinterpret_cast<vec*>(grad + (int64_t)q * s.C + c) = v;
-    }
+        for (int t = 0; t < TW; ++t) v[t] = acc[t][r][i];
+        if (q < p.rank) *reinterpret_cast<vec*>(grad + (int64_t)q * s.C + c) = v;
+      }
+  }
+  bool odd = false;
+#pragma unroll
+  for (int t = 0; t < TW; ++t) odd |= any_infinite(acc[t]);
+  if (__any(odd)) outer_again<F32, TW, RW>(p, s, seg, grad, c0);
 }
 
 // Block (columns of either factor, segment).  Both factors in one launch: the

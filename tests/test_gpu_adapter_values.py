@@ -1,11 +1,11 @@
 """Low-rank adapters on the GPU at values where the bf16 parts of a float32 could
-show: full mantissas, the largest floats, signed
-zeros."""
+show: full mantissas, infinities, the largest floats, signed zeros."""
 import numpy as np
 import pytest
 
 from oracle import formats as F
-from tests.test_gpu_adapter import Case, each
+from oracle import train as OT
+from tests.test_gpu_adapter import Case, each, one
 
 pytestmark = pytest.mark.gpu
 
@@ -119,3 +119,42 @@ def test_the_largest_floats_stay_finite(T):
     dx = np.zeros((T, T))
     dx += (c.scale.astype(np.float64)[c.ids] * np.diag(c.dout).astype(np.float64) * c.b[0, 0])[:, None]
     assert np.all(np.abs(r["dx"] - dx) <= (2.0 ** -8 + 2.0 ** -16) * np.abs(dx))
+
+
+INFINITE = ["x", "a", "b", "dout"]
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("T,L,R", [(40, 3, 2), (40, 3, 70), (700, 2, 20), (700, 3, 100), (1100, 1, 40), (3, 3, 1)])
+@pytest.mark.parametrize("where", INFINITE)
+def test_infinities_in_every_operand(where, T, L, R, out):
+    """An infinite element of x, of a factor or of dout: infinities and NaN where
+    the float64 definition has them, with its signs, in the results and in all
+    gradients; everything else the same bits as without it."""
+    K, N = 264, 200
+    c = Case(T, L, R, K, N, out, one if L == 1 else each, 77)
+    clean = c.run()
+    last = L - 1
+    t = int(np.nonzero(c.ids == last)[0][-1])
+    if where == "x":
+        c.x[t, 9] = np.inf
+    elif where == "a":
+        c.a[last, R // 2, 130] = -np.inf
+    elif where == "b":
+        c.b[last, R - 1, 17] = np.inf
+        c.b[last, 0, 199] = -np.inf
+    else:
+        c.dout[t, 63] = -np.inf
+    r = c.run()
+    f = lambda v: v.astype(np.float64)  # noqa: E731
+    with np.errstate(invalid="ignore"):
+        x, a, b, s, d = f(c.x), f(c.a), f(c.b), f(c.scale), f(c.dout)
+        ref = {"out": OT.adapter_apply(x, c.ids, a, b, s, f(c.base))}
+        ref["dx"], ref["da"], ref["db"] = OT.adapter_backward(d, x, c.ids, a, b, s, f(c.dxb))
+    assert any(np.isinf(v).any() for v in ref.values())
+    for k in r:
+        fin = np.isfinite(ref[k])
+        other = ~((r[k] == ref[k]) | np.isnan(r[k]) & np.isnan(ref[k]))[~fin]
+        assert not other.any(), (k, int(other.sum()), int((~fin).sum()))
+        changed = (r[k] != clean[k])[fin]
+        assert not changed.any(), (k, int(changed.sum()))
