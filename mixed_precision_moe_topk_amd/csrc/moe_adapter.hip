@@ -274,20 +274,19 @@ __device__ __forceinline__ int64_t plan_token(const PlanView& v, int64_t row) {
   return t < v.tokens ? t : -1;
 }
 
-// v as a sum of N bf16 parts; an infinite v leaves the others 0, and a finite one
-// that would round up to infinity (from 2^128 - 2^119 on) is cut instead.  No
-// product is fused into the differences: the parts are those of the rounded v
-// wherever they are made.
+// v as a sum of N bf16 parts; the first part of an infinity or NaN is all of it,
+// and that of a finite v stays finite (from 2^128 - 2^119 on the nearest bf16 is
+// infinite).  No product is fused into the differences: the parts are those of
+// the rounded v wherever they are made.
 template <int N>
 __device__ __forceinline__ void split_bf16(float v, __bf16 (&part)[N]) {
 #pragma clang fp contract(off)
-  part[0] = (__bf16)v;
-  // (an infinity or a NaN is the same cut; NaN is not infinite)
-  if (__builtin_isinf((float)part[0])) part[0] = (__bf16)__uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
-  const bool inf = __builtin_isinf((float)part[0]);
+  constexpr float kTop = 0x1.FEp127f;  // the largest bf16
+  const bool finite = __builtin_isfinite(v);
+  part[0] = (__bf16)(finite ? __builtin_amdgcn_fmed3f(v, -kTop, kTop) : v);
 #pragma unroll
   for (int i = 1; i < N; ++i) {
-    v = inf ? 0.0f : v - (float)part[i - 1];
+    v = finite ? v - (float)part[i - 1] : 0.0f;
     part[i] = (__bf16)v;
   }
 }
