@@ -123,8 +123,7 @@ __device__ int32_t plan_scan(const PlanParams& p, const PlanLayout& l, int32_t n
     if (e == G - 1) {  // the group without an adapter comes last
       p.plan[l.first + G] = row0 + pad;
       p.plan[0] = tile0 + nt;
-      p.plan[1] = row0 + pad;
-      p.plan[2] = tile0;
+      p.plan[1] = tile0;
     }
   }
   return row0;
@@ -454,7 +453,7 @@ struct ShrinkRuns {
 __device__ __forceinline__ ShrinkRuns shrink_runs(const PlanView& v, const ShrinkShape& s) {
   ShrinkRuns r;
   r.units = s.units;
-  const int64_t tiles = max(0, min(v.head[2], (int32_t)v.max_tiles));
+  const int64_t tiles = max(0, min(v.head[1], (int32_t)v.max_tiles));
   r.total = tiles * s.units;
   const int64_t each = (r.total + kShrinkBlocks - 1) / kShrinkBlocks;
   r.run = (int32_t)max((int64_t)s.min_run, each);

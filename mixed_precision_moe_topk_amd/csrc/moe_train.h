@@ -71,7 +71,7 @@ constexpr int kPlanGroup = 1024;     // tokens per block of the plan kernels
 constexpr int kPlanOne = 8 * kPlanGroup;  // tokens planned in one launch
 
 // Plan of a batch: its tokens grouped by adapter.  Int32 words:
-//   head [4]: tiles, padded rows, tiles of tokens with an adapter (the first)
+//   head [2]: tiles, and how many of them, the first, hold tokens with an adapter
 //   first [L + 2]: first row of each group (multiples of kAdapterPad); group L
 //                  holds the tokens without an adapter
 //   rows [max_rows]: token of each row, -1 in the padding behind a group
