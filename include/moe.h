@@ -477,7 +477,8 @@ moe_status moe_router_backward(const moe_dims* dims, const float* router_logits,
  *   dweights: device float [num_tokens, top_k] out
  *   dy2:      device out [num_tokens * top_k, hidden], float or bf16 bits by
  *             dy2_type (moe_type; rounded once, to nearest even), or null when
- *             not wanted; float dy2 may be y2
+ *             not wanted; float dy2 may be y2.  The gradient ends here: no
+ *             call takes it back through the packed experts
  * num_tokens = 0 returns MOE_OK without launching.  Errors as moe_run_ws, and
  * MOE_ERR_INVALID_ARG when num_tokens * hidden / 4 reaches about 2^32 (one
  * launch holds fewer threads). */
@@ -557,6 +558,9 @@ moe_status moe_adapter_apply(const moe_adapter_dims* dims, const void* x, int64_
  *                                        dx_base[t]
  *   da[a] = sum over its tokens of v[t]^T x[t]
  *   db[a] = sum over its tokens of scale[a] * (x[t] A_a^T)^T dout[t]
+ * (dx is the adapters' part alone: that of the projection they stand beside
+ * comes in as dx_base.)  Parts as in moe_adapter_apply: two of v for dx, three of
+ * the low-rank rows and of a float dout for da and db.
  *   dout:   device [num_tokens, out_features] of out_type
  *   saved:  as moe_adapter_apply wrote it (with da and db)
  *   da, db: device float [num_adapters, rank, in_features] and [num_adapters,

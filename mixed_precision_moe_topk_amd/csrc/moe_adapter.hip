@@ -16,14 +16,17 @@
 //
 // Bound by memory but for the smallest batches: x, base and out pass once, and
 // the products, 2 R (K + N) a token, are a few percent of the matrix cores' rate.
+// The factors' gradients take three times the products of theirs (parts, below):
+// above rank 64 the matrix cores bound them (4096 tokens, rank 128: 45 GFLOP, 37 us
+// at the 1214 TFLOP/s of a large product, against 23 us of reads).
 // What is measured below is one launch beside a projection of 7168 x 7168
 // features; a copy of 1 GiB moves 5.16 TB/s on this card.
 //
 // x and the factors are bf16, u and v float32.  Where float32 values enter a
 // matrix instruction they are split into bf16 parts, v = v0 + v1 (+ v2): two
-// parts hold v to 2^-18 and serve bf16 results, three hold all of a float32 and
+// parts hold v to 2^-17 and serve bf16 results, three hold all of a float32 and
 // serve float32 results (the factors' gradients, float32 out).  A single bf16
-// part would cost 2^-9.
+// part would cost 2^-8.
 //
 // An infinity in the operand opposite the parts would meet parts of both signs
 // and zeros, whose sum is NaN where v times the infinity is infinite.  The first
@@ -1136,8 +1139,8 @@ __device__ __forceinline__ void outer_again(const OuterParams& p, const OuterSid
 // registers into lines of 8 rows, and hands them to the block through LDS; the
 // saved values already lie so.  The waves then sum a quarter of the columns
 // each, over all rows: no partial sums to join.  F32: X is float32,
-// three bf16 parts like the saved values; products of parts whose sizes lie
-// 2^-27 or more apart are left out.
+// three bf16 parts like the saved values; the products of a second with a third
+// part (2^-25 of the term, twice) and of the third parts (2^-34) are left out.
 // Measured: 4096 tokens, rank 32, both factors: 32 us (117 MB of x and dout, 3.7
 // TB/s; rank 64: 45, 128: 72 us), beside the router (7168 and 256 float32
 // columns, rank 12) 19.5 us.  Bound by memory: without the products 3 us less, without

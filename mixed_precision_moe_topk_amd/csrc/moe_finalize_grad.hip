@@ -32,7 +32,9 @@ enum RowGrad : int { kNoRows = 0, kRowsBf16 = 1, kRowsF32 = 2 };
 // of a column group are read together, each wave a whole kilobyte of a row.  dy2
 // may be y2: a thread writes an element after it has read it.
 // Measured (hidden 7168): 16384 tokens x 6 rows, bf16 gradients: 878 us, 5.09
-// TB/s, 98 % of the copy's rate; 64 tokens x 8, float32: 6.6 us.
+// TB/s, 98 % of the copy's rate; 64 tokens x 8, float32: 6.6 us.  dweights alone
+// (the form of a training step with packed experts): 16384 x 6 432 us, 6.5 TB/s,
+// 64 x 8 3.4 us.
 template <int KC, int ROWS>
 __global__ __launch_bounds__(kGradThreads) void k_finalize_grad(const uint16_t* __restrict__ dout,
                                                        const float* __restrict__ weights,
@@ -124,7 +126,15 @@ hipError_t launch_finalize_grad(const uint16_t* dout, const float* weights, cons
                                 const int32_t* slot_row, int64_t T, int32_t k, int32_t H,
                                 float* dweights, void* dy2, bool dy2_f32, hipStream_t st) {
   if (T == 0) return hipSuccess;
-  // Few tokens: one slot a block, so that the rows spread over the CUs.
+  // Few tokens: one slot a block, so that the rows spread over the CUs (us, bf16
+  // gradients, hidden 7168, one slot and all: 64 x 8 4.9 and 10.1, 512 x 6 23.8 and
+  // 26.0, 1024 x 6 50 and 53, 2048 x 8 145 and 143; dweights alone: 512 x 6 15.7 and
+  // 14.9, 1024 x 6 37 and 29).
+  // Many: a block reads dout once for all its slots, so the fewest slots that hold
+  // top_k (4096 tokens, dweights alone: 4 of 4 79.6, of 6 80.9; 6 of 6 113.6, of 8
+  // 114.9; 16384 with bf16 gradients: 6 of 6 832, of 8 840).  Slots behind the last
+  // read row 0, from the caches: 5 of 8 102, 7 of 8 131, against 115 and 148 of
+  // all used; 9 as 8 and 1: 205, where 16 take 288.
   if (T < 1024) launch_kc<1>(dout, weights, y2, slot_row, T, k, H, dweights, dy2, dy2_f32, st);
   else if (k <= 2) launch_kc<2>(dout, weights, y2, slot_row, T, k, H, dweights, dy2, dy2_f32, st);
   else if (k <= 4) launch_kc<4>(dout, weights, y2, slot_row, T, k, H, dweights, dy2, dy2_f32, st);

@@ -30,7 +30,10 @@ extern "C" __device__ __attribute__((const)) float __ockl_wfred_add_f32(float);
 
 namespace moe {
 
-// Logits per lane: the fewest of these that hold all experts.
+// Logits per lane: the fewest of these that hold all experts; the reads behind
+// the last expert and a smaller batch cost the rest.  4096 tokens, losses and
+// gradient: 384 experts 14.2 and 7.9 us, 512: 15.3 and 8.8, 520: 18.1 and 8.9,
+// 1024: 18.7 and 10.8.
 static int per_lane(int experts) {
   return experts <= 64 ? 1 : experts <= 128 ? 2 : experts <= 256 ? 4 : experts <= 384 ? 6
        : experts <= 512 ? 8 : 16;
@@ -85,11 +88,10 @@ struct SeqCursor {
     s = lo + hits - 1;
     end = boundary(s + 1);
   }
-  // Moves to token t (ascending calls); true when the sequence changed.
-  __device__ __forceinline__ bool next() {
+  // Moves to the next sequence.
+  __device__ __forceinline__ void next() {
     ++s;
     end = boundary(s + 1);
-    return true;
   }
   __device__ __forceinline__ bool inside(int64_t t) const { return t < end && s >= 0; }
 };
@@ -121,7 +123,10 @@ constexpr int batch_of() { return PER <= 8 ? 4 : 2; }
 static_assert(kMaxTopK <= 16, "a token's selections fit 16 lanes");
 
 // exp(x - m) in place of the logits x of B tokens, their sums and largest
-// logits.  A token without a logit above -inf gets zeros and sum 0.
+// logits.  A token without a logit above -inf gets zeros and sum 0.  The hardware's
+// exp2 of a rounded product: off by at most (3 |x - m| + 4) 2^-24 relative, which
+// the largest terms feel least (losses and gradients of 4096 x 256 and 16384 x 384:
+// within 1.2e-7 and 2e-7 of their largest, like float32 exp and log).
 template <int PER, int B>
 __device__ __forceinline__ void exponentials(float (&x)[B][PER], float (&m)[B], float (&sum)[B]) {
 #pragma unroll
@@ -657,7 +662,10 @@ __global__ __launch_bounds__(256) void k_router_grad(RouterGradParams p) {
     const int64_t t = t0 + b;
     if (t >= t1) break;
     bool next = false;
-    while (t >= seq.end && seq.s + 1 < p.seqs) next = seq.next();
+    while (t >= seq.end && seq.s + 1 < p.seqs) {
+      seq.next();
+      next = true;
+    }
     if (!seq.inside(t)) continue;  // in no sequence: left as it is
     moved |= next;
     if (next && losses) factors();
