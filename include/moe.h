@@ -544,7 +544,7 @@ moe_status moe_adapter_saved_query(const moe_adapter_dims* dims, int64_t num_tok
  * for a float out, 2^-24).
  * Infinities and NaN in x, the factors, base or dout give the infinities and NaN
  * that the formulas have, here and in the gradients, and reach no other adapter
- * (a low-rank value below 2^-126 counts as 0 where it meets an infinity).
+ * (a low-rank value below 2^-126 may count as 0 where it meets an infinity).
  * num_tokens = 0 returns MOE_OK without launching.  Errors as moe_run_ws. */
 moe_status moe_adapter_apply(const moe_adapter_dims* dims, const void* x, int64_t x_stride,
                              int64_t num_tokens, const void* plan, size_t plan_bytes,

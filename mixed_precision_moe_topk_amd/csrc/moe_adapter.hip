@@ -30,7 +30,7 @@
 //
 // An infinity in the operand opposite the parts would meet parts of both signs
 // and zeros, whose sum is NaN where v times the infinity is infinite.  The first
-// part alone has v's sign and zeros (but for v below 2^-126, which counts as 0
+// part alone has v's sign and zeros (but for v below 2^-126, which may count as 0
 // there).  So where a wave's sums are not all finite they are taken again: expand
 // lets only the first parts meet a factor's infinities, shrink of float32 rows
 // and outer take the sums of the first parts alone where both are not finite.
@@ -441,7 +441,7 @@ __device__ __forceinline__ void put_low(const LowRows& o, int64_t row0, int r, c
 // sums meet in the join or in expand.
 // Measured: 4096 tokens, rank 32: 13.7 us (58.7 MB of x, 4.3 TB/s); 16384,
 // rank 64: 55 us (4.3 TB/s: every 64 rows of x read as many of the factor, from
-// L2); 64 tokens of 64 adapters, rank 32: 8.8 us (29 MB of factors, 3.3 TB/s, of
+// L2); 64 tokens of 64 adapters, rank 32: 9.4 us (29 MB of factors, 3.1 TB/s, of
 // which 3.8 us are the launch's, as one token takes).
 // Blocks a CU: two with two LDS buffers; four with one buffer took 22 and 62 us.
 __device__ __forceinline__ int64_t quotient(int64_t a, int32_t b) {  // a >= 0, b > 0
@@ -843,9 +843,9 @@ __device__ __forceinline__ void expand_again(const ExpandParams& p, const Tile& 
 // for itself, and the first columns' writes to `saved` when it is wanted: less
 // time than a launch that does it once, where rows are few.
 // Measured: 4096 tokens, rank 32: 27 us (117 MB of base and out, 4.3 TB/s);
-// 16384, rank 64: 97 us (470 MB, 4.85 TB/s; 109 us with each step's reads behind
-// the last one's stores); 64 tokens of 64 adapters, rank 32: 7.6 us (32 MB), one
-// token 5.1.
+// 16384, rank 64: 98 us (470 MB, 4.8 TB/s; 109 us with each step's reads behind
+// the last one's stores); 64 tokens of 64 adapters, rank 32: 7.2 us (32 MB; 2 us
+// more with registers for two waves a SIMD in place of three), one token 5.1.
 template <int RT, typename T, bool JOINED>
 __global__ __launch_bounds__(256, JOINED ? (RT == 1 && sizeof(T) == 2 ? 4 : RT <= 2 ? 3 : 2) : RT == 1 && sizeof(T) == 2 ? 3 : 1) void k_adapter_expand(ExpandParams p) {
   constexpr int PARTS = sizeof(T) == 4 ? 3 : 2;
@@ -1143,7 +1143,7 @@ __device__ __forceinline__ void outer_again(const OuterParams& p, const OuterSid
 // part (2^-25 of the term, twice) and of the third parts (2^-34) are left out.
 // Measured: 4096 tokens, rank 32, both factors: 32 us (117 MB of x and dout, 3.7
 // TB/s; rank 64: 45, 128: 72 us), beside the router (7168 and 256 float32
-// columns, rank 12) 19.5 us.  Bound by memory: without the products 3 us less, without
+// columns, rank 12) 19.8 us.  Bound by memory up to rank 64: without the products 3 us less, without
 // the sums' stores 3.7, a launch without rows 6.5.  Four waves that split the rows
 // and transpose straight into operands, without LDS, took 36 us: each reads the
 // saved values for 128 columns in place of 256.  Rank 64 by eight waves, 256

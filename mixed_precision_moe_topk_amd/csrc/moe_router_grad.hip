@@ -577,7 +577,7 @@ __device__ __forceinline__ float row_same(float v, int32_t key, bool& first, std
 // numbers give, then what the sequence and the selections give; with a wave for
 // so few tokens their latency is most of its life.  A batch that enters
 // another sequence reads that one's factors again.
-// Measured: 64 tokens x 256 experts 5.9 us; 16384 x 384 15.9 us (51 MB read and
+// Measured: 64 tokens x 256 experts 6.0 us; 16384 x 384 16.2 us (51 MB read and
 // written, 3.2 TB/s).
 template <int PER>
 __global__ __launch_bounds__(256) void k_router_grad(RouterGradParams p) {
