@@ -582,6 +582,123 @@ moe_status moe_adapter_backward(const moe_adapter_dims* dims, const void* dout,
                                 int64_t dx_stride, void* workspace, size_t workspace_bytes,
                                 hipStream_t stream);
 
+/* ---------------------------------------------------------------- dense block
+ * The gated feed-forward block that every token passes, beside the layer (a
+ * shared expert) or in its place (a dense layer): with w1 [2*inter, hidden] (rows
+ * [0, inter) gate, [inter, 2*inter) up) and w2 [hidden, inter], row-major as the
+ * layer's masters are,
+ *   g = x w1_gate^T, u = x w1_up^T, h = silu(g) * u, out = base + h w2^T
+ * in bf16 with gradients, or with both products in 8-bit integers.  base is what
+ * the layer gave.  Conventions as above: asynchronous on `stream`, no allocation,
+ * no synchronisation, no memset, capturable, the same bits on every run.
+ * num_tokens up to 2^26; row strides are multiples of 8 elements, at least the
+ * features and at most 2^22; hidden * inter at most 2^30.  A workspace needs no
+ * initialisation, calls that may run at the same time need their own, and one
+ * of some number of tokens serves all smaller numbers too. */
+typedef struct {
+  int32_t hidden; /* multiples of 8 up to 2^18; int8: of 16, up to 131056 */
+  int32_t inter;
+} moe_ffn_dims;
+
+/* Bytes of the workspace of moe_ffn_apply and moe_ffn_backward, and of what the
+ * forward pass saves for the backward pass (g, u and h of every token, bf16). */
+moe_status moe_ffn_workspace_query(const moe_ffn_dims* dims, int64_t num_tokens, size_t* bytes);
+moe_status moe_ffn_saved_query(const moe_ffn_dims* dims, int64_t num_tokens, size_t* bytes);
+
+/* out = base + h w2^T.
+ *   x:      device bf16 [num_tokens, hidden], x_stride elements between rows
+ *   w1, w2: device bf16, contiguous
+ *   base:   device bf16 [num_tokens, hidden]; may be out (with the same stride)
+ *           or x; null: 0
+ *   out:    device bf16 [num_tokens, hidden]; may be x (with the same stride)
+ *   saved:  device buffer of moe_ffn_saved_query bytes for the backward pass, or
+ *           null
+ * Sums are float32.  h is rounded to bf16 before the second product, out once.
+ * num_tokens = 0 returns MOE_OK without launching.  Errors as moe_run_ws. */
+moe_status moe_ffn_apply(const moe_ffn_dims* dims, const void* x, int64_t x_stride,
+                         int64_t num_tokens, const void* w1, const void* w2, const void* base,
+                         int64_t base_stride, void* out, int64_t out_stride, void* saved,
+                         size_t saved_bytes, void* workspace, size_t workspace_bytes,
+                         hipStream_t stream);
+
+/* Gradients of moe_ffn_apply.  With s = sigmoid(g) and dh = dout w2:
+ *   dg = dh u s (1 + g (1 - s)),  du = dh g s
+ *   dx = dx_base + dg w1_gate + du w1_up     (the block's part alone: that of
+ *                                  the layer beside it comes in as dx_base)
+ *   dw1 = [dg du]^T x,  dw2 = dout^T h       (sums over the tokens)
+ *   dout:  device bf16 [num_tokens, hidden]
+ *   x:     as in the forward pass (with dw1 and dw2)
+ *   saved: as moe_ffn_apply wrote it for the same tokens
+ *   dw1, dw2: device out of w1's and w2's shapes, float or bf16 bits by dw_type
+ *          (moe_type; rounded once), fully overwritten; both null when the
+ *          weights are not trained
+ *   dx:    device bf16 [num_tokens, hidden] out, or null; may be x or dout (with
+ *          the same stride)
+ *   dx_base: device bf16 [num_tokens, hidden]; may be dx (with the same stride);
+ *          null: 0
+ * Sums are float32; g, u and h are the forward pass's, rounded to bf16, and dg
+ * and du are rounded to bf16 before the products behind them.
+ * num_tokens = 0 writes zeros into dw1 and dw2, or returns MOE_OK without
+ * launching when they are null.  Errors as moe_run_ws, and MOE_ERR_INVALID_ARG
+ * when no gradient of some tokens is wanted. */
+moe_status moe_ffn_backward(const moe_ffn_dims* dims, const void* dout, int64_t dout_stride,
+                            const void* x, int64_t x_stride, int64_t num_tokens, const void* w1,
+                            const void* w2, const void* saved, size_t saved_bytes, void* dw1,
+                            void* dw2, int32_t dw_type, const void* dx_base,
+                            int64_t dx_base_stride, void* dx, int64_t dx_stride, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream);
+
+/* Rows of x (tokens, or the channels of a weight matrix) as 8-bit integers, one
+ * scale a row: scales[r] = amax / 127 (float32 division; at least 2^-126, and 1 for
+ * an all-zero row), codes[r] = x[r] / scales[r] rounded to the nearest integer,
+ * ties to even (of the exact quotient).  A row with an infinity or NaN gets scale
+ * NaN and codes 0, so that its products are NaN.
+ *   x:      device [rows, features] of x_type (moe_type), x_stride elements
+ *           between rows; features a multiple of 16 up to 131056
+ *   codes:  device int8 [rows, features] out
+ *   scales: device float [rows] out
+ * rows = 0 returns MOE_OK without launching.  Errors as moe_run_ws. */
+moe_status moe_int8_quantize(const void* x, int32_t x_type, int64_t x_stride, int64_t rows,
+                             int32_t features, void* codes, float* scales, hipStream_t stream);
+
+/* A product of 8-bit integers with a scale for each token and each channel. */
+typedef struct {
+  int32_t in_features;  /* a multiple of 16 up to 131056: int32 sums are exact */
+  int32_t out_features; /* a multiple of 8 up to 2^18 */
+  int32_t out_type;     /* moe_type of base and out */
+} moe_int8_dims;
+
+moe_status moe_int8_workspace_query(const moe_int8_dims* dims, int64_t num_tokens, size_t* bytes);
+
+/* out[t, n] = base[t, n] + scales[t] * w_scales[n] * sum_k codes[t, k] w[n, k], the
+ * sum an exact int32, the rest float32, rounded once.
+ *   codes, scales:  device int8 [num_tokens, in_features], float [num_tokens], as
+ *                   moe_int8_quantize writes them (any int8 value is allowed)
+ *   w, w_scales:    device int8 [out_features, in_features], float [out_features]
+ *   base:  device [num_tokens, out_features] of out_type; may be out (with the
+ *          same stride); null: 0
+ *   workspace: device buffer of moe_int8_workspace_query bytes (null when it is 0)
+ * num_tokens = 0 returns MOE_OK without launching.  Errors as moe_run_ws. */
+moe_status moe_int8_matmul(const moe_int8_dims* dims, const void* codes, const float* scales,
+                           int64_t num_tokens, const void* w, const float* w_scales,
+                           const void* base, int64_t base_stride, void* out, int64_t out_stride,
+                           void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+moe_status moe_ffn_int8_workspace_query(const moe_ffn_dims* dims, int64_t num_tokens,
+                                        size_t* bytes);
+
+/* moe_ffn_apply with both products in 8-bit integers: x is quantised as
+ * moe_int8_quantize does, h (float32) again, and the weights are codes and one scale
+ * a row:
+ *   w1, w1_scales: device int8 [2*inter, hidden], float [2*inter]
+ *   w2, w2_scales: device int8 [hidden, inter], float [hidden]
+ * The rest, base and out among it, as in moe_ffn_apply. */
+moe_status moe_ffn_int8_apply(const moe_ffn_dims* dims, const void* x, int64_t x_stride,
+                              int64_t num_tokens, const void* w1, const float* w1_scales,
+                              const void* w2, const float* w2_scales, const void* base,
+                              int64_t base_stride, void* out, int64_t out_stride, void* workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

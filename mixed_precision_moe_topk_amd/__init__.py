@@ -30,7 +30,10 @@ EXPORTS = ("moe_abi_version", "moe_last_error", "moe_weights_query", "moe_prepar
            "moe_set_fc2_fused", "moe_run_noalloc", "moe_router_loss_query", "moe_router_loss",
            "moe_router_backward", "moe_finalize_backward", "moe_adapter_plan_query",
            "moe_adapter_plan", "moe_adapter_workspace_query", "moe_adapter_saved_query",
-           "moe_adapter_apply", "moe_adapter_backward")
+           "moe_adapter_apply", "moe_adapter_backward", "moe_ffn_workspace_query",
+           "moe_ffn_saved_query", "moe_ffn_apply", "moe_ffn_backward", "moe_int8_quantize",
+           "moe_int8_workspace_query", "moe_int8_matmul", "moe_ffn_int8_workspace_query",
+           "moe_ffn_int8_apply")
 NOALLOC_SCRATCH_BYTES = 64 << 20  # MOE_NOALLOC_SCRATCH_BYTES
 T_BF16, T_F32 = 0, 1
 OUT_TYPE = {"bf16": T_BF16, "f32": T_F32}
@@ -51,6 +54,15 @@ class Dims(ctypes.Structure):
 class CAdapterDims(ctypes.Structure):
     _fields_ = [("num_adapters", ctypes.c_int32), ("rank", ctypes.c_int32),
                 ("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32),
+                ("out_type", ctypes.c_int32)]
+
+
+class CFfnDims(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int32), ("inter", ctypes.c_int32)]
+
+
+class CInt8Dims(ctypes.Structure):
+    _fields_ = [("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32),
                 ("out_type", ctypes.c_int32)]
 
 
@@ -83,6 +95,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         DP, AP = ctypes.POINTER(Dims), ctypes.POINTER(CAdapterDims)
+        FP, IP = ctypes.POINTER(CFfnDims), ctypes.POINTER(CInt8Dims)
         L.moe_abi_version.restype = I32
         L.moe_last_error.restype = ctypes.c_char_p
         sig = {
@@ -115,6 +128,16 @@ def lib():
             "moe_adapter_apply": [AP, P, I64, I64, P, SZ, P, P, P, P, I64, P, I64, P, SZ, P, SZ, P],
             "moe_adapter_backward": [AP, P, I64, P, I64, I64, P, SZ, P, P, P, P, SZ, P, P, P, I64,
                                      P, I64, P, SZ, P],
+            "moe_ffn_workspace_query": [FP, I64, ctypes.POINTER(SZ)],
+            "moe_ffn_saved_query": [FP, I64, ctypes.POINTER(SZ)],
+            "moe_ffn_apply": [FP, P, I64, I64, P, P, P, I64, P, I64, P, SZ, P, SZ, P],
+            "moe_ffn_backward": [FP, P, I64, P, I64, I64, P, P, P, SZ, P, P, I32, P, I64, P, I64, P,
+                                 SZ, P],
+            "moe_int8_quantize": [P, I32, I64, I64, I32, P, P, P],
+            "moe_int8_workspace_query": [IP, I64, ctypes.POINTER(SZ)],
+            "moe_int8_matmul": [IP, P, P, I64, P, P, P, I64, P, I64, P, SZ, P],
+            "moe_ffn_int8_workspace_query": [FP, I64, ctypes.POINTER(SZ)],
+            "moe_ffn_int8_apply": [FP, P, I64, I64, P, P, P, P, P, I64, P, I64, P, SZ, P],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -342,7 +365,7 @@ def _types():
     if _dtypes is None:
         import torch
 
-        _dtypes = dict(f32=(torch.float32,), i32=(torch.int32,), u8=(torch.uint8,),
+        _dtypes = dict(f32=(torch.float32,), i32=(torch.int32,), u8=(torch.uint8,), i8=(torch.int8,),
                        bf16=(torch.bfloat16, torch.int16),
                        row=(torch.float32, torch.bfloat16, torch.int16))
     return _dtypes
@@ -552,3 +575,142 @@ def adapter_backward(d: AdapterDims, dout, x, plan, a, b, scale, saved, da, db, 
         _tensor("da", da, ty["f32"], (L, R, K), dev), _tensor("db", db, ty["f32"], (L, R, N), dev),
         _tensor("dx_base", dx_base, bits, (T, K), dev, True), _stride(dx_base, K),
         _tensor("dx", dx, bits, (T, K), dev, True), _stride(dx, K), ws, room, st))
+
+
+# ---------------------------------------------------------------- dense block
+@dataclass(frozen=True)
+class FfnDims:
+    """Gated feed-forward block: w1 [2 * inter, hidden] (gate rows, then up rows),
+    w2 [hidden, inter]."""
+
+    hidden: int
+    inter: int
+
+    def c(self) -> CFfnDims:
+        return CFfnDims(self.hidden, self.inter)
+
+    @functools.cache
+    def ref(self):
+        return ctypes.byref(self.c())
+
+
+def ffn_workspace_query(d: FfnDims, num_tokens: int) -> int:
+    return _size(lib().moe_ffn_workspace_query, d.ref(), num_tokens)
+
+
+def ffn_saved_query(d: FfnDims, num_tokens: int) -> int:
+    return _size(lib().moe_ffn_saved_query, d.ref(), num_tokens)
+
+
+def ffn_apply(d: FfnDims, x, w1, w2, base, out, workspace, saved=None, stream=None):
+    """out = base + (silu(x w1_gate^T) * (x w1_up^T)) w2^T.  x, base (or None) and out
+    bf16 cuda [T, H], each with a row stride if need be (out may be base or x); w1
+    bf16 [2I, H]; w2 bf16 [H, I]; workspace: uint8 of ffn_workspace_query bytes;
+    saved: uint8 of ffn_saved_query bytes for ffn_backward."""
+    dev, st = _current(x, stream)
+    bits = _types()["bf16"]
+    T, H, I = x.shape[0], d.hidden, d.inter
+    sv, saved_room = _buffer("saved", saved, dev)
+    ws, room = _buffer("workspace", workspace, dev)
+    _check(lib().moe_ffn_apply(
+        d.ref(), _tensor("x", x, bits, (T, H), dev, True), _stride(x, H), T,
+        _tensor("w1", w1, bits, (2 * I, H), dev), _tensor("w2", w2, bits, (H, I), dev),
+        _tensor("base", base, bits, (T, H), dev, True), _stride(base, H),
+        _tensor("out", out, bits, (T, H), dev, True), _stride(out, H), sv, saved_room, ws, room,
+        st))
+
+
+def ffn_backward(d: FfnDims, dout, x, w1, w2, saved, dw1, dw2, workspace, dx=None, dx_base=None,
+                 stream=None):
+    """Gradients of ffn_apply: dw1, dw2 of the weights' shapes, both float32 or both
+    bf16 (or both None), and dx = dx_base + ... bf16 [T, H] (or None).  saved: as
+    ffn_apply left it for the same tokens."""
+    dev, st = _current(dout, stream)
+    ty = _types()
+    bits = ty["bf16"]
+    T, H, I = dout.shape[0], d.hidden, d.inter
+    kind = T_F32 if dw1 is not None and dw1.dtype in ty["f32"] else T_BF16
+    grads = ty["f32"] if kind == T_F32 else bits
+    sv, saved_room = _buffer("saved", saved, dev)
+    ws, room = _buffer("workspace", workspace, dev)
+    _check(lib().moe_ffn_backward(
+        d.ref(), _tensor("dout", dout, bits, (T, H), dev, True), _stride(dout, H),
+        _tensor("x", x, bits, (T, H), dev, True), _stride(x, H), T,
+        _tensor("w1", w1, bits, (2 * I, H), dev), _tensor("w2", w2, bits, (H, I), dev), sv,
+        saved_room, _tensor("dw1", dw1, grads, (2 * I, H), dev),
+        _tensor("dw2", dw2, grads, (H, I), dev), kind,
+        _tensor("dx_base", dx_base, bits, (T, H), dev, True), _stride(dx_base, H),
+        _tensor("dx", dx, bits, (T, H), dev, True), _stride(dx, H), ws, room, st))
+
+
+def int8_quantize(x, codes, scales, stream=None):
+    """Rows of x (bf16 or float32 cuda [R, K], row stride allowed) as codes int8
+    [R, K] and scales float32 [R]: tokens, or the channels of a weight matrix."""
+    dev, st = _current(x, stream)
+    ty = _types()
+    R, K = x.shape
+    kind = T_F32 if x.dtype in ty["f32"] else T_BF16
+    _check(lib().moe_int8_quantize(
+        _tensor("x", x, ty["row"], (R, K), dev, True), kind, _stride(x, K), R, K,
+        _tensor("codes", codes, ty["i8"], (R, K), dev),
+        _tensor("scales", scales, ty["f32"], (R,), dev), st))
+
+
+@dataclass(frozen=True)
+class Int8Dims:
+    """Product of int8 tokens with int8 weights [out_features, in_features];
+    out_type: "bf16" or "f32" (base and out)."""
+
+    in_features: int
+    out_features: int
+    out_type: str = "bf16"
+
+    def c(self) -> CInt8Dims:
+        return CInt8Dims(self.in_features, self.out_features, OUT_TYPE[self.out_type])
+
+    @functools.cache
+    def ref(self):
+        return ctypes.byref(self.c())
+
+
+def int8_workspace_query(d: Int8Dims, num_tokens: int) -> int:
+    return _size(lib().moe_int8_workspace_query, d.ref(), num_tokens)
+
+
+def int8_matmul(d: Int8Dims, codes, scales, w, w_scales, base, out, workspace, stream=None):
+    """out = base + scales * w_scales * (codes w^T).  codes int8 cuda [T, K] and scales
+    float32 [T] as int8_quantize writes them; w int8 [N, K]; w_scales float32 [N];
+    base (or None) and out [T, N] of the dims' type, row strides allowed;
+    workspace: uint8 of int8_workspace_query bytes."""
+    dev, st = _current(codes, stream)
+    ty = _types()
+    T, K, N = codes.shape[0], d.in_features, d.out_features
+    ot = ty[d.out_type]
+    ws, room = _buffer("workspace", workspace, dev)
+    _check(lib().moe_int8_matmul(
+        d.ref(), _tensor("codes", codes, ty["i8"], (T, K), dev),
+        _tensor("scales", scales, ty["f32"], (T,), dev), T, _tensor("w", w, ty["i8"], (N, K), dev),
+        _tensor("w_scales", w_scales, ty["f32"], (N,), dev),
+        _tensor("base", base, ot, (T, N), dev, True), _stride(base, N),
+        _tensor("out", out, ot, (T, N), dev, True), _stride(out, N), ws, room, st))
+
+
+def ffn_int8_workspace_query(d: FfnDims, num_tokens: int) -> int:
+    return _size(lib().moe_ffn_int8_workspace_query, d.ref(), num_tokens)
+
+
+def ffn_int8_apply(d: FfnDims, x, w1, w1_scales, w2, w2_scales, base, out, workspace, stream=None):
+    """ffn_apply with both products in 8-bit integers.  w1 int8 [2I, H], w1_scales
+    float32 [2I], w2 int8 [H, I], w2_scales float32 [H] (int8_quantize of the
+    weights); x, base (or None) and out bf16 cuda [T, H] as in ffn_apply."""
+    dev, st = _current(x, stream)
+    ty = _types()
+    bits, f32, i8 = ty["bf16"], ty["f32"], ty["i8"]
+    T, H, I = x.shape[0], d.hidden, d.inter
+    ws, room = _buffer("workspace", workspace, dev)
+    _check(lib().moe_ffn_int8_apply(
+        d.ref(), _tensor("x", x, bits, (T, H), dev, True), _stride(x, H), T,
+        _tensor("w1", w1, i8, (2 * I, H), dev), _tensor("w1_scales", w1_scales, f32, (2 * I,), dev),
+        _tensor("w2", w2, i8, (H, I), dev), _tensor("w2_scales", w2_scales, f32, (H,), dev),
+        _tensor("base", base, bits, (T, H), dev, True), _stride(base, H),
+        _tensor("out", out, bits, (T, H), dev, True), _stride(out, H), ws, room, st))

@@ -1,0 +1,69 @@
+// Launch parameters of the dense operators beside the layer: the gated block in
+// bf16 and its gradients, products in 8-bit integers, and their quantiser.
+#pragma once
+
+#include "moe_common.h"
+
+namespace moe {
+
+// What becomes of the sums of a product.
+enum DenseMode : int {
+  kDenseStore = 0,  // out = base + sum
+  kDenseGate = 1,   // columns are gate and up: out = silu(gate) * up
+  kDenseDgate = 2,  // sum is the gradient of silu(gate) * up: out = its gradients
+};
+
+struct DenseEpilogue {
+  const float* row_scale;  // int8: scale of each row (token)
+  const float* col_scale;  // int8: scale of each column (channel)
+  const void* base;        // kDenseStore: of out's type, or null
+  int64_t base_stride;     // elements between rows, as all strides here
+  void* out;               // kDenseGate: [M, inter]; kDenseDgate: bf16 [M, 2 inter]
+  int64_t out_stride;
+  int32_t out_f32;         // float32 or bf16 out
+  int32_t inter;
+  uint16_t* gu_out;        // kDenseGate: gate and up as bf16 [M, 2 inter], or null
+  const uint16_t* gu_in;   // kDenseDgate: the same
+};
+
+// Product of rows and columns over k: sum_k a(m, k) b(n, k).  An operand lies
+// either along k (element (m, k) at m * stride + k) or across it (k * stride + m).
+struct DenseGemm {
+  const uint8_t* a;
+  int64_t a_stride;  // bytes, as b_stride
+  const uint8_t* b;
+  int64_t b_stride;
+  int64_t M;         // rows
+  int32_t N;         // columns; kDenseGate: 2 inter
+  int64_t K;
+  int32_t split;     // parts of K, each summed by blocks of their own
+  int32_t steps;     // K steps (128 bytes) of a part
+  void* part;        // split > 1: sums [split, M, N], float32 or int32
+  DenseEpilogue e;
+};
+
+// Operand layouts and element types of the products.
+enum DenseKind : int {
+  kDenseNT = 0,  // bf16, both operands along k
+  kDenseNN = 1,  // bf16, b across k
+  kDenseTN = 2,  // bf16, both across k
+  kDenseI8 = 3,  // int8, both along k
+};
+
+constexpr int kDenseStepBytes = 128;  // K step of an operand row
+constexpr int dense_step(int kind) { return kind == kDenseI8 ? 128 : 64; }
+
+// Tile of a product: 256 x 256 by 8 waves or 128 x 128 by 4.
+constexpr int dense_tile(bool big) { return big ? 256 : 128; }
+
+hipError_t launch_dense_gemm_bf16(int kind, int mode, bool big, const DenseGemm& p, hipStream_t st);
+hipError_t launch_dense_gemm_int8(int mode, bool big, const DenseGemm& p, hipStream_t st);
+// Adds up the parts (split > 1) and finishes them.
+hipError_t launch_dense_join(bool int8, int mode, const DenseGemm& p, hipStream_t st);
+
+// Codes int8 [rows, cols] and scales [rows] of x, bf16 or float32, stride elements
+// between rows.
+hipError_t launch_int8_quant(const void* x, bool x_f32, int64_t x_stride, int64_t rows, int32_t cols,
+                             int8_t* codes, float* scales, hipStream_t st);
+
+}  // namespace moe

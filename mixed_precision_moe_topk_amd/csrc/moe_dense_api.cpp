@@ -1,0 +1,402 @@
+// Host side of the dense entry points of include/moe.h: argument checks, size
+// queries and launch sequences.  As in the run calls every check comes before
+// any launch, and nothing allocates or synchronises.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "../../include/moe.h"
+#include "moe_dense.h"
+#include "moe_host.h"
+
+namespace {
+
+using moe::ceil_div;
+using moe::DenseGemm;
+using moe::is_aligned16;
+using moe::set_error;
+using moe::set_errorf;
+
+constexpr int64_t kMaxTokens = (int64_t)1 << 26;
+constexpr int32_t kMaxFeatures = 1 << 18;
+// 2^31 / 128^2 less one piece: int32 sums of int8 products cannot overflow
+constexpr int32_t kMaxInt8Features = (1 << 17) - 16;
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+moe_status check_pointers(std::initializer_list<const void*> ps) {
+  for (const void* p : ps) {
+    if (!p) return set_error(MOE_ERR_INVALID_ARG, "null pointer argument");
+    if (!is_aligned16(p)) return set_error(MOE_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+  }
+  return MOE_OK;
+}
+// A pointer that may be null.
+moe_status check_optional(const void* p) {
+  return is_aligned16(p) ? MOE_OK : set_error(MOE_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+}
+moe_status check_room(size_t have, size_t need, const char* what) {
+  if (have < need)
+    return set_errorf(MOE_ERR_WORKSPACE, "%s %zu bytes < %zu required", what, have, need);
+  return MOE_OK;
+}
+moe_status check_tokens(int64_t num_tokens) {
+  if (num_tokens < 0 || num_tokens > kMaxTokens)
+    return set_errorf(MOE_ERR_INVALID_ARG, "num_tokens %lld outside [0, 2^26]", (long long)num_tokens);
+  return MOE_OK;
+}
+moe_status check_features(int32_t n, int32_t unit, int32_t limit) {
+  if (n < unit || n % unit != 0 || n > limit)
+    return set_errorf(MOE_ERR_INVALID_ARG, "%d features: a multiple of %d in [%d, %d] is needed", n, unit,
+                      unit, limit);
+  return MOE_OK;
+}
+moe_status check_type(int32_t type, const char* what) {
+  if (type != MOE_T_BF16 && type != MOE_T_F32)
+    return set_errorf(MOE_ERR_INVALID_ARG, "unknown %s type %d", what, type);
+  return MOE_OK;
+}
+// Strides in elements; a tile's rows lie within 32-bit byte offsets.
+moe_status check_stride(int64_t stride, int64_t features) {
+  if (stride < features || stride % 8 != 0 || stride > ((int64_t)1 << 22))
+    return set_errorf(MOE_ERR_INVALID_ARG,
+                      "row stride %lld: a multiple of 8 in [%lld, 2^22] is needed", (long long)stride,
+                      (long long)features);
+  return MOE_OK;
+}
+moe_status check_base(const void* base, int64_t base_stride, const void* out, int64_t out_stride,
+                      int64_t features, const char* what) {
+  MOE_RETURN_IF(check_optional(base));
+  if (!base) return MOE_OK;
+  MOE_RETURN_IF(check_stride(base_stride, features));
+  if (base == out && base_stride != out_stride)
+    return set_errorf(MOE_ERR_INVALID_ARG, "%s with another row stride", what);
+  return MOE_OK;
+}
+
+moe_status check_ffn(const moe_ffn_dims* d, int64_t num_tokens, int32_t unit, int32_t limit) {
+  if (!d) return set_error(MOE_ERR_INVALID_ARG, "dims is null");
+  MOE_RETURN_IF(check_tokens(num_tokens));
+  MOE_RETURN_IF(check_features(d->hidden, unit, limit));
+  MOE_RETURN_IF(check_features(d->inter, unit, limit));
+  if ((int64_t)d->hidden * d->inter > (int64_t)1 << 30)
+    return set_errorf(MOE_ERR_INVALID_ARG, "hidden %d x inter %d: more than 2^30 weights a matrix",
+                      d->hidden, d->inter);
+  return MOE_OK;
+}
+moe_status check_ffn_bf16(const moe_ffn_dims* d, int64_t num_tokens) {
+  return check_ffn(d, num_tokens, 8, kMaxFeatures);
+}
+moe_status check_ffn_int8(const moe_ffn_dims* d, int64_t num_tokens) {
+  return check_ffn(d, num_tokens, 16, kMaxInt8Features);
+}
+moe_status check_int8(const moe_int8_dims* d, int64_t num_tokens) {
+  if (!d) return set_error(MOE_ERR_INVALID_ARG, "dims is null");
+  MOE_RETURN_IF(check_tokens(num_tokens));
+  MOE_RETURN_IF(check_features(d->in_features, 16, kMaxInt8Features));
+  MOE_RETURN_IF(check_features(d->out_features, 8, kMaxFeatures));
+  return check_type(d->out_type, "output");
+}
+
+// ---------------------------------------------------------------- tiles and parts
+// Tiles of 256 x 256 where they are enough for the 256 CUs, else of 128 x 128,
+// two blocks a CU, with K cut into parts (of 4 steps at least) until there are
+// kFullGrid blocks.
+constexpr int64_t kFullGrid = 512, kMinPartSteps = 4, kManyTiles = 192;
+
+struct Shape {
+  bool big;
+  int32_t split, steps;
+};
+Shape dense_shape(int kind, int64_t M, int64_t N, int64_t K) {
+  const int64_t steps = ceil_div(K, moe::dense_step(kind));
+  Shape s = {ceil_div(M, 256) * ceil_div(N, 256) >= kManyTiles, 1, (int32_t)steps};
+  if (s.big) return s;
+  const int64_t tiles = ceil_div(M, 128) * ceil_div(N, 128);
+  const int64_t parts = std::min(kFullGrid / tiles, steps / kMinPartSteps);
+  if (parts > 1) {
+    s.steps = (int32_t)ceil_div(steps, parts);
+    s.split = (int32_t)ceil_div(steps, s.steps);
+  }
+  return s;
+}
+// Room for the parts of a product at any number of rows up to M and any K up to K.
+size_t part_bytes(int kind, int64_t M, int64_t N, int64_t K) {
+  const int64_t most = ceil_div(K, moe::dense_step(kind)) / kMinPartSteps;
+  if (most < 2) return 0;
+  const size_t sums = (size_t)std::min(M, kFullGrid * 128) * N * 4;
+  return align256(std::min((size_t)most * sums, (size_t)kFullGrid * 128 * 128 * 4));
+}
+
+moe_status run_product(int kind, int mode, DenseGemm g, void* parts, const char* what, hipStream_t stream) {
+  const Shape s = dense_shape(kind, g.M, g.N, g.K);
+  g.split = s.split;
+  g.steps = s.steps;
+  g.part = parts;
+  const bool int8 = kind == moe::kDenseI8;
+  MOE_RETURN_IF(moe::check_hip(int8 ? moe::launch_dense_gemm_int8(mode, s.big, g, stream)
+                                    : moe::launch_dense_gemm_bf16(kind, mode, s.big, g, stream),
+                               what, stream));
+  if (s.split > 1) MOE_RETURN_IF(moe::check_hip(moe::launch_dense_join(int8, mode, g, stream), what, stream));
+  return MOE_OK;
+}
+
+DenseGemm product(const void* a, int64_t a_stride, const void* b, int64_t b_stride, int64_t M, int64_t N,
+                  int64_t K, int element) {
+  DenseGemm g = {};
+  g.a = static_cast<const uint8_t*>(a);
+  g.a_stride = a_stride * element;
+  g.b = static_cast<const uint8_t*>(b);
+  g.b_stride = b_stride * element;
+  g.M = M;
+  g.N = (int32_t)N;
+  g.K = K;
+  return g;
+}
+void store_to(DenseGemm& g, void* out, int64_t stride, bool f32, const void* base, int64_t base_stride) {
+  g.e.out = out;
+  g.e.out_stride = stride;
+  g.e.out_f32 = f32;
+  g.e.base = base;
+  g.e.base_stride = base_stride;
+}
+
+// Workspace of the bf16 block: h or its gradients, then the parts.
+struct FfnLayout {
+  size_t gu_bytes, h_bytes, rows, part;
+  FfnLayout(const moe_ffn_dims* d, int64_t T) {
+    const int64_t H = d->hidden, I = d->inter;
+    gu_bytes = align256((size_t)T * 2 * I * 2);
+    h_bytes = align256((size_t)T * I * 2);
+    rows = gu_bytes;  // the larger of h and the gradients of gate and up
+    part = std::max({part_bytes(moe::kDenseNT, T, 2 * I, H), part_bytes(moe::kDenseNT, T, H, I),
+                     part_bytes(moe::kDenseNN, T, I, H), part_bytes(moe::kDenseNN, T, H, 2 * I),
+                     part_bytes(moe::kDenseTN, 2 * I, H, T), part_bytes(moe::kDenseTN, H, I, T)});
+  }
+  size_t workspace() const { return rows + part; }
+  size_t saved() const { return gu_bytes + h_bytes; }
+};
+
+// Workspace of the int8 block.
+struct Int8FfnLayout {
+  size_t x_scales, h, h_codes, h_scales, part, total;
+  Int8FfnLayout(const moe_ffn_dims* d, int64_t T) {
+    const int64_t H = d->hidden, I = d->inter;
+    x_scales = align256((size_t)T * H);
+    h = x_scales + align256((size_t)T * 4);
+    h_codes = h + align256((size_t)T * I * 4);
+    h_scales = h_codes + align256((size_t)T * I);
+    part = h_scales + align256((size_t)T * 4);
+    total = part + std::max(part_bytes(moe::kDenseI8, T, 2 * I, H), part_bytes(moe::kDenseI8, T, H, I));
+  }
+};
+
+size_t int8_parts(const moe_int8_dims* d, int64_t T) {
+  return part_bytes(moe::kDenseI8, T, d->out_features, d->in_features);
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_ffn_workspace_query(const moe_ffn_dims* dims, int64_t num_tokens, size_t* bytes) {
+  if (!bytes) return set_error(MOE_ERR_INVALID_ARG, "null output pointer");
+  MOE_RETURN_IF(check_ffn_bf16(dims, num_tokens));
+  *bytes = FfnLayout(dims, num_tokens).workspace();
+  return moe::set_ok();
+}
+
+moe_status moe_ffn_saved_query(const moe_ffn_dims* dims, int64_t num_tokens, size_t* bytes) {
+  if (!bytes) return set_error(MOE_ERR_INVALID_ARG, "null output pointer");
+  MOE_RETURN_IF(check_ffn_bf16(dims, num_tokens));
+  *bytes = FfnLayout(dims, num_tokens).saved();
+  return moe::set_ok();
+}
+
+moe_status moe_ffn_apply(const moe_ffn_dims* dims, const void* x, int64_t x_stride, int64_t num_tokens,
+                         const void* w1, const void* w2, const void* base, int64_t base_stride,
+                         void* out, int64_t out_stride, void* saved, size_t saved_bytes,
+                         void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  MOE_RETURN_IF(check_ffn_bf16(dims, num_tokens));
+  if (num_tokens == 0) return moe::set_ok();
+  const int64_t T = num_tokens, H = dims->hidden, I = dims->inter;
+  MOE_RETURN_IF(check_pointers({x, w1, w2, out, workspace}));
+  MOE_RETURN_IF(check_optional(saved));
+  MOE_RETURN_IF(check_stride(x_stride, H));
+  MOE_RETURN_IF(check_stride(out_stride, H));
+  MOE_RETURN_IF(check_base(base, base_stride, out, out_stride, H, "base is out"));
+  const FfnLayout l(dims, T);
+  MOE_RETURN_IF(check_room(workspace_bytes, l.workspace(), "workspace"));
+  if (saved) MOE_RETURN_IF(check_room(saved_bytes, l.saved(), "saved"));
+  MOE_RETURN_IF(moe::check_gfx950());
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* h = saved ? static_cast<uint8_t*>(saved) + l.gu_bytes : ws;
+  DenseGemm up = product(x, x_stride, w1, H, T, 2 * I, H, 2);
+  store_to(up, h, I, false, nullptr, 0);
+  up.e.inter = (int32_t)I;
+  up.e.gu_out = static_cast<uint16_t*>(saved);
+  MOE_RETURN_IF(run_product(moe::kDenseNT, moe::kDenseGate, up, ws + l.rows, "block gate and up", stream));
+  DenseGemm down = product(h, I, w2, I, T, H, I, 2);
+  store_to(down, out, out_stride, false, base, base_stride);
+  MOE_RETURN_IF(run_product(moe::kDenseNT, moe::kDenseStore, down, ws + l.rows, "block down", stream));
+  return moe::set_ok();
+}
+
+moe_status moe_ffn_backward(const moe_ffn_dims* dims, const void* dout, int64_t dout_stride,
+                            const void* x, int64_t x_stride, int64_t num_tokens, const void* w1,
+                            const void* w2, const void* saved, size_t saved_bytes, void* dw1,
+                            void* dw2, int32_t dw_type, const void* dx_base, int64_t dx_base_stride,
+                            void* dx, int64_t dx_stride, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream) {
+  MOE_RETURN_IF(check_ffn_bf16(dims, num_tokens));
+  MOE_RETURN_IF(check_type(dw_type, "gradient"));
+  if ((dw1 == nullptr) != (dw2 == nullptr))
+    return set_error(MOE_ERR_INVALID_ARG, "dw1 and dw2 are wanted together or not at all");
+  // (dx of no tokens has no address)
+  if (!dw1 && !dx && num_tokens > 0)
+    return set_error(MOE_ERR_INVALID_ARG, "neither dx nor dw1 and dw2: no gradient");
+  if (dw1) MOE_RETURN_IF(check_pointers({dw1, dw2}));
+  MOE_RETURN_IF(check_optional(dx));
+  const int64_t T = num_tokens, H = dims->hidden, I = dims->inter;
+  const FfnLayout l(dims, T);
+  if (T > 0) {
+    MOE_RETURN_IF(check_pointers({dout, w2, saved, workspace}));
+    MOE_RETURN_IF(check_stride(dout_stride, H));
+    if (dw1) {
+      MOE_RETURN_IF(check_pointers({x}));
+      MOE_RETURN_IF(check_stride(x_stride, H));
+    }
+    if (dx) {
+      MOE_RETURN_IF(check_pointers({w1}));
+      MOE_RETURN_IF(check_stride(dx_stride, H));
+      MOE_RETURN_IF(check_base(dx_base, dx_base_stride, dx, dx_stride, H, "dx_base is dx"));
+    }
+    MOE_RETURN_IF(check_room(workspace_bytes, l.workspace(), "workspace"));
+    MOE_RETURN_IF(check_room(saved_bytes, l.saved(), "saved"));
+  }
+  if (T == 0 && !dw1) return moe::set_ok();
+  MOE_RETURN_IF(moe::check_gfx950());
+  uint8_t* dgu = static_cast<uint8_t*>(workspace);
+  uint8_t* parts = T > 0 ? dgu + l.rows : nullptr;
+  const uint8_t* h = T > 0 ? static_cast<const uint8_t*>(saved) + l.gu_bytes : nullptr;
+  if (T > 0) {
+    DenseGemm dh = product(dout, dout_stride, w2, I, T, I, H, 2);
+    dh.e.out = dgu;
+    dh.e.inter = (int32_t)I;
+    dh.e.gu_in = static_cast<const uint16_t*>(saved);
+    MOE_RETURN_IF(run_product(moe::kDenseNN, moe::kDenseDgate, dh, parts, "block dh", stream));
+  }
+  // the weights' gradients first: dx may then be x or dout
+  if (dw1) {
+    const bool f32 = dw_type == MOE_T_F32;
+    DenseGemm g1 = product(dgu, 2 * I, x, T > 0 ? x_stride : H, 2 * I, H, T, 2);
+    store_to(g1, dw1, H, f32, nullptr, 0);
+    MOE_RETURN_IF(run_product(moe::kDenseTN, moe::kDenseStore, g1, parts, "block dw1", stream));
+    DenseGemm g2 = product(dout, T > 0 ? dout_stride : H, h, I, H, I, T, 2);
+    store_to(g2, dw2, I, f32, nullptr, 0);
+    MOE_RETURN_IF(run_product(moe::kDenseTN, moe::kDenseStore, g2, parts, "block dw2", stream));
+  }
+  if (dx && T > 0) {
+    DenseGemm gx = product(dgu, 2 * I, w1, H, T, H, 2 * I, 2);
+    store_to(gx, dx, dx_stride, false, dx_base, dx_base_stride);
+    MOE_RETURN_IF(run_product(moe::kDenseNN, moe::kDenseStore, gx, parts, "block dx", stream));
+  }
+  return moe::set_ok();
+}
+
+moe_status moe_int8_quantize(const void* x, int32_t x_type, int64_t x_stride, int64_t rows,
+                             int32_t features, void* codes, float* scales, hipStream_t stream) {
+  MOE_RETURN_IF(check_tokens(rows));
+  MOE_RETURN_IF(check_type(x_type, "input"));
+  MOE_RETURN_IF(check_features(features, 16, kMaxInt8Features));
+  if (rows == 0) return moe::set_ok();
+  MOE_RETURN_IF(check_pointers({x, codes, scales}));
+  MOE_RETURN_IF(check_stride(x_stride, features));
+  MOE_RETURN_IF(moe::check_gfx950());
+  MOE_RETURN_IF(moe::check_hip(
+      moe::launch_int8_quant(x, x_type == MOE_T_F32, x_stride, rows, features,
+                             static_cast<int8_t*>(codes), scales, stream),
+      "int8 quantize", stream));
+  return moe::set_ok();
+}
+
+moe_status moe_int8_workspace_query(const moe_int8_dims* dims, int64_t num_tokens, size_t* bytes) {
+  if (!bytes) return set_error(MOE_ERR_INVALID_ARG, "null output pointer");
+  MOE_RETURN_IF(check_int8(dims, num_tokens));
+  *bytes = int8_parts(dims, num_tokens);
+  return moe::set_ok();
+}
+
+moe_status moe_int8_matmul(const moe_int8_dims* dims, const void* codes, const float* scales,
+                           int64_t num_tokens, const void* w, const float* w_scales,
+                           const void* base, int64_t base_stride, void* out, int64_t out_stride,
+                           void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  MOE_RETURN_IF(check_int8(dims, num_tokens));
+  if (num_tokens == 0) return moe::set_ok();
+  const int64_t T = num_tokens, K = dims->in_features, N = dims->out_features;
+  MOE_RETURN_IF(check_pointers({codes, scales, w, w_scales, out}));
+  MOE_RETURN_IF(check_optional(workspace));
+  MOE_RETURN_IF(check_stride(out_stride, N));
+  MOE_RETURN_IF(check_base(base, base_stride, out, out_stride, N, "base is out"));
+  const size_t need = int8_parts(dims, T);
+  if (need > 0) MOE_RETURN_IF(check_pointers({workspace}));
+  MOE_RETURN_IF(check_room(workspace_bytes, need, "workspace"));
+  MOE_RETURN_IF(moe::check_gfx950());
+  DenseGemm g = product(codes, K, w, K, T, N, K, 1);
+  store_to(g, out, out_stride, dims->out_type == MOE_T_F32, base, base_stride);
+  g.e.row_scale = scales;
+  g.e.col_scale = w_scales;
+  MOE_RETURN_IF(run_product(moe::kDenseI8, moe::kDenseStore, g, workspace, "int8 product", stream));
+  return moe::set_ok();
+}
+
+moe_status moe_ffn_int8_workspace_query(const moe_ffn_dims* dims, int64_t num_tokens, size_t* bytes) {
+  if (!bytes) return set_error(MOE_ERR_INVALID_ARG, "null output pointer");
+  MOE_RETURN_IF(check_ffn_int8(dims, num_tokens));
+  *bytes = Int8FfnLayout(dims, num_tokens).total;
+  return moe::set_ok();
+}
+
+moe_status moe_ffn_int8_apply(const moe_ffn_dims* dims, const void* x, int64_t x_stride,
+                              int64_t num_tokens, const void* w1, const float* w1_scales,
+                              const void* w2, const float* w2_scales, const void* base,
+                              int64_t base_stride, void* out, int64_t out_stride, void* workspace,
+                              size_t workspace_bytes, hipStream_t stream) {
+  MOE_RETURN_IF(check_ffn_int8(dims, num_tokens));
+  if (num_tokens == 0) return moe::set_ok();
+  const int64_t T = num_tokens, H = dims->hidden, I = dims->inter;
+  MOE_RETURN_IF(check_pointers({x, w1, w1_scales, w2, w2_scales, out, workspace}));
+  MOE_RETURN_IF(check_stride(x_stride, H));
+  MOE_RETURN_IF(check_stride(out_stride, H));
+  MOE_RETURN_IF(check_base(base, base_stride, out, out_stride, H, "base is out"));
+  const Int8FfnLayout l(dims, T);
+  MOE_RETURN_IF(check_room(workspace_bytes, l.total, "workspace"));
+  MOE_RETURN_IF(moe::check_gfx950());
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  int8_t* codes = reinterpret_cast<int8_t*>(ws);
+  float* scales = reinterpret_cast<float*>(ws + l.x_scales);
+  float* h = reinterpret_cast<float*>(ws + l.h);
+  int8_t* h_codes = reinterpret_cast<int8_t*>(ws + l.h_codes);
+  float* h_scales = reinterpret_cast<float*>(ws + l.h_scales);
+  MOE_RETURN_IF(moe::check_hip(
+      moe::launch_int8_quant(x, false, x_stride, T, (int32_t)H, codes, scales, stream),
+      "int8 block quantize", stream));
+  DenseGemm up = product(codes, H, w1, H, T, 2 * I, H, 1);
+  store_to(up, h, I, true, nullptr, 0);
+  up.e.inter = (int32_t)I;
+  up.e.row_scale = scales;
+  up.e.col_scale = w1_scales;
+  MOE_RETURN_IF(run_product(moe::kDenseI8, moe::kDenseGate, up, ws + l.part, "int8 block gate and up", stream));
+  MOE_RETURN_IF(moe::check_hip(
+      moe::launch_int8_quant(h, true, I, T, (int32_t)I, h_codes, h_scales, stream),
+      "int8 block requantize", stream));
+  DenseGemm down = product(h_codes, I, w2, I, T, H, I, 1);
+  store_to(down, out, out_stride, false, base, base_stride);
+  down.e.row_scale = h_scales;
+  down.e.col_scale = w2_scales;
+  MOE_RETURN_IF(run_product(moe::kDenseI8, moe::kDenseStore, down, ws + l.part, "int8 block down", stream));
+  return moe::set_ok();
+}
+
+}  // extern "C"

@@ -1,0 +1,129 @@
+// What the dense products do with a row's eight consecutive sums (device code
+// shared by the tile kernels, the joins and the kernels of few rows).
+#pragma once
+
+#include "moe_dense.h"
+
+namespace moe {
+
+// float32 -> two bf16 in a word, to nearest even, NaN and infinities kept.
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+  const v2bf v = {(__bf16)lo, (__bf16)hi};
+  return __builtin_bit_cast(uint32_t, v);
+}
+__device__ __forceinline__ uint4 bf16_pack8(const float (&v)[8]) {
+  return make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
+                    bf16_pair(v[6], v[7]));
+}
+__device__ __forceinline__ void bf16_unpack8(const uint4& u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = __uint_as_float(w[j] << 16);
+    v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+  }
+}
+// Eight sums as they left the matrix cores.
+__device__ __forceinline__ void sums_to_float(bool int8, const uint4& lo, const uint4& hi, float (&v)[8]) {
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = int8 ? (float)(int32_t)w[j] : __uint_as_float(w[j]);
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 lo = reinterpret_cast<const float4*>(p)[0], hi = reinterpret_cast<const float4*>(p)[1];
+  v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w;
+  v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// 1 / (1 + e^-g): within 4 ulp and, from the exponential's argument, 2^-24 |g|.
+__device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
+
+// Scales of eight int8 sums: the token's, then the channels'.
+__device__ __forceinline__ void scale8(const DenseEpilogue& e, int64_t m, int64_t n, float (&v)[8]) {
+  const float rs = e.row_scale[m];
+  float cs[8];
+  load8(e.col_scale + n, cs);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = v[j] * rs * cs[j];
+}
+
+// kDenseStore: columns n .. n + 7 of row m.
+template <bool I8>
+__device__ __forceinline__ void finish_store(const DenseEpilogue& e, int64_t m, int64_t n, float (&v)[8]) {
+  if constexpr (I8) scale8(e, m, n, v);
+  if (e.out_f32) {
+    if (e.base) {
+      float b[8];
+      load8(static_cast<const float*>(e.base) + m * e.base_stride + n, b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += b[j];
+    }
+    store8(static_cast<float*>(e.out) + m * e.out_stride + n, v);
+  } else {
+    if (e.base) {
+      float b[8];
+      bf16_unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.base) +
+                                                   m * e.base_stride + n), b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += b[j];
+    }
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.out) + m * e.out_stride + n) = bf16_pack8(v);
+  }
+}
+
+// kDenseGate: gates and ups of hidden units n .. n + 7 of row m.  bf16: gate and
+// up are rounded once for the backward pass, h once for the second product (as
+// the layer's bf16 experts do); the products and silu are float32.
+template <bool I8>
+__device__ __forceinline__ void finish_gate(const DenseEpilogue& e, int64_t m, int64_t n, float (&g)[8],
+                                            float (&u)[8]) {
+  if constexpr (I8) {
+    scale8(e, m, n, g);
+    scale8(e, m, e.inter + n, u);
+  } else if (e.gu_out) {
+    uint16_t* row = e.gu_out + m * 2 * e.inter + n;
+    *reinterpret_cast<uint4*>(row) = bf16_pack8(g);
+    *reinterpret_cast<uint4*>(row + e.inter) = bf16_pack8(u);
+  }
+  float h[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) h[j] = g[j] * sigmoid(g[j]) * u[j];
+  if constexpr (I8)
+    store8(static_cast<float*>(e.out) + m * e.out_stride + n, h);
+  else
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.out) + m * e.out_stride + n) = bf16_pack8(h);
+}
+
+// kDenseDgate: v is the gradient of h = silu(gate) * up.  With s = sigmoid(gate),
+// dgate = v up s (1 + gate (1 - s)) and dup = v gate s, each rounded once to bf16,
+// the operands of the products behind.
+__device__ __forceinline__ void finish_dgate(const DenseEpilogue& e, int64_t m, int64_t n, float (&v)[8]) {
+  const uint16_t* in = e.gu_in + m * 2 * e.inter + n;
+  uint16_t* out = static_cast<uint16_t*>(e.out) + m * 2 * e.inter + n;
+  float g[8], u[8];
+  bf16_unpack8(*reinterpret_cast<const uint4*>(in), g);
+  bf16_unpack8(*reinterpret_cast<const uint4*>(in + e.inter), u);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float s = sigmoid(g[j]);
+    const float up = v[j] * (g[j] * s);
+    g[j] = v[j] * u[j] * s * (1.0f + g[j] * (1.0f - s));
+    u[j] = up;
+  }
+  *reinterpret_cast<uint4*>(out) = bf16_pack8(g);
+  *reinterpret_cast<uint4*>(out + e.inter) = bf16_pack8(u);
+}
+
+template <bool I8, int MODE>
+__device__ __forceinline__ void finish(const DenseEpilogue& e, int64_t m, int64_t n, float (&v)[8]) {
+  static_assert(MODE != kDenseGate, "gate and up are finished together");
+  if constexpr (MODE == kDenseDgate) finish_dgate(e, m, n, v);
+  else finish_store<I8>(e, m, n, v);
+}
+
+}  // namespace moe

@@ -1,0 +1,210 @@
+"""Products in 8-bit integers on the GPU against oracle/dense.py.
+
+The quantiser's codes and scales are compared bit for bit, sums of products are
+exact in int32.  A product's result is then three roundings off (the sum as a
+float32, the two scales), its base's addition one, and the result's own: 4 2^-24 of
+the product, 2^-24 of the sum, half a step."""
+import numpy as np
+import pytest
+
+from oracle import dense as OD
+from tests.test_gpu_dense import HALF, STEP, bf16, close, device, host
+
+pytestmark = pytest.mark.gpu
+
+
+def codes_of(x, kind="bf16", pad=0):
+    import torch
+
+    import mixed_precision_moe_topk_amd as M
+
+    t = device(x, pad, kind)
+    codes = torch.full(x.shape, 77, dtype=torch.int8, device="cuda")
+    scales = torch.full((x.shape[0],), -1.0, device="cuda")
+    M.int8_quantize(t, codes, scales)
+    return codes, scales
+
+
+@pytest.mark.parametrize("R, K", [(1, 16), (1, 7168), (3, 528), (5, 2048), (7, 2064), (9, 8192), (4, 8208), (300, 144),
+                                  (2, 40000)])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_quantize_bit_for_bit(R, K, kind):
+    rng = np.random.default_rng([R, K])
+    x = rng.standard_normal((R, K)).astype(np.float32) * np.exp2(rng.integers(-40, 40, (R, 1))).astype(np.float32)
+    if kind == "bf16":
+        x = bf16(x)
+    for pad in (0, 24):
+        codes, scales = codes_of(x, kind, pad)
+        want, ws = OD.int8_quantize(x)
+        assert np.array_equal(scales.cpu().numpy(), ws) and np.array_equal(codes.cpu().numpy(), want)
+
+
+def test_quantize_halves_and_extremes():
+    """Values at and beside the halves between two codes; rows of subnormal and of the
+    largest numbers; zero, infinite and NaN rows."""
+    rows = []
+    for amax in (1.0, 3.0, 127.0, 1e-30, 3.4028235e38, 2.0 ** -126, 2.0 ** -120, 2.0 ** -133, 1e-45, 0.7):
+        s = OD.int8_scale(amax)
+        half = ((np.arange(-40, 40) + 0.5) * np.float64(s)).astype(np.float32)
+        row = np.concatenate([half, np.nextafter(half, np.float32(np.inf)), np.nextafter(half, np.float32(-np.inf)),
+                              np.array([amax, -amax, 0.0, -0.0], np.float32)])
+        row = np.clip(row, -np.float32(amax), np.float32(amax))
+        rows.append(np.pad(row, (0, 256 - row.size)))
+    rows += [np.zeros(256, np.float32), np.full(256, -np.inf, np.float32), np.full(256, np.nan, np.float32)]
+    x = np.stack(rows).astype(np.float32)
+    x[-2, 1:] = 1.0
+    codes, scales = codes_of(x, "f32")
+    want, ws = OD.int8_quantize(x)
+    assert np.array_equal(scales.cpu().numpy(), ws, equal_nan=True)
+    assert np.array_equal(codes.cpu().numpy(), want)
+
+
+def product_case(T, K, N, out, base="given", pads=(0, 0), extreme=False, seed=0, stale=0xA5):
+    import torch
+
+    import mixed_precision_moe_topk_amd as M
+
+    rng = np.random.default_rng([seed, T, K, N])
+    lo, hi = (-128, 128) if extreme else (-127, 128)
+    codes, w = (rng.integers(lo, hi, s).astype(np.int8) for s in ((T, K), (N, K)))
+    if extreme:  # the largest sums there are
+        codes[0], w[0], w[1] = -128, -128, 127
+    scales = np.exp2(rng.uniform(-8, 0, T)).astype(np.float32)
+    w_scales = np.exp2(rng.uniform(-8, 0, N)).astype(np.float32)
+    b = rng.standard_normal((T, N)).astype(np.float32)
+    b = bf16(b) if out == "bf16" else b
+    d = M.Int8Dims(K, N, out)
+    ws = torch.full((M.int8_workspace_query(d, T),), stale, dtype=torch.uint8, device="cuda")
+    dev = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    bt = device(b, pads[0], out)
+    o = bt if base == "in place" else device(np.full((T, N), np.nan), pads[1], out)
+    M.int8_matmul(d, dev(codes), dev(scales), dev(w), dev(w_scales), None if base == "none" else bt, o, ws)
+    got = host(o)
+    b = 0.0 if base == "none" else b.astype(np.float64)
+    y = OD.int8_matmul(codes, scales, w, w_scales)
+    err = 4 * 2.0 ** -24 * np.abs(y) + 2.0 ** -24 * np.abs(y + b)
+    close("out", got, y + b, err + HALF[out] * (np.abs(y + b) + err))
+    return got
+
+
+@pytest.mark.parametrize("T, K, N", [
+    (1, 16, 8), (1, 7168, 264), (2, 144, 72), (7, 528, 1000), (15, 4096, 136), (16, 256, 512), (17, 1040, 120),
+    (33, 2064, 328), (64, 7168, 520), (65, 112, 136), (100, 1104, 200), (128, 128, 128), (129, 272, 264),
+    (257, 400, 520), (500, 7168, 264), (3600, 272, 3592), (7, 30000, 24)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_product(T, K, N, out):
+    product_case(T, K, N, out)
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("T, K, N", [(3, 272, 72), (40, 4096, 136), (140, 528, 264)])
+def test_product_bases_and_strides(T, K, N, out):
+    for base in ("given", "none", "in place"):
+        product_case(T, K, N, out, base, pads=(8, 40), seed=1)
+
+
+def test_largest_sums():
+    for T, K in ((2, 131056), (70, 131056), (200, 4096)):
+        product_case(T, K, 136, "f32", extreme=True, seed=2)
+
+
+def test_same_bits_on_every_run():
+    for T, K, N in ((1, 7168, 520), (30, 4096, 264), (200, 2064, 520)):
+        a, b = (product_case(T, K, N, "f32", seed=3, stale=s) for s in (0, 0xFF))
+        assert np.array_equal(a, b)
+
+
+class Block8:
+    def __init__(self, T, H, I, seed=0):
+        rng = np.random.default_rng([seed, T, H, I])
+        n = lambda *s: rng.standard_normal(s).astype(np.float32)  # noqa: E731
+        self.dims = T, H, I
+        self.x, self.base = bf16(n(T, H)), bf16(n(T, H))
+        self.w1, self.s1 = OD.int8_quantize(n(2 * I, H) / np.float32(H ** 0.5))
+        self.w2, self.s2 = OD.int8_quantize(n(H, I) / np.float32(I ** 0.5))
+
+    def run(self, base="given", pads=(0, 0, 0), stale=0xA5):
+        import torch
+
+        import mixed_precision_moe_topk_amd as M
+
+        T, H, I = self.dims
+        d = M.FfnDims(H, I)
+        ws = torch.full((M.ffn_int8_workspace_query(d, T),), stale, dtype=torch.uint8, device="cuda")
+        dev = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+        b = device(self.base, pads[1])
+        out = b if base == "in place" else device(np.full((T, H), np.nan), pads[2])
+        M.ffn_int8_apply(d, device(self.x, pads[0]), dev(self.w1), dev(self.s1), dev(self.w2), dev(self.s2),
+                         None if base == "none" else b, out, ws)
+        return host(out)
+
+    def check(self, got, base="given"):
+        """h is off by 6 2^-24 of a gate and an up (their roundings, see above) and by
+        sigmoid's error; where that reaches a half between two codes, the code may be
+        the other one: one scale of h more."""
+        I = self.dims[2]
+        codes, s = OD.int8_quantize(self.x)
+        gu = OD.int8_matmul(codes, s, self.w1, self.s1)
+        g, u = gu[:, :I], gu[:, I:]
+        h = OD.silu_mul(g, u)
+        err = 2.0 ** -21 * (1.1 * np.abs(g * u) + np.abs(h)) + (2.0 ** -20 + 2 * STEP * np.abs(g)) * np.abs(h)
+        scale = np.abs(h).max(axis=1, keepdims=True) / 127
+        scale[scale == 0] = 1
+        q = h / scale
+        hq = np.rint(q)
+        # the scale is off by as much, relative to it, as the largest h
+        off = err / scale + np.abs(q) * (err.max(axis=1, keepdims=True) / (127 * scale) + 2.0 ** -23)
+        flip = (np.abs(np.abs(q - np.floor(q)) - 0.5) <= off).astype(np.float64)
+        w = np.abs(self.w2.astype(np.float64)) * self.s2.astype(np.float64)[:, None]
+        b = 0.0 if base == "none" else self.base.astype(np.float64)
+        # (the sum of whole numbers first: it may be exactly 0)
+        want = b + (hq @ self.w2.astype(np.float64).T) * scale * self.s2.astype(np.float64)
+        wrong = (flip * scale) @ w.T
+        rel = err.max(axis=1, keepdims=True) / (127 * scale) + 8 * STEP
+        tol = wrong + rel * (np.abs(want) + np.abs(b)) + rel * wrong
+        close("out", got, want, tol + 2.0 ** -8 * (np.abs(want) + tol))
+
+
+@pytest.mark.parametrize("T, H, I", [(1, 16, 16), (1, 7168, 2048), (3, 272, 144), (16, 256, 512), (17, 1040, 528),
+                                     (64, 2048, 1024), (65, 144, 272), (129, 400, 144), (300, 1040, 272),
+                                     (3600, 272, 1808), (3600, 3344, 144)])
+def test_block(T, H, I):
+    b = Block8(T, H, I)
+    b.check(b.run())
+
+
+def test_block_bases_and_strides():
+    for T in (1, 40, 140):
+        b = Block8(T, 272, 144, seed=1)
+        for base in ("given", "none", "in place"):
+            b.check(b.run(base, pads=(8, 24, 40)), base)
+        assert np.array_equal(b.run(stale=0), b.run(stale=0xFF))
+
+
+def test_block_of_special_tokens():
+    b = Block8(20, 272, 144, seed=2)
+    b.x[3] = 0.0
+    b.x[5, 7], b.x[6, 8] = np.nan, np.inf
+    got = b.run()
+    assert np.array_equal(got[3], b.base[3].astype(np.float64))
+    assert np.isnan(got[5]).all() and np.isnan(got[6]).all()
+    rest = [t for t in range(20) if t not in (5, 6)]
+    clean = Block8(20, 272, 144, seed=2)
+    clean.x[3] = 0.0
+    assert np.array_equal(got[rest], clean.run()[rest])
+
+
+def test_no_tokens():
+    import torch
+
+    import mixed_precision_moe_topk_amd as M
+
+    e = torch.empty(0, 272, dtype=torch.bfloat16, device="cuda")
+    codes, scales = codes_of(np.zeros((0, 272), np.float32))
+    w, s = torch.zeros(64, 272, dtype=torch.int8, device="cuda"), torch.ones(64, device="cuda")
+    M.int8_matmul(M.Int8Dims(272, 64), codes, scales, w, s, None, torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"),
+                  None)
+    w1, s1 = torch.zeros(64, 272, dtype=torch.int8, device="cuda"), torch.ones(64, device="cuda")
+    w2, s2 = torch.zeros(272, 32, dtype=torch.int8, device="cuda"), torch.ones(272, device="cuda")
+    M.ffn_int8_apply(M.FfnDims(272, 32), e, w1, s1, w2, s2, None, e, None)
+
