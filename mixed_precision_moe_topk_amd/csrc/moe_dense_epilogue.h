@@ -43,36 +43,75 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
 // 1 / (1 + e^-g): within 4 ulp and, from the exponential's argument, 2^-24 |g|.
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
-// Scales of eight int8 sums: the token's, then the channels'.
-__device__ __forceinline__ void scale8(const DenseEpilogue& e, int64_t m, int64_t n, float (&v)[8]) {
-  const float rs = e.row_scale[m];
-  float cs[8];
-  load8(e.col_scale + n, cs);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = v[j] * rs * cs[j];
+// What finishing eight sums reads from memory.  Read ahead (`Ahead::load`), with
+// clamped rows and columns, so that no sum waits for its own reads.
+struct Bytes32 {
+  uint4 lo, hi;
+};
+__device__ __forceinline__ Bytes32 load32(const void* p) {
+  return {static_cast<const uint4*>(p)[0], static_cast<const uint4*>(p)[1]};
+}
+__device__ __forceinline__ void floats(const Bytes32& b, float (&v)[8]) {
+  sums_to_float(false, b.lo, b.hi, v);
 }
 
-// kDenseStore: columns n .. n + 7 of row m.
+template <bool I8, int MODE>
+struct Ahead;
+
+// kDenseStore: the base of columns n .. n + 7 of row m.
 template <bool I8>
-__device__ __forceinline__ void finish_store(const DenseEpilogue& e, int64_t m, int64_t n, float (&v)[8]) {
-  if constexpr (I8) scale8(e, m, n, v);
+struct Ahead<I8, kDenseStore> {
+  Bytes32 base;
+  __device__ __forceinline__ void load(const DenseEpilogue& e, int64_t m, int64_t n) {
+    base = {};
+    if (!e.base) return;
+    const int64_t at = m * e.base_stride + n;
+    if (e.out_f32) base = load32(static_cast<const float*>(e.base) + at);
+    else base.lo = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.base) + at);
+  }
+};
+template <bool I8>
+struct Ahead<I8, kDenseGate> {
+  __device__ __forceinline__ void load(const DenseEpilogue&, int64_t, int64_t) {}
+};
+// kDenseDgate: gates and ups of hidden units n .. n + 7 of row m.
+template <>
+struct Ahead<false, kDenseDgate> {
+  Bytes32 gu;
+  __device__ __forceinline__ void load(const DenseEpilogue& e, int64_t m, int64_t n) {
+    const uint16_t* in = e.gu_in + m * 2 * e.inter + n;
+    gu.lo = *reinterpret_cast<const uint4*>(in);
+    gu.hi = *reinterpret_cast<const uint4*>(in + e.inter);
+  }
+};
+
+// Scales of eight int8 sums: the token's, then the channels'.
+__device__ __forceinline__ void scale8(float row, const Bytes32& columns, float (&v)[8]) {
+  float cs[8];
+  floats(columns, cs);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = v[j] * row * cs[j];
+}
+
+// kDenseStore: out = base + v, columns n .. n + 7 of row m.
+__device__ __forceinline__ void finish_store(const DenseEpilogue& e, int64_t m, int64_t n, float (&v)[8],
+                                             const Bytes32& base) {
+  const int64_t at = m * e.out_stride + n;
+  float b[8];
   if (e.out_f32) {
     if (e.base) {
-      float b[8];
-      load8(static_cast<const float*>(e.base) + m * e.base_stride + n, b);
+      floats(base, b);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] += b[j];
     }
-    store8(static_cast<float*>(e.out) + m * e.out_stride + n, v);
+    store8(static_cast<float*>(e.out) + at, v);
   } else {
     if (e.base) {
-      float b[8];
-      bf16_unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.base) +
-                                                   m * e.base_stride + n), b);
+      bf16_unpack8(base.lo, b);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] += b[j];
     }
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.out) + m * e.out_stride + n) = bf16_pack8(v);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.out) + at) = bf16_pack8(v);
   }
 }
 
@@ -82,10 +121,7 @@ __device__ __forceinline__ void finish_store(const DenseEpilogue& e, int64_t m, 
 template <bool I8>
 __device__ __forceinline__ void finish_gate(const DenseEpilogue& e, int64_t m, int64_t n, float (&g)[8],
                                             float (&u)[8]) {
-  if constexpr (I8) {
-    scale8(e, m, n, g);
-    scale8(e, m, e.inter + n, u);
-  } else if (e.gu_out) {
+  if (!I8 && e.gu_out) {
     uint16_t* row = e.gu_out + m * 2 * e.inter + n;
     *reinterpret_cast<uint4*>(row) = bf16_pack8(g);
     *reinterpret_cast<uint4*>(row + e.inter) = bf16_pack8(u);
@@ -102,12 +138,12 @@ __device__ __forceinline__ void finish_gate(const DenseEpilogue& e, int64_t m, i
 // kDenseDgate: v is the gradient of h = silu(gate) * up.  With s = sigmoid(gate),
 // dgate = v up s (1 + gate (1 - s)) and dup = v gate s, each rounded once to bf16,
 // the operands of the products behind.
-__device__ __forceinline__ void finish_dgate(const DenseEpilogue& e, int64_t m, int64_t n, float (&v)[8]) {
-  const uint16_t* in = e.gu_in + m * 2 * e.inter + n;
+__device__ __forceinline__ void finish_dgate(const DenseEpilogue& e, int64_t m, int64_t n, float (&v)[8],
+                                             const Bytes32& gu) {
   uint16_t* out = static_cast<uint16_t*>(e.out) + m * 2 * e.inter + n;
   float g[8], u[8];
-  bf16_unpack8(*reinterpret_cast<const uint4*>(in), g);
-  bf16_unpack8(*reinterpret_cast<const uint4*>(in + e.inter), u);
+  bf16_unpack8(gu.lo, g);
+  bf16_unpack8(gu.hi, u);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float s = sigmoid(g[j]);
@@ -120,10 +156,11 @@ __device__ __forceinline__ void finish_dgate(const DenseEpilogue& e, int64_t m, 
 }
 
 template <bool I8, int MODE>
-__device__ __forceinline__ void finish(const DenseEpilogue& e, int64_t m, int64_t n, float (&v)[8]) {
+__device__ __forceinline__ void finish(const DenseEpilogue& e, int64_t m, int64_t n, float (&v)[8],
+                                       const Ahead<I8, MODE>& ahead) {
   static_assert(MODE != kDenseGate, "gate and up are finished together");
-  if constexpr (MODE == kDenseDgate) finish_dgate(e, m, n, v);
-  else finish_store<I8>(e, m, n, v);
+  if constexpr (MODE == kDenseDgate) finish_dgate(e, m, n, v, ahead.gu);
+  else finish_store(e, m, n, v, ahead.base);
 }
 
 }  // namespace moe

@@ -23,6 +23,11 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef short v8s __attribute__((ext_vector_type(8)));
 
+template <int V>
+struct Int {
+  static constexpr int value = V;
+};
+
 // 16 bytes of zeros: the source of pieces behind the end of k.
 __device__ const uint4 g_zero = {0, 0, 0, 0};
 
@@ -73,21 +78,17 @@ struct Tile {
       }
     }
   }
-  __device__ __forceinline__ void issue(uint32_t lds, int wave) {
-#pragma unroll
-    for (int u = 0; u < kLoads; ++u)
-      lds_dma16_s(reinterpret_cast<const uint8_t*>(next), off[u], lds + (u * NW + wave) * 1024);
-    next += advance;
+  // Load u of the step at `next`; the last one moves on.
+  __device__ __forceinline__ void issue(int u, uint32_t lds, int wave) {
+    lds_dma16_s(reinterpret_cast<const uint8_t*>(next), off[u], lds + (u * NW + wave) * 1024);
+    if (u == kLoads - 1) next += advance;
   }
-  // The last step: `left` bytes of each row (along k) or k rows (across).
-  __device__ __forceinline__ void issue_tail(int left, uint32_t lds, int wave) const {
+  // The same for the last step: `left` bytes of each row (along k) or k rows (across).
+  __device__ __forceinline__ void issue_tail(int u, int left, uint32_t lds, int wave) const {
     const uint8_t* zero = reinterpret_cast<const uint8_t*>(&g_zero);
-#pragma unroll
-    for (int u = 0; u < kLoads; ++u) {
-      const int r = first + u * NW * kRowsPerLoad;
-      const bool in = ACROSS ? r < left : ((lane_id() ^ r) & 7) * 16 < left;
-      lds_dma16(in ? reinterpret_cast<const uint8_t*>(next) + off[u] : zero, lds + (u * NW + wave) * 1024);
-    }
+    const int r = first + u * NW * kRowsPerLoad;
+    const bool in = ACROSS ? r < left : ((lane_id() ^ r) & 7) * 16 < left;
+    lds_dma16(in ? reinterpret_cast<const uint8_t*>(next) + off[u] : zero, lds + (u * NW + wave) * 1024);
   }
 };
 
@@ -137,26 +138,17 @@ __device__ __forceinline__ v4i mma(v4i a, v4i b, v4i c) {
   }
 }
 
-// Orders a wave's own LDS writes and reads.
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 template <bool I8, bool AT, bool BT, int MODE, int WAVES_M, int WAVES_N, int WM, int WN>
 __global__ __launch_bounds__(WAVES_M* WAVES_N* kWave, 2) void k_dense(DenseGemm p) {
   constexpr int NW = WAVES_M * WAVES_N, BM = WAVES_M * WM, BN = WAVES_N * WN;
   constexpr bool GATE = MODE == kDenseGate;
   using TA = Tile<BM, AT, NW>;
   using TB = Tile<BN, BT, NW>;
-  constexpr int kStage = TA::kBytes + TB::kBytes;
-  constexpr int kPitch = WN * 4 + 16;  // bytes of a row in the epilogue's staging
-  static_assert(NW * 16 * kPitch <= 2 * kStage, "the epilogue stages in the operands' place");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage];
+  constexpr int kLds = 2 * TA::kBytes + 3 * TB::kBytes;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
 
   // Blocks go round the 8 XCDs: each takes a contiguous range of the tiles, in
-  // groups of 8 rows of tiles, so that the blocks at work on one XCD share their
+  // groups of 4 rows of tiles, so that the blocks at work on one XCD share their
   // operands in its L2.
   const int64_t tiles_m = (p.M + BM - 1) / BM;
   const int tiles_n = (p.N + BN - 1) / BN;
@@ -165,9 +157,9 @@ __global__ __launch_bounds__(WAVES_M* WAVES_N* kWave, 2) void k_dense(DenseGemm 
   const int64_t tiles = tiles_m * tiles_n;
   const int part = uniform((int)(t / tiles));
   t -= part * tiles;
-  const int64_t group = t / (8 * tiles_n), first_m = group * 8;
-  const int gm = (int)min((int64_t)8, tiles_m - first_m);
-  const int r = (int)(t - group * 8 * tiles_n);
+  const int64_t group = t / (4 * tiles_n), first_m = group * 4;
+  const int gm = (int)min((int64_t)4, tiles_m - first_m);
+  const int r = (int)(t - group * 4 * tiles_n);
   const int64_t m0 = (first_m + r % gm) * BM;
   const int nt = r / gm;
   const int64_t n0 = (int64_t)nt * BN;
@@ -207,84 +199,177 @@ __global__ __launch_bounds__(WAVES_M* WAVES_N* kWave, 2) void k_dense(DenseGemm 
 #pragma unroll
     for (int j = 0; j < WN / 16; ++j) acc[i][j] = v4i{0, 0, 0, 0};
 
-  auto issue = [&](int s) __attribute__((always_inline)) {
-    const uint32_t at = lds0 + (uint32_t)((s - s0) & 1) * kStage;
-    if (rest != 0 && s == all - 1) {
-      ta.issue_tail(AT ? rest : rest * (I8 ? 1 : 2), at, wave);
-      tb.issue_tail(BT ? rest : rest * (I8 ? 1 : 2), at + TA::kBytes, wave);
-    } else {
-      ta.issue(at, wave);
-      tb.issue(at + TA::kBytes, wave);
-    }
+  auto tail = [&](int s) __attribute__((always_inline)) { return rest != 0 && s == all - 1; };
+  // rows: stages s % 2; columns: stages s % 3
+  int a_cur = 0, b_cur = 0;  // stages of the step at work, relative to the first
+  auto a_stage = [&](int d) __attribute__((always_inline)) { return (uint32_t)((a_cur + d) & 1) * TA::kBytes; };
+  auto b_stage = [&](int d) __attribute__((always_inline)) {
+    const int b = b_cur + d;
+    return 2 * TA::kBytes + (uint32_t)(b >= 3 ? b - 3 : b) * TB::kBytes;
   };
-  if (s0 < s1) issue(s0);
-  for (int s = s0; s < s1; ++s) {
-    wait_barrier<0>();
-    if (s + 1 < s1) issue(s + 1);
-    const uint8_t* la = lds + ((s - s0) & 1) * kStage;
-    const uint8_t* lb = la + TA::kBytes;
+  // load u of the rows (columns) of the step d behind the one at work; `last`: the
+  // end of k lies in it
+  auto issue_a = [&](bool last, int d, int u) __attribute__((always_inline)) {
+    if (last) ta.issue_tail(u, AT ? rest : rest * (I8 ? 1 : 2), lds0 + a_stage(d), wave);
+    else ta.issue(u, lds0 + a_stage(d), wave);
+  };
+  auto issue_b = [&](bool last, int d, int u) __attribute__((always_inline)) {
+    if (last) tb.issue_tail(u, BT ? rest : rest * (I8 ? 1 : 2), lds0 + b_stage(d), wave);
+    else tb.issue(u, lds0 + b_stage(d), wave);
+  };
+  // Fragments of the two half steps: those of the next half are read under the
+  // products of this one, a group of products (one fragment of rows with all
+  // fragments of columns) at a time, and the loads go out between the products of
+  // a group: the columns of step s + 2 in the first half of step s, its rows in
+  // the second, as soon as all waves hold the last fragments of step s, whose
+  // place they take.
+  constexpr int FM = WM / 16, FN = WN / 16, kPerGroup = FN / FM;
+  static_assert(TA::kLoads == FM && TB::kLoads == FM, "a load of each operand a group");
+  v4i af[2][FM], bf[2][FN];
+  auto read = [&](int buf, int d, int h, int i) __attribute__((always_inline)) {
+    const uint8_t* la = lds + a_stage(d);
+    const uint8_t* lb = lds + b_stage(d);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      v4i bf[WN / 16];
+    for (int j = i * kPerGroup; j < (i + 1) * kPerGroup; ++j) bf[buf][j] = fb.read(lb, j, h);
+    af[buf][i] = fa.read(la, i, h);
+  };
+  auto multiply = [&](int buf, int i, int half) __attribute__((always_inline)) {
 #pragma unroll
-      for (int j = 0; j < WN / 16; ++j) bf[j] = fb.read(lb, j, h);
+    for (int j = half * FN / 2; j < (half + 1) * FN / 2; ++j) acc[i][j] = mma<I8>(bf[buf][j], af[buf][i], acc[i][j]);
+  };
+  // Of the two waves of a SIMD the older one is served first, and the other falls
+  // behind by half a step until the barrier, where the first waits for it alone:
+  // behind the barrier the younger one goes first (16384 x 4096 x 7168: 732 -> 701 us).
+  const bool late = NW == 8 && wave >= NW / 2;
+  // One step.  LOAD: step s + 2 is loaded, 0 not, 1 whole, 2 with the end of k;
+  // MORE: step s + 1 follows.  No branches in a step: behind one the compiler
+  // waits for every fragment.
+  auto step = [&](auto load_c, auto more_c) __attribute__((always_inline)) {
+    constexpr int LOAD = decltype(load_c)::value;
+    constexpr bool MORE = decltype(more_c)::value;
 #pragma unroll
-      for (int i = 0; i < WM / 16; ++i) {
-        const v4i af = fa.read(la, i, h);
-#pragma unroll
-        for (int j = 0; j < WN / 16; ++j) acc[i][j] = mma<I8>(bf[j], af, acc[i][j]);
-      }
+    for (int i = 0; i < FM; ++i) {
+      read(1, 0, 1, i);
+      multiply(0, i, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (LOAD != 0) issue_b(LOAD == 2, 2, i);
+      multiply(0, i, 1);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    // step s + 1 has landed, and no wave reads the rows of step s any more
+    wait_barrier<LOAD != 0 ? FM : 0>();
+    if (late) __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      if constexpr (MORE) read(0, 1, 0, i);
+      multiply(1, i, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (LOAD != 0) issue_a(LOAD == 2, 2, i);
+      multiply(1, i, 1);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (late) __builtin_amdgcn_s_setprio(0);
+    a_cur ^= 1;
+    b_cur = b_cur == 2 ? 0 : b_cur + 1;
+  };
+  const int n = s1 - s0;
+  if (n > 0) {
+    const bool last0 = tail(s0), last1 = tail(s0 + 1);
+#pragma unroll
+    for (int u = 0; u < FM; ++u) issue_a(last0, 0, u), issue_b(last0, 0, u);
+    if (n > 1) {
+#pragma unroll
+      for (int u = 0; u < FM; ++u) issue_b(last1, 1, u);
+#pragma unroll
+      for (int u = 0; u < FM; ++u) issue_a(last1, 1, u);
+      wait_barrier<2 * FM>();
+    } else {
+      wait_barrier<0>();
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) read(0, 0, 0, i);
+    const bool ends = n > 2 && tail(s1 - 1);
+    for (int s = ends ? 3 : 2; s < n; ++s) step(Int<1>(), Int<1>());
+    if (ends) step(Int<2>(), Int<1>());
+    if (n > 1) step(Int<0>(), Int<1>());
+    step(Int<0>(), Int<0>());
   }
-  // all waves are done with the operands; each stages its sums in a place of its
-  // own, 16 rows at a time, and takes them back eight columns a lane
-  wait_barrier<0>();
-  uint8_t* mine = lds + wave * 16 * kPitch;
+  // A lane holds columns 4 (lane / 16) + 0 .. 3 of each 16 x 16 sums.  Of two
+  // neighbours, the odd quarters of the wave give theirs of the first for the even
+  // quarters' of the second: every lane then has eight consecutive columns.
   constexpr int kUnits = GATE ? WN / 2 : WN;  // finished columns of a row
-  constexpr int kLanes = kUnits / 8;          // lanes of a row
-  const int row = lane / kLanes, c = lane % kLanes * 8;
-  const int64_t unit = (int64_t)nt * (GATE ? BN / 2 : BN) + wn * kUnits + c;
   const int64_t units = GATE ? p.N / 2 : p.N;
+  const int64_t unit0 = (int64_t)nt * (GATE ? BN / 2 : BN) + wn * kUnits + ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
+  auto eight = [&](int i, int j, uint4& lo, uint4& hi) __attribute__((always_inline)) {
+    uint32_t a[4], b[4];
 #pragma unroll
-  for (int i = 0; i < WM / 16; ++i) {
+    for (int r = 0; r < 4; ++r) {
+      const auto x = __builtin_amdgcn_permlane16_swap((uint32_t)acc[i][j][r], (uint32_t)acc[i][j + 1][r], false, false);
+      a[r] = x[0], b[r] = x[1];
+    }
+    lo = make_uint4(a[0], a[1], a[2], a[3]);
+    hi = make_uint4(b[0], b[1], b[2], b[3]);
+  };
+  constexpr int kPairs = kUnits / 32;
+  const int64_t row0 = m0 + wm * WM + (lane & 15);
+  if (p.split > 1) {
+    uint32_t* sums = static_cast<uint32_t*>(p.part) + (int64_t)part * p.M * p.N;
 #pragma unroll
-    for (int j = 0; j < WN / 16; ++j)
-      *reinterpret_cast<v4i*>(mine + (lane & 15) * kPitch + (16 * j + 4 * (lane >> 4)) * 4) = acc[i][j];
-    wave_sync();
+    for (int i = 0; i < FM; ++i) {
+      const int64_t m = row0 + 16 * i;
 #pragma unroll
-    for (int pass = 0; pass < 16 * kLanes / 64; ++pass) {
-      const int rr = pass * (64 / kLanes) + row;
-      const int64_t m = m0 + wm * WM + 16 * i + rr;
-      const uint4* src = reinterpret_cast<const uint4*>(mine + rr * kPitch + c * 4);
-      const uint4 lo = src[0], hi = src[1];
-      uint4 lo2, hi2;
-      if constexpr (GATE) {
-        const uint4* up = reinterpret_cast<const uint4*>(mine + rr * kPitch + (WN / 2 + c) * 4);
-        lo2 = up[0], hi2 = up[1];
-      }
-      if (m < p.M && unit < units) {
-        if (p.split > 1) {
-          uint32_t* at = static_cast<uint32_t*>(p.part) + ((int64_t)part * p.M + m) * p.N + unit;
-          reinterpret_cast<uint4*>(at)[0] = lo;
-          reinterpret_cast<uint4*>(at)[1] = hi;
-          if constexpr (GATE) {
-            reinterpret_cast<uint4*>(at + units)[0] = lo2;
-            reinterpret_cast<uint4*>(at + units)[1] = hi2;
-          }
-        } else {
-          float v[8];
-          sums_to_float(I8, lo, hi, v);
-          if constexpr (GATE) {
-            float up[8];
-            sums_to_float(I8, lo2, hi2, up);
-            finish_gate<I8>(p.e, m, unit, v, up);
-          } else {
-            finish<I8, MODE>(p.e, m, unit, v);
-          }
+      for (int j = 0; j < (GATE ? 2 : 1) * kPairs; ++j) {
+        uint4 lo, hi;
+        eight(i, 2 * j, lo, hi);
+        const int64_t unit = unit0 + 32 * (j % kPairs);
+        if (m < p.M && unit < units) {
+          uint4* at = reinterpret_cast<uint4*>(sums + m * p.N + (j / kPairs) * units + unit);
+          at[0] = lo, at[1] = hi;
         }
       }
     }
-    wave_sync();
+    return;
+  }
+  // reads of a group of rows are under way while the one before is finished (int8:
+  // the columns' scales take the registers)
+  constexpr int kDeep = I8 ? 1 : 2;
+  Ahead<I8, MODE> ahead[kDeep][kPairs];
+  float row_scale = 1.0f;
+  Bytes32 col_scale[I8 ? (GATE ? 2 : 1) * kPairs : 1];
+  auto load = [&](int i) __attribute__((always_inline)) {
+    const int64_t m = min(row0 + 16 * i, p.M - 1);
+    if constexpr (I8) row_scale = p.e.row_scale[m];
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) ahead[i % kDeep][j].load(p.e, m, min(unit0 + 32 * j, units - 8));
+  };
+  if constexpr (kDeep == 2) load(0);
+  if constexpr (I8) {
+#pragma unroll
+    for (int j = 0; j < (GATE ? 2 : 1) * kPairs; ++j)
+      col_scale[j] = load32(p.e.col_scale + (j / kPairs) * units + min(unit0 + 32 * (j % kPairs), units - 8));
+  }
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int64_t m = row0 + 16 * i;
+    if (kDeep == 1 || i + 1 < FM) load(i + kDeep - 1);
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) {
+      const int64_t unit = unit0 + 32 * j;
+      uint4 lo, hi;
+      float v[8], up[8];
+      eight(i, 2 * j, lo, hi);
+      sums_to_float(I8, lo, hi, v);
+      if constexpr (I8) scale8(row_scale, col_scale[j], v);
+      if constexpr (GATE) {
+        eight(i, 2 * (j + kPairs), lo, hi);
+        sums_to_float(I8, lo, hi, up);
+        if constexpr (I8) scale8(row_scale, col_scale[j + kPairs], up);
+      }
+      if (m < p.M && unit < units) {
+        if constexpr (GATE) finish_gate<I8>(p.e, m, unit, v, up);
+        else finish<I8, MODE>(p.e, m, unit, v, ahead[i % kDeep][j]);
+      }
+    }
   }
 }
 

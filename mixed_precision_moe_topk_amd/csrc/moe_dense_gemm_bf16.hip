@@ -39,14 +39,17 @@ __global__ __launch_bounds__(256) void k_dense_join(DenseGemm p) {
     }
     if constexpr (I8) sums_to_float(true, lo, hi, v);
   };
-  float v[8];
+  float v[8], u[8];
+  Ahead<I8, MODE> ahead;
+  ahead.load(p.e, m, n);
   sum(n, v);
+  if constexpr (I8) scale8(p.e.row_scale[m], load32(p.e.col_scale + n), v);
   if constexpr (GATE) {
-    float u[8];
     sum(units + n, u);
+    if constexpr (I8) scale8(p.e.row_scale[m], load32(p.e.col_scale + units + n), u);
     finish_gate<I8>(p.e, m, n, v, u);
   } else {
-    finish<I8, MODE>(p.e, m, n, v);
+    finish<I8, MODE>(p.e, m, n, v, ahead);
   }
 }
 
