@@ -632,8 +632,8 @@ moe_status moe_ffn_apply(const moe_ffn_dims* dims, const void* x, int64_t x_stri
  *   dw1, dw2: device out of w1's and w2's shapes, float or bf16 bits by dw_type
  *          (moe_type; rounded once), fully overwritten; both null when the
  *          weights are not trained
- *   dx:    device bf16 [num_tokens, hidden] out, or null; may be x or dout (with
- *          the same stride)
+ *   dx:    device bf16 [num_tokens, hidden] out, or null; not x or dout when dw1
+ *          and dw2 are wanted
  *   dx_base: device bf16 [num_tokens, hidden]; may be dx (with the same stride);
  *          null: 0
  * Sums are float32; g, u and h are the forward pass's, rounded to bf16, and dg

@@ -42,22 +42,21 @@ struct DenseGemm {
   DenseEpilogue e;
 };
 
-// Operand layouts and element types of the products.
-enum DenseKind : int {
-  kDenseNT = 0,  // bf16, both operands along k
-  kDenseNN = 1,  // bf16, b across k
-  kDenseTN = 2,  // bf16, both across k
-  kDenseI8 = 3,  // int8, both along k
-};
-
 constexpr int kDenseStepBytes = 128;  // K step of an operand row
-constexpr int dense_step(int kind) { return kind == kDenseI8 ? 128 : 64; }
+constexpr int dense_step(bool int8) { return int8 ? 128 : 64; }
 
 // Tile of a product: 256 x 256 by 8 waves or 128 x 128 by 4.
 constexpr int dense_tile(bool big) { return big ? 256 : 128; }
 
-hipError_t launch_dense_gemm_bf16(int kind, int mode, bool big, const DenseGemm& p, hipStream_t st);
+// Both operands along k: kDenseStore or kDenseGate.
+hipError_t launch_dense_gemm_bf16(int mode, bool big, const DenseGemm& p, hipStream_t st);
 hipError_t launch_dense_gemm_int8(int mode, bool big, const DenseGemm& p, hipStream_t st);
+// b across k: the gradients of gate and up.
+hipError_t launch_dense_dgate(bool big, const DenseGemm& p, hipStream_t st);
+// The weights' gradients (both operands across k) and the input's (b across k) in
+// one launch; one with M = 0 is left out.
+hipError_t launch_dense_grads(bool big, const DenseGemm& dw1, const DenseGemm& dw2, const DenseGemm& dx,
+                              hipStream_t st);
 // Adds up the parts (split > 1) and finishes them.
 hipError_t launch_dense_join(bool int8, int mode, const DenseGemm& p, hipStream_t st);
 

@@ -100,45 +100,50 @@ moe_status check_int8(const moe_int8_dims* d, int64_t num_tokens) {
 }
 
 // ---------------------------------------------------------------- tiles and parts
-// Tiles of 256 x 256 where they are enough for the 256 CUs, else of 128 x 128,
-// two blocks a CU, with K cut into parts (of 4 steps at least) until there are
-// kFullGrid blocks.
-constexpr int64_t kFullGrid = 512, kMinPartSteps = 4, kManyTiles = 192;
+// A launch's products take tiles of 256 x 256 where those are enough for the 256
+// CUs, else of 128 x 128, two blocks a CU.  Where a tile's K is longer than a
+// block's fair share of the launch, it is cut into parts (of kMinPartSteps at
+// least) that a join adds up.
+constexpr int64_t kMidSlots = 512, kBigSlots = 256, kMinPartSteps = 4, kManyTiles = 192;
 
-struct Shape {
-  bool big;
-  int32_t split, steps;
-};
-Shape dense_shape(int kind, int64_t M, int64_t N, int64_t K) {
-  const int64_t steps = ceil_div(K, moe::dense_step(kind));
-  Shape s = {ceil_div(M, 256) * ceil_div(N, 256) >= kManyTiles, 1, (int32_t)steps};
-  if (s.big) return s;
-  const int64_t tiles = ceil_div(M, 128) * ceil_div(N, 128);
-  const int64_t parts = std::min(kFullGrid / tiles, steps / kMinPartSteps);
-  if (parts > 1) {
-    s.steps = (int32_t)ceil_div(steps, parts);
-    s.split = (int32_t)ceil_div(steps, s.steps);
+int64_t tiles_of(const DenseGemm& g, bool big) {
+  const int t = moe::dense_tile(big);
+  return ceil_div(g.M, t) * ceil_div(g.N, t);
+}
+// -> tiles of 256 x 256; sets the products' parts.
+bool choose(DenseGemm* g, int n, bool int8) {
+  int64_t big_tiles = 0, work = 0;
+  for (int q = 0; q < n; ++q) big_tiles += tiles_of(g[q], true);
+  const bool big = big_tiles >= kManyTiles;
+  for (int q = 0; q < n; ++q) work += tiles_of(g[q], big) * ceil_div(g[q].K, moe::dense_step(int8));
+  const int64_t share = std::max(kMinPartSteps, ceil_div(work, big ? kBigSlots : kMidSlots));
+  for (int q = 0; q < n; ++q) {
+    const int64_t steps = ceil_div(g[q].K, moe::dense_step(int8));
+    const int64_t parts = std::max((int64_t)1, steps / share);
+    g[q].steps = (int32_t)std::max((int64_t)1, ceil_div(steps, parts));
+    g[q].split = (int32_t)std::max((int64_t)1, ceil_div(steps, g[q].steps));
   }
-  return s;
+  return big;
 }
-// Room for the parts of a product at any number of rows up to M and any K up to K.
-size_t part_bytes(int kind, int64_t M, int64_t N, int64_t K) {
-  const int64_t most = ceil_div(K, moe::dense_step(kind)) / kMinPartSteps;
+// Room for the parts of a launch: at most as many tiles as run at once, 32 MB by
+// either tile, and one more each; with at most `rows` x `columns` sums of at most K
+// terms.  Never less for fewer rows or terms.
+size_t part_bytes(int64_t rows, int64_t columns, int64_t K, bool int8) {
+  const int64_t most = ceil_div(K, moe::dense_step(int8)) / kMinPartSteps;
   if (most < 2) return 0;
-  const size_t sums = (size_t)std::min(M, kFullGrid * 128) * N * 4;
-  return align256(std::min((size_t)most * sums, (size_t)kFullGrid * 128 * 128 * 4));
+  const double sums = (double)rows * (double)columns * 4.0 * (double)most;
+  const size_t cap = (size_t)2 * kMidSlots * 128 * 128 * 4;
+  return align256(sums < (double)cap ? (size_t)sums : cap);
 }
 
-moe_status run_product(int kind, int mode, DenseGemm g, void* parts, const char* what, hipStream_t stream) {
-  const Shape s = dense_shape(kind, g.M, g.N, g.K);
-  g.split = s.split;
-  g.steps = s.steps;
+moe_status run_product(int mode, DenseGemm g, bool int8, void* parts, const char* what, hipStream_t stream) {
+  const bool big = choose(&g, 1, int8);
   g.part = parts;
-  const bool int8 = kind == moe::kDenseI8;
-  MOE_RETURN_IF(moe::check_hip(int8 ? moe::launch_dense_gemm_int8(mode, s.big, g, stream)
-                                    : moe::launch_dense_gemm_bf16(kind, mode, s.big, g, stream),
+  MOE_RETURN_IF(moe::check_hip(mode == moe::kDenseDgate ? moe::launch_dense_dgate(big, g, stream)
+                               : int8 ? moe::launch_dense_gemm_int8(mode, big, g, stream)
+                                      : moe::launch_dense_gemm_bf16(mode, big, g, stream),
                                what, stream));
-  if (s.split > 1) MOE_RETURN_IF(moe::check_hip(moe::launch_dense_join(int8, mode, g, stream), what, stream));
+  if (g.split > 1) MOE_RETURN_IF(moe::check_hip(moe::launch_dense_join(int8, mode, g, stream), what, stream));
   return MOE_OK;
 }
 
@@ -170,9 +175,10 @@ struct FfnLayout {
     gu_bytes = align256((size_t)T * 2 * I * 2);
     h_bytes = align256((size_t)T * I * 2);
     rows = gu_bytes;  // the larger of h and the gradients of gate and up
-    part = std::max({part_bytes(moe::kDenseNT, T, 2 * I, H), part_bytes(moe::kDenseNT, T, H, I),
-                     part_bytes(moe::kDenseNN, T, I, H), part_bytes(moe::kDenseNN, T, H, 2 * I),
-                     part_bytes(moe::kDenseTN, 2 * I, H, T), part_bytes(moe::kDenseTN, H, I, T)});
+    // (the gradients of weights and input in one launch need room together)
+    part = std::max({part_bytes(T, 2 * I, H, false), part_bytes(T, H, I, false), part_bytes(T, I, H, false),
+                     part_bytes(T, H, 2 * I, false) + part_bytes(2 * I, H, T, false) +
+                         part_bytes(H, I, T, false)});
   }
   size_t workspace() const { return rows + part; }
   size_t saved() const { return gu_bytes + h_bytes; }
@@ -188,12 +194,12 @@ struct Int8FfnLayout {
     h_codes = h + align256((size_t)T * I * 4);
     h_scales = h_codes + align256((size_t)T * I);
     part = h_scales + align256((size_t)T * 4);
-    total = part + std::max(part_bytes(moe::kDenseI8, T, 2 * I, H), part_bytes(moe::kDenseI8, T, H, I));
+    total = part + std::max(part_bytes(T, 2 * I, H, true), part_bytes(T, H, I, true));
   }
 };
 
 size_t int8_parts(const moe_int8_dims* d, int64_t T) {
-  return part_bytes(moe::kDenseI8, T, d->out_features, d->in_features);
+  return part_bytes(T, d->out_features, d->in_features, true);
 }
 
 }  // namespace
@@ -236,10 +242,10 @@ moe_status moe_ffn_apply(const moe_ffn_dims* dims, const void* x, int64_t x_stri
   store_to(up, h, I, false, nullptr, 0);
   up.e.inter = (int32_t)I;
   up.e.gu_out = static_cast<uint16_t*>(saved);
-  MOE_RETURN_IF(run_product(moe::kDenseNT, moe::kDenseGate, up, ws + l.rows, "block gate and up", stream));
+  MOE_RETURN_IF(run_product(moe::kDenseGate, up, false, ws + l.rows, "block gate and up", stream));
   DenseGemm down = product(h, I, w2, I, T, H, I, 2);
   store_to(down, out, out_stride, false, base, base_stride);
-  MOE_RETURN_IF(run_product(moe::kDenseNT, moe::kDenseStore, down, ws + l.rows, "block down", stream));
+  MOE_RETURN_IF(run_product(moe::kDenseStore, down, false, ws + l.rows, "block down", stream));
   return moe::set_ok();
 }
 
@@ -261,6 +267,9 @@ moe_status moe_ffn_backward(const moe_ffn_dims* dims, const void* dout, int64_t 
   const int64_t T = num_tokens, H = dims->hidden, I = dims->inter;
   const FfnLayout l(dims, T);
   if (T > 0) {
+    // the products of one launch read x and dout while dx is written
+    if (dw1 && dx && (dx == x || dx == dout))
+      return set_error(MOE_ERR_INVALID_ARG, "dx must not be x or dout");
     MOE_RETURN_IF(check_pointers({dout, w2, saved, workspace}));
     MOE_RETURN_IF(check_stride(dout_stride, H));
     if (dw1) {
@@ -285,23 +294,30 @@ moe_status moe_ffn_backward(const moe_ffn_dims* dims, const void* dout, int64_t 
     dh.e.out = dgu;
     dh.e.inter = (int32_t)I;
     dh.e.gu_in = static_cast<const uint16_t*>(saved);
-    MOE_RETURN_IF(run_product(moe::kDenseNN, moe::kDenseDgate, dh, parts, "block dh", stream));
+    MOE_RETURN_IF(run_product(moe::kDenseDgate, dh, false, parts, "block dh", stream));
   }
-  // the weights' gradients first: dx may then be x or dout
+  DenseGemm g[3] = {};  // dw1, dw2, dx
   if (dw1) {
     const bool f32 = dw_type == MOE_T_F32;
-    DenseGemm g1 = product(dgu, 2 * I, x, T > 0 ? x_stride : H, 2 * I, H, T, 2);
-    store_to(g1, dw1, H, f32, nullptr, 0);
-    MOE_RETURN_IF(run_product(moe::kDenseTN, moe::kDenseStore, g1, parts, "block dw1", stream));
-    DenseGemm g2 = product(dout, T > 0 ? dout_stride : H, h, I, H, I, T, 2);
-    store_to(g2, dw2, I, f32, nullptr, 0);
-    MOE_RETURN_IF(run_product(moe::kDenseTN, moe::kDenseStore, g2, parts, "block dw2", stream));
+    g[0] = product(dgu, 2 * I, x, T > 0 ? x_stride : H, 2 * I, H, T, 2);
+    store_to(g[0], dw1, H, f32, nullptr, 0);
+    g[1] = product(dout, T > 0 ? dout_stride : H, h, I, H, I, T, 2);
+    store_to(g[1], dw2, I, f32, nullptr, 0);
   }
   if (dx && T > 0) {
-    DenseGemm gx = product(dgu, 2 * I, w1, H, T, H, 2 * I, 2);
-    store_to(gx, dx, dx_stride, false, dx_base, dx_base_stride);
-    MOE_RETURN_IF(run_product(moe::kDenseNN, moe::kDenseStore, gx, parts, "block dx", stream));
+    g[2] = product(dgu, 2 * I, w1, H, T, H, 2 * I, 2);
+    store_to(g[2], dx, dx_stride, false, dx_base, dx_base_stride);
   }
+  const bool big = choose(g, 3, false);
+  for (DenseGemm& q : g) {
+    q.part = parts;
+    if (q.split > 1) parts += align256((size_t)q.split * q.M * q.N * 4);
+  }
+  MOE_RETURN_IF(moe::check_hip(moe::launch_dense_grads(big, g[0], g[1], g[2], stream), "block gradients", stream));
+  for (const DenseGemm& q : g)
+    if (q.M > 0 && q.split > 1)
+      MOE_RETURN_IF(moe::check_hip(moe::launch_dense_join(false, moe::kDenseStore, q, stream),
+                                   "block gradients' join", stream));
   return moe::set_ok();
 }
 
@@ -347,7 +363,7 @@ moe_status moe_int8_matmul(const moe_int8_dims* dims, const void* codes, const f
   store_to(g, out, out_stride, dims->out_type == MOE_T_F32, base, base_stride);
   g.e.row_scale = scales;
   g.e.col_scale = w_scales;
-  MOE_RETURN_IF(run_product(moe::kDenseI8, moe::kDenseStore, g, workspace, "int8 product", stream));
+  MOE_RETURN_IF(run_product(moe::kDenseStore, g, true, workspace, "int8 product", stream));
   return moe::set_ok();
 }
 
@@ -387,7 +403,7 @@ moe_status moe_ffn_int8_apply(const moe_ffn_dims* dims, const void* x, int64_t x
   up.e.inter = (int32_t)I;
   up.e.row_scale = scales;
   up.e.col_scale = w1_scales;
-  MOE_RETURN_IF(run_product(moe::kDenseI8, moe::kDenseGate, up, ws + l.part, "int8 block gate and up", stream));
+  MOE_RETURN_IF(run_product(moe::kDenseGate, up, true, ws + l.part, "int8 block gate and up", stream));
   MOE_RETURN_IF(moe::check_hip(
       moe::launch_int8_quant(h, true, I, T, (int32_t)I, h_codes, h_scales, stream),
       "int8 block requantize", stream));
@@ -395,7 +411,7 @@ moe_status moe_ffn_int8_apply(const moe_ffn_dims* dims, const void* x, int64_t x
   store_to(down, out, out_stride, false, base, base_stride);
   down.e.row_scale = h_scales;
   down.e.col_scale = w2_scales;
-  MOE_RETURN_IF(run_product(moe::kDenseI8, moe::kDenseStore, down, ws + l.part, "int8 block down", stream));
+  MOE_RETURN_IF(run_product(moe::kDenseStore, down, true, ws + l.part, "int8 block down", stream));
   return moe::set_ok();
 }
 

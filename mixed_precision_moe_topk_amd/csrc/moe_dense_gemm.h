@@ -138,21 +138,29 @@ __device__ __forceinline__ v4i mma(v4i a, v4i b, v4i c) {
   }
 }
 
-template <bool I8, bool AT, bool BT, int MODE, int WAVES_M, int WAVES_N, int WM, int WN>
-__global__ __launch_bounds__(WAVES_M* WAVES_N* kWave, 2) void k_dense(DenseGemm p) {
-  constexpr int NW = WAVES_M * WAVES_N, BM = WAVES_M * WM, BN = WAVES_N * WN;
+// Waves and their tiles of a block; what the block takes of LDS.
+template <int WAVES_M_, int WAVES_N_, int WM_, int WN_>
+struct Shape {
+  static constexpr int WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, WM = WM_, WN = WN_;
+  static constexpr int NW = WAVES_M * WAVES_N, BM = WAVES_M * WM, BN = WAVES_N * WN;
+  static constexpr int kLds = (2 * BM + 3 * BN) * kDenseStepBytes;
+};
+using Big = Shape<4, 2, 64, 128>;
+using Mid = Shape<2, 2, 64, 64>;
+
+// Block b of `total` that share the product p.
+template <bool I8, bool AT, bool BT, int MODE, class S>
+__device__ __forceinline__ void dense_block(const DenseGemm& p, int64_t b, int64_t total, uint8_t* lds) {
+  constexpr int NW = S::NW, BM = S::BM, BN = S::BN, WAVES_N = S::WAVES_N, WM = S::WM, WN = S::WN;
   constexpr bool GATE = MODE == kDenseGate;
   using TA = Tile<BM, AT, NW>;
   using TB = Tile<BN, BT, NW>;
-  constexpr int kLds = 2 * TA::kBytes + 3 * TB::kBytes;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
-
   // Blocks go round the 8 XCDs: each takes a contiguous range of the tiles, in
   // groups of 4 rows of tiles, so that the blocks at work on one XCD share their
   // operands in its L2.
   const int64_t tiles_m = (p.M + BM - 1) / BM;
   const int tiles_n = (p.N + BN - 1) / BN;
-  const int64_t total = (int64_t)gridDim.x, b = blockIdx.x, x = b & 7;
+  const int64_t x = b & 7;
   int64_t t = x * (total >> 3) + min(x, total & 7) + (b >> 3);
   const int64_t tiles = tiles_m * tiles_n;
   const int part = uniform((int)(t / tiles));
@@ -373,14 +381,24 @@ __global__ __launch_bounds__(WAVES_M* WAVES_N* kWave, 2) void k_dense(DenseGemm 
   }
 }
 
+template <bool I8, bool AT, bool BT, int MODE, class S>
+__global__ __launch_bounds__(S::NW* kWave, 2) void k_dense(DenseGemm p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
+  dense_block<I8, AT, BT, MODE, S>(p, blockIdx.x, gridDim.x, lds);
+}
+
+inline int64_t dense_blocks(bool big, const DenseGemm& p) {
+  const int t = dense_tile(big);
+  return (p.M + t - 1) / t * ((p.N + t - 1) / t) * p.split;
+}
+
 template <bool I8, bool AT, bool BT, int MODE>
 hipError_t launch(bool big, const DenseGemm& p, hipStream_t st) {
-  const int t = dense_tile(big);
-  const int64_t blocks = (p.M + t - 1) / t * ((p.N + t - 1) / t) * p.split;
+  const int64_t blocks = dense_blocks(big, p);
   if (blocks == 0) return hipSuccess;
   if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
-  if (big) k_dense<I8, AT, BT, MODE, 4, 2, 64, 128><<<(unsigned)blocks, 512, 0, st>>>(p);
-  else k_dense<I8, AT, BT, MODE, 2, 2, 64, 64><<<(unsigned)blocks, 256, 0, st>>>(p);
+  if (big) k_dense<I8, AT, BT, MODE, Big><<<(unsigned)blocks, Big::NW * kWave, 0, st>>>(p);
+  else k_dense<I8, AT, BT, MODE, Mid><<<(unsigned)blocks, Mid::NW * kWave, 0, st>>>(p);
   return hipGetLastError();
 }
 

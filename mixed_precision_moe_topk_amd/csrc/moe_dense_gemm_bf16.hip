@@ -1,14 +1,11 @@
-// Products of the gated block in bf16 and of its gradients, and the joins.
+// Products of the gated block in bf16, and the joins of all dense products.
 #include "moe_dense_gemm.h"
 
 namespace moe {
 
-hipError_t launch_dense_gemm_bf16(int kind, int mode, bool big, const DenseGemm& p, hipStream_t st) {
-  if (kind == kDenseNT && mode == kDenseGate) return dense::launch<false, false, false, kDenseGate>(big, p, st);
-  if (kind == kDenseNT && mode == kDenseStore) return dense::launch<false, false, false, kDenseStore>(big, p, st);
-  if (kind == kDenseNN && mode == kDenseDgate) return dense::launch<false, false, true, kDenseDgate>(big, p, st);
-  if (kind == kDenseNN && mode == kDenseStore) return dense::launch<false, false, true, kDenseStore>(big, p, st);
-  if (kind == kDenseTN && mode == kDenseStore) return dense::launch<false, true, true, kDenseStore>(big, p, st);
+hipError_t launch_dense_gemm_bf16(int mode, bool big, const DenseGemm& p, hipStream_t st) {
+  if (mode == kDenseGate) return dense::launch<false, false, false, kDenseGate>(big, p, st);
+  if (mode == kDenseStore) return dense::launch<false, false, false, kDenseStore>(big, p, st);
   return hipErrorInvalidValue;
 }
 

@@ -8,6 +8,7 @@ import pytest
 import mixed_precision_moe_topk_amd as M
 
 OK, BAD = ctypes.c_void_p(0x1000), ctypes.c_void_p(0x1000 + 8)
+OTHER = ctypes.c_void_p(0x2000)
 BIG = 1 << 50
 
 
@@ -84,7 +85,7 @@ def test_apply_refuses(L):
 
 def test_backward_refuses(L):
     def f(d=_ffn(), dout=OK, ds=256, x=OK, xs=256, T=4, w1=OK, w2=OK, saved=OK, sr=BIG, dw1=OK, dw2=OK, kind=1,
-          dxb=OK, dxbs=256, dx=OK, dxs=256, ws=OK, room=BIG):
+          dxb=OTHER, dxbs=256, dx=OTHER, dxs=256, ws=OK, room=BIG):
         return L.moe_ffn_backward(d, dout, ds, x, xs, T, w1, w2, saved, sr, dw1, dw2, kind, dxb, dxbs, dx, dxs, ws,
                                   room, None)
 
@@ -97,6 +98,7 @@ def test_backward_refuses(L):
         for s in (248, 260, -256, (1 << 22) + 8):
             assert f(**{name: s}) == 1, (name, s)
     assert f(dxbs=264) == 1 and b"another row stride" in L.moe_last_error()
+    assert f(dx=OK, dxb=None) == 1 and b"x or dout" in L.moe_last_error()
     assert f(room=16) == 3 and b"workspace" in L.moe_last_error()
     assert f(sr=16) == 3 and b"saved" in L.moe_last_error()
 

@@ -211,10 +211,15 @@ def test_strides_and_bases(T, H, I):
 
 
 def test_gradient_over_its_inputs():
+    """Where the weights are frozen; refused where they are not."""
+    import mixed_precision_moe_topk_amd as M
+
     for dx in ("over x", "over dout"):
         b = Block(150, 264, 136, seed=5)
         f = b.forward()
-        b.check_backward(f, b.backward(dx=dx), dx=dx)
+        with pytest.raises(M.MoeError):
+            b.backward(dx=dx)
+        b.check_backward(f, b.backward(dx=dx, weights=False), dx=dx)
 
 
 def test_rows_behind_the_batch_and_padding_stay():
