@@ -26,6 +26,15 @@ struct DenseEpilogue {
   const uint16_t* gu_in;   // kDenseDgate: the same
 };
 
+// Tiles of a block.
+enum DenseShape : int {
+  kDenseBig = 0,  // 256 x 256, 8 waves
+  kDenseMid = 1,  // 128 x 128, 2 groups of 4 waves
+  kDenseLow = 2,  // 64 x 128, 4 waves; not for rows across k
+};
+constexpr int dense_rows(int shape) { return shape == kDenseBig ? 256 : shape == kDenseLow ? 64 : 128; }
+constexpr int dense_columns(int shape) { return shape == kDenseBig ? 256 : 128; }
+
 // Product of rows and columns over k: sum_k a(m, k) b(n, k).  An operand lies
 // either along k (element (m, k) at m * stride + k) or across it (k * stride + m).
 struct DenseGemm {
@@ -36,6 +45,7 @@ struct DenseGemm {
   int64_t M;         // rows
   int32_t N;         // columns; kDenseGate: 2 inter
   int64_t K;
+  int32_t shape;     // DenseShape
   int32_t split;     // parts of K, each summed by blocks of their own
   int32_t steps;     // K steps (128 bytes) of a part
   void* part;        // split > 1: sums [split, M, N], float32 or int32
@@ -45,18 +55,22 @@ struct DenseGemm {
 constexpr int kDenseStepBytes = 128;  // K step of an operand row
 constexpr int dense_step(bool int8) { return int8 ? 128 : 64; }
 
-// Tile of a product: 256 x 256 by 8 waves or 128 x 128 by 4.
-constexpr int dense_tile(bool big) { return big ? 256 : 128; }
+inline int64_t dense_tiles(const DenseGemm& p) {
+  return (p.M + dense_rows(p.shape) - 1) / dense_rows(p.shape) *
+         ((p.N + dense_columns(p.shape) - 1) / dense_columns(p.shape));
+}
 
 // Both operands along k: kDenseStore or kDenseGate.
-hipError_t launch_dense_gemm_bf16(int mode, bool big, const DenseGemm& p, hipStream_t st);
-hipError_t launch_dense_gemm_int8(int mode, bool big, const DenseGemm& p, hipStream_t st);
+hipError_t launch_dense_gemm_bf16(int mode, const DenseGemm& p, hipStream_t st);
+hipError_t launch_dense_gemm_int8(int mode, const DenseGemm& p, hipStream_t st);
+// The same for at most kDenseFew rows, in one launch whatever K.
+constexpr int64_t kDenseFew = 64;
+hipError_t launch_dense_few(bool int8, int mode, const DenseGemm& p, hipStream_t st);
 // b across k: the gradients of gate and up.
-hipError_t launch_dense_dgate(bool big, const DenseGemm& p, hipStream_t st);
+hipError_t launch_dense_dgate(const DenseGemm& p, hipStream_t st);
 // The weights' gradients (both operands across k) and the input's (b across k) in
-// one launch; one with M = 0 is left out.
-hipError_t launch_dense_grads(bool big, const DenseGemm& dw1, const DenseGemm& dw2, const DenseGemm& dx,
-                              hipStream_t st);
+// one launch, of one shape (kDenseBig or kDenseMid); one with M = 0 is left out.
+hipError_t launch_dense_grads(const DenseGemm& dw1, const DenseGemm& dw2, const DenseGemm& dx, hipStream_t st);
 // Adds up the parts (split > 1) and finishes them.
 hipError_t launch_dense_join(bool int8, int mode, const DenseGemm& p, hipStream_t st);
 

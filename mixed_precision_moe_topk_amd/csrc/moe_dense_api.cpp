@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <cstdlib>
 
 #include "../../include/moe.h"
 #include "moe_dense.h"
@@ -100,48 +101,101 @@ moe_status check_int8(const moe_int8_dims* d, int64_t num_tokens) {
 }
 
 // ---------------------------------------------------------------- tiles and parts
-// A launch's products take tiles of 256 x 256 where those are enough for the 256
-// CUs, else of 128 x 128, two blocks a CU.  Where a tile's K is longer than a
-// block's fair share of the launch, it is cut into parts (of kMinPartSteps at
-// least) that a join adds up.
-constexpr int64_t kMidSlots = 512, kBigSlots = 256, kMinPartSteps = 4, kManyTiles = 192;
+// Which tiles a product takes, and into how many parts K is cut so that the 256 CUs
+// have work, goes by an estimate of its time: rounds of one block a CU, each so many
+// K steps, and for parts the join, which reads them.  Measured on full grids, us a
+// step and besides (launch, first reads, sums' way out): 256 x 256 1.5 and 13, 128 x
+// 128 0.40 and 8, 64 x 128 0.40 and 4.5, bf16 and int8 alike; a join 3 and 1 for 4
+// MB.  (us, gate and up of T tokens x 7168 x 4096 by each tile: T = 64: -, 36, 33; 512:
+// 91, 68, 85; 2048: 171, 201, 301.)
+constexpr int64_t kSlots = 256, kMinPartSteps = 4;
+constexpr int kShapes = 3;
+struct Cost {
+  double step, fixed;
+};
+constexpr Cost kCost[kShapes] = {{1.5, 13.0}, {0.40, 8.0}, {0.40, 4.5}};
 
-int64_t tiles_of(const DenseGemm& g, bool big) {
-  const int t = moe::dense_tile(big);
-  return ceil_div(g.M, t) * ceil_div(g.N, t);
+double join_cost(const DenseGemm& g, int64_t parts) {
+  return parts > 1 ? 3.0 + (double)parts * (double)g.M * (double)g.N * 1e-6 : 0.0;
 }
-// -> tiles of 256 x 256; sets the products' parts.
-bool choose(DenseGemm* g, int n, bool int8) {
-  int64_t big_tiles = 0, work = 0;
-  for (int q = 0; q < n; ++q) big_tiles += tiles_of(g[q], true);
-  const bool big = big_tiles >= kManyTiles;
-  for (int q = 0; q < n; ++q) work += tiles_of(g[q], big) * ceil_div(g[q].K, moe::dense_step(int8));
-  const int64_t share = std::max(kMinPartSteps, ceil_div(work, big ? kBigSlots : kMidSlots));
-  for (int q = 0; q < n; ++q) {
-    const int64_t steps = ceil_div(g[q].K, moe::dense_step(int8));
-    const int64_t parts = std::max((int64_t)1, steps / share);
-    g[q].steps = (int32_t)std::max((int64_t)1, ceil_div(steps, parts));
-    g[q].split = (int32_t)std::max((int64_t)1, ceil_div(steps, g[q].steps));
+int64_t steps_of(const DenseGemm& g, bool int8) { return ceil_div(g.K, moe::dense_step(int8)); }
+void set_parts(DenseGemm& g, int64_t steps, int64_t parts) {
+  g.steps = (int32_t)std::max((int64_t)1, ceil_div(steps, std::max((int64_t)1, parts)));
+  g.split = (int32_t)std::max((int64_t)1, ceil_div(steps, g.steps));
+}
+
+// One product alone.
+void choose(DenseGemm& g, bool int8) {
+  const int64_t steps = steps_of(g, int8);
+  double best = 1e300;
+  int shape = 0;
+  int64_t parts = 1;
+  for (int s = 0; s < kShapes; ++s) {
+    g.shape = s;
+    const int64_t tiles = moe::dense_tiles(g);
+    const int64_t most = std::max((int64_t)1, std::min(kSlots / std::max((int64_t)1, tiles), steps / kMinPartSteps));
+    for (int64_t n = 1; n <= most; ++n) {
+      const double t = (double)ceil_div(tiles * n, kSlots) * ((double)ceil_div(steps, n) * kCost[s].step + kCost[s].fixed) +
+                       join_cost(g, n);
+      if (t < best) best = t, shape = s, parts = n;
+    }
   }
-  return big;
+  g.shape = shape;
+  set_parts(g, steps, parts);
 }
-// Room for the parts of a launch: at most as many tiles as run at once, 32 MB by
-// either tile, and one more each; with at most `rows` x `columns` sums of at most K
+
+// Products of one launch, of one shape: K is cut where it is longer than a CU's fair
+// share of the launch.
+void choose(DenseGemm* g, int n) {
+  double best = 1e300;
+  int shape = 0;
+  for (int s : {(int)moe::kDenseBig, (int)moe::kDenseMid}) {
+    int64_t work = 0, blocks = 0, share = 0;
+    double t = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+      for (int q = 0; q < n; ++q) {
+        g[q].shape = s;
+        const int64_t tiles = moe::dense_tiles(g[q]), steps = steps_of(g[q], false);
+        if (pass == 0) {
+          work += tiles * steps;
+          continue;
+        }
+        set_parts(g[q], steps, steps / share);
+        blocks += tiles * g[q].split;
+        t += tiles > 0 ? join_cost(g[q], g[q].split) : 0.0;
+      }
+      share = std::max(kMinPartSteps, ceil_div(work, kSlots));
+    }
+    t += (double)work / kSlots * kCost[s].step + (double)ceil_div(blocks, kSlots) * kCost[s].fixed;
+    if (t < best) best = t, shape = s;
+  }
+  int64_t work = 0;
+  for (int q = 0; q < n; ++q) {
+    g[q].shape = shape;
+    work += moe::dense_tiles(g[q]) * steps_of(g[q], false);
+  }
+  const int64_t share = std::max(kMinPartSteps, ceil_div(work, kSlots));
+  for (int q = 0; q < n; ++q) set_parts(g[q], steps_of(g[q], false), steps_of(g[q], false) / share);
+}
+// Room for the parts of a launch: at most as many tiles as run at once, 64 MB by the
+// largest; with at most `rows` x `columns` sums of at most K
 // terms.  Never less for fewer rows or terms.
 size_t part_bytes(int64_t rows, int64_t columns, int64_t K, bool int8) {
   const int64_t most = ceil_div(K, moe::dense_step(int8)) / kMinPartSteps;
   if (most < 2) return 0;
   const double sums = (double)rows * (double)columns * 4.0 * (double)most;
-  const size_t cap = (size_t)2 * kMidSlots * 128 * 128 * 4;
+  const size_t cap = (size_t)kSlots * 256 * 256 * 4;
   return align256(sums < (double)cap ? (size_t)sums : cap);
 }
 
 moe_status run_product(int mode, DenseGemm g, bool int8, void* parts, const char* what, hipStream_t stream) {
-  const bool big = choose(&g, 1, int8);
+  if (mode != moe::kDenseDgate && g.M <= (getenv("FEW") ? atoi(getenv("FEW")) : 4))
+    return moe::check_hip(moe::launch_dense_few(int8, mode, g, stream), what, stream);
+  choose(g, int8);
   g.part = parts;
-  MOE_RETURN_IF(moe::check_hip(mode == moe::kDenseDgate ? moe::launch_dense_dgate(big, g, stream)
-                               : int8 ? moe::launch_dense_gemm_int8(mode, big, g, stream)
-                                      : moe::launch_dense_gemm_bf16(mode, big, g, stream),
+  MOE_RETURN_IF(moe::check_hip(mode == moe::kDenseDgate ? moe::launch_dense_dgate(g, stream)
+                               : int8 ? moe::launch_dense_gemm_int8(mode, g, stream)
+                                      : moe::launch_dense_gemm_bf16(mode, g, stream),
                                what, stream));
   if (g.split > 1) MOE_RETURN_IF(moe::check_hip(moe::launch_dense_join(int8, mode, g, stream), what, stream));
   return MOE_OK;
@@ -308,12 +362,12 @@ moe_status moe_ffn_backward(const moe_ffn_dims* dims, const void* dout, int64_t 
     g[2] = product(dgu, 2 * I, w1, H, T, H, 2 * I, 2);
     store_to(g[2], dx, dx_stride, false, dx_base, dx_base_stride);
   }
-  const bool big = choose(g, 3, false);
+  choose(g, 3);
   for (DenseGemm& q : g) {
     q.part = parts;
     if (q.split > 1) parts += align256((size_t)q.split * q.M * q.N * 4);
   }
-  MOE_RETURN_IF(moe::check_hip(moe::launch_dense_grads(big, g[0], g[1], g[2], stream), "block gradients", stream));
+  MOE_RETURN_IF(moe::check_hip(moe::launch_dense_grads(g[0], g[1], g[2], stream), "block gradients", stream));
   for (const DenseGemm& q : g)
     if (q.M > 0 && q.split > 1)
       MOE_RETURN_IF(moe::check_hip(moe::launch_dense_join(false, moe::kDenseStore, q, stream),

@@ -4,8 +4,8 @@
 
 namespace moe {
 
-hipError_t launch_dense_dgate(bool big, const DenseGemm& p, hipStream_t st) {
-  return dense::launch<false, false, true, kDenseDgate>(big, p, st);
+hipError_t launch_dense_dgate(const DenseGemm& p, hipStream_t st) {
+  return dense::launch<false, false, true, kDenseDgate>(p, st);
 }
 
 // dw1 and dw2 (both operands across k) and dx (b across k) need the same and not
@@ -18,7 +18,7 @@ struct DenseGrads {
   int64_t blocks[3];
 };
 template <class S>
-__global__ __launch_bounds__(S::NW* kWave, 2) void k_dense_grads(DenseGrads g) {
+__global__ __launch_bounds__(S::kThreads, 2) void k_dense_grads(DenseGrads g) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
   const int64_t b = blockIdx.x;
   if (b < g.first[2]) {
@@ -31,18 +31,20 @@ __global__ __launch_bounds__(S::NW* kWave, 2) void k_dense_grads(DenseGrads g) {
   }
 }
 
-hipError_t launch_dense_grads(bool big, const DenseGemm& dw1, const DenseGemm& dw2, const DenseGemm& dx,
-                              hipStream_t st) {
+hipError_t launch_dense_grads(const DenseGemm& dw1, const DenseGemm& dw2, const DenseGemm& dx, hipStream_t st) {
   DenseGrads g = {{dw1, dw2}, dx, {}, {}};
   for (int q = 0; q < 3; ++q) {
-    g.blocks[q] = dense::dense_blocks(big, q < 2 ? g.w[q] : g.x);
+    const DenseGemm& p = q < 2 ? g.w[q] : g.x;
+    if (p.shape != dw1.shape) return hipErrorInvalidValue;
+    g.blocks[q] = dense_tiles(p) * p.split;
     g.first[q + 1] = g.first[q] + (g.blocks[q] + 7) / 8 * 8;
   }
   if (g.first[3] == 0) return hipSuccess;
   if (g.first[3] > 0x7FFFFFFFLL) return hipErrorInvalidValue;
   const unsigned n = (unsigned)g.first[3];
-  if (big) k_dense_grads<dense::Big><<<n, dense::Big::NW * kWave, 0, st>>>(g);
-  else k_dense_grads<dense::Mid><<<n, dense::Mid::NW * kWave, 0, st>>>(g);
+  if (dw1.shape == kDenseBig) k_dense_grads<dense::Big><<<n, dense::Big::kThreads, 0, st>>>(g);
+  else if (dw1.shape == kDenseMid) k_dense_grads<dense::Mid><<<n, dense::Mid::kThreads, 0, st>>>(g);
+  else return hipErrorInvalidValue;
   return hipGetLastError();
 }
 

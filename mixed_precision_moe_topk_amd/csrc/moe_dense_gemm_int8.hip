@@ -4,9 +4,9 @@
 
 namespace moe {
 
-hipError_t launch_dense_gemm_int8(int mode, bool big, const DenseGemm& p, hipStream_t st) {
-  if (mode == kDenseGate) return dense::launch<true, false, false, kDenseGate>(big, p, st);
-  if (mode == kDenseStore) return dense::launch<true, false, false, kDenseStore>(big, p, st);
+hipError_t launch_dense_gemm_int8(int mode, const DenseGemm& p, hipStream_t st) {
+  if (mode == kDenseGate) return dense::launch<true, false, false, kDenseGate>(p, st);
+  if (mode == kDenseStore) return dense::launch<true, false, false, kDenseStore>(p, st);
   return hipErrorInvalidValue;
 }
 
