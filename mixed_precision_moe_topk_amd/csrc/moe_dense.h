@@ -29,8 +29,8 @@ struct DenseEpilogue {
 // Tiles of a block.
 enum DenseShape : int {
   kDenseBig = 0,  // 256 x 256, 8 waves
-  kDenseMid = 1,  // 128 x 128, 2 groups of 4 waves
-  kDenseLow = 2,  // 64 x 128, 4 waves; not for rows across k
+  kDenseMid = 1,  // 128 x 128, 4 waves, two blocks a CU
+  kDenseLow = 2,  // 64 x 128, 4 waves, two blocks a CU; not for rows across k
 };
 constexpr int dense_rows(int shape) { return shape == kDenseBig ? 256 : shape == kDenseLow ? 64 : 128; }
 constexpr int dense_columns(int shape) { return shape == kDenseBig ? 256 : 128; }
@@ -63,9 +63,8 @@ inline int64_t dense_tiles(const DenseGemm& p) {
 // Both operands along k: kDenseStore or kDenseGate.
 hipError_t launch_dense_gemm_bf16(int mode, const DenseGemm& p, hipStream_t st);
 hipError_t launch_dense_gemm_int8(int mode, const DenseGemm& p, hipStream_t st);
-// The same for at most kDenseFew rows, in one launch whatever K.
-constexpr int64_t kDenseFew = 64;
-hipError_t launch_dense_few(bool int8, int mode, const DenseGemm& p, hipStream_t st);
+// The same for M = 1, without parts.
+hipError_t launch_dense_one(bool int8, int mode, const DenseGemm& p, hipStream_t st);
 // b across k: the gradients of gate and up.
 hipError_t launch_dense_dgate(const DenseGemm& p, hipStream_t st);
 // The weights' gradients (both operands across k) and the input's (b across k) in
@@ -73,6 +72,10 @@ hipError_t launch_dense_dgate(const DenseGemm& p, hipStream_t st);
 hipError_t launch_dense_grads(const DenseGemm& dw1, const DenseGemm& dw2, const DenseGemm& dx, hipStream_t st);
 // Adds up the parts (split > 1) and finishes them.
 hipError_t launch_dense_join(bool int8, int mode, const DenseGemm& p, hipStream_t st);
+
+// The same for an int8 kDenseGate and the quantiser behind it: codes [M, N / 2] and
+// scales [M] of the rows of the gated sums (e.out is not written).
+hipError_t launch_dense_join_quant(const DenseGemm& p, int8_t* codes, float* scales, hipStream_t st);
 
 // Codes int8 [rows, cols] and scales [rows] of x, bf16 or float32, stride elements
 // between rows.

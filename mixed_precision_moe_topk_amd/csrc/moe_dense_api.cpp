@@ -5,7 +5,6 @@
 
 #include <algorithm>
 #include <cstdint>
-#include <cstdlib>
 
 #include "../../include/moe.h"
 #include "moe_dense.h"
@@ -102,21 +101,33 @@ moe_status check_int8(const moe_int8_dims* d, int64_t num_tokens) {
 
 // ---------------------------------------------------------------- tiles and parts
 // Which tiles a product takes, and into how many parts K is cut so that the 256 CUs
-// have work, goes by an estimate of its time: rounds of one block a CU, each so many
-// K steps, and for parts the join, which reads them.  Measured on full grids, us a
-// step and besides (launch, first reads, sums' way out): 256 x 256 1.5 and 13, 128 x
-// 128 0.40 and 8, 64 x 128 0.40 and 4.5, bf16 and int8 alike; a join 3 and 1 for 4
-// MB.  (us, gate and up of T tokens x 7168 x 4096 by each tile: T = 64: -, 36, 33; 512:
-// 91, 68, 85; 2048: 171, 201, 301.)
-constexpr int64_t kSlots = 256, kMinPartSteps = 4;
-constexpr int kShapes = 3;
+// have work, goes by an estimate of its time: rounds of blocks that run at once, each
+// a number of K steps, and for parts the join that reads them.  Measured on full
+// grids of 4 to 64 steps, us a step and besides (launch, first reads, the sums' way
+// out), bf16 and int8 alike within a tenth:
+//                one block a CU     two
+//   256 x 256    1.40 + 15
+//   128 x 128    0.50 + 7.2         0.80 + 9.6
+//    64 x 128    0.44 + 4.0         0.60 + 5.5
+// a join 4 (with its launch) + 1 for 4 MB.  (The block in bf16, T tokens of 7168 x 2048, by 64, 128 and
+// 256 rows: T = 64: 33, 35, -; 512: 86, 71, 91; 2048: 266, 180, 171.)
+constexpr int64_t kCus = 256, kMinPartSteps = 4;
 struct Cost {
   double step, fixed;
 };
-constexpr Cost kCost[kShapes] = {{1.5, 13.0}, {0.40, 8.0}, {0.40, 4.5}};
+constexpr Cost kOne[3] = {{1.40, 15.0}, {0.50, 7.2}, {0.44, 4.0}};
+constexpr Cost kTwo[3] = {{}, {0.80, 9.6}, {0.60, 5.5}};
 
+int64_t slots(int shape) { return shape == moe::kDenseBig ? kCus : 2 * kCus; }
+// `blocks` blocks of `steps` each.
+double run_cost(int shape, int64_t blocks, double steps) {
+  const Cost one = kOne[shape], all = shape == moe::kDenseBig ? one : kTwo[shape];
+  const int64_t rounds = blocks / slots(shape), rest = blocks % slots(shape);
+  const double full = steps * all.step + all.fixed;
+  return (double)rounds * full + (rest > kCus ? full : rest > 0 ? steps * one.step + one.fixed : 0.0);
+}
 double join_cost(const DenseGemm& g, int64_t parts) {
-  return parts > 1 ? 3.0 + (double)parts * (double)g.M * (double)g.N * 1e-6 : 0.0;
+  return parts > 1 ? 4.0 + (double)parts * (double)g.M * (double)g.N * 1e-6 : 0.0;
 }
 int64_t steps_of(const DenseGemm& g, bool int8) { return ceil_div(g.K, moe::dense_step(int8)); }
 void set_parts(DenseGemm& g, int64_t steps, int64_t parts) {
@@ -130,13 +141,12 @@ void choose(DenseGemm& g, bool int8) {
   double best = 1e300;
   int shape = 0;
   int64_t parts = 1;
-  for (int s = 0; s < kShapes; ++s) {
+  for (int s = 0; s < 3; ++s) {
     g.shape = s;
-    const int64_t tiles = moe::dense_tiles(g);
-    const int64_t most = std::max((int64_t)1, std::min(kSlots / std::max((int64_t)1, tiles), steps / kMinPartSteps));
+    const int64_t tiles = std::max((int64_t)1, moe::dense_tiles(g));
+    const int64_t most = std::max((int64_t)1, std::min(slots(s) / tiles, steps / kMinPartSteps));
     for (int64_t n = 1; n <= most; ++n) {
-      const double t = (double)ceil_div(tiles * n, kSlots) * ((double)ceil_div(steps, n) * kCost[s].step + kCost[s].fixed) +
-                       join_cost(g, n);
+      const double t = run_cost(s, tiles * n, (double)ceil_div(steps, n)) + join_cost(g, n);
       if (t < best) best = t, shape = s, parts = n;
     }
   }
@@ -144,38 +154,42 @@ void choose(DenseGemm& g, bool int8) {
   set_parts(g, steps, parts);
 }
 
-// Products of one launch, of one shape: K is cut where it is longer than a CU's fair
-// share of the launch.
+// Products of one launch, of one shape, their K cut into parts of `share` steps at
+// most.  Returns the estimate.
+double share_out(DenseGemm* g, int n, int shape, int64_t share) {
+  int64_t work = 0, blocks = 0, longest = 0;
+  double joins = 0;
+  for (int q = 0; q < n; ++q) {
+    g[q].shape = shape;
+    const int64_t steps = steps_of(g[q], false), tiles = moe::dense_tiles(g[q]);
+    set_parts(g[q], steps, steps / share);
+    if (tiles == 0) continue;
+    work += tiles * steps;
+    blocks += tiles * g[q].split;
+    longest = std::max(longest, (int64_t)g[q].steps);
+    joins += join_cost(g[q], g[q].split);
+  }
+  const double mean = blocks > 0 ? (double)work / (double)blocks : 0.0;
+  return joins + std::max(run_cost(shape, blocks, mean), run_cost(shape, std::min(blocks, kCus), (double)longest));
+}
 void choose(DenseGemm* g, int n) {
   double best = 1e300;
   int shape = 0;
+  int64_t share = 1;
   for (int s : {(int)moe::kDenseBig, (int)moe::kDenseMid}) {
-    int64_t work = 0, blocks = 0, share = 0;
-    double t = 0;
-    for (int pass = 0; pass < 2; ++pass) {
-      for (int q = 0; q < n; ++q) {
-        g[q].shape = s;
-        const int64_t tiles = moe::dense_tiles(g[q]), steps = steps_of(g[q], false);
-        if (pass == 0) {
-          work += tiles * steps;
-          continue;
-        }
-        set_parts(g[q], steps, steps / share);
-        blocks += tiles * g[q].split;
-        t += tiles > 0 ? join_cost(g[q], g[q].split) : 0.0;
-      }
-      share = std::max(kMinPartSteps, ceil_div(work, kSlots));
+    int64_t work = 0;
+    for (int q = 0; q < n; ++q) {
+      g[q].shape = s;
+      work += moe::dense_tiles(g[q]) * steps_of(g[q], false);
     }
-    t += (double)work / kSlots * kCost[s].step + (double)ceil_div(blocks, kSlots) * kCost[s].fixed;
-    if (t < best) best = t, shape = s;
+    // a block's fair share of the launch, or a longer one
+    const int64_t fair = std::max(kMinPartSteps, ceil_div(work, slots(s)));
+    for (int64_t m : {2, 3, 4, 8, 16, 1 << 20}) {
+      const double t = share_out(g, n, s, fair * m / 2);
+      if (t < best) best = t, shape = s, share = fair * m / 2;
+    }
   }
-  int64_t work = 0;
-  for (int q = 0; q < n; ++q) {
-    g[q].shape = shape;
-    work += moe::dense_tiles(g[q]) * steps_of(g[q], false);
-  }
-  const int64_t share = std::max(kMinPartSteps, ceil_div(work, kSlots));
-  for (int q = 0; q < n; ++q) set_parts(g[q], steps_of(g[q], false), steps_of(g[q], false) / share);
+  share_out(g, n, shape, share);
 }
 // Room for the parts of a launch: at most as many tiles as run at once, 64 MB by the
 // largest; with at most `rows` x `columns` sums of at most K
@@ -184,13 +198,15 @@ size_t part_bytes(int64_t rows, int64_t columns, int64_t K, bool int8) {
   const int64_t most = ceil_div(K, moe::dense_step(int8)) / kMinPartSteps;
   if (most < 2) return 0;
   const double sums = (double)rows * (double)columns * 4.0 * (double)most;
-  const size_t cap = (size_t)kSlots * 256 * 256 * 4;
+  const size_t cap = (size_t)kCus * 256 * 256 * 4;
   return align256(sums < (double)cap ? (size_t)sums : cap);
 }
 
 moe_status run_product(int mode, DenseGemm g, bool int8, void* parts, const char* what, hipStream_t stream) {
-  if (mode != moe::kDenseDgate && g.M <= (getenv("FEW") ? atoi(getenv("FEW")) : 4))
-    return moe::check_hip(moe::launch_dense_few(int8, mode, g, stream), what, stream);
+  // (T = 1 of 7168 x 2048: 23.0 us, by tiles 26.5; two rows read side by side took
+  // 27.7, as by tiles)
+  if (g.M == 1 && mode != moe::kDenseDgate)
+    return moe::check_hip(moe::launch_dense_one(int8, mode, g, stream), what, stream);
   choose(g, int8);
   g.part = parts;
   MOE_RETURN_IF(moe::check_hip(mode == moe::kDenseDgate ? moe::launch_dense_dgate(g, stream)
@@ -457,10 +473,20 @@ moe_status moe_ffn_int8_apply(const moe_ffn_dims* dims, const void* x, int64_t x
   up.e.inter = (int32_t)I;
   up.e.row_scale = scales;
   up.e.col_scale = w1_scales;
-  MOE_RETURN_IF(run_product(moe::kDenseGate, up, true, ws + l.part, "int8 block gate and up", stream));
-  MOE_RETURN_IF(moe::check_hip(
-      moe::launch_int8_quant(h, true, I, T, (int32_t)I, h_codes, h_scales, stream),
-      "int8 block requantize", stream));
+  choose(up, true);
+  if (T > 1 && up.split > 1) {
+    // the join of the parts quantises h and never stores it
+    up.part = ws + l.part;
+    MOE_RETURN_IF(moe::check_hip(moe::launch_dense_gemm_int8(moe::kDenseGate, up, stream),
+                                 "int8 block gate and up", stream));
+    MOE_RETURN_IF(moe::check_hip(moe::launch_dense_join_quant(up, h_codes, h_scales, stream),
+                                 "int8 block requantize", stream));
+  } else {
+    MOE_RETURN_IF(run_product(moe::kDenseGate, up, true, ws + l.part, "int8 block gate and up", stream));
+    MOE_RETURN_IF(moe::check_hip(
+        moe::launch_int8_quant(h, true, I, T, (int32_t)I, h_codes, h_scales, stream),
+        "int8 block requantize", stream));
+  }
   DenseGemm down = product(h_codes, I, w2, I, T, H, I, 1);
   store_to(down, out, out_stride, false, base, base_stride);
   down.e.row_scale = h_scales;

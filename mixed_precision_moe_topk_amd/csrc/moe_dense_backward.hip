@@ -18,7 +18,7 @@ struct DenseGrads {
   int64_t blocks[3];
 };
 template <class S>
-__global__ __launch_bounds__(S::kThreads, 2) void k_dense_grads(DenseGrads g) {
+__global__ __launch_bounds__(S::NW* kWave, 2) void k_dense_grads(DenseGrads g) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
   const int64_t b = blockIdx.x;
   if (b < g.first[2]) {
@@ -42,8 +42,8 @@ hipError_t launch_dense_grads(const DenseGemm& dw1, const DenseGemm& dw2, const 
   if (g.first[3] == 0) return hipSuccess;
   if (g.first[3] > 0x7FFFFFFFLL) return hipErrorInvalidValue;
   const unsigned n = (unsigned)g.first[3];
-  if (dw1.shape == kDenseBig) k_dense_grads<dense::Big><<<n, dense::Big::kThreads, 0, st>>>(g);
-  else if (dw1.shape == kDenseMid) k_dense_grads<dense::Mid><<<n, dense::Mid::kThreads, 0, st>>>(g);
+  if (dw1.shape == kDenseBig) k_dense_grads<dense::Big><<<n, dense::Big::NW * kWave, 0, st>>>(g);
+  else if (dw1.shape == kDenseMid) k_dense_grads<dense::Mid><<<n, dense::Mid::NW * kWave, 0, st>>>(g);
   else return hipErrorInvalidValue;
   return hipGetLastError();
 }

@@ -163,4 +163,29 @@ __device__ __forceinline__ void finish(const DenseEpilogue& e, int64_t m, int64_
   else finish_store(e, m, n, v, ahead.base);
 }
 
+// Sums of the parts of columns col .. col + 7 of row m, in the parts' order, eight
+// parts' reads under way at a time.
+template <bool I8>
+__device__ __forceinline__ void join_sums(const DenseGemm& p, int64_t m, int64_t col, float (&v)[8]) {
+  constexpr int kReads = 8;
+  const uint32_t* first = static_cast<const uint32_t*>(p.part) + m * p.N + col;
+  uint32_t t[8] = {};
+  for (int s = 0; s < p.split; s += kReads) {
+    Bytes32 b[kReads];
+#pragma unroll
+    for (int r = 0; r < kReads; ++r) b[r] = load32(first + min(s + r, p.split - 1) * (p.M * p.N));
+#pragma unroll
+    for (int r = 0; r < kReads; ++r) {
+      const uint32_t w[8] = {b[r].lo.x, b[r].lo.y, b[r].lo.z, b[r].lo.w, b[r].hi.x, b[r].hi.y, b[r].hi.z, b[r].hi.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (I8) t[j] += s + r < p.split ? w[j] : 0u;
+        else t[j] = s + r < p.split ? __float_as_uint(__uint_as_float(t[j]) + __uint_as_float(w[j])) : t[j];
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = I8 ? (float)(int32_t)t[j] : __uint_as_float(t[j]);
+}
+
 }  // namespace moe

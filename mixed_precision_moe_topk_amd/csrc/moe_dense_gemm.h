@@ -1,9 +1,8 @@
 // Tile kernel of the dense products.
 //
 // A block takes BM rows and BN columns; a K step is 128 bytes of every operand
-// row.  Both operands' tiles go straight into LDS, two or four steps ahead; one
-// barrier a step.  The
-// columns are the matrix instruction's first operand, so that a lane holds four
+// row.  Both operands' tiles go straight into LDS, up to two steps ahead; one barrier a
+// step.  The columns are the matrix instruction's first operand, so that a lane holds four
 // consecutive columns of one row.
 //
 // An operand along k lies in LDS as [row][128 bytes], its 16-byte pieces at
@@ -139,29 +138,22 @@ __device__ __forceinline__ v4i mma(v4i a, v4i b, v4i c) {
 }
 
 // Waves and their tiles of a block; what the block takes of LDS.
-// A block holds DEPTH steps' rows and one step's more of columns.  GROUPS > 1: as
-// many times so many waves, each group with its share of the block's K steps and
-// LDS; their sums meet in LDS.
-template <int WAVES_M_, int WAVES_N_, int WM_, int WN_, int DEPTH_, int GROUPS_>
+// A block holds two steps' rows and three steps' columns.
+template <int WAVES_M_, int WAVES_N_, int WM_, int WN_>
 struct Shape {
-  static constexpr int WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, WM = WM_, WN = WN_, DEPTH = DEPTH_;
-  static constexpr int GROUPS = GROUPS_;
+  static constexpr int WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, WM = WM_, WN = WN_;
   static constexpr int NW = WAVES_M * WAVES_N, BM = WAVES_M * WM, BN = WAVES_N * WN;
-  static constexpr int kThreads = GROUPS * NW * kWave;
-  static constexpr int kGroupLds = (DEPTH * BM + (DEPTH + 1) * BN) * kDenseStepBytes;
-  static constexpr int kLds = GROUPS * kGroupLds;
+  static constexpr int kLds = (2 * BM + 3 * BN) * kDenseStepBytes;
   static_assert(kLds <= 160 * 1024, "LDS of a CU");
-  static_assert(GROUPS <= 2 && kLds >= GROUPS * NW * WM * WN * 2, "half of the groups' sums");
 };
-using Big = Shape<4, 2, 64, 128, 2, 1>;  // 256 x 256, 160 KB of LDS
-using Mid = Shape<2, 2, 64, 64, 2, 2>;   // 128 x 128, twice 80 KB
-using Low = Shape<2, 2, 32, 64, 4, 1>;   // 64 x 128, 112 KB
+using Big = Shape<4, 2, 64, 128>;  // 256 x 256, 160 KB of LDS
+using Mid = Shape<2, 2, 64, 64>;   // 128 x 128, 80 KB: two blocks a CU
+using Low = Shape<2, 2, 32, 64>;   // 64 x 128, 64 KB: two blocks a CU
 
 // Block b of `total` that share the product p.
 template <bool I8, bool AT, bool BT, int MODE, class S>
 __device__ __forceinline__ void dense_block(const DenseGemm& p, int64_t b, int64_t total, uint8_t* lds) {
   constexpr int NW = S::NW, BM = S::BM, BN = S::BN, WAVES_N = S::WAVES_N, WM = S::WM, WN = S::WN;
-  constexpr int D = S::DEPTH;
   constexpr bool GATE = MODE == kDenseGate;
   using TA = Tile<BM, AT, NW>;
   using TB = Tile<BN, BT, NW>;
@@ -182,19 +174,13 @@ __device__ __forceinline__ void dense_block(const DenseGemm& p, int64_t b, int64
   const int nt = r / gm;
   const int64_t n0 = (int64_t)nt * BN;
 
-  const int all_wave = uniform((int)threadIdx.x / kWave), lane = lane_id();
-  const int group_id = all_wave / NW, wave = all_wave % NW;
+  const int wave = uniform((int)threadIdx.x / kWave), lane = lane_id();
   const int wm = wave / WAVES_N, wn = wave % WAVES_N;
-  uint8_t* const block_lds = lds;
-  lds += group_id * S::kGroupLds;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
 
   constexpr int kStep = I8 ? 128 : 64;
   const int all = uniform((int)((p.K + kStep - 1) / kStep));
-  int s0 = min(all, part * p.steps), s1 = min(all, s0 + p.steps);
-  const int most = (s1 - s0 + S::GROUPS - 1) / S::GROUPS;  // steps of the first group
-  s0 = min(s1, s0 + group_id * most);
-  s1 = min(s1, s0 + most);
+  const int s0 = min(all, part * p.steps), s1 = min(all, s0 + p.steps);
   const int rest = (int)(p.K % kStep);  // of the last step, 0: whole
   TA ta;
   TB tb;
@@ -224,15 +210,12 @@ __device__ __forceinline__ void dense_block(const DenseGemm& p, int64_t b, int64
     for (int j = 0; j < WN / 16; ++j) acc[i][j] = v4i{0, 0, 0, 0};
 
   auto tail = [&](int s) __attribute__((always_inline)) { return rest != 0 && s == all - 1; };
-  // rows: stages s % D; columns: stages s % (D + 1)
+  // rows: stages s % 2; columns: stages s % 3
   int a_cur = 0, b_cur = 0;  // stages of the step at work, relative to the first
-  auto a_stage = [&](int d) __attribute__((always_inline)) {
-    const int a = a_cur + d;
-    return (uint32_t)(a >= D ? a - D : a) * TA::kBytes;
-  };
+  auto a_stage = [&](int d) __attribute__((always_inline)) { return (uint32_t)((a_cur + d) & 1) * TA::kBytes; };
   auto b_stage = [&](int d) __attribute__((always_inline)) {
     const int b = b_cur + d;
-    return D * TA::kBytes + (uint32_t)(b > D ? b - D - 1 : b) * TB::kBytes;
+    return 2 * TA::kBytes + (uint32_t)(b >= 3 ? b - 3 : b) * TB::kBytes;
   };
   // load u of the rows (columns) of the step d behind the one at work; `last`: the
   // end of k lies in it
@@ -247,7 +230,7 @@ __device__ __forceinline__ void dense_block(const DenseGemm& p, int64_t b, int64
   // Fragments of the two half steps: those of the next half are read under the
   // products of this one, a group of products (one fragment of rows with all
   // fragments of columns) at a time, and the loads go out between the products of
-  // a group: the columns of step s + D in the first half of step s, in the place
+  // a group: the columns of step s + 2 in the first half of step s, in the place
   // of those of step s - 1, its rows in the second, as soon as all waves hold the
   // last fragments of step s, whose place they take.
   constexpr int FM = WM / 16, FN = WN / 16, kPerGroup = FN / FM;
@@ -268,12 +251,13 @@ __device__ __forceinline__ void dense_block(const DenseGemm& p, int64_t b, int64
   // Of the two waves of a SIMD the older one is served first, and the other falls
   // behind by half a step until the barrier, where the first waits for it alone:
   // behind the barrier the younger one goes first (16384 x 4096 x 7168: 732 -> 701 us).
-  const bool late = S::GROUPS * NW == 8 && all_wave >= 4;
-  // One step.  LOAD: step s + D is loaded, 0 not, 1 whole, 2 with the end of k;
-  // REST (without loads): steps that follow.  No branches in a step: behind one the
+  const bool late = NW == 8 && wave >= 4;
+  // One step.  LOAD: step s + 2 is loaded, 0 not, 1 whole, 2 with the end of k;
+  // MORE: step s + 1 follows.  No branches in a step: behind one the
   // compiler waits for every fragment.
-  auto step = [&](auto load_c, auto rest_c) __attribute__((always_inline)) {
-    constexpr int LOAD = decltype(load_c)::value, REST = decltype(rest_c)::value;
+  auto step = [&](auto load_c, auto more_c) __attribute__((always_inline)) {
+    constexpr int LOAD = decltype(load_c)::value;
+    constexpr bool MORE = decltype(more_c)::value;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       read(1, 0, 1, i);
@@ -281,74 +265,47 @@ __device__ __forceinline__ void dense_block(const DenseGemm& p, int64_t b, int64
       __builtin_amdgcn_sched_barrier(0);
       if constexpr (LOAD != 0)
 #pragma unroll
-        for (int u = i * LB / FM; u < (i + 1) * LB / FM; ++u) issue_b(LOAD == 2, D, u);
+        for (int u = i * LB / FM; u < (i + 1) * LB / FM; ++u) issue_b(LOAD == 2, 2, u);
       multiply(0, i, 1);
       __builtin_amdgcn_sched_barrier(0);
     }
     // step s + 1 has landed (what was issued behind its rows may be under way), and
     // no wave reads the rows of step s any more
-    constexpr int kBehind = LOAD != 0 ? (D - 1) * LB + (D - 2) * LA : REST > 1 ? (REST - 1) * (LA + LB) : 0;
-    wait_barrier<kBehind>();
+    wait_barrier<LOAD != 0 ? LB : 0>();
     if (late) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-      if constexpr (LOAD != 0 || REST > 0) read(0, 1, 0, i);
+      if constexpr (MORE) read(0, 1, 0, i);
       multiply(1, i, 0);
       __builtin_amdgcn_sched_barrier(0);
       if constexpr (LOAD != 0)
 #pragma unroll
-        for (int u = i * LA / FM; u < (i + 1) * LA / FM; ++u) issue_a(LOAD == 2, D, u);
+        for (int u = i * LA / FM; u < (i + 1) * LA / FM; ++u) issue_a(LOAD == 2, 2, u);
       multiply(1, i, 1);
       __builtin_amdgcn_sched_barrier(0);
     }
     if (late) __builtin_amdgcn_s_setprio(0);
-    a_cur = a_cur == D - 1 ? 0 : a_cur + 1;
-    b_cur = b_cur == D ? 0 : b_cur + 1;
+    a_cur ^= 1;
+    b_cur = b_cur == 2 ? 0 : b_cur + 1;
   };
   const int n = s1 - s0;
   if (n > 0) {
-    for (int d = 0; d < min(n, D); ++d) {
+    for (int d = 0; d < min(n, 2); ++d) {
       const bool last = tail(s0 + d);
 #pragma unroll
       for (int u = 0; u < LB; ++u) issue_b(last, d, u);
 #pragma unroll
       for (int u = 0; u < LA; ++u) issue_a(last, d, u);
     }
-    if (n >= D) wait_barrier<(D - 1) * (LA + LB)>();
+    if (n > 1) wait_barrier<LA + LB>();
     else wait_barrier<0>();
 #pragma unroll
     for (int i = 0; i < FM; ++i) read(0, 0, 0, i);
-    const bool ends = n > D && tail(s1 - 1);
-    for (int s = D + (ends ? 1 : 0); s < n; ++s) step(Int<1>(), Int<0>());
-    if (ends) step(Int<2>(), Int<0>());
-    if constexpr (D > 3)
-      if (n > 3) step(Int<0>(), Int<3>());
-    if constexpr (D > 2)
-      if (n > 2) step(Int<0>(), Int<2>());
+    const bool ends = n > 2 && tail(s1 - 1);
+    for (int s = ends ? 3 : 2; s < n; ++s) step(Int<1>(), Int<1>());
+    if (ends) step(Int<2>(), Int<1>());
     if (n > 1) step(Int<0>(), Int<1>());
     step(Int<0>(), Int<0>());
-    static_assert(D == 2 || D == 4, "the steps without loads");
-  }
-  // The groups' sums meet: each finishes the half of its rows that the other one
-  // gives it.  (Every wave joins as many barriers as those of the first group.)
-  constexpr int FH = FM / S::GROUPS;  // fragments of rows that a wave finishes
-  if constexpr (S::GROUPS == 2) {
-    for (int k = n > 0 ? n : -1; k < most; ++k) wait_barrier<0>();
-    v4i* give = reinterpret_cast<v4i*>(block_lds) + ((group_id * NW + wave) * FH * FN) * kWave + lane;
-    const v4i* take = reinterpret_cast<const v4i*>(block_lds) + (((1 - group_id) * NW + wave) * FH * FN) * kWave + lane;
-#pragma unroll
-    for (int i = 0; i < FH; ++i)
-#pragma unroll
-      for (int j = 0; j < FN; ++j) give[(i * FN + j) * kWave] = group_id == 0 ? acc[FH + i][j] : acc[i][j];
-    wait_barrier<0>();
-#pragma unroll
-    for (int i = 0; i < FH; ++i)
-#pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const v4i mine = group_id == 0 ? acc[i][j] : acc[FH + i][j], other = take[(i * FN + j) * kWave];
-        if constexpr (I8) acc[i][j] = mine + other;
-        else acc[i][j] = __builtin_bit_cast(v4i, __builtin_bit_cast(v4f, mine) + __builtin_bit_cast(v4f, other));
-      }
   }
   // A lane holds columns 4 (lane / 16) + 0 .. 3 of each 16 x 16 sums.  Of two
   // neighbours, the odd quarters of the wave give theirs of the first for the even
@@ -367,11 +324,11 @@ __device__ __forceinline__ void dense_block(const DenseGemm& p, int64_t b, int64
     hi = make_uint4(b[0], b[1], b[2], b[3]);
   };
   constexpr int kPairs = kUnits / 32;
-  const int64_t row0 = m0 + wm * WM + group_id * FH * 16 + (lane & 15);
+  const int64_t row0 = m0 + wm * WM + (lane & 15);
   if (p.split > 1) {
     uint32_t* sums = static_cast<uint32_t*>(p.part) + (int64_t)part * p.M * p.N;
 #pragma unroll
-    for (int i = 0; i < FH; ++i) {
+    for (int i = 0; i < FM; ++i) {
       const int64_t m = row0 + 16 * i;
 #pragma unroll
       for (int j = 0; j < (GATE ? 2 : 1) * kPairs; ++j) {
@@ -405,9 +362,9 @@ __device__ __forceinline__ void dense_block(const DenseGemm& p, int64_t b, int64
       col_scale[j] = load32(p.e.col_scale + (j / kPairs) * units + min(unit0 + 32 * (j % kPairs), units - 8));
   }
 #pragma unroll
-  for (int i = 0; i < FH; ++i) {
+  for (int i = 0; i < FM; ++i) {
     const int64_t m = row0 + 16 * i;
-    if (kDeep == 1 || i + 1 < FH) load(i + kDeep - 1);
+    if (kDeep == 1 || i + 1 < FM) load(i + kDeep - 1);
 #pragma unroll
     for (int j = 0; j < kPairs; ++j) {
       const int64_t unit = unit0 + 32 * j;
@@ -430,7 +387,7 @@ __device__ __forceinline__ void dense_block(const DenseGemm& p, int64_t b, int64
 }
 
 template <bool I8, bool AT, bool BT, int MODE, class S>
-__global__ __launch_bounds__(S::kThreads, 2) void k_dense(DenseGemm p) {
+__global__ __launch_bounds__(S::NW* kWave, 2) void k_dense(DenseGemm p) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
   dense_block<I8, AT, BT, MODE, S>(p, blockIdx.x, gridDim.x, lds);
 }
@@ -440,7 +397,7 @@ hipError_t launch_shape(const DenseGemm& p, hipStream_t st) {
   const int64_t blocks = dense_tiles(p) * p.split;
   if (blocks == 0) return hipSuccess;
   if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
-  k_dense<I8, AT, BT, MODE, S><<<(unsigned)blocks, S::kThreads, 0, st>>>(p);
+  k_dense<I8, AT, BT, MODE, S><<<(unsigned)blocks, S::NW * kWave, 0, st>>>(p);
   return hipGetLastError();
 }
 template <bool I8, bool AT, bool BT, int MODE>
