@@ -648,6 +648,8 @@ def int8_quantize(x, codes, scales, stream=None):
     [R, K] and scales float32 [R]: tokens, or the channels of a weight matrix."""
     dev, st = _current(x, stream)
     ty = _types()
+    if x.dim() != 2:
+        _refuse(f"x has shape {tuple(x.shape)}, rows and features are needed")
     R, K = x.shape
     kind = T_F32 if x.dtype in ty["f32"] else T_BF16
     _check(lib().moe_int8_quantize(
