@@ -591,8 +591,9 @@ moe_status moe_adapter_backward(const moe_adapter_dims* dims, const void* dout,
  * in bf16 with gradients, or with both products in 8-bit integers.  base is what
  * the layer gave.  Conventions as above: asynchronous on `stream`, no allocation,
  * no synchronisation, no memset, capturable, the same bits on every run.
- * num_tokens up to 2^26; row strides are multiples of 8 elements, at least the
- * features and at most 2^22; hidden * inter at most 2^30.  A workspace needs no
+ * num_tokens up to 2^26, with fewer than 2^37 results of a product; row strides are
+ * multiples of 8 elements, at least the features and at most 2^22; hidden * inter
+ * at most 2^30.  A workspace needs no
  * initialisation, calls that may run at the same time need their own, and one
  * of some number of tokens serves all smaller numbers too. */
 typedef struct {

@@ -75,6 +75,14 @@ moe_status check_base(const void* base, int64_t base_stride, const void* out, in
   return MOE_OK;
 }
 
+// Tiles of 64 x 128 by 256 threads, fewer than 2^32 of them in a launch.
+moe_status check_grid(int64_t rows, int64_t columns) {
+  if (ceil_div(rows, 64) * ceil_div(columns, 128) >= (int64_t)1 << 24)
+    return set_errorf(MOE_ERR_INVALID_ARG, "%lld tokens by %lld columns: more results than a launch holds",
+                      (long long)rows, (long long)columns);
+  return MOE_OK;
+}
+
 moe_status check_ffn(const moe_ffn_dims* d, int64_t num_tokens, int32_t unit, int32_t limit) {
   if (!d) return set_error(MOE_ERR_INVALID_ARG, "dims is null");
   MOE_RETURN_IF(check_tokens(num_tokens));
@@ -83,7 +91,7 @@ moe_status check_ffn(const moe_ffn_dims* d, int64_t num_tokens, int32_t unit, in
   if ((int64_t)d->hidden * d->inter > (int64_t)1 << 30)
     return set_errorf(MOE_ERR_INVALID_ARG, "hidden %d x inter %d: more than 2^30 weights a matrix",
                       d->hidden, d->inter);
-  return MOE_OK;
+  return check_grid(num_tokens, std::max(d->hidden, 2 * d->inter));
 }
 moe_status check_ffn_bf16(const moe_ffn_dims* d, int64_t num_tokens) {
   return check_ffn(d, num_tokens, 8, kMaxFeatures);
@@ -96,6 +104,7 @@ moe_status check_int8(const moe_int8_dims* d, int64_t num_tokens) {
   MOE_RETURN_IF(check_tokens(num_tokens));
   MOE_RETURN_IF(check_features(d->in_features, 16, kMaxInt8Features));
   MOE_RETURN_IF(check_features(d->out_features, 8, kMaxFeatures));
+  MOE_RETURN_IF(check_grid(num_tokens, d->out_features));
   return check_type(d->out_type, "output");
 }
 
@@ -109,7 +118,7 @@ moe_status check_int8(const moe_int8_dims* d, int64_t num_tokens) {
 //   256 x 256    1.40 + 15
 //   128 x 128    0.50 + 7.2         0.80 + 9.6
 //    64 x 128    0.44 + 4.0         0.60 + 5.5
-// a join 4 (with its launch) + 1 for 4 MB.  (The block in bf16, T tokens of 7168 x 2048, by 64, 128 and
+// a join 6.5 (with its launch on the host) + 1 for 4 MB.  (The block in bf16, T tokens of 7168 x 2048, by 64, 128 and
 // 256 rows: T = 64: 33, 35, -; 512: 86, 71, 91; 2048: 266, 180, 171.)
 constexpr int64_t kCus = 256, kMinPartSteps = 4;
 struct Cost {
@@ -127,7 +136,7 @@ double run_cost(int shape, int64_t blocks, double steps) {
   return (double)rounds * full + (rest > kCus ? full : rest > 0 ? steps * one.step + one.fixed : 0.0);
 }
 double join_cost(const DenseGemm& g, int64_t parts) {
-  return parts > 1 ? 4.0 + (double)parts * (double)g.M * (double)g.N * 1e-6 : 0.0;
+  return parts > 1 ? 6.5 + (double)parts * (double)g.M * (double)g.N * 1e-6 : 0.0;
 }
 int64_t steps_of(const DenseGemm& g, bool int8) { return ceil_div(g.K, moe::dense_step(int8)); }
 void set_parts(DenseGemm& g, int64_t steps, int64_t parts) {
@@ -154,42 +163,44 @@ void choose(DenseGemm& g, bool int8) {
   set_parts(g, steps, parts);
 }
 
-// Products of one launch, of one shape, their K cut into parts of `share` steps at
-// most.  Returns the estimate.
-double share_out(DenseGemm* g, int n, int shape, int64_t share) {
+// Two products of one launch, of one shape, their K cut into parts of `share` steps
+// at most.  Returns the estimate.
+double share_out(DenseGemm (&g)[2], int shape, int64_t share) {
   int64_t work = 0, blocks = 0, longest = 0;
   double joins = 0;
-  for (int q = 0; q < n; ++q) {
-    g[q].shape = shape;
-    const int64_t steps = steps_of(g[q], false), tiles = moe::dense_tiles(g[q]);
-    set_parts(g[q], steps, steps / share);
+  for (DenseGemm& q : g) {
+    q.shape = shape;
+    const int64_t steps = steps_of(q, false), tiles = moe::dense_tiles(q);
+    set_parts(q, steps, steps / share);
     if (tiles == 0) continue;
     work += tiles * steps;
-    blocks += tiles * g[q].split;
-    longest = std::max(longest, (int64_t)g[q].steps);
-    joins += join_cost(g[q], g[q].split);
+    blocks += tiles * q.split;
+    longest = std::max(longest, (int64_t)q.steps);
+    joins += join_cost(q, q.split);
   }
-  const double mean = blocks > 0 ? (double)work / (double)blocks : 0.0;
-  return joins + std::max(run_cost(shape, blocks, mean), run_cost(shape, std::min(blocks, kCus), (double)longest));
+  const Cost one = kOne[shape], all = shape == moe::kDenseBig ? one : kTwo[shape];
+  const double full = (double)work / (double)slots(shape) * all.step + (double)ceil_div(blocks, slots(shape)) * all.fixed;
+  const double least = (double)longest * one.step + one.fixed;
+  return joins + std::max(blocks > kCus ? full : 0.0, least);
 }
-void choose(DenseGemm* g, int n) {
+void choose(DenseGemm (&g)[2]) {
   double best = 1e300;
   int shape = 0;
   int64_t share = 1;
   for (int s : {(int)moe::kDenseBig, (int)moe::kDenseMid}) {
     int64_t work = 0;
-    for (int q = 0; q < n; ++q) {
-      g[q].shape = s;
-      work += moe::dense_tiles(g[q]) * steps_of(g[q], false);
+    for (DenseGemm& q : g) {
+      q.shape = s;
+      work += moe::dense_tiles(q) * steps_of(q, false);
     }
     // a block's fair share of the launch, or a longer one
     const int64_t fair = std::max(kMinPartSteps, ceil_div(work, slots(s)));
     for (int64_t m : {2, 3, 4, 8, 16, 1 << 20}) {
-      const double t = share_out(g, n, s, fair * m / 2);
+      const double t = share_out(g, s, fair * m / 2);
       if (t < best) best = t, shape = s, share = fair * m / 2;
     }
   }
-  share_out(g, n, shape, share);
+  share_out(g, shape, share);
 }
 // Room for the parts of a launch: at most as many tiles as run at once, 64 MB by the
 // largest; with at most `rows` x `columns` sums of at most K
@@ -205,13 +216,12 @@ size_t part_bytes(int64_t rows, int64_t columns, int64_t K, bool int8) {
 moe_status run_product(int mode, DenseGemm g, bool int8, void* parts, const char* what, hipStream_t stream) {
   // (T = 1 of 7168 x 2048: 23.0 us, by tiles 26.5; two rows read side by side took
   // 27.7, as by tiles)
-  if (g.M == 1 && mode != moe::kDenseDgate)
+  if (g.M == 1)
     return moe::check_hip(moe::launch_dense_one(int8, mode, g, stream), what, stream);
   choose(g, int8);
   g.part = parts;
-  MOE_RETURN_IF(moe::check_hip(mode == moe::kDenseDgate ? moe::launch_dense_dgate(g, stream)
-                               : int8 ? moe::launch_dense_gemm_int8(mode, g, stream)
-                                      : moe::launch_dense_gemm_bf16(mode, g, stream),
+  MOE_RETURN_IF(moe::check_hip(int8 ? moe::launch_dense_gemm_int8(mode, g, stream)
+                                    : moe::launch_dense_gemm_bf16(mode, g, stream),
                                what, stream));
   if (g.split > 1) MOE_RETURN_IF(moe::check_hip(moe::launch_dense_join(int8, mode, g, stream), what, stream));
   return MOE_OK;
@@ -237,18 +247,35 @@ void store_to(DenseGemm& g, void* out, int64_t stride, bool f32, const void* bas
   g.e.base_stride = base_stride;
 }
 
+// Two products in one launch, then the joins of their parts.
+moe_status run_pair(DenseGemm x, int mode, DenseGemm y, void* parts, size_t parts_y,
+                    hipError_t (*launch)(const DenseGemm&, const DenseGemm&, hipStream_t), const char* what,
+                    hipStream_t stream) {
+  DenseGemm g[2] = {x, y};
+  choose(g);
+  g[0].part = parts;
+  g[1].part = static_cast<uint8_t*>(parts) + parts_y;
+  MOE_RETURN_IF(moe::check_hip(launch(g[0], g[1], stream), what, stream));
+  for (int q = 0; q < 2; ++q)
+    if (g[q].M > 0 && g[q].split > 1)
+      MOE_RETURN_IF(moe::check_hip(moe::launch_dense_join(false, q == 0 ? mode : moe::kDenseStore, g[q], stream),
+                                   what, stream));
+  return MOE_OK;
+}
+
 // Workspace of the bf16 block: h or its gradients, then the parts.
 struct FfnLayout {
-  size_t gu_bytes, h_bytes, rows, part;
+  size_t gu_bytes, h_bytes, rows, part, dgate_part, dw1_part;
   FfnLayout(const moe_ffn_dims* d, int64_t T) {
     const int64_t H = d->hidden, I = d->inter;
     gu_bytes = align256((size_t)T * 2 * I * 2);
     h_bytes = align256((size_t)T * I * 2);
     rows = gu_bytes;  // the larger of h and the gradients of gate and up
-    // (the gradients of weights and input in one launch need room together)
-    part = std::max({part_bytes(T, 2 * I, H, false), part_bytes(T, H, I, false), part_bytes(T, I, H, false),
-                     part_bytes(T, H, 2 * I, false) + part_bytes(2 * I, H, T, false) +
-                         part_bytes(H, I, T, false)});
+    dgate_part = part_bytes(T, I, H, false);
+    dw1_part = part_bytes(2 * I, H, T, false);
+    // (two products of a launch need room together)
+    part = std::max({part_bytes(T, 2 * I, H, false), part_bytes(T, H, I, false),
+                     dgate_part + part_bytes(H, I, T, false), dw1_part + part_bytes(T, H, 2 * I, false)});
   }
   size_t workspace() const { return rows + part; }
   size_t saved() const { return gu_bytes + h_bytes; }
@@ -359,35 +386,28 @@ moe_status moe_ffn_backward(const moe_ffn_dims* dims, const void* dout, int64_t 
   uint8_t* dgu = static_cast<uint8_t*>(workspace);
   uint8_t* parts = T > 0 ? dgu + l.rows : nullptr;
   const uint8_t* h = T > 0 ? static_cast<const uint8_t*>(saved) + l.gu_bytes : nullptr;
+  DenseGemm dgate = {}, dw1_sum = {}, dw2_sum = {}, dx_sum = {};
   if (T > 0) {
-    DenseGemm dh = product(dout, dout_stride, w2, I, T, I, H, 2);
-    dh.e.out = dgu;
-    dh.e.inter = (int32_t)I;
-    dh.e.gu_in = static_cast<const uint16_t*>(saved);
-    MOE_RETURN_IF(run_product(moe::kDenseDgate, dh, false, parts, "block dh", stream));
+    dgate = product(dout, dout_stride, w2, I, T, I, H, 2);
+    dgate.e.out = dgu;
+    dgate.e.inter = (int32_t)I;
+    dgate.e.gu_in = static_cast<const uint16_t*>(saved);
   }
-  DenseGemm g[3] = {};  // dw1, dw2, dx
   if (dw1) {
     const bool f32 = dw_type == MOE_T_F32;
-    g[0] = product(dgu, 2 * I, x, T > 0 ? x_stride : H, 2 * I, H, T, 2);
-    store_to(g[0], dw1, H, f32, nullptr, 0);
-    g[1] = product(dout, T > 0 ? dout_stride : H, h, I, H, I, T, 2);
-    store_to(g[1], dw2, I, f32, nullptr, 0);
+    dw1_sum = product(dgu, 2 * I, x, T > 0 ? x_stride : H, 2 * I, H, T, 2);
+    store_to(dw1_sum, dw1, H, f32, nullptr, 0);
+    dw2_sum = product(dout, T > 0 ? dout_stride : H, h, I, H, I, T, 2);
+    store_to(dw2_sum, dw2, I, f32, nullptr, 0);
   }
   if (dx && T > 0) {
-    g[2] = product(dgu, 2 * I, w1, H, T, H, 2 * I, 2);
-    store_to(g[2], dx, dx_stride, false, dx_base, dx_base_stride);
+    dx_sum = product(dgu, 2 * I, w1, H, T, H, 2 * I, 2);
+    store_to(dx_sum, dx, dx_stride, false, dx_base, dx_base_stride);
   }
-  choose(g, 3);
-  for (DenseGemm& q : g) {
-    q.part = parts;
-    if (q.split > 1) parts += align256((size_t)q.split * q.M * q.N * 4);
-  }
-  MOE_RETURN_IF(moe::check_hip(moe::launch_dense_grads(g[0], g[1], g[2], stream), "block gradients", stream));
-  for (const DenseGemm& q : g)
-    if (q.M > 0 && q.split > 1)
-      MOE_RETURN_IF(moe::check_hip(moe::launch_dense_join(false, moe::kDenseStore, q, stream),
-                                   "block gradients' join", stream));
+  MOE_RETURN_IF(run_pair(dgate, moe::kDenseDgate, dw2_sum, parts, l.dgate_part, moe::launch_dense_dgate_dw2,
+                         "block gradients of gate, up and w2", stream));
+  MOE_RETURN_IF(run_pair(dw1_sum, moe::kDenseStore, dx_sum, parts, l.dw1_part, moe::launch_dense_dw1_dx,
+                         "block gradients of w1 and x", stream));
   return moe::set_ok();
 }
 

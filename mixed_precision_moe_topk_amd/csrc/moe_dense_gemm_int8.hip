@@ -1,5 +1,7 @@
 // Products of 8-bit integers with scales of tokens and channels, and the
 // quantiser of their rows.
+#include <algorithm>
+
 #include "moe_dense_gemm.h"
 
 namespace moe {
@@ -107,9 +109,11 @@ __device__ __forceinline__ void quant_row(int32_t cols, F values, int8_t* __rest
 }
 
 template <bool F32, int NT>
-__global__ __launch_bounds__(NT) void k_int8_quant(const void* __restrict__ x, int64_t stride, int32_t cols,
-                                                   int8_t* __restrict__ codes, float* __restrict__ scales) {
-  const int64_t row = blockIdx.x;
+__global__ __launch_bounds__(NT) void k_int8_quant(const void* __restrict__ x, int64_t stride, int64_t rows,
+                                                   int32_t cols, int8_t* __restrict__ codes,
+                                                   float* __restrict__ scales) {
+  const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (row >= rows) return;
   quant_row<NT, 4>(
       cols,
       [&](int c, float (&v)[8]) __attribute__((always_inline)) {
@@ -152,13 +156,15 @@ hipError_t launch_dense_join_quant(const DenseGemm& p, int8_t* codes, float* sca
 hipError_t launch_int8_quant(const void* x, bool x_f32, int64_t x_stride, int64_t rows, int32_t cols,
                              int8_t* codes, float* scales, hipStream_t st) {
   if (rows == 0) return hipSuccess;
-  if (rows > 0x7FFFFFFFLL) return hipErrorInvalidValue;
-  const unsigned g = (unsigned)rows;
+  // (a dimension of a grid holds fewer than 2^32 threads)
+  constexpr int64_t kRow = 1 << 20;
+  const dim3 g((unsigned)std::min(rows, kRow), (unsigned)((rows + kRow - 1) / kRow));
+  if (g.y > 65535) return hipErrorInvalidValue;
   const bool wide = cols > 2048;
-  if (x_f32 && wide) k_int8_quant<true, 256><<<g, 256, 0, st>>>(x, x_stride, cols, codes, scales);
-  else if (x_f32) k_int8_quant<true, 64><<<g, 64, 0, st>>>(x, x_stride, cols, codes, scales);
-  else if (wide) k_int8_quant<false, 256><<<g, 256, 0, st>>>(x, x_stride, cols, codes, scales);
-  else k_int8_quant<false, 64><<<g, 64, 0, st>>>(x, x_stride, cols, codes, scales);
+  if (x_f32 && wide) k_int8_quant<true, 256><<<g, 256, 0, st>>>(x, x_stride, rows, cols, codes, scales);
+  else if (x_f32) k_int8_quant<true, 64><<<g, 64, 0, st>>>(x, x_stride, rows, cols, codes, scales);
+  else if (wide) k_int8_quant<false, 256><<<g, 256, 0, st>>>(x, x_stride, rows, cols, codes, scales);
+  else k_int8_quant<false, 64><<<g, 64, 0, st>>>(x, x_stride, rows, cols, codes, scales);
   return hipGetLastError();
 }
 

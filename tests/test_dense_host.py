@@ -43,6 +43,8 @@ def test_sizes(L):
             assert _status(q, M.FfnDims(H, I), 4) == 1, (q, H, I)
     assert _status(M.ffn_int8_workspace_query, M.FfnDims(264, 512), 4) == 1  # 16 bytes of codes
     assert M.ffn_workspace_query(M.FfnDims(264, 512), 4) > 0
+    assert _status(M.ffn_workspace_query, M.FfnDims(4096, 512), 1 << 26) == 1  # 2^38 results
+    assert _status(M.int8_workspace_query, M.Int8Dims(256, 4096), 1 << 26) == 1
     for K, N, t in ((8, 512, "bf16"), (131072, 512, "bf16"), (256, 4, "f32"), (256, (1 << 18) + 8, "f32")):
         assert _status(M.int8_workspace_query, M.Int8Dims(K, N, t), 4) == 1
     bad = M.CInt8Dims(256, 512, 7)
