@@ -28,7 +28,7 @@ struct DenseEpilogue {
 
 // Tiles of a block.
 enum DenseShape : int {
-  kDenseBig = 0,  // 256 x 256, 8 waves
+  kDenseBig = 0,  // 256 x 256, 8 waves; see dense_halves
   kDenseMid = 1,  // 128 x 128, 4 waves, two blocks a CU
   kDenseLow = 2,  // 64 x 128, 4 waves, two blocks a CU; not for rows across k
 };
@@ -48,6 +48,7 @@ struct DenseGemm {
   int32_t shape;     // DenseShape
   int32_t split;     // parts of K, each summed by blocks of their own
   int32_t steps;     // K steps (128 bytes) of a part
+  int32_t halves;    // kDenseBig: so many tiles, the last, by two blocks each
   void* part;        // split > 1: sums [split, M, N], float32 or int32
   DenseEpilogue e;
 };
@@ -59,6 +60,15 @@ inline int64_t dense_tiles(const DenseGemm& p) {
   return (p.M + dense_rows(p.shape) - 1) / dense_rows(p.shape) *
          ((p.N + dense_columns(p.shape) - 1) / dense_columns(p.shape));
 }
+// Big tiles of a launch that two blocks of 256 x 128 each take: those of the last
+// round of 256 (one block a CU) when they are at most half of one, which then takes
+// little more than half as long.
+constexpr int64_t kCus = 256;
+inline int64_t dense_halves(int shape, int64_t tiles) {
+  const int64_t rest = tiles % kCus;
+  return shape == kDenseBig && rest <= kCus / 2 ? rest : 0;
+}
+inline int64_t dense_blocks(const DenseGemm& p) { return dense_tiles(p) * p.split + p.halves; }
 
 // Both operands along k: kDenseStore or kDenseGate.
 hipError_t launch_dense_gemm_bf16(int mode, const DenseGemm& p, hipStream_t st);

@@ -115,23 +115,28 @@ moe_status check_int8(const moe_int8_dims* d, int64_t num_tokens) {
 // grids of 4 to 64 steps, us a step and besides (launch, first reads, the sums' way
 // out), bf16 and int8 alike within a tenth:
 //                one block a CU     two
-//   256 x 256    1.40 + 15
+//   256 x 256    1.40 + 15         (256 x 128, the last round's: 0.80 + 10)
 //   128 x 128    0.50 + 7.2         0.80 + 9.6
 //    64 x 128    0.44 + 4.0         0.60 + 5.5
 // a join 6.5 (with its launch on the host) + 1 for 4 MB.  (The block in bf16, T tokens of 7168 x 2048, by 64, 128 and
 // 256 rows: T = 64: 33, 35, -; 512: 86, 71, 91; 2048: 266, 180, 171.)
-constexpr int64_t kCus = 256, kMinPartSteps = 4;
+constexpr int64_t kMinPartSteps = 4;
+using moe::kCus;
 struct Cost {
   double step, fixed;
 };
 constexpr Cost kOne[3] = {{1.40, 15.0}, {0.50, 7.2}, {0.44, 4.0}};
 constexpr Cost kTwo[3] = {{}, {0.80, 9.6}, {0.60, 5.5}};
 
+constexpr Cost kHalf = {0.80, 10.0};
+
 int64_t slots(int shape) { return shape == moe::kDenseBig ? kCus : 2 * kCus; }
 // `blocks` blocks of `steps` each.
 double run_cost(int shape, int64_t blocks, double steps) {
   const Cost one = kOne[shape], all = shape == moe::kDenseBig ? one : kTwo[shape];
   const int64_t rounds = blocks / slots(shape), rest = blocks % slots(shape);
+  if (moe::dense_halves(shape, blocks) > 0)
+    return (double)rounds * (steps * one.step + one.fixed) + steps * kHalf.step + kHalf.fixed;
   const double full = steps * all.step + all.fixed;
   return (double)rounds * full + (rest > kCus ? full : rest > 0 ? steps * one.step + one.fixed : 0.0);
 }
@@ -161,6 +166,7 @@ void choose(DenseGemm& g, bool int8) {
   }
   g.shape = shape;
   set_parts(g, steps, parts);
+  g.halves = (int32_t)moe::dense_halves(shape, moe::dense_tiles(g) * g.split);
 }
 
 // Two products of one launch, of one shape, their K cut into parts of `share` steps
@@ -179,6 +185,11 @@ double share_out(DenseGemm (&g)[2], int shape, int64_t share) {
     joins += join_cost(q, q.split);
   }
   const Cost one = kOne[shape], all = shape == moe::kDenseBig ? one : kTwo[shape];
+  g[0].halves = 0;
+  // (blocks of different lengths do not end in rounds)
+  const int64_t tiles_y = moe::dense_tiles(g[1]) * g[1].split;
+  g[1].halves = g[0].steps == g[1].steps || tiles_y == blocks
+                    ? (int32_t)std::min(moe::dense_halves(shape, blocks), tiles_y) : 0;
   const double full = (double)work / (double)slots(shape) * all.step + (double)ceil_div(blocks, slots(shape)) * all.fixed;
   const double least = (double)longest * one.step + one.fixed;
   return joins + std::max(blocks > kCus ? full : 0.0, least);

@@ -10,7 +10,7 @@ namespace moe {
 // the longer K, come first.
 struct DensePair {
   DenseGemm x, y;
-  int64_t blocks_x, first_y, blocks_y;
+  int64_t blocks_x, first_y;
 };
 
 // XT, XMODE: layout of x's rows and its mode; y's rows alike (columns across k).
@@ -19,18 +19,18 @@ __global__ __launch_bounds__(S::NW* kWave, 2) void k_dense_pair(DensePair g) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
   const int64_t b = blockIdx.x;
   if (b < g.first_y) {
-    if (b < g.blocks_x) dense::dense_block<false, XT, true, XMODE, S>(g.x, b, g.blocks_x, lds);
+    if (b < g.blocks_x) dense::dense_block<false, XT, true, XMODE, S>(g.x, b, lds);
   } else {
-    dense::dense_block<false, YT, true, kDenseStore, S>(g.y, b - g.first_y, g.blocks_y, lds);
+    dense::dense_block<false, YT, true, kDenseStore, S>(g.y, b - g.first_y, lds);
   }
 }
 
 template <bool XT, int XMODE, bool YT>
 hipError_t launch_pair(const DenseGemm& x, const DenseGemm& y, hipStream_t st) {
   if (x.shape != y.shape) return hipErrorInvalidValue;
-  DensePair g = {x, y, dense_tiles(x) * x.split, 0, dense_tiles(y) * y.split};
+  DensePair g = {x, y, dense_blocks(x), 0};
   g.first_y = (g.blocks_x + 7) / 8 * 8;
-  const int64_t blocks = g.first_y + g.blocks_y;
+  const int64_t blocks = g.first_y + dense_blocks(y);
   if (blocks == 0) return hipSuccess;
   if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
   const unsigned n = (unsigned)blocks;

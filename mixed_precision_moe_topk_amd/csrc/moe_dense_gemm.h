@@ -147,33 +147,19 @@ struct Shape {
   static_assert(kLds <= 160 * 1024, "LDS of a CU");
 };
 using Big = Shape<4, 2, 64, 128>;  // 256 x 256, 160 KB of LDS
+using Half = Shape<4, 2, 64, 64>;  // 256 x 128: half of a Big one, by as many waves
 using Mid = Shape<2, 2, 64, 64>;   // 128 x 128, 80 KB: two blocks a CU
 using Low = Shape<2, 2, 32, 64>;   // 64 x 128, 64 KB: two blocks a CU
 
-// Block b of `total` that share the product p.
+// Tile (mt, nt) of part `part` of the product p.
 template <bool I8, bool AT, bool BT, int MODE, class S>
-__device__ __forceinline__ void dense_block(const DenseGemm& p, int64_t b, int64_t total, uint8_t* lds) {
+__device__ __forceinline__ void dense_tile(const DenseGemm& p, int part, int64_t mt, int nt, uint8_t* lds) {
   constexpr int NW = S::NW, BM = S::BM, BN = S::BN, WAVES_N = S::WAVES_N, WM = S::WM, WN = S::WN;
   constexpr bool GATE = MODE == kDenseGate;
   using TA = Tile<BM, AT, NW>;
   using TB = Tile<BN, BT, NW>;
-  // Blocks go round the 8 XCDs: each takes a contiguous range of the tiles, in
-  // groups of 4 rows of tiles, so that the blocks at work on one XCD share their
-  // operands in its L2.
-  const int64_t tiles_m = (p.M + BM - 1) / BM;
-  const int tiles_n = (p.N + BN - 1) / BN;
-  const int64_t x = b & 7;
-  int64_t t = x * (total >> 3) + min(x, total & 7) + (b >> 3);
-  const int64_t tiles = tiles_m * tiles_n;
-  const int part = uniform((int)(t / tiles));
-  t -= part * tiles;
-  const int64_t group = t / (4 * tiles_n), first_m = group * 4;
-  const int gm = (int)min((int64_t)4, tiles_m - first_m);
-  const int r = (int)(t - group * 4 * tiles_n);
-  const int64_t m0 = (first_m + r % gm) * BM;
-  const int nt = r / gm;
-  const int64_t n0 = (int64_t)nt * BN;
-
+  const int64_t m0 = mt * BM, n0 = (int64_t)nt * BN;
+  if (n0 >= p.N) return;  // (a half behind the last column)
   const int wave = uniform((int)threadIdx.x / kWave), lane = lane_id();
   const int wm = wave / WAVES_N, wn = wave % WAVES_N;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
@@ -189,7 +175,7 @@ __device__ __forceinline__ void dense_block(const DenseGemm& p, int64_t b, int64
           [&](int row) { return min((int64_t)row, left_m - 1); });
   if constexpr (GATE) {
     // a wave's columns are as many gates, then the ups of the same hidden units
-    const int64_t inter = p.N / 2, c0 = (int64_t)nt * (BN / 2);
+    const int64_t inter = p.N / 2, c0 = n0 / 2;
     tb.init(p.b + c0 * p.b_stride, p.b_stride, left_n, s0, wave, [&](int row) {
       const int64_t unit = min(c0 + row / WN * (WN / 2) + row % (WN / 2), inter - 1);
       return unit - c0 + (row % WN >= WN / 2 ? inter : 0);
@@ -235,7 +221,6 @@ __device__ __forceinline__ void dense_block(const DenseGemm& p, int64_t b, int64
   // last fragments of step s, whose place they take.
   constexpr int FM = WM / 16, FN = WN / 16, kPerGroup = FN / FM;
   constexpr int LA = TA::kLoads, LB = TB::kLoads;
-  static_assert(LA % FM == 0 && LB % FM == 0, "as many loads every group");
   v4i af[2][FM], bf[2][FN];
   auto read = [&](int buf, int d, int h, int i) __attribute__((always_inline)) {
     const uint8_t* la = lds + a_stage(d);
@@ -386,15 +371,45 @@ __device__ __forceinline__ void dense_block(const DenseGemm& p, int64_t b, int64
   }
 }
 
+// Block b of those that share the product p (dense_blocks of them).  Blocks go round
+// the 8 XCDs: each takes a contiguous range of the tiles, in groups of 4 rows of
+// tiles, so that the blocks at work on one XCD share their operands in its L2.
+template <bool I8, bool AT, bool BT, int MODE, class S>
+__device__ __forceinline__ void dense_block(const DenseGemm& p, int64_t b, uint8_t* lds) {
+  const int64_t tiles_m = (p.M + S::BM - 1) / S::BM;
+  const int tiles_n = (p.N + S::BN - 1) / S::BN;
+  const int64_t tiles = tiles_m * tiles_n, all = tiles * p.split;
+  const int64_t halves = p.halves, whole = all - halves;
+  const bool half = b >= whole;
+  const int64_t total = half ? 2 * halves : whole, c = half ? b - whole : b, x = c & 7;
+  int64_t t = x * (total >> 3) + min(x, total & 7) + (c >> 3);
+  const int side = half ? (int)(t & 1) : 0;
+  if (half) t = whole + (t >> 1);
+  const int part = uniform((int)(t / tiles));
+  t -= part * tiles;
+  const int64_t group = t / (4 * tiles_n), first_m = group * 4;
+  const int gm = (int)min((int64_t)4, tiles_m - first_m);
+  const int r = (int)(t - group * 4 * tiles_n);
+  const int64_t mt = first_m + r % gm;
+  const int nt = r / gm;
+  if constexpr (S::BN == Big::BN) {
+    if (half) {
+      dense_tile<I8, AT, BT, MODE, Half>(p, part, mt, 2 * nt + side, lds);
+      return;
+    }
+  }
+  dense_tile<I8, AT, BT, MODE, S>(p, part, mt, nt, lds);
+}
+
 template <bool I8, bool AT, bool BT, int MODE, class S>
 __global__ __launch_bounds__(S::NW* kWave, 2) void k_dense(DenseGemm p) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
-  dense_block<I8, AT, BT, MODE, S>(p, blockIdx.x, gridDim.x, lds);
+  dense_block<I8, AT, BT, MODE, S>(p, blockIdx.x, lds);
 }
 
 template <bool I8, bool AT, bool BT, int MODE, class S>
 hipError_t launch_shape(const DenseGemm& p, hipStream_t st) {
-  const int64_t blocks = dense_tiles(p) * p.split;
+  const int64_t blocks = dense_blocks(p);
   if (blocks == 0) return hipSuccess;
   if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
   k_dense<I8, AT, BT, MODE, S><<<(unsigned)blocks, S::NW * kWave, 0, st>>>(p);
@@ -413,6 +428,7 @@ hipError_t launch(const DenseGemm& p, hipStream_t st) {
 }
 
 static_assert(Big::BM == dense_rows(kDenseBig) && Big::BN == dense_columns(kDenseBig), "tiles");
+static_assert(Half::BM == Big::BM && 2 * Half::BN == Big::BN && Half::NW == Big::NW && Half::kLds <= Big::kLds, "halves");
 static_assert(Mid::BM == dense_rows(kDenseMid) && Mid::BN == dense_columns(kDenseMid), "tiles");
 static_assert(Low::BM == dense_rows(kDenseLow) && Low::BN == dense_columns(kDenseLow), "tiles");
 

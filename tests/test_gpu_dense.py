@@ -179,7 +179,9 @@ def test_long_sums(T):
 
 
 # enough tiles of 256 x 256 for each product in turn, none of them whole
-@pytest.mark.parametrize("T, H, I", [(3589, 72, 3400), (3589, 3400, 72), (2309, 2824, 1416), (77, 4104, 3848)])
+# (the last three: a last round of tiles that two blocks each take, in every direction)
+@pytest.mark.parametrize("T, H, I", [(3589, 72, 3400), (3589, 3400, 72), (2309, 2824, 1416), (77, 4104, 3848),
+                                     (6140, 2056, 2040), (6140, 4040, 1032), (4090, 2552, 2048)])
 def test_large_tiles(T, H, I):
     b = Block(T, H, I, seed=2)
     f = b.forward()

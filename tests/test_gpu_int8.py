@@ -90,7 +90,8 @@ def product_case(T, K, N, out, base="given", pads=(0, 0), extreme=False, seed=0,
 @pytest.mark.parametrize("T, K, N", [
     (1, 16, 8), (1, 7168, 264), (2, 144, 72), (7, 528, 1000), (15, 4096, 136), (16, 256, 512), (17, 1040, 120),
     (33, 2064, 328), (64, 7168, 520), (65, 112, 136), (100, 1104, 200), (128, 128, 128), (129, 272, 264),
-    (257, 400, 520), (500, 7168, 264), (3600, 272, 3592), (7, 30000, 24)])
+    (257, 400, 520), (500, 7168, 264), (3600, 272, 3592), (7, 30000, 24),
+    (6140, 4112, 4040)])  # the last: a last round of tiles that two blocks each take
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 def test_product(T, K, N, out):
     product_case(T, K, N, out)
