@@ -602,7 +602,8 @@ typedef struct {
 } moe_ffn_dims;
 
 /* Bytes of the workspace of moe_ffn_apply and moe_ffn_backward, and of what the
- * forward pass saves for the backward pass (g, u and h of every token, bf16). */
+ * forward pass saves for the backward pass (12 bytes a token and hidden unit: g and
+ * u in float32, h in two bf16 terms). */
 moe_status moe_ffn_workspace_query(const moe_ffn_dims* dims, int64_t num_tokens, size_t* bytes);
 moe_status moe_ffn_saved_query(const moe_ffn_dims* dims, int64_t num_tokens, size_t* bytes);
 
@@ -637,8 +638,9 @@ moe_status moe_ffn_apply(const moe_ffn_dims* dims, const void* x, int64_t x_stri
  *          and dw2 are wanted
  *   dx_base: device bf16 [num_tokens, hidden]; may be dx (with the same stride);
  *          null: 0
- * Sums are float32; g, u and h are the forward pass's, rounded to bf16, and dg
- * and du are rounded to bf16 before the products behind them.
+ * Sums are float32.  For dx and for bf16 dw1 and dw2, dg, du and h enter the products
+ * rounded to bf16; for float dw1 and dw2 as two bf16 terms (within 2^-17), at twice
+ * those products' work.  (An infinity in x or dout may then come out as NaN.)
  * num_tokens = 0 writes zeros into dw1 and dw2, or returns MOE_OK without
  * launching when they are null.  Errors as moe_run_ws, and MOE_ERR_INVALID_ARG
  * when no gradient of some tokens is wanted. */

@@ -22,8 +22,9 @@ struct DenseEpilogue {
   int64_t out_stride;
   int32_t out_f32;         // float32 or bf16 out
   int32_t inter;
-  uint16_t* gu_out;        // kDenseGate: gate and up as bf16 [M, 2 inter], or null
-  const uint16_t* gu_in;   // kDenseDgate: the same
+  float* gu_out;           // kDenseGate: gate and up [M, 2 inter], or null
+  const float* gu_in;      // kDenseDgate: the same
+  uint16_t* out_lo;        // bf16 of kDenseGate and kDenseDgate: what out's rounding left, or null
 };
 
 // Tiles of a block.
@@ -42,12 +43,16 @@ struct DenseGemm {
   int64_t a_stride;  // bytes, as b_stride
   const uint8_t* b;
   int64_t b_stride;
+  // terms = 2: an operand is the sum of two bf16 matrices, the second so many bytes
+  // behind the first; 0 for the other operand, which has one
+  int32_t terms;
+  int64_t a_lo, b_lo;
   int64_t M;         // rows
   int32_t N;         // columns; kDenseGate: 2 inter
   int64_t K;
   int32_t shape;     // DenseShape
   int32_t split;     // parts of K, each summed by blocks of their own
-  int32_t steps;     // K steps (128 bytes) of a part
+  int32_t steps;     // K steps (128 bytes, of one term) of a part
   int32_t halves;    // kDenseBig: so many tiles, the last, by two blocks each
   void* part;        // split > 1: sums [split, M, N], float32 or int32
   DenseEpilogue e;

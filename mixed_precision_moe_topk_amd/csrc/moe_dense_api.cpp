@@ -143,7 +143,7 @@ double run_cost(int shape, int64_t blocks, double steps) {
 double join_cost(const DenseGemm& g, int64_t parts) {
   return parts > 1 ? 6.5 + (double)parts * (double)g.M * (double)g.N * 1e-6 : 0.0;
 }
-int64_t steps_of(const DenseGemm& g, bool int8) { return ceil_div(g.K, moe::dense_step(int8)); }
+int64_t steps_of(const DenseGemm& g, bool int8) { return ceil_div(g.K, moe::dense_step(int8)) * g.terms; }
 void set_parts(DenseGemm& g, int64_t steps, int64_t parts) {
   g.steps = (int32_t)std::max((int64_t)1, ceil_div(steps, std::max((int64_t)1, parts)));
   g.split = (int32_t)std::max((int64_t)1, ceil_div(steps, g.steps));
@@ -245,6 +245,7 @@ DenseGemm product(const void* a, int64_t a_stride, const void* b, int64_t b_stri
   g.a_stride = a_stride * element;
   g.b = static_cast<const uint8_t*>(b);
   g.b_stride = b_stride * element;
+  g.terms = 1;
   g.M = M;
   g.N = (int32_t)N;
   g.K = K;
@@ -274,19 +275,21 @@ moe_status run_pair(DenseGemm x, int mode, DenseGemm y, void* parts, size_t part
   return MOE_OK;
 }
 
-// Workspace of the bf16 block: h or its gradients, then the parts.
+// Workspace of the bf16 block: h or the gradients of gate and up in two terms, then
+// the parts.  Saved: gate and up, then h in two terms.
 struct FfnLayout {
   size_t gu_bytes, h_bytes, rows, part, dgate_part, dw1_part;
   FfnLayout(const moe_ffn_dims* d, int64_t T) {
     const int64_t H = d->hidden, I = d->inter;
-    gu_bytes = align256((size_t)T * 2 * I * 2);
-    h_bytes = align256((size_t)T * I * 2);
-    rows = gu_bytes;  // the larger of h and the gradients of gate and up
+    gu_bytes = align256((size_t)T * 2 * I * 4);
+    h_bytes = align256((size_t)T * 2 * I * 2);
+    rows = align256((size_t)T * 4 * I * 2);
     dgate_part = part_bytes(T, I, H, false);
-    dw1_part = part_bytes(2 * I, H, T, false);
-    // (two products of a launch need room together)
+    const int64_t twice = 2 * ceil_div(T, 64) * 64;
+    dw1_part = part_bytes(2 * I, H, twice, false);
+    // (two products of a launch need room together, the weights' for twice the terms)
     part = std::max({part_bytes(T, 2 * I, H, false), part_bytes(T, H, I, false),
-                     dgate_part + part_bytes(H, I, T, false), dw1_part + part_bytes(T, H, 2 * I, false)});
+                     dgate_part + part_bytes(H, I, twice, false), dw1_part + part_bytes(T, H, 2 * I, false)});
   }
   size_t workspace() const { return rows + part; }
   size_t saved() const { return gu_bytes + h_bytes; }
@@ -349,7 +352,8 @@ moe_status moe_ffn_apply(const moe_ffn_dims* dims, const void* x, int64_t x_stri
   DenseGemm up = product(x, x_stride, w1, H, T, 2 * I, H, 2);
   store_to(up, h, I, false, nullptr, 0);
   up.e.inter = (int32_t)I;
-  up.e.gu_out = static_cast<uint16_t*>(saved);
+  up.e.gu_out = static_cast<float*>(saved);
+  up.e.out_lo = saved ? reinterpret_cast<uint16_t*>(h) + T * I : nullptr;
   MOE_RETURN_IF(run_product(moe::kDenseGate, up, false, ws + l.rows, "block gate and up", stream));
   DenseGemm down = product(h, I, w2, I, T, H, I, 2);
   store_to(down, out, out_stride, false, base, base_stride);
@@ -402,14 +406,19 @@ moe_status moe_ffn_backward(const moe_ffn_dims* dims, const void* dout, int64_t 
     dgate = product(dout, dout_stride, w2, I, T, I, H, 2);
     dgate.e.out = dgu;
     dgate.e.inter = (int32_t)I;
-    dgate.e.gu_in = static_cast<const uint16_t*>(saved);
+    dgate.e.gu_in = static_cast<const float*>(saved);
+    if (dw1 && dw_type == MOE_T_F32) dgate.e.out_lo = reinterpret_cast<uint16_t*>(dgu) + T * 2 * I;
   }
   if (dw1) {
     const bool f32 = dw_type == MOE_T_F32;
     dw1_sum = product(dgu, 2 * I, x, T > 0 ? x_stride : H, 2 * I, H, T, 2);
     store_to(dw1_sum, dw1, H, f32, nullptr, 0);
+    dw1_sum.terms = f32 ? 2 : 1;
+    dw1_sum.a_lo = T * 2 * I * 2;
     dw2_sum = product(dout, T > 0 ? dout_stride : H, h, I, H, I, T, 2);
     store_to(dw2_sum, dw2, I, f32, nullptr, 0);
+    dw2_sum.terms = dw1_sum.terms;
+    dw2_sum.b_lo = T * I * 2;
   }
   if (dx && T > 0) {
     dx_sum = product(dgu, 2 * I, w1, H, T, H, 2 * I, 2);

@@ -14,18 +14,19 @@ struct DensePair {
 };
 
 // XT, XMODE: layout of x's rows and its mode; y's rows alike (columns across k).
-template <bool XT, int XMODE, bool YT, class S>
+// XTERMS, YTERMS: float32 gradients of weights take both terms of their operand.
+template <bool XT, int XMODE, bool YT, class S, int XTERMS, int YTERMS>
 __global__ __launch_bounds__(S::NW* kWave, 2) void k_dense_pair(DensePair g) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
   const int64_t b = blockIdx.x;
   if (b < g.first_y) {
-    if (b < g.blocks_x) dense::dense_block<false, XT, true, XMODE, S>(g.x, b, lds);
+    if (b < g.blocks_x) dense::dense_block<false, XT, true, XMODE, S, XTERMS>(g.x, b, lds);
   } else {
-    dense::dense_block<false, YT, true, kDenseStore, S>(g.y, b - g.first_y, lds);
+    dense::dense_block<false, YT, true, kDenseStore, S, YTERMS>(g.y, b - g.first_y, lds);
   }
 }
 
-template <bool XT, int XMODE, bool YT>
+template <bool XT, int XMODE, bool YT, int XTERMS, int YTERMS>
 hipError_t launch_pair(const DenseGemm& x, const DenseGemm& y, hipStream_t st) {
   if (x.shape != y.shape) return hipErrorInvalidValue;
   DensePair g = {x, y, dense_blocks(x), 0};
@@ -36,17 +37,19 @@ hipError_t launch_pair(const DenseGemm& x, const DenseGemm& y, hipStream_t st) {
   const unsigned n = (unsigned)blocks;
   using dense::Big;
   using dense::Mid;
-  if (x.shape == kDenseBig) k_dense_pair<XT, XMODE, YT, Big><<<n, Big::NW * kWave, 0, st>>>(g);
-  else if (x.shape == kDenseMid) k_dense_pair<XT, XMODE, YT, Mid><<<n, Mid::NW * kWave, 0, st>>>(g);
+  if (x.shape == kDenseBig) k_dense_pair<XT, XMODE, YT, Big, XTERMS, YTERMS><<<n, Big::NW * kWave, 0, st>>>(g);
+  else if (x.shape == kDenseMid) k_dense_pair<XT, XMODE, YT, Mid, XTERMS, YTERMS><<<n, Mid::NW * kWave, 0, st>>>(g);
   else return hipErrorInvalidValue;
   return hipGetLastError();
 }
 
 hipError_t launch_dense_dgate_dw2(const DenseGemm& dgate, const DenseGemm& dw2, hipStream_t st) {
-  return launch_pair<false, kDenseDgate, true>(dgate, dw2, st);
+  return dw2.terms == 2 ? launch_pair<false, kDenseDgate, true, 1, 2>(dgate, dw2, st)
+                        : launch_pair<false, kDenseDgate, true, 1, 1>(dgate, dw2, st);
 }
 hipError_t launch_dense_dw1_dx(const DenseGemm& dw1, const DenseGemm& dx, hipStream_t st) {
-  return launch_pair<true, kDenseStore, false>(dw1, dx, st);
+  return dw1.terms == 2 ? launch_pair<true, kDenseStore, false, 2, 1>(dw1, dx, st)
+                        : launch_pair<true, kDenseStore, false, 1, 1>(dw1, dx, st);
 }
 
 }  // namespace moe

@@ -16,6 +16,18 @@ __device__ __forceinline__ uint4 bf16_pack8(const float (&v)[8]) {
   return make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
                     bf16_pair(v[6], v[7]));
 }
+// What the rounding of v to bf16 (packed in `hi`) left, rounded in turn: together
+// within 2^-17 of v.  0 where that is not finite.
+__device__ __forceinline__ uint4 bf16_rest8(const float (&v)[8], const uint4& hi) {
+  const uint32_t w[4] = {hi.x, hi.y, hi.z, hi.w};
+  float r[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float h = __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+    r[j] = fabsf(h) < __builtin_inff() ? v[j] - h : 0.0f;
+  }
+  return bf16_pack8(r);
+}
 __device__ __forceinline__ void bf16_unpack8(const uint4& u, float (&v)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -77,11 +89,11 @@ struct Ahead<I8, kDenseGate> {
 // kDenseDgate: gates and ups of hidden units n .. n + 7 of row m.
 template <>
 struct Ahead<false, kDenseDgate> {
-  Bytes32 gu;
+  Bytes32 g, u;
   __device__ __forceinline__ void load(const DenseEpilogue& e, int64_t m, int64_t n) {
-    const uint16_t* in = e.gu_in + m * 2 * e.inter + n;
-    gu.lo = *reinterpret_cast<const uint4*>(in);
-    gu.hi = *reinterpret_cast<const uint4*>(in + e.inter);
+    const float* in = e.gu_in + m * 2 * e.inter + n;
+    g = load32(in);
+    u = load32(in + e.inter);
   }
 };
 
@@ -116,50 +128,61 @@ __device__ __forceinline__ void finish_store(const DenseEpilogue& e, int64_t m, 
 }
 
 // kDenseGate: gates and ups of hidden units n .. n + 7 of row m.  bf16: gate and
-// up are rounded once for the backward pass, h once for the second product (as
-// the layer's bf16 experts do); the products and silu are float32.
+// up stay float32 for the backward pass; h is rounded to bf16 for the second
+// product (as the layer's bf16 experts do), and what that leaves is kept for w2's
+// gradient in float32.
 template <bool I8>
 __device__ __forceinline__ void finish_gate(const DenseEpilogue& e, int64_t m, int64_t n, float (&g)[8],
                                             float (&u)[8]) {
   if (!I8 && e.gu_out) {
-    uint16_t* row = e.gu_out + m * 2 * e.inter + n;
-    *reinterpret_cast<uint4*>(row) = bf16_pack8(g);
-    *reinterpret_cast<uint4*>(row + e.inter) = bf16_pack8(u);
+    float* row = e.gu_out + m * 2 * e.inter + n;
+    store8(row, g);
+    store8(row + e.inter, u);
   }
   float h[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) h[j] = g[j] * sigmoid(g[j]) * u[j];
-  if constexpr (I8)
-    store8(static_cast<float*>(e.out) + m * e.out_stride + n, h);
-  else
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.out) + m * e.out_stride + n) = bf16_pack8(h);
+  const int64_t at = m * e.out_stride + n;
+  if constexpr (I8) {
+    store8(static_cast<float*>(e.out) + at, h);
+  } else {
+    const uint4 hi = bf16_pack8(h);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.out) + at) = hi;
+    if (e.out_lo) *reinterpret_cast<uint4*>(e.out_lo + at) = bf16_rest8(h, hi);
+  }
 }
 
 // kDenseDgate: v is the gradient of h = silu(gate) * up.  With s = sigmoid(gate),
-// dgate = v up s (1 + gate (1 - s)) and dup = v gate s, each rounded once to bf16,
-// the operands of the products behind.
+// dgate = v up s (1 + gate (1 - s)) and dup = v gate s, rounded to bf16 for the
+// products behind; what that leaves is kept for float32 gradients of w1.
 __device__ __forceinline__ void finish_dgate(const DenseEpilogue& e, int64_t m, int64_t n, float (&v)[8],
-                                             const Bytes32& gu) {
-  uint16_t* out = static_cast<uint16_t*>(e.out) + m * 2 * e.inter + n;
+                                             const Bytes32& gate, const Bytes32& up) {
+  const int64_t at = m * 2 * e.inter + n;
   float g[8], u[8];
-  bf16_unpack8(gu.lo, g);
-  bf16_unpack8(gu.hi, u);
+  floats(gate, g);
+  floats(up, u);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float s = sigmoid(g[j]);
-    const float up = v[j] * (g[j] * s);
+    const float du = v[j] * (g[j] * s);
     g[j] = v[j] * u[j] * s * (1.0f + g[j] * (1.0f - s));
-    u[j] = up;
+    u[j] = du;
   }
-  *reinterpret_cast<uint4*>(out) = bf16_pack8(g);
-  *reinterpret_cast<uint4*>(out + e.inter) = bf16_pack8(u);
+  uint16_t* out = static_cast<uint16_t*>(e.out) + at;
+  const uint4 dg = bf16_pack8(g), du = bf16_pack8(u);
+  *reinterpret_cast<uint4*>(out) = dg;
+  *reinterpret_cast<uint4*>(out + e.inter) = du;
+  if (e.out_lo) {
+    *reinterpret_cast<uint4*>(e.out_lo + at) = bf16_rest8(g, dg);
+    *reinterpret_cast<uint4*>(e.out_lo + at + e.inter) = bf16_rest8(u, du);
+  }
 }
 
 template <bool I8, int MODE>
 __device__ __forceinline__ void finish(const DenseEpilogue& e, int64_t m, int64_t n, float (&v)[8],
                                        const Ahead<I8, MODE>& ahead) {
   static_assert(MODE != kDenseGate, "gate and up are finished together");
-  if constexpr (MODE == kDenseDgate) finish_dgate(e, m, n, v, ahead.gu);
+  if constexpr (MODE == kDenseDgate) finish_dgate(e, m, n, v, ahead.g, ahead.u);
   else finish_store(e, m, n, v, ahead.base);
 }
 

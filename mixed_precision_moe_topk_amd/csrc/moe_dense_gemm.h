@@ -35,8 +35,9 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
   return (int64_t)(uint32_t)uniform((int)v) | (int64_t)uniform((int)(v >> 32)) << 32;
 }
 
-// One operand's tile of ROWS rows (or columns) in LDS, loaded by NW waves.
-template <int ROWS, bool ACROSS, int NW>
+// One operand's tile of ROWS rows (or columns) in LDS, loaded by NW waves.  TERMS = 2:
+// every K step comes twice, once for each term.
+template <int ROWS, bool ACROSS, int NW, int TERMS>
 struct Tile {
   static constexpr int kBytes = ROWS * kDenseStepBytes;
   static constexpr int kLoads = kBytes / 1024 / NW;  // 1-KB loads of a wave and step
@@ -44,7 +45,8 @@ struct Tile {
   static constexpr int kRowsPerLoad = ACROSS ? 64 / kPieces : 8;
 
   int64_t next;          // address of the K step to load next
-  int64_t advance;       // bytes of a K step
+  int64_t advance;       // bytes to the one behind it
+  int64_t advance2;      // TERMS = 2: and from that one on
   uint32_t off[kLoads];  // this lane's piece of each load
   int first;             // this lane's row (k row when across) of load 0
 
@@ -55,11 +57,19 @@ struct Tile {
   // rows: what is left of the operand from the tile on (the last one is repeated).
   // source(r): which row of the operand the tile's row r is.
   template <class F>
-  __device__ __forceinline__ void init(const uint8_t* p, int64_t stride, int64_t rows, int64_t step,
+  __device__ __forceinline__ void init(const uint8_t* p, int64_t stride, int64_t rows, int64_t step, int64_t lo,
                                        int wave, F source) {
     const int lane = lane_id();
-    advance = uniform(ACROSS ? stride * 64 : (int64_t)kDenseStepBytes);
-    next = uniform((int64_t)p + step * advance);
+    const int64_t whole = ACROSS ? stride * 64 : (int64_t)kDenseStepBytes;
+    if constexpr (TERMS == 2) {
+      const bool second = step & 1;
+      next = uniform((int64_t)p + (step >> 1) * whole + (second ? lo : 0));
+      advance = uniform(second ? whole - lo : lo);
+      advance2 = uniform(second ? lo : whole - lo);
+    } else {
+      advance = uniform(whole);
+      next = uniform((int64_t)p + step * whole);
+    }
     if constexpr (ACROSS) {
       first = wave * kRowsPerLoad + lane / kPieces;
 #pragma unroll
@@ -80,14 +90,23 @@ struct Tile {
   // Load u of the step at `next`; the last one moves on.
   __device__ __forceinline__ void issue(int u, uint32_t lds, int wave) {
     lds_dma16_s(reinterpret_cast<const uint8_t*>(next), off[u], lds + (u * NW + wave) * 1024);
-    if (u == kLoads - 1) next += advance;
+    if (u == kLoads - 1) move_on();
   }
-  // The same for the last step: `left` bytes of each row (along k) or k rows (across).
-  __device__ __forceinline__ void issue_tail(int u, int left, uint32_t lds, int wave) const {
+  __device__ __forceinline__ void move_on() {
+    next += advance;
+    if constexpr (TERMS == 2) {
+      const int64_t t = advance;
+      advance = advance2;
+      advance2 = t;
+    }
+  }
+  // The same for the end of k: `left` bytes of each row (along k) or k rows (across).
+  __device__ __forceinline__ void issue_tail(int u, int left, uint32_t lds, int wave) {
     const uint8_t* zero = reinterpret_cast<const uint8_t*>(&g_zero);
     const int r = first + u * NW * kRowsPerLoad;
     const bool in = ACROSS ? r < left : ((lane_id() ^ r) & 7) * 16 < left;
     lds_dma16(in ? reinterpret_cast<const uint8_t*>(next) + off[u] : zero, lds + (u * NW + wave) * 1024);
+    if (u == kLoads - 1) move_on();
   }
 };
 
@@ -152,12 +171,12 @@ using Mid = Shape<2, 2, 64, 64>;   // 128 x 128, 80 KB: two blocks a CU
 using Low = Shape<2, 2, 32, 64>;   // 64 x 128, 64 KB: two blocks a CU
 
 // Tile (mt, nt) of part `part` of the product p.
-template <bool I8, bool AT, bool BT, int MODE, class S>
+template <bool I8, bool AT, bool BT, int MODE, class S, int TERMS = 1>
 __device__ __forceinline__ void dense_tile(const DenseGemm& p, int part, int64_t mt, int nt, uint8_t* lds) {
   constexpr int NW = S::NW, BM = S::BM, BN = S::BN, WAVES_N = S::WAVES_N, WM = S::WM, WN = S::WN;
   constexpr bool GATE = MODE == kDenseGate;
-  using TA = Tile<BM, AT, NW>;
-  using TB = Tile<BN, BT, NW>;
+  using TA = Tile<BM, AT, NW, TERMS>;
+  using TB = Tile<BN, BT, NW, TERMS>;
   const int64_t m0 = mt * BM, n0 = (int64_t)nt * BN;
   if (n0 >= p.N) return;  // (a half behind the last column)
   const int wave = uniform((int)threadIdx.x / kWave), lane = lane_id();
@@ -165,23 +184,23 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& p, int part, int64_t
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
 
   constexpr int kStep = I8 ? 128 : 64;
-  const int all = uniform((int)((p.K + kStep - 1) / kStep));
+  const int all = uniform((int)((p.K + kStep - 1) / kStep)) * TERMS;
   const int s0 = min(all, part * p.steps), s1 = min(all, s0 + p.steps);
-  const int rest = (int)(p.K % kStep);  // of the last step, 0: whole
+  const int rest = (int)(p.K % kStep);  // of the last step (of each term), 0: whole
   TA ta;
   TB tb;
   const int64_t left_m = p.M - m0, left_n = p.N - n0;
-  ta.init(p.a + m0 * (AT ? 2 : p.a_stride), p.a_stride, left_m, s0, wave,
+  ta.init(p.a + m0 * (AT ? 2 : p.a_stride), p.a_stride, left_m, s0, p.a_lo, wave,
           [&](int row) { return min((int64_t)row, left_m - 1); });
   if constexpr (GATE) {
     // a wave's columns are as many gates, then the ups of the same hidden units
     const int64_t inter = p.N / 2, c0 = n0 / 2;
-    tb.init(p.b + c0 * p.b_stride, p.b_stride, left_n, s0, wave, [&](int row) {
+    tb.init(p.b + c0 * p.b_stride, p.b_stride, left_n, s0, p.b_lo, wave, [&](int row) {
       const int64_t unit = min(c0 + row / WN * (WN / 2) + row % (WN / 2), inter - 1);
       return unit - c0 + (row % WN >= WN / 2 ? inter : 0);
     });
   } else {
-    tb.init(p.b + n0 * (BT ? 2 : p.b_stride), p.b_stride, left_n, s0, wave,
+    tb.init(p.b + n0 * (BT ? 2 : p.b_stride), p.b_stride, left_n, s0, p.b_lo, wave,
             [&](int row) { return min((int64_t)row, left_n - 1); });
   }
   Fragments<BM, AT, WM> fa;
@@ -195,7 +214,7 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& p, int part, int64_t
 #pragma unroll
     for (int j = 0; j < WN / 16; ++j) acc[i][j] = v4i{0, 0, 0, 0};
 
-  auto tail = [&](int s) __attribute__((always_inline)) { return rest != 0 && s == all - 1; };
+  auto tail = [&](int s) __attribute__((always_inline)) { return rest != 0 && s >= all - TERMS; };
   // rows: stages s % 2; columns: stages s % 3
   int a_cur = 0, b_cur = 0;  // stages of the step at work, relative to the first
   auto a_stage = [&](int d) __attribute__((always_inline)) { return (uint32_t)((a_cur + d) & 1) * TA::kBytes; };
@@ -286,9 +305,11 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& p, int part, int64_t
     else wait_barrier<0>();
 #pragma unroll
     for (int i = 0; i < FM; ++i) read(0, 0, 0, i);
-    const bool ends = n > 2 && tail(s1 - 1);
-    for (int s = ends ? 3 : 2; s < n; ++s) step(Int<1>(), Int<1>());
-    if (ends) step(Int<2>(), Int<1>());
+    int ends = n > 2 && tail(s1 - 1);  // steps behind the first two that hold the end of k
+    if (TERMS == 2) ends += n > 3 && tail(s1 - 2);
+    for (int s = 2 + ends; s < n; ++s) step(Int<1>(), Int<1>());
+    if (ends > 0) step(Int<2>(), Int<1>());
+    if (TERMS == 2 && ends > 1) step(Int<2>(), Int<1>());
     if (n > 1) step(Int<0>(), Int<1>());
     step(Int<0>(), Int<0>());
   }
@@ -329,8 +350,8 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& p, int part, int64_t
     return;
   }
   // reads of a group of rows are under way while the one before is finished (int8:
-  // the columns' scales take the registers)
-  constexpr int kDeep = I8 ? 1 : 2;
+  // the columns' scales take the registers; float32 gates and ups are too many)
+  constexpr int kDeep = I8 || MODE == kDenseDgate ? 1 : 2;
   Ahead<I8, MODE> ahead[kDeep][kPairs];
   float row_scale = 1.0f;
   Bytes32 col_scale[I8 ? (GATE ? 2 : 1) * kPairs : 1];
@@ -374,7 +395,7 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& p, int part, int64_t
 // Block b of those that share the product p (dense_blocks of them).  Blocks go round
 // the 8 XCDs: each takes a contiguous range of the tiles, in groups of 4 rows of
 // tiles, so that the blocks at work on one XCD share their operands in its L2.
-template <bool I8, bool AT, bool BT, int MODE, class S>
+template <bool I8, bool AT, bool BT, int MODE, class S, int TERMS = 1>
 __device__ __forceinline__ void dense_block(const DenseGemm& p, int64_t b, uint8_t* lds) {
   const int64_t tiles_m = (p.M + S::BM - 1) / S::BM;
   const int tiles_n = (p.N + S::BN - 1) / S::BN;
@@ -394,20 +415,20 @@ __device__ __forceinline__ void dense_block(const DenseGemm& p, int64_t b, uint8
   const int nt = r / gm;
   if constexpr (S::BN == Big::BN) {
     if (half) {
-      dense_tile<I8, AT, BT, MODE, Half>(p, part, mt, 2 * nt + side, lds);
+      dense_tile<I8, AT, BT, MODE, Half, TERMS>(p, part, mt, 2 * nt + side, lds);
       return;
     }
   }
-  dense_tile<I8, AT, BT, MODE, S>(p, part, mt, nt, lds);
+  dense_tile<I8, AT, BT, MODE, S, TERMS>(p, part, mt, nt, lds);
 }
 
-template <bool I8, bool AT, bool BT, int MODE, class S>
+template <bool I8, bool AT, bool BT, int MODE, class S, int TERMS = 1>
 __global__ __launch_bounds__(S::NW* kWave, 2) void k_dense(DenseGemm p) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
-  dense_block<I8, AT, BT, MODE, S>(p, blockIdx.x, lds);
+  dense_block<I8, AT, BT, MODE, S, TERMS>(p, blockIdx.x, lds);
 }
 
-template <bool I8, bool AT, bool BT, int MODE, class S>
+template <bool I8, bool AT, bool BT, int MODE, class S, int TERMS = 1>
 hipError_t launch_shape(const DenseGemm& p, hipStream_t st) {
   const int64_t blocks = dense_blocks(p);
   if (blocks == 0) return hipSuccess;

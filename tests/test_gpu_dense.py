@@ -3,12 +3,15 @@
 product of the operands that the GPU itself rounded (g, u, h in what the forward
 pass saves, the gradients of g and u in the workspace), and the roundings with the
 formulas, so that no tolerance has to cover a rounding that a later sum hides.
+float32 gradients of the weights are compared with the formulas end to end besides.
 
 Tolerances, element by element: a sum of n products of bf16 numbers in float32 is
 off by at most (n + 34) 2^-23 of the sum of its absolute terms (each addition
 rounds or truncates once, some 34 of them in joins and bases); sigmoid is off by
 2^-21 and 2^-23 |g| of itself (the exponential's argument, rounded twice, and a
-reciprocal of one step); a bf16 result by half a step, 2^-8 of itself."""
+reciprocal of one step); a bf16 result by half a step, 2^-8 of itself, one in two
+bf16 terms by 2^-17 (the first leaves 2^-8 of it at most, and half a step of that
+is 2^-9 of its own power of two)."""
 import numpy as np
 import pytest
 
@@ -17,7 +20,7 @@ from oracle import formats as F
 
 pytestmark = pytest.mark.gpu
 STEP = 2.0 ** -23
-HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24, "two terms": 2.0 ** -17}
 
 
 def bf16(x):
@@ -87,9 +90,10 @@ class Block:
         self.kept = d, x, w1, w2, sv
         r = {"out": host(out)}
         if saved:
-            gu = sv[:T * 2 * I * 2].view(torch.bfloat16).view(T, 2 * I)
-            at = (T * 2 * I * 2 + 255) // 256 * 256
-            r.update(g=host(gu[:, :I]), u=host(gu[:, I:]), h=host(sv[at:at + T * I * 2].view(torch.bfloat16).view(T, I)))
+            gu = sv[:T * 2 * I * 4].view(torch.float32).view(T, 2 * I)
+            at = (T * 2 * I * 4 + 255) // 256 * 256
+            h = sv[at:at + T * 2 * I * 2].view(torch.bfloat16).view(2, T, I)
+            r.update(g=host(gu[:, :I]), u=host(gu[:, I:]), h=host(h[0]), h2=host(h[0]) + host(h[1]))
         return r
 
     def check_forward(self, r, base="given"):
@@ -97,12 +101,13 @@ class Block:
         I = self.dims[2]
         g, eg = product(x, w1[:I])
         u, eu = product(x, w1[I:])
-        close("g", r["g"], g, rounded(g, eg, "bf16"))
-        close("u", r["u"], u, rounded(u, eu, "bf16"))
+        close("g", r["g"], g, rounded(g, eg, "f32"))
+        close("u", r["u"], u, rounded(u, eu, "f32"))
         # |d silu| <= 1.1; |silu(g)| <= |g|
         h = OD.silu_mul(g, u)
         eh = 1.1 * np.abs(u) * eg + np.abs(g) * eu + 1.1 * eg * eu + (2.0 ** -20 + 2 * STEP * np.abs(g)) * np.abs(h)
         close("h", r["h"], h, rounded(h, eh, "bf16"))
+        close("h in two terms", r["h2"], h, rounded(h, eh, "two terms"))
         out, eo = product(r["h"], w2, 0.0 if base == "none" else self.base.astype(np.float64))
         close("out", r["out"], out, rounded(out, eo, "bf16"))
 
@@ -123,13 +128,15 @@ class Block:
         r = {} if out is None else {"dx": host(out)}
         if weights:
             r.update(dw1=host(dw1), dw2=host(dw2))
-        dgu = host(ws[:T * 4 * I].view(torch.bfloat16).view(T, 2 * I))
-        r.update(dg=dgu[:, :I], du=dgu[:, I:])
+        dgu = ws[:T * 8 * I].view(torch.bfloat16).view(2, T, 2 * I)
+        r["dgu"] = host(dgu[0])
+        if weights and kind == "f32":
+            r["dgu2"] = host(dgu[0]) + host(dgu[1])
         return r
 
     def check_backward(self, f, r, kind="f32", dx="base"):
         x, w1, w2, dout = (v.astype(np.float64) for v in (self.x, self.w1, self.w2, self.dout))
-        g, u, h = f["g"], f["u"], f["h"]
+        g, u = f["g"], f["u"]
         dh, ed = product(dout, w2.T)
         dg, du = OD.silu_mul_backward(g, u, dh)
         s = OD.sigmoid(g)
@@ -139,17 +146,32 @@ class Block:
         part = np.abs(1 + g * (1 - s))
         # sigmoid enters dg three times, once times g; a few products round besides
         eg = np.abs(u) * s * part * ed + np.abs(dh * u) * s * (es * (part + np.abs(g)) + 8 * STEP * (1 + np.abs(g)))
-        close("dg", r["dg"], dg, rounded(dg, eg, "bf16") + 2.0 ** -126)
-        close("du", r["du"], du, rounded(du, np.abs(g) * s * (ed + np.abs(dh) * (es + 8 * STEP)), "bf16") + 2.0 ** -126)
-        d = np.concatenate([r["dg"], r["du"]], axis=1)
+        eu = np.abs(g) * s * (ed + np.abs(dh) * (es + 8 * STEP))
+        want, err = np.concatenate([dg, du], axis=1), np.concatenate([eg, eu], axis=1)
+        close("dg, du", r["dgu"], want, rounded(want, err, "bf16") + 2.0 ** -126)
+        terms = 1
+        d, h = r["dgu"], f["h"]
+        if "dgu2" in r:
+            close("dg, du in two terms", r["dgu2"], want, rounded(want, err, "two terms") + 2.0 ** -126)
+            terms, h = 2, f["h2"]
         if "dx" in r:
             want, err = product(d, w1.T, 0.0 if dx == "no base" else self.dxb.astype(np.float64))
             close("dx", r["dx"], want, rounded(want, err, "bf16"))
         if "dw1" in r:
-            want, err = product(d.T, x.T)
-            close("dw1", r["dw1"], want, rounded(want, err, kind))
-            want, err = product(dout.T, h.T)
-            close("dw2", r["dw2"], want, rounded(want, err, kind))
+            for name, a, b in (("dw1", r["dgu2"] if terms == 2 else d, x), ("dw2", dout, h)):
+                want = a.T @ b
+                err = (terms * a.shape[0] + 34) * STEP * (1 + 2.0 ** -7) * (np.abs(a).T @ np.abs(b))
+                close(name, r[name], want, rounded(want, err, kind))
+
+    def check_precise(self, r):
+        """float32 gradients of the weights against the formulas, end to end: in the
+        2-norm, where errors of either sign do not add up, 2^-17 of the operands is
+        at most 2^-17 of a result without cancellation; 8 times that is far below what
+        one bf16 term (2^-9 and more of the norm) would leave."""
+        x, w1, w2, dout = (v.astype(np.float64) for v in (self.x, self.w1, self.w2, self.dout))
+        _, dw1, dw2 = OD.ffn_backward(dout, x, w1, w2)
+        for name, want in (("dw1", dw1), ("dw2", dw2)):
+            assert np.linalg.norm(r[name] - want) <= 2.0 ** -14 * np.linalg.norm(want), name
 
 
 SMALL = [
@@ -166,7 +188,9 @@ def test_forward_and_backward(T, H, I):
     b = Block(T, H, I)
     f = b.forward()
     b.check_forward(f)
-    b.check_backward(f, b.backward())
+    r = b.backward()
+    b.check_backward(f, r)
+    b.check_precise(r)
 
 
 # few rows with long sums: K in parts, and the kernels of few tokens
@@ -176,6 +200,7 @@ def test_long_sums(T):
     f = b.forward()
     b.check_forward(f)
     b.check_backward(f, b.backward("bf16"), "bf16")
+    b.check_precise(b.backward())
 
 
 # enough tiles of 256 x 256 for each product in turn, none of them whole

@@ -39,7 +39,7 @@ def test_beside_the_layer(T):
     M.run_ws(p.dims, p.h_dev, p.l_dev, p.weights, p.scales, k, out, layer_ws)
     routed = bits(out)
     M.ffn_apply(d, p.h_dev, w1, w2, out, out, ws, saved=saved)
-    h = host(saved[(T * 4 * 136 + 255) // 256 * 256:][:T * 2 * 136].view(torch.bfloat16).view(T, 136))
+    h = host(saved[(T * 8 * 136 + 255) // 256 * 256:][:T * 2 * 136].view(torch.bfloat16).view(T, 136))
     want, err = product(h, b.w2.astype(np.float64), routed)
     close("out", bits(out), want, rounded(want, err, "bf16"))
 
@@ -56,11 +56,11 @@ def test_beside_the_layer(T):
     dx = device(b.dxb)
     dw1, dw2 = torch.empty(w1.shape, device="cuda"), torch.empty(w2.shape, device="cuda")
     M.ffn_backward(d, dout, p.h_dev, w1, w2, saved, dw1, dw2, ws, dx=dx, dx_base=dx)
-    dgu = host(ws[:T * 4 * 136].view(torch.bfloat16).view(T, 272))
+    dgu, rest = host(ws[:T * 8 * 136].view(torch.bfloat16).view(2, T, 272))
     want, err = product(dgu, b.w1.T.astype(np.float64), b.dxb.astype(np.float64))
     close("dx", host(dx), want, rounded(want, err, "bf16"))
-    want, err = product(dgu.T, b.x.T.astype(np.float64))
-    close("dw1", host(dw1), want, rounded(want, err, "f32"))
+    want, err = product((dgu + rest).T, b.x.T.astype(np.float64))
+    close("dw1", host(dw1), want, rounded(want, 2 * err, "f32"))
 
     # serving: the same weights in 8 bits
     e = Block8(T, H, 144, seed=12)
@@ -238,13 +238,14 @@ def test_long_batches():
     dw1, dw2 = torch.empty(w1.shape, device="cuda"), torch.empty(w2.shape, device="cuda")
     M.ffn_apply(d, x, w1, w2, None, out, ws, saved=saved)
     M.ffn_backward(d, dout, x, w1, w2, saved, dw1, dw2, ws, dx=dx)
-    h = saved[(T * 4 * I + 255) // 256 * 256:][:T * 2 * I].view(torch.bfloat16).view(T, I).double()
-    dgu = ws[:T * 4 * I].view(torch.bfloat16).view(T, 2 * I).double()
+    h = saved[(T * 8 * I + 255) // 256 * 256:][:T * 4 * I].view(torch.bfloat16).view(2, T, I).double()
+    dgu = ws[:T * 8 * I].view(torch.bfloat16).view(2, T, 2 * I).double()
     f = lambda t: t.double()  # noqa: E731
-    for name, got, a, c, kind in (("out", out, h, f(w2).T, 2.0 ** -8), ("dx", dx, dgu, f(w1), 2.0 ** -8),
-                                  ("dw1", dw1, dgu.T, f(x), 2.0 ** -24), ("dw2", dw2, f(dout).T, h, 2.0 ** -24)):
+    for name, got, a, c, kind in (("out", out, h[0], f(w2).T, 2.0 ** -8), ("dx", dx, dgu[0], f(w1), 2.0 ** -8),
+                                  ("dw1", dw1, dgu.sum(0).T, f(x), 2.0 ** -24),
+                                  ("dw2", dw2, f(dout).T, h.sum(0), 2.0 ** -24)):
         want, bound = a @ c, a.abs() @ c.abs()
-        err = (a.shape[1] + 34) * STEP * bound
+        err = (2 * a.shape[1] + 34) * STEP * bound
         assert ((f(got) - want).abs() <= err + kind * (want.abs() + err)).all(), name
 
 
