@@ -80,11 +80,11 @@ hipError_t launch_dense_gemm_bf16(int mode, const DenseGemm& p, hipStream_t st);
 hipError_t launch_dense_gemm_int8(int mode, const DenseGemm& p, hipStream_t st);
 // The same for M = 1, without parts.
 hipError_t launch_dense_one(bool int8, int mode, const DenseGemm& p, hipStream_t st);
-// The gradients of gate and up (columns across k) with dw2 (both across k), dw1
-// (both) with dx (columns): a launch each, both products of one shape (kDenseBig or
-// kDenseMid); one with M = 0 is left out.
-hipError_t launch_dense_dgate_dw2(const DenseGemm& dgate, const DenseGemm& dw2, hipStream_t st);
-hipError_t launch_dense_dw1_dx(const DenseGemm& dw1, const DenseGemm& dx, hipStream_t st);
+// The gradients of gate and up (columns across k).
+hipError_t launch_dense_dgate(const DenseGemm& p, hipStream_t st);
+// dw1, dw2 (both operands across k) and dx (columns) in one launch, all of one shape
+// (kDenseBig or kDenseMid); one with M = 0 is left out.
+hipError_t launch_dense_grads(const DenseGemm (&p)[3], hipStream_t st);
 // Adds up the parts (split > 1) and finishes them.
 hipError_t launch_dense_join(bool int8, int mode, const DenseGemm& p, hipStream_t st);
 

@@ -169,32 +169,70 @@ void choose(DenseGemm& g, bool int8) {
   g.halves = (int32_t)moe::dense_halves(shape, moe::dense_tiles(g) * g.split);
 }
 
-// Two products of one launch, of one shape, their K cut into parts of `share` steps
-// at most.  Returns the estimate.
-double share_out(DenseGemm (&g)[2], int shape, int64_t share) {
-  int64_t work = 0, blocks = 0, longest = 0;
-  double joins = 0;
+// Products of one launch, of one shape, their K cut into parts of `share` steps at
+// most.  Returns the estimate: blocks taken in the order of the launch (longer sums
+// first) by whichever slot is free.
+double share_out(DenseGemm (&g)[3], int shape, int64_t share) {
+  int64_t blocks = 0;
+  double total = 0, joins = 0;
+  DenseGemm* order[3] = {&g[0], &g[1], &g[2]};
+  const Cost each = shape == moe::kDenseBig ? kOne[shape] : kTwo[shape];
   for (DenseGemm& q : g) {
     q.shape = shape;
-    const int64_t steps = steps_of(q, false), tiles = moe::dense_tiles(q);
+    q.halves = 0;
+    const int64_t steps = steps_of(q, false);
     set_parts(q, steps, steps / share);
-    if (tiles == 0) continue;
-    work += tiles * steps;
-    blocks += tiles * q.split;
-    longest = std::max(longest, (int64_t)q.steps);
+    const int64_t n = moe::dense_tiles(q) * q.split;
+    if (n == 0) continue;
+    blocks += n;
+    total += (double)n * ((double)q.steps * each.step + each.fixed);
     joins += join_cost(q, q.split);
   }
-  const Cost one = kOne[shape], all = shape == moe::kDenseBig ? one : kTwo[shape];
-  g[0].halves = 0;
-  // (blocks of different lengths do not end in rounds)
-  const int64_t tiles_y = moe::dense_tiles(g[1]) * g[1].split;
-  g[1].halves = g[0].steps == g[1].steps || tiles_y == blocks
-                    ? (int32_t)std::min(moe::dense_halves(shape, blocks), tiles_y) : 0;
-  const double full = (double)work / (double)slots(shape) * all.step + (double)ceil_div(blocks, slots(shape)) * all.fixed;
-  const double least = (double)longest * one.step + one.fixed;
-  return joins + std::max(blocks > kCus ? full : 0.0, least);
+  std::stable_sort(order, order + 3, [](const DenseGemm* a, const DenseGemm* b) { return a->steps > b->steps; });
+  // where all blocks are as long, those of the last round may be cut in two
+  bool alike = true;
+  const DenseGemm* last = nullptr;
+  for (DenseGemm* q : order)
+    if (moe::dense_tiles(*q) > 0) {
+      alike = alike && (!last || last->steps == q->steps);
+      last = q;
+    }
+  if (!last) return 0.0;
+  if (alike) {
+    DenseGemm& q = *const_cast<DenseGemm*>(last);
+    q.halves = (int32_t)std::min(moe::dense_halves(shape, blocks), moe::dense_tiles(q) * q.split);
+    return joins + run_cost(shape, blocks, (double)q.steps);
+  }
+  if (blocks > 64 * slots(shape)) return joins + total / (double)slots(shape);
+  struct Free {
+    double at;
+    int64_t n;
+  } free[8] = {{0.0, slots(shape)}};
+  int groups = 1;
+  double end = 0;
+  for (const DenseGemm* q : order) {
+    const double cost = (double)q->steps * each.step + each.fixed;
+    for (int64_t n = moe::dense_tiles(*q) * q->split; n > 0;) {
+      int f = 0;
+      for (int k = 1; k < groups; ++k)
+        if (free[k].at < free[f].at) f = k;
+      const int64_t take = std::min(n, free[f].n);
+      const double done = free[f].at + cost;
+      n -= take;
+      end = std::max(end, done);
+      free[f].n -= take;
+      if (free[f].n == 0) free[f] = free[--groups];
+      int into = -1;
+      for (int k = 0; k < groups; ++k)
+        if (free[k].at == done) into = k;
+      if (into < 0 && groups == 8) return joins + std::max(end, total / (double)slots(shape));
+      if (into < 0) free[into = groups++] = {done, 0};
+      free[into].n += take;
+    }
+  }
+  return joins + end;
 }
-void choose(DenseGemm (&g)[2]) {
+void choose(DenseGemm (&g)[3]) {
   double best = 1e300;
   int shape = 0;
   int64_t share = 1;
@@ -227,12 +265,13 @@ size_t part_bytes(int64_t rows, int64_t columns, int64_t K, bool int8) {
 moe_status run_product(int mode, DenseGemm g, bool int8, void* parts, const char* what, hipStream_t stream) {
   // (T = 1 of 7168 x 2048: 23.0 us, by tiles 26.5; two rows read side by side took
   // 27.7, as by tiles)
-  if (g.M == 1)
+  if (g.M == 1 && mode != moe::kDenseDgate)
     return moe::check_hip(moe::launch_dense_one(int8, mode, g, stream), what, stream);
   choose(g, int8);
   g.part = parts;
-  MOE_RETURN_IF(moe::check_hip(int8 ? moe::launch_dense_gemm_int8(mode, g, stream)
-                                    : moe::launch_dense_gemm_bf16(mode, g, stream),
+  MOE_RETURN_IF(moe::check_hip(mode == moe::kDenseDgate ? moe::launch_dense_dgate(g, stream)
+                               : int8 ? moe::launch_dense_gemm_int8(mode, g, stream)
+                                      : moe::launch_dense_gemm_bf16(mode, g, stream),
                                what, stream));
   if (g.split > 1) MOE_RETURN_IF(moe::check_hip(moe::launch_dense_join(int8, mode, g, stream), what, stream));
   return MOE_OK;
@@ -259,37 +298,20 @@ void store_to(DenseGemm& g, void* out, int64_t stride, bool f32, const void* bas
   g.e.base_stride = base_stride;
 }
 
-// Two products in one launch, then the joins of their parts.
-moe_status run_pair(DenseGemm x, int mode, DenseGemm y, void* parts, size_t parts_y,
-                    hipError_t (*launch)(const DenseGemm&, const DenseGemm&, hipStream_t), const char* what,
-                    hipStream_t stream) {
-  DenseGemm g[2] = {x, y};
-  choose(g);
-  g[0].part = parts;
-  g[1].part = static_cast<uint8_t*>(parts) + parts_y;
-  MOE_RETURN_IF(moe::check_hip(launch(g[0], g[1], stream), what, stream));
-  for (int q = 0; q < 2; ++q)
-    if (g[q].M > 0 && g[q].split > 1)
-      MOE_RETURN_IF(moe::check_hip(moe::launch_dense_join(false, q == 0 ? mode : moe::kDenseStore, g[q], stream),
-                                   what, stream));
-  return MOE_OK;
-}
-
 // Workspace of the bf16 block: h or the gradients of gate and up in two terms, then
 // the parts.  Saved: gate and up, then h in two terms.
 struct FfnLayout {
-  size_t gu_bytes, h_bytes, rows, part, dgate_part, dw1_part;
+  size_t gu_bytes, h_bytes, rows, part;
   FfnLayout(const moe_ffn_dims* d, int64_t T) {
     const int64_t H = d->hidden, I = d->inter;
     gu_bytes = align256((size_t)T * 2 * I * 4);
     h_bytes = align256((size_t)T * 2 * I * 2);
     rows = align256((size_t)T * 4 * I * 2);
-    dgate_part = part_bytes(T, I, H, false);
     const int64_t twice = 2 * ceil_div(T, 64) * 64;
-    dw1_part = part_bytes(2 * I, H, twice, false);
-    // (two products of a launch need room together, the weights' for twice the terms)
-    part = std::max({part_bytes(T, 2 * I, H, false), part_bytes(T, H, I, false),
-                     dgate_part + part_bytes(H, I, twice, false), dw1_part + part_bytes(T, H, 2 * I, false)});
+    // (the products of a launch need room together, the weights' for twice the terms)
+    part = std::max({part_bytes(T, 2 * I, H, false), part_bytes(T, H, I, false), part_bytes(T, I, H, false),
+                     part_bytes(2 * I, H, twice, false) + part_bytes(H, I, twice, false) +
+                         part_bytes(T, H, 2 * I, false)});
   }
   size_t workspace() const { return rows + part; }
   size_t saved() const { return gu_bytes + h_bytes; }
@@ -401,33 +423,39 @@ moe_status moe_ffn_backward(const moe_ffn_dims* dims, const void* dout, int64_t 
   uint8_t* dgu = static_cast<uint8_t*>(workspace);
   uint8_t* parts = T > 0 ? dgu + l.rows : nullptr;
   const uint8_t* h = T > 0 ? static_cast<const uint8_t*>(saved) + l.gu_bytes : nullptr;
-  DenseGemm dgate = {}, dw1_sum = {}, dw2_sum = {}, dx_sum = {};
+  const bool f32 = dw_type == MOE_T_F32;
   if (T > 0) {
-    dgate = product(dout, dout_stride, w2, I, T, I, H, 2);
-    dgate.e.out = dgu;
-    dgate.e.inter = (int32_t)I;
-    dgate.e.gu_in = static_cast<const float*>(saved);
-    if (dw1 && dw_type == MOE_T_F32) dgate.e.out_lo = reinterpret_cast<uint16_t*>(dgu) + T * 2 * I;
+    DenseGemm dh = product(dout, dout_stride, w2, I, T, I, H, 2);
+    dh.e.out = dgu;
+    dh.e.inter = (int32_t)I;
+    dh.e.gu_in = static_cast<const float*>(saved);
+    if (dw1 && f32) dh.e.out_lo = reinterpret_cast<uint16_t*>(dgu) + T * 2 * I;
+    MOE_RETURN_IF(run_product(moe::kDenseDgate, dh, false, parts, "block gradients of gate and up", stream));
   }
+  DenseGemm g[3] = {};  // dw1, dw2, dx
   if (dw1) {
-    const bool f32 = dw_type == MOE_T_F32;
-    dw1_sum = product(dgu, 2 * I, x, T > 0 ? x_stride : H, 2 * I, H, T, 2);
-    store_to(dw1_sum, dw1, H, f32, nullptr, 0);
-    dw1_sum.terms = f32 ? 2 : 1;
-    dw1_sum.a_lo = T * 2 * I * 2;
-    dw2_sum = product(dout, T > 0 ? dout_stride : H, h, I, H, I, T, 2);
-    store_to(dw2_sum, dw2, I, f32, nullptr, 0);
-    dw2_sum.terms = dw1_sum.terms;
-    dw2_sum.b_lo = T * I * 2;
+    g[0] = product(dgu, 2 * I, x, T > 0 ? x_stride : H, 2 * I, H, T, 2);
+    store_to(g[0], dw1, H, f32, nullptr, 0);
+    g[1] = product(dout, T > 0 ? dout_stride : H, h, I, H, I, T, 2);
+    store_to(g[1], dw2, I, f32, nullptr, 0);
+    g[0].terms = g[1].terms = f32 ? 2 : 1;
+    g[0].a_lo = T * 2 * I * 2;
+    g[1].b_lo = T * I * 2;
   }
   if (dx && T > 0) {
-    dx_sum = product(dgu, 2 * I, w1, H, T, H, 2 * I, 2);
-    store_to(dx_sum, dx, dx_stride, false, dx_base, dx_base_stride);
+    g[2] = product(dgu, 2 * I, w1, H, T, H, 2 * I, 2);
+    store_to(g[2], dx, dx_stride, false, dx_base, dx_base_stride);
   }
-  MOE_RETURN_IF(run_pair(dgate, moe::kDenseDgate, dw2_sum, parts, l.dgate_part, moe::launch_dense_dgate_dw2,
-                         "block gradients of gate, up and w2", stream));
-  MOE_RETURN_IF(run_pair(dw1_sum, moe::kDenseStore, dx_sum, parts, l.dw1_part, moe::launch_dense_dw1_dx,
-                         "block gradients of w1 and x", stream));
+  choose(g);
+  for (DenseGemm& q : g) {
+    q.part = parts;
+    if (q.split > 1) parts += align256((size_t)q.split * q.M * q.N * 4);
+  }
+  MOE_RETURN_IF(moe::check_hip(moe::launch_dense_grads(g, stream), "block gradients", stream));
+  for (const DenseGemm& q : g)
+    if (q.M > 0 && q.split > 1)
+      MOE_RETURN_IF(moe::check_hip(moe::launch_dense_join(false, moe::kDenseStore, q, stream),
+                                   "block gradients' join", stream));
   return moe::set_ok();
 }
 

@@ -1,55 +1,64 @@
-// Gradients of the gated block in two launches of two products each.
+// Gradients of the gated block: of gate and up, then of the weights and of the
+// input in one launch.
+#include <algorithm>
+
 #include "moe_dense_gemm.h"
 
 namespace moe {
 
-// Products that do not need one another share a launch: fewer CUs are idle at its
-// end, and a short one costs 5 us less.  4096 tokens of 7168 x 2048: the gradients of
-// gate and up alone left half of the CUs without a tile of 256 x 256.  The blocks of
-// y start at a multiple of 8, so that they keep their XCD; those of x, which has
-// the longer K, come first.
-struct DensePair {
-  DenseGemm x, y;
-  int64_t blocks_x, first_y;
+hipError_t launch_dense_dgate(const DenseGemm& p, hipStream_t st) {
+  return dense::launch<false, false, true, kDenseDgate>(p, st);
+}
+
+// dw1, dw2 (both operands across k) and dx (columns across k) do not need one another:
+// in one launch fewer CUs are idle at its end than in three, and a short one costs 5
+// us less each.  first[q]: first block of product q, multiples of 8 so that blocks
+// keep their XCD; the products with the longer sums come first (4096 tokens of 7168 x
+// 2048, float32 gradients: 1000 us with dw2 beside the gradients of gate and up,
+// 830 so).
+struct DenseGrads {
+  DenseGemm p[3];  // dw1, dw2, dx
+  int64_t first[3], blocks[3];
 };
 
-// XT, XMODE: layout of x's rows and its mode; y's rows alike (columns across k).
-// XTERMS, YTERMS: float32 gradients of weights take both terms of their operand.
-template <bool XT, int XMODE, bool YT, class S, int XTERMS, int YTERMS>
-__global__ __launch_bounds__(S::NW* kWave, 2) void k_dense_pair(DensePair g) {
+// TERMS: of the weights' gradients (2 for float32).
+template <class S, int TERMS>
+__global__ __launch_bounds__(S::NW* kWave, 2) void k_dense_grads(DenseGrads g) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
   const int64_t b = blockIdx.x;
-  if (b < g.first_y) {
-    if (b < g.blocks_x) dense::dense_block<false, XT, true, XMODE, S, XTERMS>(g.x, b, lds);
+  const int64_t cx = b - g.first[2], c1 = b - g.first[1], c0 = b - g.first[0];
+  if (cx >= 0 && cx < g.blocks[2]) {
+    dense::dense_block<false, false, true, kDenseStore, S>(g.p[2], cx, lds);
   } else {
-    dense::dense_block<false, YT, true, kDenseStore, S, YTERMS>(g.y, b - g.first_y, lds);
+    const int q = c1 >= 0 && c1 < g.blocks[1];
+    const int64_t c = q ? c1 : c0;
+    if (c >= 0 && c < g.blocks[q]) dense::dense_block<false, true, true, kDenseStore, S, TERMS>(g.p[q], c, lds);
   }
 }
 
-template <bool XT, int XMODE, bool YT, int XTERMS, int YTERMS>
-hipError_t launch_pair(const DenseGemm& x, const DenseGemm& y, hipStream_t st) {
-  if (x.shape != y.shape) return hipErrorInvalidValue;
-  DensePair g = {x, y, dense_blocks(x), 0};
-  g.first_y = (g.blocks_x + 7) / 8 * 8;
-  const int64_t blocks = g.first_y + dense_blocks(y);
+hipError_t launch_dense_grads(const DenseGemm (&p)[3], hipStream_t st) {
+  DenseGrads g = {{p[0], p[1], p[2]}, {}, {}};
+  int order[3] = {0, 1, 2};
+  std::stable_sort(order, order + 3, [&](int a, int b) { return p[a].steps > p[b].steps; });
+  int64_t blocks = 0;
+  for (const int q : order) {
+    if (p[q].shape != p[0].shape || (q < 2 && p[q].terms != p[0].terms)) return hipErrorInvalidValue;
+    g.first[q] = blocks;
+    g.blocks[q] = dense_blocks(p[q]);
+    blocks += (g.blocks[q] + 7) / 8 * 8;
+  }
   if (blocks == 0) return hipSuccess;
   if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
   const unsigned n = (unsigned)blocks;
   using dense::Big;
   using dense::Mid;
-  if (x.shape == kDenseBig) k_dense_pair<XT, XMODE, YT, Big, XTERMS, YTERMS><<<n, Big::NW * kWave, 0, st>>>(g);
-  else if (x.shape == kDenseMid) k_dense_pair<XT, XMODE, YT, Mid, XTERMS, YTERMS><<<n, Mid::NW * kWave, 0, st>>>(g);
+  const bool two = p[0].terms == 2;
+  if (p[0].shape == kDenseBig && two) k_dense_grads<Big, 2><<<n, Big::NW * kWave, 0, st>>>(g);
+  else if (p[0].shape == kDenseBig) k_dense_grads<Big, 1><<<n, Big::NW * kWave, 0, st>>>(g);
+  else if (p[0].shape == kDenseMid && two) k_dense_grads<Mid, 2><<<n, Mid::NW * kWave, 0, st>>>(g);
+  else if (p[0].shape == kDenseMid) k_dense_grads<Mid, 1><<<n, Mid::NW * kWave, 0, st>>>(g);
   else return hipErrorInvalidValue;
   return hipGetLastError();
-}
-
-hipError_t launch_dense_dgate_dw2(const DenseGemm& dgate, const DenseGemm& dw2, hipStream_t st) {
-  return dw2.terms == 2 ? launch_pair<false, kDenseDgate, true, 1, 2>(dgate, dw2, st)
-                        : launch_pair<false, kDenseDgate, true, 1, 1>(dgate, dw2, st);
-}
-hipError_t launch_dense_dw1_dx(const DenseGemm& dw1, const DenseGemm& dx, hipStream_t st) {
-  return dw1.terms == 2 ? launch_pair<true, kDenseStore, false, 2, 1>(dw1, dx, st)
-                        : launch_pair<true, kDenseStore, false, 1, 1>(dw1, dx, st);
 }
 
 }  // namespace moe
