@@ -43,23 +43,23 @@ struct DenseGemm {
   int64_t a_stride;  // bytes, as b_stride
   const uint8_t* b;
   int64_t b_stride;
-  // terms = 2: an operand is the sum of two bf16 matrices, the second so many bytes
-  // behind the first; 0 for the other operand, which has one
+  // not 0: an operand (1: of the rows, 2: of the columns) is the sum of two bf16
+  // matrices, the second so many bytes behind the first
   int32_t terms;
-  int64_t a_lo, b_lo;
+  int64_t lo;
   int64_t M;         // rows
   int32_t N;         // columns; kDenseGate: 2 inter
   int64_t K;
   int32_t shape;     // DenseShape
   int32_t split;     // parts of K, each summed by blocks of their own
-  int32_t steps;     // K steps (128 bytes, of one term) of a part
+  int32_t steps;     // K steps (see dense_step) of a part
   int32_t halves;    // kDenseBig: so many tiles, the last, by two blocks each
   void* part;        // split > 1: sums [split, M, N], float32 or int32
   DenseEpilogue e;
 };
 
 constexpr int kDenseStepBytes = 128;  // K step of an operand row
-constexpr int dense_step(bool int8) { return int8 ? 128 : 64; }
+constexpr int dense_step(bool int8, int terms) { return int8 ? 128 : terms ? 32 : 64; }
 
 inline int64_t dense_tiles(const DenseGemm& p) {
   return (p.M + dense_rows(p.shape) - 1) / dense_rows(p.shape) *

@@ -143,7 +143,7 @@ double run_cost(int shape, int64_t blocks, double steps) {
 double join_cost(const DenseGemm& g, int64_t parts) {
   return parts > 1 ? 6.5 + (double)parts * (double)g.M * (double)g.N * 1e-6 : 0.0;
 }
-int64_t steps_of(const DenseGemm& g, bool int8) { return ceil_div(g.K, moe::dense_step(int8)) * g.terms; }
+int64_t steps_of(const DenseGemm& g, bool int8) { return ceil_div(g.K, moe::dense_step(int8, g.terms)); }
 void set_parts(DenseGemm& g, int64_t steps, int64_t parts) {
   g.steps = (int32_t)std::max((int64_t)1, ceil_div(steps, std::max((int64_t)1, parts)));
   g.split = (int32_t)std::max((int64_t)1, ceil_div(steps, g.steps));
@@ -255,7 +255,7 @@ void choose(DenseGemm (&g)[3]) {
 // largest; with at most `rows` x `columns` sums of at most K
 // terms.  Never less for fewer rows or terms.
 size_t part_bytes(int64_t rows, int64_t columns, int64_t K, bool int8) {
-  const int64_t most = ceil_div(K, moe::dense_step(int8)) / kMinPartSteps;
+  const int64_t most = ceil_div(K, moe::dense_step(int8, 0)) / kMinPartSteps;
   if (most < 2) return 0;
   const double sums = (double)rows * (double)columns * 4.0 * (double)most;
   const size_t cap = (size_t)kCus * 256 * 256 * 4;
@@ -284,7 +284,6 @@ DenseGemm product(const void* a, int64_t a_stride, const void* b, int64_t b_stri
   g.a_stride = a_stride * element;
   g.b = static_cast<const uint8_t*>(b);
   g.b_stride = b_stride * element;
-  g.terms = 1;
   g.M = M;
   g.N = (int32_t)N;
   g.K = K;
@@ -438,9 +437,10 @@ moe_status moe_ffn_backward(const moe_ffn_dims* dims, const void* dout, int64_t 
     store_to(g[0], dw1, H, f32, nullptr, 0);
     g[1] = product(dout, T > 0 ? dout_stride : H, h, I, H, I, T, 2);
     store_to(g[1], dw2, I, f32, nullptr, 0);
-    g[0].terms = g[1].terms = f32 ? 2 : 1;
-    g[0].a_lo = T * 2 * I * 2;
-    g[1].b_lo = T * I * 2;
+    g[0].terms = f32 ? 1 : 0;  // of the gradients of gate and up
+    g[0].lo = T * 2 * I * 2;
+    g[1].terms = f32 ? 2 : 0;  // of h
+    g[1].lo = T * I * 2;
   }
   if (dx && T > 0) {
     g[2] = product(dgu, 2 * I, w1, H, T, H, 2 * I, 2);

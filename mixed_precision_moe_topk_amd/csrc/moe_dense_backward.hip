@@ -21,18 +21,19 @@ struct DenseGrads {
   int64_t first[3], blocks[3];
 };
 
-// TERMS: of the weights' gradients (2 for float32).
-template <class S, int TERMS>
+// TERMS: the weights' gradients are float32, of operands in two terms.
+template <class S, bool TERMS>
 __global__ __launch_bounds__(S::NW* kWave, 2) void k_dense_grads(DenseGrads g) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
   const int64_t b = blockIdx.x;
   const int64_t cx = b - g.first[2], c1 = b - g.first[1], c0 = b - g.first[0];
+  using namespace dense;
   if (cx >= 0 && cx < g.blocks[2]) {
-    dense::dense_block<false, false, true, kDenseStore, S>(g.p[2], cx, lds);
-  } else {
-    const int q = c1 >= 0 && c1 < g.blocks[1];
-    const int64_t c = q ? c1 : c0;
-    if (c >= 0 && c < g.blocks[q]) dense::dense_block<false, true, true, kDenseStore, S, TERMS>(g.p[q], c, lds);
+    dense_block<false, false, true, kDenseStore, S>(g.p[2], cx, lds);
+  } else if (c1 >= 0 && c1 < g.blocks[1]) {
+    dense_block<false, true, true, kDenseStore, S, TERMS ? kColumnTerms : kPlain>(g.p[1], c1, lds);
+  } else if (c0 >= 0 && c0 < g.blocks[0]) {
+    dense_block<false, true, true, kDenseStore, S, TERMS ? kRowTerms : kPlain>(g.p[0], c0, lds);
   }
 }
 
@@ -42,7 +43,7 @@ hipError_t launch_dense_grads(const DenseGemm (&p)[3], hipStream_t st) {
   std::stable_sort(order, order + 3, [&](int a, int b) { return p[a].steps > p[b].steps; });
   int64_t blocks = 0;
   for (const int q : order) {
-    if (p[q].shape != p[0].shape || (q < 2 && p[q].terms != p[0].terms)) return hipErrorInvalidValue;
+    if (p[q].shape != p[0].shape) return hipErrorInvalidValue;
     g.first[q] = blocks;
     g.blocks[q] = dense_blocks(p[q]);
     blocks += (g.blocks[q] + 7) / 8 * 8;
@@ -52,11 +53,12 @@ hipError_t launch_dense_grads(const DenseGemm (&p)[3], hipStream_t st) {
   const unsigned n = (unsigned)blocks;
   using dense::Big;
   using dense::Mid;
-  const bool two = p[0].terms == 2;
-  if (p[0].shape == kDenseBig && two) k_dense_grads<Big, 2><<<n, Big::NW * kWave, 0, st>>>(g);
-  else if (p[0].shape == kDenseBig) k_dense_grads<Big, 1><<<n, Big::NW * kWave, 0, st>>>(g);
-  else if (p[0].shape == kDenseMid && two) k_dense_grads<Mid, 2><<<n, Mid::NW * kWave, 0, st>>>(g);
-  else if (p[0].shape == kDenseMid) k_dense_grads<Mid, 1><<<n, Mid::NW * kWave, 0, st>>>(g);
+  const bool two = p[0].terms != 0;
+  if (two != (p[1].terms != 0)) return hipErrorInvalidValue;
+  if (p[0].shape == kDenseBig && two) k_dense_grads<Big, true><<<n, Big::NW * kWave, 0, st>>>(g);
+  else if (p[0].shape == kDenseBig) k_dense_grads<Big, false><<<n, Big::NW * kWave, 0, st>>>(g);
+  else if (p[0].shape == kDenseMid && two) k_dense_grads<Mid, true><<<n, Mid::NW * kWave, 0, st>>>(g);
+  else if (p[0].shape == kDenseMid) k_dense_grads<Mid, false><<<n, Mid::NW * kWave, 0, st>>>(g);
   else return hipErrorInvalidValue;
   return hipGetLastError();
 }

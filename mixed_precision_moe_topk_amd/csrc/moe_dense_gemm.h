@@ -35,18 +35,27 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
   return (int64_t)(uint32_t)uniform((int)v) | (int64_t)uniform((int)(v >> 32)) << 32;
 }
 
-// One operand's tile of ROWS rows (or columns) in LDS, loaded by NW waves.  TERMS = 2:
-// every K step comes twice, once for each term.
-template <int ROWS, bool ACROSS, int NW, int TERMS>
+// An operand that is the sum of two bf16 terms: a K step is then 32 k of it, the first
+// term's in the place of a plain step's first half, the second's in the other's, and
+// as many k of the other operand, whose fragments serve both halves.
+enum Terms : int { kPlain = 0, kRowTerms = 1, kColumnTerms = 2 };
+
+// One operand's tile of ROWS rows (or columns) in LDS, loaded by NW waves.  STEP: what
+// a K step takes of it, 128 bytes of every row (kWholeStep), half of that
+// (kHalfStep), or half of that of each of its two terms (kTwoTerms).
+enum StepKind : int { kWholeStep = 0, kHalfStep = 1, kTwoTerms = 2 };
+template <int ROWS, bool ACROSS, int NW, int STEP>
 struct Tile {
-  static constexpr int kBytes = ROWS * kDenseStepBytes;
+  static_assert(ACROSS || STEP == kWholeStep, "halves of steps across k");
+  static constexpr int kBytes = ROWS * kDenseStepBytes / (STEP == kHalfStep ? 2 : 1);
   static constexpr int kLoads = kBytes / 1024 / NW;  // 1-KB loads of a wave and step
   static constexpr int kPieces = ROWS / 8;           // across k: 16-byte pieces of a k row
   static constexpr int kRowsPerLoad = ACROSS ? 64 / kPieces : 8;
+  static_assert(STEP != kTwoTerms || 32 % (NW * kRowsPerLoad) == 0, "a load is of one term");
 
   int64_t next;          // address of the K step to load next
   int64_t advance;       // bytes to the one behind it
-  int64_t advance2;      // TERMS = 2: and from that one on
+  int64_t lo;            // kTwoTerms: bytes to the second term
   uint32_t off[kLoads];  // this lane's piece of each load
   int first;             // this lane's row (k row when across) of load 0
 
@@ -57,26 +66,19 @@ struct Tile {
   // rows: what is left of the operand from the tile on (the last one is repeated).
   // source(r): which row of the operand the tile's row r is.
   template <class F>
-  __device__ __forceinline__ void init(const uint8_t* p, int64_t stride, int64_t rows, int64_t step, int64_t lo,
+  __device__ __forceinline__ void init(const uint8_t* p, int64_t stride, int64_t rows, int64_t step, int64_t second,
                                        int wave, F source) {
     const int lane = lane_id();
-    const int64_t whole = ACROSS ? stride * 64 : (int64_t)kDenseStepBytes;
-    if constexpr (TERMS == 2) {
-      const bool second = step & 1;
-      next = uniform((int64_t)p + (step >> 1) * whole + (second ? lo : 0));
-      advance = uniform(second ? whole - lo : lo);
-      advance2 = uniform(second ? lo : whole - lo);
-    } else {
-      advance = uniform(whole);
-      next = uniform((int64_t)p + step * whole);
-    }
+    advance = uniform(ACROSS ? stride * (STEP == kWholeStep ? 64 : 32) : (int64_t)kDenseStepBytes);
+    next = uniform((int64_t)p + step * advance);
+    if constexpr (STEP == kTwoTerms) lo = uniform(second);
     if constexpr (ACROSS) {
       first = wave * kRowsPerLoad + lane / kPieces;
 #pragma unroll
       for (int u = 0; u < kLoads; ++u) {
         const int k = first + u * NW * kRowsPerLoad;
         const int piece = (lane % kPieces) ^ (swizzle(k) << 1);
-        off[u] = (uint32_t)(k * stride + min((int64_t)piece, rows / 8 - 1) * 16);
+        off[u] = (uint32_t)((STEP == kTwoTerms ? k % 32 : k) * stride + min((int64_t)piece, rows / 8 - 1) * 16);
       }
     } else {
       first = wave * 8 + lane / 8;
@@ -87,26 +89,21 @@ struct Tile {
       }
     }
   }
+  // Where load u of the step at `next` reads from.
+  __device__ __forceinline__ const uint8_t* source_of(int u) const {
+    return reinterpret_cast<const uint8_t*>(STEP == kTwoTerms && u >= kLoads / 2 ? next + lo : next);
+  }
   // Load u of the step at `next`; the last one moves on.
   __device__ __forceinline__ void issue(int u, uint32_t lds, int wave) {
-    lds_dma16_s(reinterpret_cast<const uint8_t*>(next), off[u], lds + (u * NW + wave) * 1024);
-    if (u == kLoads - 1) move_on();
+    lds_dma16_s(source_of(u), off[u], lds + (u * NW + wave) * 1024);
+    if (u == kLoads - 1) next += advance;
   }
-  __device__ __forceinline__ void move_on() {
-    next += advance;
-    if constexpr (TERMS == 2) {
-      const int64_t t = advance;
-      advance = advance2;
-      advance2 = t;
-    }
-  }
-  // The same for the end of k: `left` bytes of each row (along k) or k rows (across).
-  __device__ __forceinline__ void issue_tail(int u, int left, uint32_t lds, int wave) {
+  // The same for the last step: `left` bytes of each row (along k) or k rows (across).
+  __device__ __forceinline__ void issue_tail(int u, int left, uint32_t lds, int wave) const {
     const uint8_t* zero = reinterpret_cast<const uint8_t*>(&g_zero);
     const int r = first + u * NW * kRowsPerLoad;
-    const bool in = ACROSS ? r < left : ((lane_id() ^ r) & 7) * 16 < left;
-    lds_dma16(in ? reinterpret_cast<const uint8_t*>(next) + off[u] : zero, lds + (u * NW + wave) * 1024);
-    if (u == kLoads - 1) move_on();
+    const bool in = ACROSS ? (STEP == kTwoTerms ? r % 32 : r) < left : ((lane_id() ^ r) & 7) * 16 < left;
+    lds_dma16(in ? source_of(u) + off[u] : zero, lds + (u * NW + wave) * 1024);
   }
 };
 
@@ -171,36 +168,36 @@ using Mid = Shape<2, 2, 64, 64>;   // 128 x 128, 80 KB: two blocks a CU
 using Low = Shape<2, 2, 32, 64>;   // 64 x 128, 64 KB: two blocks a CU
 
 // Tile (mt, nt) of part `part` of the product p.
-template <bool I8, bool AT, bool BT, int MODE, class S, int TERMS = 1>
+template <bool I8, bool AT, bool BT, int MODE, class S, int TERMS = kPlain>
 __device__ __forceinline__ void dense_tile(const DenseGemm& p, int part, int64_t mt, int nt, uint8_t* lds) {
   constexpr int NW = S::NW, BM = S::BM, BN = S::BN, WAVES_N = S::WAVES_N, WM = S::WM, WN = S::WN;
   constexpr bool GATE = MODE == kDenseGate;
-  using TA = Tile<BM, AT, NW, TERMS>;
-  using TB = Tile<BN, BT, NW, TERMS>;
+  using TA = Tile<BM, AT, NW, TERMS == kPlain ? kWholeStep : TERMS == kRowTerms ? kTwoTerms : kHalfStep>;
+  using TB = Tile<BN, BT, NW, TERMS == kPlain ? kWholeStep : TERMS == kColumnTerms ? kTwoTerms : kHalfStep>;
   const int64_t m0 = mt * BM, n0 = (int64_t)nt * BN;
   if (n0 >= p.N) return;  // (a half behind the last column)
   const int wave = uniform((int)threadIdx.x / kWave), lane = lane_id();
   const int wm = wave / WAVES_N, wn = wave % WAVES_N;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
 
-  constexpr int kStep = I8 ? 128 : 64;
-  const int all = uniform((int)((p.K + kStep - 1) / kStep)) * TERMS;
+  constexpr int kStep = I8 ? 128 : TERMS == kPlain ? 64 : 32;
+  const int all = uniform((int)((p.K + kStep - 1) / kStep));
   const int s0 = min(all, part * p.steps), s1 = min(all, s0 + p.steps);
-  const int rest = (int)(p.K % kStep);  // of the last step (of each term), 0: whole
+  const int rest = (int)(p.K % kStep);  // of the last step, 0: whole
   TA ta;
   TB tb;
   const int64_t left_m = p.M - m0, left_n = p.N - n0;
-  ta.init(p.a + m0 * (AT ? 2 : p.a_stride), p.a_stride, left_m, s0, p.a_lo, wave,
+  ta.init(p.a + m0 * (AT ? 2 : p.a_stride), p.a_stride, left_m, s0, p.lo, wave,
           [&](int row) { return min((int64_t)row, left_m - 1); });
   if constexpr (GATE) {
     // a wave's columns are as many gates, then the ups of the same hidden units
     const int64_t inter = p.N / 2, c0 = n0 / 2;
-    tb.init(p.b + c0 * p.b_stride, p.b_stride, left_n, s0, p.b_lo, wave, [&](int row) {
+    tb.init(p.b + c0 * p.b_stride, p.b_stride, left_n, s0, p.lo, wave, [&](int row) {
       const int64_t unit = min(c0 + row / WN * (WN / 2) + row % (WN / 2), inter - 1);
       return unit - c0 + (row % WN >= WN / 2 ? inter : 0);
     });
   } else {
-    tb.init(p.b + n0 * (BT ? 2 : p.b_stride), p.b_stride, left_n, s0, p.b_lo, wave,
+    tb.init(p.b + n0 * (BT ? 2 : p.b_stride), p.b_stride, left_n, s0, p.lo, wave,
             [&](int row) { return min((int64_t)row, left_n - 1); });
   }
   Fragments<BM, AT, WM> fa;
@@ -214,7 +211,7 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& p, int part, int64_t
 #pragma unroll
     for (int j = 0; j < WN / 16; ++j) acc[i][j] = v4i{0, 0, 0, 0};
 
-  auto tail = [&](int s) __attribute__((always_inline)) { return rest != 0 && s >= all - TERMS; };
+  auto tail = [&](int s) __attribute__((always_inline)) { return rest != 0 && s == all - 1; };
   // rows: stages s % 2; columns: stages s % 3
   int a_cur = 0, b_cur = 0;  // stages of the step at work, relative to the first
   auto a_stage = [&](int d) __attribute__((always_inline)) { return (uint32_t)((a_cur + d) & 1) * TA::kBytes; };
@@ -241,16 +238,27 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& p, int part, int64_t
   constexpr int FM = WM / 16, FN = WN / 16, kPerGroup = FN / FM;
   constexpr int LA = TA::kLoads, LB = TB::kLoads;
   v4i af[2][FM], bf[2][FN];
-  auto read = [&](int buf, int d, int h, int i) __attribute__((always_inline)) {
-    const uint8_t* la = lds + a_stage(d);
-    const uint8_t* lb = lds + b_stage(d);
-#pragma unroll
-    for (int j = i * kPerGroup; j < (i + 1) * kPerGroup; ++j) bf[buf][j] = fb.read(lb, j, h);
-    af[buf][i] = fa.read(la, i, h);
+  auto read_a = [&](int buf, int d, int h, int i) __attribute__((always_inline)) {
+    af[buf][i] = fa.read(lds + a_stage(d), i, h);
   };
-  auto multiply = [&](int buf, int i, int half) __attribute__((always_inline)) {
+  auto read_b = [&](int buf, int d, int h, int i) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = half * FN / 2; j < (half + 1) * FN / 2; ++j) acc[i][j] = mma<I8>(bf[buf][j], af[buf][i], acc[i][j]);
+    for (int j = i * FN / FM; j < (i + 1) * FN / FM; ++j) bf[buf][j] = fb.read(lds + b_stage(d), j, h);
+  };
+  // Group i of the second half's fragments, and of the next step's first half's (those
+  // of the operand with one term wait in the other buffer, see below)
+  auto read_second = [&](int i) __attribute__((always_inline)) {
+    if constexpr (TERMS != kRowTerms) read_b(1, 0, 1, i);
+    if constexpr (TERMS != kColumnTerms) read_a(1, 0, 1, i);
+  };
+  auto read_first = [&](int d, int i) __attribute__((always_inline)) {
+    read_b(TERMS == kRowTerms && d == 1, d, 0, i);
+    read_a(TERMS == kColumnTerms && d == 1, d, 0, i);
+  };
+  auto multiply = [&](int h, int i, int half) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = half * FN / 2; j < (half + 1) * FN / 2; ++j)
+      acc[i][j] = mma<I8>(bf[TERMS == kRowTerms ? 0 : h][j], af[TERMS == kColumnTerms ? 0 : h][i], acc[i][j]);
   };
   // Of the two waves of a SIMD the older one is served first, and the other falls
   // behind by half a step until the barrier, where the first waits for it alone:
@@ -264,7 +272,7 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& p, int part, int64_t
     constexpr bool MORE = decltype(more_c)::value;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-      read(1, 0, 1, i);
+      read_second(i);
       multiply(0, i, 0);
       __builtin_amdgcn_sched_barrier(0);
       if constexpr (LOAD != 0)
@@ -279,7 +287,7 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& p, int part, int64_t
     if (late) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-      if constexpr (MORE) read(0, 1, 0, i);
+      if constexpr (MORE) read_first(1, i);
       multiply(1, i, 0);
       __builtin_amdgcn_sched_barrier(0);
       if constexpr (LOAD != 0)
@@ -289,6 +297,12 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& p, int part, int64_t
       __builtin_amdgcn_sched_barrier(0);
     }
     if (late) __builtin_amdgcn_s_setprio(0);
+    if constexpr (MORE && TERMS == kRowTerms)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) bf[0][j] = bf[1][j];
+    if constexpr (MORE && TERMS == kColumnTerms)
+#pragma unroll
+      for (int i = 0; i < FM; ++i) af[0][i] = af[1][i];
     a_cur ^= 1;
     b_cur = b_cur == 2 ? 0 : b_cur + 1;
   };
@@ -304,12 +318,10 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& p, int part, int64_t
     if (n > 1) wait_barrier<LA + LB>();
     else wait_barrier<0>();
 #pragma unroll
-    for (int i = 0; i < FM; ++i) read(0, 0, 0, i);
-    int ends = n > 2 && tail(s1 - 1);  // steps behind the first two that hold the end of k
-    if (TERMS == 2) ends += n > 3 && tail(s1 - 2);
-    for (int s = 2 + ends; s < n; ++s) step(Int<1>(), Int<1>());
-    if (ends > 0) step(Int<2>(), Int<1>());
-    if (TERMS == 2 && ends > 1) step(Int<2>(), Int<1>());
+    for (int i = 0; i < FM; ++i) read_first(0, i);
+    const bool ends = n > 2 && tail(s1 - 1);
+    for (int s = ends ? 3 : 2; s < n; ++s) step(Int<1>(), Int<1>());
+    if (ends) step(Int<2>(), Int<1>());
     if (n > 1) step(Int<0>(), Int<1>());
     step(Int<0>(), Int<0>());
   }
@@ -395,7 +407,7 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& p, int part, int64_t
 // Block b of those that share the product p (dense_blocks of them).  Blocks go round
 // the 8 XCDs: each takes a contiguous range of the tiles, in groups of 4 rows of
 // tiles, so that the blocks at work on one XCD share their operands in its L2.
-template <bool I8, bool AT, bool BT, int MODE, class S, int TERMS = 1>
+template <bool I8, bool AT, bool BT, int MODE, class S, int TERMS = kPlain>
 __device__ __forceinline__ void dense_block(const DenseGemm& p, int64_t b, uint8_t* lds) {
   const int64_t tiles_m = (p.M + S::BM - 1) / S::BM;
   const int tiles_n = (p.N + S::BN - 1) / S::BN;
@@ -422,13 +434,13 @@ __device__ __forceinline__ void dense_block(const DenseGemm& p, int64_t b, uint8
   dense_tile<I8, AT, BT, MODE, S, TERMS>(p, part, mt, nt, lds);
 }
 
-template <bool I8, bool AT, bool BT, int MODE, class S, int TERMS = 1>
+template <bool I8, bool AT, bool BT, int MODE, class S, int TERMS = kPlain>
 __global__ __launch_bounds__(S::NW* kWave, 2) void k_dense(DenseGemm p) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
   dense_block<I8, AT, BT, MODE, S, TERMS>(p, blockIdx.x, lds);
 }
 
-template <bool I8, bool AT, bool BT, int MODE, class S, int TERMS = 1>
+template <bool I8, bool AT, bool BT, int MODE, class S, int TERMS = kPlain>
 hipError_t launch_shape(const DenseGemm& p, hipStream_t st) {
   const int64_t blocks = dense_blocks(p);
   if (blocks == 0) return hipSuccess;
