@@ -652,10 +652,11 @@ moe_status moe_ffn_backward(const moe_ffn_dims* dims, const void* dout, int64_t 
                             size_t workspace_bytes, hipStream_t stream);
 
 /* Rows of x (tokens, or the channels of a weight matrix) as 8-bit integers, one
- * scale a row: scales[r] = amax / 127 (float32 division; at least 2^-126, and 1 for
- * an all-zero row), codes[r] = x[r] / scales[r] rounded to the nearest integer,
- * ties to even (of the exact quotient).  A row with an infinity or NaN gets scale
- * NaN and codes 0, so that its products are NaN.
+ * scale a row: scales[r] = amax * (1 / 127), both rounded to float32 (a division by the
+ * constant comes out so in most programs), at least 2^-126, and 1 for an all-zero
+ * row; codes[r] = x[r] / scales[r] rounded to the nearest integer, ties to even (of
+ * the exact quotient).  A row with an infinity or NaN gets scale NaN and codes 0, so
+ * that its products are NaN.
  *   x:      device [rows, features] of x_type (moe_type), x_stride elements
  *           between rows; features a multiple of 16 up to 131056
  *   codes:  device int8 [rows, features] out

@@ -65,10 +65,10 @@ __device__ __forceinline__ uint32_t block_top(uint32_t top) {
   }
   return top;
 }
-// Scale of a row: a zero row has 1, a row that is not finite NaN (and codes 0).
+// Scale of a row, amax times fl32(1 / 127): a zero row has 1, a row that is not finite NaN (and codes 0).
 __device__ __forceinline__ float int8_scale(uint32_t top) {
   if (top >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
-  return top == 0 ? 1.0f : fmaxf(__fdiv_rn(__uint_as_float(top), 127.0f), 0x1p-126f);
+  return top == 0 ? 1.0f : fmaxf(__uint_as_float(top) * (1.0f / 127.0f), 0x1p-126f);
 }
 
 // A block a row: eight values a thread and round, kept in registers for up to KEEP

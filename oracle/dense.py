@@ -50,7 +50,7 @@ def int8_scale(amax):
         return np.float32(np.nan)
     if amax == 0:
         return np.float32(1.0)
-    return np.maximum(amax / np.float32(127.0), np.float32(2.0 ** -126))
+    return np.maximum(amax * (np.float32(1.0) / np.float32(127.0)), np.float32(2.0 ** -126))
 
 
 def int8_code(v, scale):
