@@ -194,6 +194,32 @@ def test_a_workspace_of_a_longer_batch():
         assert np.array_equal(host(out), e.run())
 
 
+@pytest.mark.parametrize("T", [1, 50, 300])
+def test_output_over_the_input(T):
+    """out may be x, and base x as well: a residual in place."""
+    import torch
+
+    import mixed_precision_moe_topk_amd as M
+
+    b = Block(T, 272, 144, seed=35)
+    b.base = b.x
+    d, ws, _ = b.buffers(M, 0xA5)
+    w1, w2 = device(b.w1), device(b.w2)
+    for base in ("none", "given"):
+        want = b.forward(base)["out"]
+        x = device(b.x)
+        M.ffn_apply(d, x, w1, w2, None if base == "none" else x, x, ws)
+        assert np.array_equal(host(x), want)
+        e = Block8(T, 272, 144, seed=36)
+        e.base = e.x
+        want = e.run(base)
+        x = device(e.x)
+        dev = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+        ws8 = torch.empty(M.ffn_int8_workspace_query(d, T), dtype=torch.uint8, device="cuda")
+        M.ffn_int8_apply(d, x, dev(e.w1), dev(e.s1), dev(e.w2), dev(e.s2), None if base == "none" else x, x, ws8)
+        assert np.array_equal(host(x), want)
+
+
 def test_rows_far_apart():
     """Rows that lie more than 2^32 bytes behind the first."""
     import torch
