@@ -118,8 +118,9 @@ moe_status check_int8(const moe_int8_dims* d, int64_t num_tokens) {
 //   256 x 256    1.40 + 15         (256 x 128, the last round's: 0.80 + 10)
 //   128 x 128    0.50 + 7.2         0.80 + 9.6
 //    64 x 128    0.44 + 4.0         0.60 + 5.5
-// a join 6.5 (with its launch on the host) + 1 for 4 MB.  (The block in bf16, T tokens of 7168 x 2048, by 64, 128 and
-// 256 rows: T = 64: 33, 35, -; 512: 86, 71, 91; 2048: 266, 180, 171.)
+// a join 6.5 (with its launch on the host) + 1 for 4 MB.  (The block in bf16, T tokens
+// of 7168 x 2048, by 64, 128 and 256 rows: T = 64: 33, 35, -; 512: 86, 71, 91; 2048:
+// 266, 180, 171.)
 constexpr int64_t kMinPartSteps = 4;
 using moe::kCus;
 struct Cost {
@@ -263,8 +264,8 @@ size_t part_bytes(int64_t rows, int64_t columns, int64_t K, bool int8) {
 }
 
 moe_status run_product(int mode, DenseGemm g, bool int8, void* parts, const char* what, hipStream_t stream) {
-  // (T = 1 of 7168 x 2048: 23.0 us, by tiles 26.5; two rows read side by side took
-  // 27.7, as by tiles)
+  // (the block of 7168 x 2048 with one token: 20.2 us, by tiles 26.5; two tokens by a
+  // kernel of that kind took 27.7)
   if (g.M == 1 && mode != moe::kDenseDgate)
     return moe::check_hip(moe::launch_dense_one(int8, mode, g, stream), what, stream);
   choose(g, int8);

@@ -2,14 +2,25 @@
 //
 // A block takes BM rows and BN columns; a K step is 128 bytes of every operand
 // row.  Both operands' tiles go straight into LDS, up to two steps ahead; one barrier a
-// step.  The columns are the matrix instruction's first operand, so that a lane holds four
-// consecutive columns of one row.
+// step.  The columns are the matrix instruction's first operand, so that a lane holds
+// four consecutive columns of one row.
 //
 // An operand along k lies in LDS as [row][128 bytes], its 16-byte pieces at
 // piece ^ (row % 8): eight lanes that read one piece of eight rows touch all
 // banks.  An operand across k lies as [k][columns] and is read transposed
 // (ds_read_b64_tr_b16: 16 lanes read 4 k x 16 columns and get a column's four k
-// each); its 32-byte pairs of pieces are permuted by bits of k.
+// each); its 32-byte pairs of pieces are permuted by bits of k.  No bank conflicts
+// were counted either way.
+//
+// What bounds it: a 256 x 256 step is 2048 clocks of matrix instructions and moves 64
+// KB into LDS and 196 out of it, 2030 clocks at 128 bytes a clock; it takes 2250, and in
+// long launches the part lowers its clock to 1.7 GHz.  16384 tokens: gate and up of
+// 7168 x 4096 1.41 PFLOP/s, down of 2048 x 7168 1.09 (each tile's 256 KB of base and
+// result in one burst, 13 of 60 us), int8 7168 x 7168 2.5 POP/s; the library's bf16
+// product of 8192^3 takes 1.35 PFLOP/s, its int8 one 2.05.  Tried and not kept: one half
+// step's fragments at a time (1237 us for the block in place of 1070), 32 x 32 x 16
+// instructions (5 % slower, int8 10), tiles of 128 x 256 and 192 x 128 by four waves, two
+// K groups of waves in a block, four steps ahead for 128 x 128.
 #pragma once
 
 #include "moe_dense_epilogue.h"

@@ -9,7 +9,8 @@ hipError_t launch_dense_gemm_bf16(int mode, const DenseGemm& p, hipStream_t st) 
   return hipErrorInvalidValue;
 }
 
-// Adds up the parts, eight columns a thread.
+// Adds up the parts, eight columns a thread; bound by latency (64 tokens x 7168, 4
+// parts: 3.7 us; one part's reads after another's took 10).
 template <bool I8, int MODE>
 __global__ __launch_bounds__(64) void k_dense_join(DenseGemm p) {
   constexpr bool GATE = MODE == kDenseGate;

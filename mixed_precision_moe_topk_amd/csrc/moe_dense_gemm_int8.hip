@@ -79,7 +79,7 @@ __device__ __forceinline__ void quant_row(int32_t cols, F values, int8_t* __rest
   float keep[KEEP][8];
   uint32_t top = 0;
   // (all reads first, the row's last values again behind its end: a branch would wait
-  // for each; 64 rows of 7168: 6.5 -> 4.1 us)
+  // for each; 64 rows of 7168: 6.5 -> 5.2 us)
 #pragma unroll
   for (int i = 0; i < KEEP; ++i) values(min((i * NT + (int)threadIdx.x) * 8, cols - 8), keep[i]);
 #pragma unroll
@@ -108,6 +108,9 @@ __device__ __forceinline__ void quant_row(int32_t cols, F values, int8_t* __rest
   }
 }
 
+// A read of x and a write of half as many bytes: 16384 rows of 7168 bf16 take 63 us,
+// 5.6 TB/s; one row 2.6 us.  A wave a row up to 2048 columns (one round of registers),
+// four beyond.
 template <bool F32, int NT>
 __global__ __launch_bounds__(NT) void k_int8_quant(const void* __restrict__ x, int64_t stride, int64_t rows,
                                                    int32_t cols, int8_t* __restrict__ codes,
@@ -124,8 +127,8 @@ __global__ __launch_bounds__(NT) void k_int8_quant(const void* __restrict__ x, i
 }
 
 // A block a token: sums the parts of gate and up in their order (as k_dense_join
-// does), and quantises silu(gate) * up.  64 tokens of 7168 x 2048: 5 us less than the
-// join, h and the quantiser on their own.
+// does), and quantises silu(gate) * up.  64 tokens of 7168 x 2048, 4 parts: 6.4 us in
+// place of a join (3.9) and a launch of the quantiser (5.2).  Bound by latency.
 template <int NT>
 __global__ __launch_bounds__(NT) void k_dense_join_quant(DenseGemm p, int8_t* __restrict__ codes,
                                                          float* __restrict__ scales) {
