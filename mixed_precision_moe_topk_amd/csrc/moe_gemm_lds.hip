@@ -4,7 +4,6 @@
 // with codes mapped to E4M3 in registers and the group scale applied after
 // each 128-wide K step.
 #include "moe_gemm_common.h"
-#include "moe_lds_dma.h"
 
 namespace moe {
 
@@ -554,6 +553,24 @@ struct Map {
   static_assert(kBytes <= 160 * 1024, "LDS of one CU");
 };
 }  // namespace dma
+
+__device__ __forceinline__ void lds_dma16(const void* gaddr, uint32_t lds_addr) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+               :: "v"(gaddr), "s"(lds_addr) : "memory", "m0");
+}
+__device__ __forceinline__ void lds_dma16_s(const void* sbase, uint32_t voff, uint32_t lds_addr) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :: "v"(voff), "s"(sbase), "s"(lds_addr) : "memory", "m0");
+}
+__device__ __forceinline__ void lds_dma4_s(const void* sbase, uint32_t voff, uint32_t lds_addr) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+               :: "v"(voff), "s"(sbase), "s"(lds_addr) : "memory", "m0");
+}
+// Wait until at most N of this wave's loads are outstanding, then block barrier.
+template <int N>
+__device__ __forceinline__ void wait_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(N) : "memory");
+}
 
 // One code path for full and partial tiles: the per-subtile checks are scalar
 // branches, which also keep the compiler from hoisting every fragment read of
