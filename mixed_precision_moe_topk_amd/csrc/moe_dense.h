@@ -73,6 +73,14 @@ inline int64_t dense_halves(int shape, int64_t tiles) {
   const int64_t rest = tiles % kCus;
   return shape == kDenseBig && rest <= kCus / 2 ? rest : 0;
 }
+// The order of a launch of three products: the longer sums first.
+inline void dense_order(const DenseGemm (&p)[3], int (&order)[3]) {
+  for (int q = 0; q < 3; ++q) {
+    int at = q;
+    for (; at > 0 && p[order[at - 1]].steps < p[q].steps; --at) order[at] = order[at - 1];
+    order[at] = q;
+  }
+}
 inline int64_t dense_blocks(const DenseGemm& p) { return dense_tiles(p) * p.split + p.halves; }
 
 // Both operands along k: kDenseStore or kDenseGate.

@@ -176,7 +176,6 @@ void choose(DenseGemm& g, bool int8) {
 double share_out(DenseGemm (&g)[3], int shape, int64_t share) {
   int64_t blocks = 0;
   double total = 0, joins = 0;
-  DenseGemm* order[3] = {&g[0], &g[1], &g[2]};
   const Cost each = shape == moe::kDenseBig ? kOne[shape] : kTwo[shape];
   for (DenseGemm& q : g) {
     q.shape = shape;
@@ -189,20 +188,20 @@ double share_out(DenseGemm (&g)[3], int shape, int64_t share) {
     total += (double)n * ((double)q.steps * each.step + each.fixed);
     joins += join_cost(q, q.split);
   }
-  std::stable_sort(order, order + 3, [](const DenseGemm* a, const DenseGemm* b) { return a->steps > b->steps; });
+  int order[3];
+  moe::dense_order(g, order);
   // where all blocks are as long, those of the last round may be cut in two
   bool alike = true;
-  const DenseGemm* last = nullptr;
-  for (DenseGemm* q : order)
-    if (moe::dense_tiles(*q) > 0) {
-      alike = alike && (!last || last->steps == q->steps);
-      last = q;
+  DenseGemm* last = nullptr;
+  for (const int o : order)
+    if (moe::dense_tiles(g[o]) > 0) {
+      alike = alike && (!last || last->steps == g[o].steps);
+      last = &g[o];
     }
   if (!last) return 0.0;
   if (alike) {
-    DenseGemm& q = *const_cast<DenseGemm*>(last);
-    q.halves = (int32_t)std::min(moe::dense_halves(shape, blocks), moe::dense_tiles(q) * q.split);
-    return joins + run_cost(shape, blocks, (double)q.steps);
+    last->halves = (int32_t)std::min(moe::dense_halves(shape, blocks), moe::dense_tiles(*last) * last->split);
+    return joins + run_cost(shape, blocks, (double)last->steps);
   }
   if (blocks > 64 * slots(shape)) return joins + total / (double)slots(shape);
   struct Free {
@@ -211,9 +210,9 @@ double share_out(DenseGemm (&g)[3], int shape, int64_t share) {
   } free[8] = {{0.0, slots(shape)}};
   int groups = 1;
   double end = 0;
-  for (const DenseGemm* q : order) {
-    const double cost = (double)q->steps * each.step + each.fixed;
-    for (int64_t n = moe::dense_tiles(*q) * q->split; n > 0;) {
+  for (const int o : order) {
+    const double cost = (double)g[o].steps * each.step + each.fixed;
+    for (int64_t n = moe::dense_tiles(g[o]) * g[o].split; n > 0;) {
       int f = 0;
       for (int k = 1; k < groups; ++k)
         if (free[k].at < free[f].at) f = k;
@@ -253,8 +252,8 @@ void choose(DenseGemm (&g)[3]) {
   share_out(g, shape, share);
 }
 // Room for the parts of a launch: at most as many tiles as run at once, 64 MB by the
-// largest; with at most `rows` x `columns` sums of at most K
-// terms.  Never less for fewer rows or terms.
+// largest; with at most `rows` x `columns` sums of at most K terms.  Never less for
+// fewer rows or terms.
 size_t part_bytes(int64_t rows, int64_t columns, int64_t K, bool int8) {
   const int64_t most = ceil_div(K, moe::dense_step(int8, 0)) / kMinPartSteps;
   if (most < 2) return 0;

@@ -1,6 +1,5 @@
 // Gradients of the gated block: of gate and up, then of the weights and of the
 // input in one launch.
-#include <algorithm>
 
 #include "moe_dense_gemm.h"
 
@@ -41,8 +40,8 @@ __global__ __launch_bounds__(S::NW* kWave, 2) void k_dense_grads(DenseGrads g) {
 
 hipError_t launch_dense_grads(const DenseGemm (&p)[3], hipStream_t st) {
   DenseGrads g = {{p[0], p[1], p[2]}, {}, {}};
-  int order[3] = {0, 1, 2};
-  std::stable_sort(order, order + 3, [&](int a, int b) { return p[a].steps > p[b].steps; });
+  int order[3];
+  dense_order(p, order);
   int64_t blocks = 0;
   for (const int q : order) {
     if (p[q].shape != p[0].shape) return hipErrorInvalidValue;

@@ -445,13 +445,13 @@ __device__ __forceinline__ void dense_block(const DenseGemm& p, int64_t b, uint8
   dense_tile<I8, AT, BT, MODE, S, TERMS>(p, part, mt, nt, lds);
 }
 
-template <bool I8, bool AT, bool BT, int MODE, class S, int TERMS = kPlain>
+template <bool I8, bool AT, bool BT, int MODE, class S>
 __global__ __launch_bounds__(S::NW* kWave, 2) void k_dense(DenseGemm p) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
-  dense_block<I8, AT, BT, MODE, S, TERMS>(p, blockIdx.x, lds);
+  dense_block<I8, AT, BT, MODE, S>(p, blockIdx.x, lds);
 }
 
-template <bool I8, bool AT, bool BT, int MODE, class S, int TERMS = kPlain>
+template <bool I8, bool AT, bool BT, int MODE, class S>
 hipError_t launch_shape(const DenseGemm& p, hipStream_t st) {
   const int64_t blocks = dense_blocks(p);
   if (blocks == 0) return hipSuccess;

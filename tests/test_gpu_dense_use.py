@@ -246,6 +246,48 @@ def test_rows_far_apart():
     assert np.array_equal(codes.cpu().numpy(), want) and np.array_equal(scales.cpu().numpy(), ws_)
 
 
+@pytest.mark.parametrize("T", [1, 3])
+def test_largest_weights(T):
+    """2^30 weights a matrix: gates and ups lie 2^31 bytes apart, w1 ends behind 2^32."""
+    import torch
+
+    import mixed_precision_moe_topk_amd as M
+
+    H, I, last = 4096, 1 << 18, 512
+    d = M.FfnDims(H, I)
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    rand = lambda scale, *s: torch.empty(s, dtype=torch.bfloat16, device="cuda").normal_(0, scale, generator=gen)  # noqa: E731
+    x, dout = rand(1, T, H), rand(1, T, H)
+    w1, w2 = rand(H ** -0.5, 2 * I, H), rand(I ** -0.5, H, I)
+    out, dx = torch.empty_like(x), torch.empty_like(x)
+    ws = torch.empty(M.ffn_workspace_query(d, T), dtype=torch.uint8, device="cuda")
+    saved = torch.empty(M.ffn_saved_query(d, T), dtype=torch.uint8, device="cuda")
+    dw1, dw2 = torch.empty_like(w1), torch.empty_like(w2)
+    M.ffn_apply(d, x, w1, w2, None, out, ws, saved=saved)
+    M.ffn_backward(d, dout, x, w1, w2, saved, dw1, dw2, ws, dx=dx)
+    gu = saved[:T * 8 * I].view(torch.float32).view(T, 2, I)
+    h = saved[(T * 8 * I + 255) // 256 * 256:][:T * 2 * I].view(torch.bfloat16).view(T, I)
+    dgu = ws[:T * 4 * I].view(torch.bfloat16).view(T, 2 * I)
+    f = lambda t: t.double()  # noqa: E731
+    half = 2.0 ** -8
+    for name, got, a, c, kind in (
+            ("g", gu[:, 0, -last:], f(x), f(w1[I - last:I]).T, 0.0), ("u", gu[:, 1, -last:], f(x), f(w1[-last:]).T, 0.0),
+            ("out", out, f(h), f(w2).T, half), ("dx", dx[:, -last:], f(dgu), f(w1[:, -last:]), half),
+            ("dw1", dw1[-last:], f(dgu[:, -last:]).T, f(x), half), ("dw2", dw2[-last:], f(dout[:, -last:]).T, f(h), half)):
+        want, bound = a @ c, a.abs() @ c.abs()
+        err = (2 * a.shape[1] + 34) * STEP * bound
+        assert ((f(got) - want).abs() <= err + kind * (want.abs() + err)).all(), name
+    w1 = torch.randint(-127, 128, w1.shape, generator=gen, dtype=torch.int8, device="cuda")
+    d8 = M.Int8Dims(H, 1 << 18, "f32")
+    codes, scales = torch.empty((T, H), dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    M.int8_quantize(x, codes, scales)
+    got = torch.empty((T, 1 << 18), device="cuda")
+    ws8 = torch.empty(M.int8_workspace_query(d8, T), dtype=torch.uint8, device="cuda")
+    one = torch.ones(1 << 18, device="cuda")
+    M.int8_matmul(d8, codes, torch.ones(T, device="cuda"), w1[-(1 << 18):], one, None, got, ws8)
+    assert (f(got[:, -last:]) == f(codes) @ f(w1[-last:]).T).all()
+
+
 def test_long_batches():
     """More than 2^16 tokens, odd: the weights' gradients sum over all of them."""
     import torch
