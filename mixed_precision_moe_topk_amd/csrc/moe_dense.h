@@ -32,9 +32,12 @@ enum DenseShape : int {
   kDenseBig = 0,  // 256 x 256, 8 waves; see dense_halves
   kDenseMid = 1,  // 128 x 128, 4 waves, two blocks a CU
   kDenseLow = 2,  // 64 x 128, 4 waves, two blocks a CU; not for rows across k
+  kDenseFew = 3,  // 64 x 64, 4 waves, two blocks a CU, four steps under way; both
+                  // operands along k, at most kDenseFewRows rows
 };
-constexpr int dense_rows(int shape) { return shape == kDenseBig ? 256 : shape == kDenseLow ? 64 : 128; }
-constexpr int dense_columns(int shape) { return shape == kDenseBig ? 256 : 128; }
+constexpr int64_t kDenseFewRows = 256;
+constexpr int dense_rows(int shape) { return shape == kDenseBig ? 256 : shape == kDenseMid ? 128 : 64; }
+constexpr int dense_columns(int shape) { return shape == kDenseBig ? 256 : shape == kDenseFew ? 64 : 128; }
 
 // Product of rows and columns over k: sum_k a(m, k) b(n, k).  An operand lies
 // either along k (element (m, k) at m * stride + k) or across it (k * stride + m).

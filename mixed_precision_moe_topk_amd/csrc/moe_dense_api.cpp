@@ -118,17 +118,18 @@ moe_status check_int8(const moe_int8_dims* d, int64_t num_tokens) {
 //   256 x 256    1.40 + 15         (256 x 128, the last round's: 0.80 + 10)
 //   128 x 128    0.50 + 7.2         0.80 + 9.6
 //    64 x 128    0.44 + 4.0         0.60 + 5.5
+//    64 x 64     0.24 + 4.2         0.45 + 7.5
 // a join 6.5 (with its launch on the host) + 1 for 4 MB.  (The block in bf16, T tokens
-// of 7168 x 2048, by 64, 128 and 256 rows: T = 64: 33, 35, -; 512: 86, 71, 91; 2048:
-// 266, 180, 171.)
+// of 7168 x 2048, by 64 x 128, 128 and 256 rows: T = 64: 33, 35, -; 512: 86, 71, 91;
+// 2048: 266, 180, 171; with 64 x 64 among them T = 64: 30 -> 26.6, 100: 45 -> 39, 200: 52
+// still.)
 constexpr int64_t kMinPartSteps = 4;
 using moe::kCus;
 struct Cost {
   double step, fixed;
 };
-constexpr Cost kOne[3] = {{1.40, 15.0}, {0.50, 7.2}, {0.44, 4.0}};
-constexpr Cost kTwo[3] = {{}, {0.80, 9.6}, {0.60, 5.5}};
-
+constexpr Cost kOne[4] = {{1.40, 15.0}, {0.50, 7.2}, {0.44, 4.0}, {0.24, 4.2}};
+constexpr Cost kTwo[4] = {{}, {0.80, 9.6}, {0.60, 5.5}, {0.45, 7.5}};
 constexpr Cost kHalf = {0.80, 10.0};
 
 int64_t slots(int shape) { return shape == moe::kDenseBig ? kCus : 2 * kCus; }
@@ -150,13 +151,13 @@ void set_parts(DenseGemm& g, int64_t steps, int64_t parts) {
   g.split = (int32_t)std::max((int64_t)1, ceil_div(steps, g.steps));
 }
 
-// One product alone.
-void choose(DenseGemm& g, bool int8) {
+// One product alone; along: both operands lie along k.
+void choose(DenseGemm& g, bool int8, bool along) {
   const int64_t steps = steps_of(g, int8);
   double best = 1e300;
   int shape = 0;
   int64_t parts = 1;
-  for (int s = 0; s < 3; ++s) {
+  for (int s = 0; s < (along && g.M <= moe::kDenseFewRows ? 4 : 3); ++s) {
     g.shape = s;
     const int64_t tiles = std::max((int64_t)1, moe::dense_tiles(g));
     const int64_t most = std::max((int64_t)1, std::min(slots(s) / tiles, steps / kMinPartSteps));
@@ -267,7 +268,7 @@ moe_status run_product(int mode, DenseGemm g, bool int8, void* parts, const char
   // kernel of that kind took 27.7)
   if (g.M == 1 && mode != moe::kDenseDgate)
     return moe::check_hip(moe::launch_dense_one(int8, mode, g, stream), what, stream);
-  choose(g, int8);
+  choose(g, int8, mode != moe::kDenseDgate);
   g.part = parts;
   MOE_RETURN_IF(moe::check_hip(mode == moe::kDenseDgate ? moe::launch_dense_dgate(g, stream)
                                : int8 ? moe::launch_dense_gemm_int8(mode, g, stream)
@@ -541,7 +542,7 @@ moe_status moe_ffn_int8_apply(const moe_ffn_dims* dims, const void* x, int64_t x
   up.e.inter = (int32_t)I;
   up.e.row_scale = scales;
   up.e.col_scale = w1_scales;
-  choose(up, true);
+  choose(up, true, true);
   if (T > 1 && up.split > 1) {
     // the join of the parts quantises h and never stores it
     up.part = ws + l.part;

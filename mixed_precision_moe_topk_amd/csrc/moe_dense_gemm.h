@@ -177,6 +177,109 @@ using Big = Shape<4, 2, 64, 128>;  // 256 x 256, 160 KB of LDS
 using Half = Shape<4, 2, 64, 64>;  // 256 x 128: half of a Big one, by as many waves
 using Mid = Shape<2, 2, 64, 64>;   // 128 x 128, 80 KB: two blocks a CU
 using Low = Shape<2, 2, 32, 64>;   // 64 x 128, 64 KB: two blocks a CU
+// Few rows: steps of both operands in a ring of STAGES.
+template <int WAVES_M_, int WAVES_N_, int WM_, int WN_, int STAGES>
+struct Ring {
+  static constexpr int WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, WM = WM_, WN = WN_, kStages = STAGES;
+  static constexpr int NW = WAVES_M * WAVES_N, BM = WAVES_M * WM, BN = WAVES_N * WN;
+  static constexpr int kLds = STAGES * (BM + BN) * kDenseStepBytes;
+  static_assert(kLds <= 160 * 1024, "LDS of a CU");
+};
+using Few = Ring<4, 1, 16, 64, 5>;  // 64 x 64, 80 KB: two blocks a CU
+
+// Gates and ups: a wave's WN columns are as many gates, then the ups of the same hidden
+// units.  Row of the weights, from c0 on, that column `row` of a tile is.
+template <int WN>
+__device__ __forceinline__ int64_t gate_row(int row, int64_t c0, int64_t inter) {
+  const int64_t unit = min(c0 + row / WN * (WN / 2) + row % (WN / 2), inter - 1);
+  return unit - c0 + (row % WN >= WN / 2 ? inter : 0);
+}
+
+// What becomes of a block's sums: parts of them, or results.
+template <bool I8, int MODE, class S>
+__device__ __forceinline__ void dense_sums(const DenseGemm& p, int part, int64_t m0, int nt, int wm, int wn,
+                                           v4i (&acc)[S::WM / 16][S::WN / 16]) {
+  constexpr int BN = S::BN, WM = S::WM, WN = S::WN, FM = WM / 16;
+  constexpr bool GATE = MODE == kDenseGate;
+  const int lane = lane_id();
+  // A lane holds columns 4 (lane / 16) + 0 .. 3 of each 16 x 16 sums.  Of two
+  // neighbours, the odd quarters of the wave give theirs of the first for the even
+  // quarters' of the second: every lane then has eight consecutive columns.
+  constexpr int kUnits = GATE ? WN / 2 : WN;  // finished columns of a row
+  const int64_t units = GATE ? p.N / 2 : p.N;
+  const int64_t unit0 = (int64_t)nt * (GATE ? BN / 2 : BN) + wn * kUnits + ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
+  auto eight = [&](int i, int j, uint4& lo, uint4& hi) __attribute__((always_inline)) {
+    uint32_t a[4], b[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const auto x = __builtin_amdgcn_permlane16_swap((uint32_t)acc[i][j][r], (uint32_t)acc[i][j + 1][r], false, false);
+      a[r] = x[0], b[r] = x[1];
+    }
+    lo = make_uint4(a[0], a[1], a[2], a[3]);
+    hi = make_uint4(b[0], b[1], b[2], b[3]);
+  };
+  constexpr int kPairs = kUnits / 32;
+  const int64_t row0 = m0 + wm * WM + (lane & 15);
+  if (p.split > 1) {
+    uint32_t* sums = static_cast<uint32_t*>(p.part) + (int64_t)part * p.M * p.N;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int64_t m = row0 + 16 * i;
+#pragma unroll
+      for (int j = 0; j < (GATE ? 2 : 1) * kPairs; ++j) {
+        uint4 lo, hi;
+        eight(i, 2 * j, lo, hi);
+        const int64_t unit = unit0 + 32 * (j % kPairs);
+        if (m < p.M && unit < units) {
+          uint4* at = reinterpret_cast<uint4*>(sums + m * p.N + (j / kPairs) * units + unit);
+          at[0] = lo, at[1] = hi;
+        }
+      }
+    }
+    return;
+  }
+  // reads of a group of rows are under way while the one before is finished (int8:
+  // the columns' scales take the registers; float32 gates and ups are too many)
+  constexpr int kDeep = I8 || MODE == kDenseDgate ? 1 : 2;
+  Ahead<I8, MODE> ahead[kDeep][kPairs];
+  float row_scale = 1.0f;
+  Bytes32 col_scale[I8 ? (GATE ? 2 : 1) * kPairs : 1];
+  auto load = [&](int i) __attribute__((always_inline)) {
+    const int64_t m = min(row0 + 16 * i, p.M - 1);
+    if constexpr (I8) row_scale = p.e.row_scale[m];
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) ahead[i % kDeep][j].load(p.e, m, min(unit0 + 32 * j, units - 8));
+  };
+  if constexpr (kDeep == 2) load(0);
+  if constexpr (I8) {
+#pragma unroll
+    for (int j = 0; j < (GATE ? 2 : 1) * kPairs; ++j)
+      col_scale[j] = load32(p.e.col_scale + (j / kPairs) * units + min(unit0 + 32 * (j % kPairs), units - 8));
+  }
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int64_t m = row0 + 16 * i;
+    if (kDeep == 1 || i + 1 < FM) load(i + kDeep - 1);
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) {
+      const int64_t unit = unit0 + 32 * j;
+      uint4 lo, hi;
+      float v[8], up[8];
+      eight(i, 2 * j, lo, hi);
+      sums_to_float(I8, lo, hi, v);
+      if constexpr (I8) scale8(row_scale, col_scale[j], v);
+      if constexpr (GATE) {
+        eight(i, 2 * (j + kPairs), lo, hi);
+        sums_to_float(I8, lo, hi, up);
+        if constexpr (I8) scale8(row_scale, col_scale[j + kPairs], up);
+      }
+      if (m < p.M && unit < units) {
+        if constexpr (GATE) finish_gate<I8>(p.e, m, unit, v, up);
+        else finish<I8, MODE>(p.e, m, unit, v, ahead[i % kDeep][j]);
+      }
+    }
+  }
+}
 
 // Tile (mt, nt) of part `part` of the product p.
 template <bool I8, bool AT, bool BT, int MODE, class S, int TERMS = kPlain>
@@ -201,12 +304,9 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& p, int part, int64_t
   ta.init(p.a + m0 * (AT ? 2 : p.a_stride), p.a_stride, left_m, s0, p.lo, wave,
           [&](int row) { return min((int64_t)row, left_m - 1); });
   if constexpr (GATE) {
-    // a wave's columns are as many gates, then the ups of the same hidden units
     const int64_t inter = p.N / 2, c0 = n0 / 2;
-    tb.init(p.b + c0 * p.b_stride, p.b_stride, left_n, s0, p.lo, wave, [&](int row) {
-      const int64_t unit = min(c0 + row / WN * (WN / 2) + row % (WN / 2), inter - 1);
-      return unit - c0 + (row % WN >= WN / 2 ? inter : 0);
-    });
+    tb.init(p.b + c0 * p.b_stride, p.b_stride, left_n, s0, p.lo, wave,
+            [&](int row) { return gate_row<WN>(row, c0, inter); });
   } else {
     tb.init(p.b + n0 * (BT ? 2 : p.b_stride), p.b_stride, left_n, s0, p.lo, wave,
             [&](int row) { return min((int64_t)row, left_n - 1); });
@@ -336,83 +436,113 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& p, int part, int64_t
     if (n > 1) step(Int<0>(), Int<1>());
     step(Int<0>(), Int<0>());
   }
-  // A lane holds columns 4 (lane / 16) + 0 .. 3 of each 16 x 16 sums.  Of two
-  // neighbours, the odd quarters of the wave give theirs of the first for the even
-  // quarters' of the second: every lane then has eight consecutive columns.
-  constexpr int kUnits = GATE ? WN / 2 : WN;  // finished columns of a row
-  const int64_t units = GATE ? p.N / 2 : p.N;
-  const int64_t unit0 = (int64_t)nt * (GATE ? BN / 2 : BN) + wn * kUnits + ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
-  auto eight = [&](int i, int j, uint4& lo, uint4& hi) __attribute__((always_inline)) {
-    uint32_t a[4], b[4];
+  dense_sums<I8, MODE, S>(p, part, m0, nt, wm, wn, acc);
+}
+
+// Tile (mt, nt) of a product of few rows, both operands along k.  All steps but one of a
+// ring of S::kStages are under way; one barrier a step, behind which the place of the
+// step before is loaded anew.  Narrower than Low, so that more of the CUs work without
+// parts and a join: 64 tokens of 2048 x 7168 take 13.5 us (Low in 4 parts 10.2, and 4.0
+// for the join), in int8 8.5 (Low 11.8); the block of 7168 x 2048 in int8 with 2
+// tokens 27.0 -> 23.2 us, with 64 31.4 -> 26.7.  What a CU takes in of a step's 16 KB bounds it, 0.27 us
+// alone and 0.22 by two blocks, also with 64 blocks in all.  Not better: rings of 9
+// steps (28.0 us in place of 26.6 for the block in bf16, 64 tokens; 4 steps as 5), the
+// fragments read a step ahead with halves of a step to a wave (8.6 -> 10.9), blocks that
+// begin at k of their own.
+template <bool I8, int MODE, class S>
+__device__ __forceinline__ void few_tile(const DenseGemm& p, int part, int64_t mt, int nt, uint8_t* lds) {
+  constexpr int NW = S::NW, BM = S::BM, BN = S::BN, WM = S::WM, WN = S::WN, ST = S::kStages;
+  using TA = Tile<BM, false, NW, kWholeStep>;
+  using TB = Tile<BN, false, NW, kWholeStep>;
+  constexpr int kStage = TA::kBytes + TB::kBytes, L = TA::kLoads + TB::kLoads;
+  static_assert(L * (ST - 1) < 64, "loads a wave can count");
+  static_assert(S::WAVES_N == 1 && ST == 5, "a wave takes all columns; the waits below");
+  const int64_t m0 = mt * BM, n0 = (int64_t)nt * BN;
+  const int wave = uniform((int)threadIdx.x / kWave);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+  constexpr int kStep = I8 ? 128 : 64;
+  const int all = uniform((int)((p.K + kStep - 1) / kStep));
+  const int s0 = min(all, part * p.steps), s1 = min(all, s0 + p.steps), n = s1 - s0;
+  const int rest = (int)(p.K % kStep) * (I8 ? 1 : 2);  // bytes of the last step, 0: whole
+  TA ta;
+  TB tb;
+  const int64_t left_m = p.M - m0, left_n = p.N - n0;
+  ta.init(p.a + m0 * p.a_stride, p.a_stride, left_m, s0, 0, wave,
+          [&](int row) { return min((int64_t)row, left_m - 1); });
+  if constexpr (MODE == kDenseGate) {
+    const int64_t inter = p.N / 2, c0 = n0 / 2;
+    tb.init(p.b + c0 * p.b_stride, p.b_stride, left_n, s0, 0, wave,
+            [&](int row) { return gate_row<WN>(row, c0, inter); });
+  } else {
+    tb.init(p.b + n0 * p.b_stride, p.b_stride, left_n, s0, 0, wave,
+            [&](int row) { return min((int64_t)row, left_n - 1); });
+  }
+  Fragments<BM, false, WM> fa;
+  Fragments<BN, false, WN> fb;
+  fa.init(wave * WM);
+  fb.init(0);
+  v4i acc[WM / 16][WN / 16];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const auto x = __builtin_amdgcn_permlane16_swap((uint32_t)acc[i][j][r], (uint32_t)acc[i][j + 1][r], false, false);
-      a[r] = x[0], b[r] = x[1];
+  for (int i = 0; i < WM / 16; ++i)
+#pragma unroll
+    for (int j = 0; j < WN / 16; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+
+  // step s into place `at` of the ring
+  auto issue = [&](int s, int at) __attribute__((always_inline)) {
+    const uint32_t to = lds0 + at * kStage;
+    if (rest != 0 && s0 + s == all - 1) {
+#pragma unroll
+      for (int u = 0; u < TB::kLoads; ++u) tb.issue_tail(u, rest, to + TA::kBytes, wave);
+#pragma unroll
+      for (int u = 0; u < TA::kLoads; ++u) ta.issue_tail(u, rest, to, wave);
+    } else {
+#pragma unroll
+      for (int u = 0; u < TB::kLoads; ++u) tb.issue(u, to + TA::kBytes, wave);
+#pragma unroll
+      for (int u = 0; u < TA::kLoads; ++u) ta.issue(u, to, wave);
     }
-    lo = make_uint4(a[0], a[1], a[2], a[3]);
-    hi = make_uint4(b[0], b[1], b[2], b[3]);
   };
-  constexpr int kPairs = kUnits / 32;
-  const int64_t row0 = m0 + wm * WM + (lane & 15);
-  if (p.split > 1) {
-    uint32_t* sums = static_cast<uint32_t*>(p.part) + (int64_t)part * p.M * p.N;
+  for (int s = 0; s < min(n, ST - 1); ++s) issue(s, s);
+  int at = 0;
+  for (int s = 0; s < n; ++s) {
+    const int behind = n - 1 - s;  // steps that may be under way, as many as a ring holds
+    if (behind >= 3) wait_barrier<3 * L>();
+    else if (behind == 2) wait_barrier<2 * L>();
+    else if (behind == 1) wait_barrier<L>();
+    else wait_barrier<0>();
+    const uint8_t* a = lds + at * kStage;
+    const uint8_t* b = a + TA::kBytes;
+    v4i af[2][WM / 16], bf[2][WN / 16];
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const int64_t m = row0 + 16 * i;
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int j = 0; j < (GATE ? 2 : 1) * kPairs; ++j) {
-        uint4 lo, hi;
-        eight(i, 2 * j, lo, hi);
-        const int64_t unit = unit0 + 32 * (j % kPairs);
-        if (m < p.M && unit < units) {
-          uint4* at = reinterpret_cast<uint4*>(sums + m * p.N + (j / kPairs) * units + unit);
-          at[0] = lo, at[1] = hi;
-        }
-      }
+      for (int i = 0; i < WM / 16; ++i) af[h][i] = fa.read(a, i, h);
+#pragma unroll
+      for (int j = 0; j < WN / 16; ++j) bf[h][j] = fb.read(b, j, h);
     }
-    return;
+    if (s + ST - 1 < n) issue(s + ST - 1, at == 0 ? ST - 1 : at - 1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < WM / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < WN / 16; ++j) acc[i][j] = mma<I8>(bf[h][j], af[h][i], acc[i][j]);
+    at = at == ST - 1 ? 0 : at + 1;
   }
-  // reads of a group of rows are under way while the one before is finished (int8:
-  // the columns' scales take the registers; float32 gates and ups are too many)
-  constexpr int kDeep = I8 || MODE == kDenseDgate ? 1 : 2;
-  Ahead<I8, MODE> ahead[kDeep][kPairs];
-  float row_scale = 1.0f;
-  Bytes32 col_scale[I8 ? (GATE ? 2 : 1) * kPairs : 1];
-  auto load = [&](int i) __attribute__((always_inline)) {
-    const int64_t m = min(row0 + 16 * i, p.M - 1);
-    if constexpr (I8) row_scale = p.e.row_scale[m];
-#pragma unroll
-    for (int j = 0; j < kPairs; ++j) ahead[i % kDeep][j].load(p.e, m, min(unit0 + 32 * j, units - 8));
-  };
-  if constexpr (kDeep == 2) load(0);
-  if constexpr (I8) {
-#pragma unroll
-    for (int j = 0; j < (GATE ? 2 : 1) * kPairs; ++j)
-      col_scale[j] = load32(p.e.col_scale + (j / kPairs) * units + min(unit0 + 32 * (j % kPairs), units - 8));
-  }
-#pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int64_t m = row0 + 16 * i;
-    if (kDeep == 1 || i + 1 < FM) load(i + kDeep - 1);
-#pragma unroll
-    for (int j = 0; j < kPairs; ++j) {
-      const int64_t unit = unit0 + 32 * j;
-      uint4 lo, hi;
-      float v[8], up[8];
-      eight(i, 2 * j, lo, hi);
-      sums_to_float(I8, lo, hi, v);
-      if constexpr (I8) scale8(row_scale, col_scale[j], v);
-      if constexpr (GATE) {
-        eight(i, 2 * (j + kPairs), lo, hi);
-        sums_to_float(I8, lo, hi, up);
-        if constexpr (I8) scale8(row_scale, col_scale[j + kPairs], up);
-      }
-      if (m < p.M && unit < units) {
-        if constexpr (GATE) finish_gate<I8>(p.e, m, unit, v, up);
-        else finish<I8, MODE>(p.e, m, unit, v, ahead[i % kDeep][j]);
-      }
-    }
-  }
+  dense_sums<I8, MODE, S>(p, part, m0, nt, wave, 0, acc);
+}
+
+// The blocks of an XCD take parts and columns next to one another; rows' tiles go last.
+template <bool I8, int MODE, class S>
+__global__ __launch_bounds__(S::NW* kWave, 2) void k_dense_few(DenseGemm p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
+  const int tiles_n = (p.N + S::BN - 1) / S::BN;
+  const int64_t total = gridDim.x, c = blockIdx.x, x = c & 7;
+  const int64_t t = x * (total >> 3) + min(x, total & 7) + (c >> 3);
+  const int64_t tiles = total / p.split;
+  const int part = uniform((int)(t / tiles));
+  const int64_t tile = t - part * tiles;
+  few_tile<I8, MODE, S>(p, part, tile / tiles_n, (int)(tile % tiles_n), lds);
 }
 
 // Block b of those that share the product p (dense_blocks of them).  Blocks go round
@@ -467,6 +597,15 @@ hipError_t launch(const DenseGemm& p, hipStream_t st) {
     case kDenseLow:
       if constexpr (!AT) return launch_shape<I8, AT, BT, MODE, Low>(p, st);
       return hipErrorInvalidValue;
+    case kDenseFew:
+      if constexpr (!AT && !BT) {
+        const int64_t blocks = dense_blocks(p);
+        if (blocks == 0) return hipSuccess;
+        if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
+        k_dense_few<I8, MODE, Few><<<(unsigned)blocks, Few::NW * kWave, 0, st>>>(p);
+        return hipGetLastError();
+      }
+      return hipErrorInvalidValue;
     default: return hipErrorInvalidValue;
   }
 }
@@ -474,6 +613,7 @@ hipError_t launch(const DenseGemm& p, hipStream_t st) {
 static_assert(Big::BM == dense_rows(kDenseBig) && Big::BN == dense_columns(kDenseBig), "tiles");
 static_assert(Half::BM == Big::BM && 2 * Half::BN == Big::BN && Half::NW == Big::NW && Half::kLds <= Big::kLds, "halves");
 static_assert(Mid::BM == dense_rows(kDenseMid) && Mid::BN == dense_columns(kDenseMid), "tiles");
+static_assert(Few::BM == dense_rows(kDenseFew) && Few::BN == dense_columns(kDenseFew), "tiles");
 static_assert(Low::BM == dense_rows(kDenseLow) && Low::BN == dense_columns(kDenseLow), "tiles");
 
 }  // namespace dense

@@ -203,6 +203,15 @@ def test_long_sums(T):
     b.check_precise(b.backward())
 
 
+# few tokens, short sums and many columns: gates and ups, then the product behind them
+@pytest.mark.parametrize("T", [2, 40, 64, 66, 256])
+@pytest.mark.parametrize("H, I", [(8, 4104), (64, 4104), (72, 4104), (136, 4104), (256, 4104), (328, 4104), (4104, 8),
+                                  (4104, 72), (4104, 192), (4104, 264), (4104, 320)])
+def test_few_tokens_and_steps(T, H, I):
+    b = Block(T, H, I, seed=6)
+    b.check_forward(b.forward())
+
+
 # enough tiles of 256 x 256 for each product in turn, none of them whole
 # (the last three: a last round of tiles that two blocks each take, in every direction)
 @pytest.mark.parametrize("T, H, I", [(3589, 72, 3400), (3589, 3400, 72), (2309, 2824, 1416), (77, 4104, 3848),

@@ -97,6 +97,13 @@ def test_product(T, K, N, out):
     product_case(T, K, N, out)
 
 
+# few tokens: one to nine K steps, whole ones and with an end, tiles of 64 x 64 and others
+@pytest.mark.parametrize("T", [2, 20, 64, 65, 256])
+@pytest.mark.parametrize("K", [16, 128, 144, 256, 272, 384, 400, 512, 528, 640, 656, 768, 1040, 1152])
+def test_few_tokens_and_steps(T, K):
+    product_case(T, K, 7176, "f32", "none", seed=3)
+
+
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 @pytest.mark.parametrize("T, K, N", [(3, 272, 72), (40, 4096, 136), (140, 528, 264)])
 def test_product_bases_and_strides(T, K, N, out):
