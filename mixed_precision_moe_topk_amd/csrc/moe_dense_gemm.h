@@ -442,7 +442,7 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& p, int part, int64_t
 // Tile (mt, nt) of a product of few rows, both operands along k.  All steps but one of a
 // ring of S::kStages are under way; one barrier a step, behind which the place of the
 // step before is loaded anew.  Narrower than Low, so that more of the CUs work without
-// parts and a join: 64 tokens of 2048 x 7168 take 13.5 us (Low in 4 parts 10.2, and 4.0
+// parts and a join: 64 tokens of 2048 x 7168 take 11.4 us (Low in 4 parts 10.2, and 4.0
 // for the join), in int8 8.5 (Low 11.8); the block of 7168 x 2048 in int8 with 2
 // tokens 27.0 -> 23.2 us, with 64 31.4 -> 26.7.  What a CU takes in of a step's 16 KB bounds it, 0.27 us
 // alone and 0.22 by two blocks, also with 64 blocks in all.  Not better: rings of 9
