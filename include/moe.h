@@ -615,7 +615,8 @@ moe_status moe_ffn_saved_query(const moe_ffn_dims* dims, int64_t num_tokens, siz
  *   out:    device bf16 [num_tokens, hidden]; may be x (with the same stride)
  *   saved:  device buffer of moe_ffn_saved_query bytes for the backward pass, or
  *           null
- * Sums are float32.  h is rounded to bf16 before the second product, out once.
+ * Sums are float32.  h is rounded to bf16 before the second product (a finite one to
+ * a finite one), out once.
  * num_tokens = 0 returns MOE_OK without launching.  Errors as moe_run_ws. */
 moe_status moe_ffn_apply(const moe_ffn_dims* dims, const void* x, int64_t x_stride,
                          int64_t num_tokens, const void* w1, const void* w2, const void* base,
@@ -639,8 +640,8 @@ moe_status moe_ffn_apply(const moe_ffn_dims* dims, const void* x, int64_t x_stri
  *   dx_base: device bf16 [num_tokens, hidden]; may be dx (with the same stride);
  *          null: 0
  * Sums are float32.  For dx and for bf16 dw1 and dw2, dg, du and h enter the products
- * rounded to bf16; for float dw1 and dw2 as two bf16 terms (within 2^-17), at twice
- * those products' work.  (An infinity in x or dout may then come out as NaN.)
+ * rounded to bf16 (finite ones to finite ones); for float dw1 and dw2 as two bf16
+ * terms (within 2^-17), at twice those products' work.  (An infinity in x or dout may then come out as NaN.)
  * num_tokens = 0 writes zeros into dw1 and dw2, or returns MOE_OK without
  * launching when they are null.  Errors as moe_run_ws, and MOE_ERR_INVALID_ARG
  * when no gradient of some tokens is wanted. */

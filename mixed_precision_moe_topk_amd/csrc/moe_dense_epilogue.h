@@ -16,6 +16,22 @@ __device__ __forceinline__ uint4 bf16_pack8(const float (&v)[8]) {
   return make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
                     bf16_pair(v[6], v[7]));
 }
+// The same of operands of further products: a finite value stays finite.  From
+// 2^128 - 2^119 on it would round up to infinity and takes the largest bf16, 2^128 -
+// 2^120, which is within 2^-8 of it as any rounding is.  (One test of eight.)
+__device__ __forceinline__ uint4 bf16_operand8(const float (&v)[8]) {
+  constexpr float kUp = 0x1.FFp127f;
+  const uint4 u = bf16_pack8(v);
+  float top = fabsf(v[0]);
+#pragma unroll
+  for (int j = 1; j < 8; ++j) top = fmaxf(top, fabsf(v[j]));
+  if (__builtin_expect(!(top >= kUp), 1)) return u;
+  uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)  // (the bits before infinity's)
+    if (fabsf(v[j]) >= kUp && fabsf(v[j]) < __builtin_inff()) w[j / 2] -= j & 1 ? 0x10000u : 1u;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
 // What the rounding of v to bf16 (packed in `hi`) left, rounded in turn: together
 // within 2^-17 of v.  0 where that is not finite.
 __device__ __forceinline__ uint4 bf16_rest8(const float (&v)[8], const uint4& hi) {
@@ -146,7 +162,7 @@ __device__ __forceinline__ void finish_gate(const DenseEpilogue& e, int64_t m, i
   if constexpr (I8) {
     store8(static_cast<float*>(e.out) + at, h);
   } else {
-    const uint4 hi = bf16_pack8(h);
+    const uint4 hi = bf16_operand8(h);
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.out) + at) = hi;
     if (e.out_lo) *reinterpret_cast<uint4*>(e.out_lo + at) = bf16_rest8(h, hi);
   }
@@ -169,7 +185,7 @@ __device__ __forceinline__ void finish_dgate(const DenseEpilogue& e, int64_t m, 
     u[j] = du;
   }
   uint16_t* out = static_cast<uint16_t*>(e.out) + at;
-  const uint4 dg = bf16_pack8(g), du = bf16_pack8(u);
+  const uint4 dg = bf16_operand8(g), du = bf16_operand8(u);
   *reinterpret_cast<uint4*>(out) = dg;
   *reinterpret_cast<uint4*>(out + e.inter) = du;
   if (e.out_lo) {

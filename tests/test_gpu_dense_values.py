@@ -1,0 +1,59 @@
+"""The gated block at the ends of the float range: values next to the largest.
+Tolerances as in tests/test_gpu_dense.py."""
+import numpy as np
+import pytest
+
+from tests.test_gpu_dense import STEP, Block, close, product, rounded
+
+pytestmark = pytest.mark.gpu
+HUGE = 2.0 ** 127
+
+
+def large(T, H, I):
+    """One token whose h, dg and du lie next to 2^128 (1 - 2^-11): bf16 has no number
+    between 2^128 (1 - 2^-8) and 2^128, and rounds up from 2^128 (1 - 2^-9) on."""
+    b, at = Block(T, H, I, seed=60), T // 2
+    units = np.arange(I) % 3 == 0  # so large there, 0 elsewhere
+    sign = np.where(np.arange(I) % 2, -1.0, 1.0)
+    b.x[:, :2], b.x[at] = 0, 0
+    b.x[at, :2] = 1
+    near = np.array([2.0 ** 64, -2.0 ** 52])  # adds up to 2^64 (1 - 2^-12)
+    b.w1[:, :2] = 0
+    b.w1[:I, :2] = units[:, None] * near
+    b.w1[I:, :2] = (units * sign)[:, None] * near
+    b.w1[:, 2:] *= 2.0 ** -30
+    b.w2 *= 2.0 ** -30
+    b.w2[:2] = 2.0 ** -30 * np.where(np.arange(I) % 5, 1.0, -1.0)
+    b.dout[at] *= 2.0 ** -20
+    b.dout[at, :2] = 2.0 ** 94, -2.0 ** 82
+    return b, at
+
+
+@pytest.mark.parametrize("T, H, I", [(1, 72, 40), (3, 264, 136), (40, 4104, 72), (300, 264, 136), (2309, 1032, 1416)])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_finite_values_stay_finite(T, H, I, kind):
+    b, at = large(T, H, I)
+    f = b.forward()
+    assert np.abs(f["h2"][at]).max() > HUGE and np.isfinite(f["h"]).all()
+    b.check_forward(f)
+    r = b.backward(kind)
+    assert np.isfinite(r["dgu"]).all()
+    x, w1, w2, dout = (v.astype(np.float64) for v in (b.x, b.w1, b.w2, b.dout))
+    # the gradients of the large units, from what was saved: sigmoid is 1, 1 - sigmoid 0
+    dh = dout[at] @ w2
+    big = np.abs(f["g"][at]) > 0
+    want = np.concatenate([(dh * f["u"][at])[big], (dh * f["g"][at])[big]])
+    assert np.abs(want).max() > HUGE
+    both = np.concatenate([big, big])
+    err = (H + 40) * STEP * np.abs(want)
+    close("dg, du", r["dgu"][at][both], want, rounded(want, err, "bf16"))
+    if kind == "f32":
+        close("dg, du in two terms", r["dgu2"][at][both], want, rounded(want, err, "two terms"))
+    d, h = (r["dgu2"], f["h2"]) if kind == "f32" else (r["dgu"], f["h"])
+    for name, a, c, k in (("dx", r["dgu"], w1.T, "bf16"), ("dw1", d.T, x.T, kind), ("dw2", dout.T, h.T, kind)):
+        base = b.dxb.astype(np.float64) if name == "dx" else 0.0
+        want, err = product(a, c, base)
+        tol = rounded(want, 2 * err, k)
+        fits = np.abs(a) @ np.abs(c).T < 2 * HUGE * (1 - 2.0 ** -12)  # no sum on the way may overflow
+        assert fits.mean() > (0.5 if name == "dx" else 0.9)
+        close(name, np.where(fits, r[name], 0), np.where(fits, want, 0), tol)
