@@ -641,7 +641,9 @@ moe_status moe_ffn_apply(const moe_ffn_dims* dims, const void* x, int64_t x_stri
  *          null: 0
  * Sums are float32.  For dx and for bf16 dw1 and dw2, dg, du and h enter the products
  * rounded to bf16 (finite ones to finite ones); for float dw1 and dw2 as two bf16
- * terms (within 2^-17), at twice those products' work.  (An infinity in x or dout may then come out as NaN.)
+ * terms (within 2^-17), at twice those products' work.  Infinities and NaN in x or
+ * dout give those of the formulas (a dg, du or h below 2^-126 may count as 0 where it
+ * meets one), and take up to twice as long.
  * num_tokens = 0 writes zeros into dw1 and dw2, or returns MOE_OK without
  * launching when they are null.  Errors as moe_run_ws, and MOE_ERR_INVALID_ARG
  * when no gradient of some tokens is wanted. */

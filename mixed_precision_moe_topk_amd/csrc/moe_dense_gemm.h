@@ -195,6 +195,20 @@ __device__ __forceinline__ int64_t gate_row(int row, int64_t c0, int64_t inter) 
   return unit - c0 + (row % WN >= WN / 2 ? inter : 0);
 }
 
+// A lane holds columns 4 (lane / 16) + 0 .. 3 of each 16 x 16 sums.  Of two
+// neighbours, the odd quarters of the wave give theirs of the first for the even
+// quarters' of the second: every lane then has eight consecutive columns.
+__device__ __forceinline__ void eight_columns(const v4i& first, const v4i& second, uint4& lo, uint4& hi) {
+  uint32_t a[4], b[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const auto x = __builtin_amdgcn_permlane16_swap((uint32_t)first[r], (uint32_t)second[r], false, false);
+    a[r] = x[0], b[r] = x[1];
+  }
+  lo = make_uint4(a[0], a[1], a[2], a[3]);
+  hi = make_uint4(b[0], b[1], b[2], b[3]);
+}
+
 // What becomes of a block's sums: parts of them, or results.
 template <bool I8, int MODE, class S>
 __device__ __forceinline__ void dense_sums(const DenseGemm& p, int part, int64_t m0, int nt, int wm, int wn,
@@ -202,21 +216,11 @@ __device__ __forceinline__ void dense_sums(const DenseGemm& p, int part, int64_t
   constexpr int BN = S::BN, WM = S::WM, WN = S::WN, FM = WM / 16;
   constexpr bool GATE = MODE == kDenseGate;
   const int lane = lane_id();
-  // A lane holds columns 4 (lane / 16) + 0 .. 3 of each 16 x 16 sums.  Of two
-  // neighbours, the odd quarters of the wave give theirs of the first for the even
-  // quarters' of the second: every lane then has eight consecutive columns.
   constexpr int kUnits = GATE ? WN / 2 : WN;  // finished columns of a row
   const int64_t units = GATE ? p.N / 2 : p.N;
   const int64_t unit0 = (int64_t)nt * (GATE ? BN / 2 : BN) + wn * kUnits + ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
   auto eight = [&](int i, int j, uint4& lo, uint4& hi) __attribute__((always_inline)) {
-    uint32_t a[4], b[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const auto x = __builtin_amdgcn_permlane16_swap((uint32_t)acc[i][j][r], (uint32_t)acc[i][j + 1][r], false, false);
-      a[r] = x[0], b[r] = x[1];
-    }
-    lo = make_uint4(a[0], a[1], a[2], a[3]);
-    hi = make_uint4(b[0], b[1], b[2], b[3]);
+    eight_columns(acc[i][j], acc[i][j + 1], lo, hi);
   };
   constexpr int kPairs = kUnits / 32;
   const int64_t row0 = m0 + wm * WM + (lane & 15);
@@ -281,15 +285,57 @@ __device__ __forceinline__ void dense_sums(const DenseGemm& p, int part, int64_t
   }
 }
 
-// Tile (mt, nt) of part `part` of the product p.
+// The same for an operand in two terms, whose sums (or parts) are float32 without a
+// base: whether one of this lane's is not finite.  again: the sums are twice those of
+// the first terms (see dense_tile_terms); where they are not finite and neither is what the
+// lane stored before, they take its place.
+template <class S>
+__device__ __forceinline__ bool sums_of_terms(const DenseGemm& p, int part, int64_t m0, int nt, int wm, int wn,
+                                              v4i (&acc)[S::WM / 16][S::WN / 16], bool again) {
+  const int lane = lane_id();
+  const bool parts = p.split > 1;
+  float* const to = parts ? static_cast<float*>(p.part) + (int64_t)part * p.M * p.N : static_cast<float*>(p.e.out);
+  const int64_t stride = parts ? p.N : p.e.out_stride;
+  const int64_t column = (int64_t)nt * S::BN + wn * S::WN + ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
+  const int64_t row = m0 + wm * S::WM + (lane & 15);
+  constexpr float inf = __builtin_inff();
+  float odd = 0.0f;  // 0 as long as all are finite
+#pragma unroll
+  for (int i = 0; i < S::WM / 16; ++i) {
+#pragma unroll
+    for (int j = 0; j < S::WN / 32; ++j) {
+      uint4 lo, hi;
+      float v[8];
+      eight_columns(acc[i][2 * j], acc[i][2 * j + 1], lo, hi);
+      sums_to_float(false, lo, hi, v);
+      if (row + 16 * i >= p.M || column + 32 * j >= p.N) continue;
+      float* at = to + (row + 16 * i) * stride + column + 32 * j;
+      if (again) {
+        float before[8];
+        load8(at, before);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = fabsf(v[k]) < inf || fabsf(before[k]) < inf ? before[k] : v[k];
+      }
+      store8(at, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) odd = fmaf(v[k], 0.0f, odd);
+    }
+  }
+  return odd != 0.0f;
+}
+
+// Tile (mt, nt) of part `part` of the product p.  Of an operand in two terms the first is
+// taken in the place of both when `again`; returns whether a sum of this lane is then
+// not finite.
 template <bool I8, bool AT, bool BT, int MODE, class S, int TERMS = kPlain>
-__device__ __forceinline__ void dense_tile(const DenseGemm& p, int part, int64_t mt, int nt, uint8_t* lds) {
+__device__ __forceinline__ bool dense_tile(const DenseGemm& p, int part, int64_t mt, int nt, uint8_t* lds,
+                                           bool again = false) {
   constexpr int NW = S::NW, BM = S::BM, BN = S::BN, WAVES_N = S::WAVES_N, WM = S::WM, WN = S::WN;
   constexpr bool GATE = MODE == kDenseGate;
   using TA = Tile<BM, AT, NW, TERMS == kPlain ? kWholeStep : TERMS == kRowTerms ? kTwoTerms : kHalfStep>;
   using TB = Tile<BN, BT, NW, TERMS == kPlain ? kWholeStep : TERMS == kColumnTerms ? kTwoTerms : kHalfStep>;
   const int64_t m0 = mt * BM, n0 = (int64_t)nt * BN;
-  if (n0 >= p.N) return;  // (a half behind the last column)
+  if (n0 >= p.N) return false;  // (a half behind the last column)
   const int wave = uniform((int)threadIdx.x / kWave), lane = lane_id();
   const int wm = wave / WAVES_N, wn = wave % WAVES_N;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
@@ -300,15 +346,16 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& p, int part, int64_t
   const int rest = (int)(p.K % kStep);  // of the last step, 0: whole
   TA ta;
   TB tb;
+  const int64_t second = again ? 0 : p.lo;  // bytes to the second term
   const int64_t left_m = p.M - m0, left_n = p.N - n0;
-  ta.init(p.a + m0 * (AT ? 2 : p.a_stride), p.a_stride, left_m, s0, p.lo, wave,
+  ta.init(p.a + m0 * (AT ? 2 : p.a_stride), p.a_stride, left_m, s0, second, wave,
           [&](int row) { return min((int64_t)row, left_m - 1); });
   if constexpr (GATE) {
     const int64_t inter = p.N / 2, c0 = n0 / 2;
-    tb.init(p.b + c0 * p.b_stride, p.b_stride, left_n, s0, p.lo, wave,
+    tb.init(p.b + c0 * p.b_stride, p.b_stride, left_n, s0, second, wave,
             [&](int row) { return gate_row<WN>(row, c0, inter); });
   } else {
-    tb.init(p.b + n0 * (BT ? 2 : p.b_stride), p.b_stride, left_n, s0, p.lo, wave,
+    tb.init(p.b + n0 * (BT ? 2 : p.b_stride), p.b_stride, left_n, s0, second, wave,
             [&](int row) { return min((int64_t)row, left_n - 1); });
   }
   Fragments<BM, AT, WM> fa;
@@ -436,8 +483,35 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& p, int part, int64_t
     if (n > 1) step(Int<0>(), Int<1>());
     step(Int<0>(), Int<0>());
   }
+  if constexpr (TERMS != kPlain) return sums_of_terms<S>(p, part, m0, nt, wm, wn, acc, again);
   dense_sums<I8, MODE, S>(p, part, m0, nt, wm, wn, acc);
+  return false;
 }
+
+// The same of an operand in two terms.  An infinity of the other operand, times terms of
+// opposite signs or one of them 0, makes NaN of what the formula has as an infinity.  So
+// where a sum of the block is not finite its tile is taken again, from the first terms
+// in both terms' place: they have the operand's signs, infinities and NaN, and twice
+// their sums has the infinities and NaN of the formula.  (4093 tokens of 7168 x 2048,
+// trained: 1112 -> 1121 us for the test alone.)
+template <bool AT, bool BT, class S, int TERMS>
+__device__ __forceinline__ void dense_tile_terms(const DenseGemm& p, int part, int64_t mt, int nt, uint8_t* lds) {
+  const int wave = uniform((int)threadIdx.x / kWave);
+  int* odd = reinterpret_cast<int*>(lds);  // (no wave reads its operands any more)
+  for (bool again = false;; again = true) {
+    const bool mine = dense_tile<false, AT, BT, kDenseStore, S, TERMS>(p, part, mt, nt, lds, again);
+    if (again) return;
+    const bool any = __any(mine);
+    if (lane_id() == 0) odd[wave] = any;
+    __syncthreads();
+    int all = 0;
+#pragma unroll
+    for (int w = 0; w < S::NW; ++w) all |= odd[w];
+    if (uniform(all) == 0) return;
+    __syncthreads();
+  }
+}
+
 
 // Tile (mt, nt) of a product of few rows, both operands along k.  All steps but one of a
 // ring of S::kStages are under way; one barrier a step, behind which the place of the
@@ -568,11 +642,13 @@ __device__ __forceinline__ void dense_block(const DenseGemm& p, int64_t b, uint8
   const int nt = r / gm;
   if constexpr (S::BN == Big::BN) {
     if (half) {
-      dense_tile<I8, AT, BT, MODE, Half, TERMS>(p, part, mt, 2 * nt + side, lds);
+      if constexpr (TERMS != kPlain) dense_tile_terms<AT, BT, Half, TERMS>(p, part, mt, 2 * nt + side, lds);
+      else dense_tile<I8, AT, BT, MODE, Half>(p, part, mt, 2 * nt + side, lds);
       return;
     }
   }
-  dense_tile<I8, AT, BT, MODE, S, TERMS>(p, part, mt, nt, lds);
+  if constexpr (TERMS != kPlain) dense_tile_terms<AT, BT, S, TERMS>(p, part, mt, nt, lds);
+  else dense_tile<I8, AT, BT, MODE, S>(p, part, mt, nt, lds);
 }
 
 template <bool I8, bool AT, bool BT, int MODE, class S>

@@ -1,9 +1,11 @@
-"""The gated block at the ends of the float range: values next to the largest.
-Tolerances as in tests/test_gpu_dense.py."""
+"""The gated block at the ends of the float range: values next to the largest, and
+infinities.  Tolerances as in tests/test_gpu_dense.py, where results are finite; an
+infinity or NaN of the formulas (in float64, from the operands that the GPU saved) has to
+come out as that infinity or NaN."""
 import numpy as np
 import pytest
 
-from tests.test_gpu_dense import STEP, Block, close, product, rounded
+from tests.test_gpu_dense import HALF, STEP, Block, close, product, rounded
 
 pytestmark = pytest.mark.gpu
 HUGE = 2.0 ** 127
@@ -57,3 +59,28 @@ def test_finite_values_stay_finite(T, H, I, kind):
         fits = np.abs(a) @ np.abs(c).T < 2 * HUGE * (1 - 2.0 ** -12)  # no sum on the way may overflow
         assert fits.mean() > (0.5 if name == "dx" else 0.9)
         close(name, np.where(fits, r[name], 0), np.where(fits, want, 0), tol)
+
+
+@pytest.mark.parametrize("T, H, I, dx", [(1, 72, 40, "base"), (5, 136, 72, "base"), (40, 264, 136, "base"),
+                                         (300, 520, 264, "base"), (5000, 64, 72, "base"), (2309, 1032, 1416, "base"),
+                                         (2309, 2824, 1416, "none"), (130, 5752, 904, "none")])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_infinities(T, H, I, dx, kind):
+    b = Block(T, H, I, seed=61)
+    b.dout[0, 3], b.dout[T // 2, 5], b.dout[T - 1, 6] = np.inf, -np.inf, np.inf
+    b.x[T // 3, 4], b.x[2 * T // 3, 2] = np.inf, -np.inf
+    f = b.forward()
+    r = b.backward(kind, dx=dx)
+    x, dout = b.x.astype(np.float64), b.dout.astype(np.float64)
+    d, h = (r["dgu2"], f["h2"]) if kind == "f32" else (r["dgu"], f["h"])
+    seen = 0
+    with np.errstate(invalid="ignore", over="ignore"):
+        for name, a, c in (("dw1", d, x), ("dw2", dout, h)):
+            want = a.T @ c
+            odd = ~np.isfinite(want)
+            seen += int(np.isinf(want).sum())
+            assert np.array_equal(r[name][odd], want[odd], equal_nan=True), name
+            err = (2 * T + 34) * STEP * (1 + 2.0 ** -7) * (np.abs(a).T @ np.abs(c))
+            tol = err + HALF[kind] * (np.abs(want) + err)
+            close(name, np.where(odd, 0, r[name]), np.where(odd, 0, want), np.where(odd, 0, tol))
+    assert seen > 0
