@@ -34,7 +34,8 @@ __global__ __launch_bounds__(S::NW* kWave, 2) void k_dense_grads(DenseGrads g) {
   } else if (c1 >= 0 && c1 < g.blocks[1]) {
     dense_block<false, true, true, kDenseStore, S, TERMS ? kColumnTerms : kPlain>(g.p[1], c1, lds);
   } else if (c0 >= 0 && c0 < g.blocks[0]) {
-    dense_block<false, true, true, kDenseStore, S, TERMS ? kRowTerms : kPlain>(g.p[0], c0, lds);
+    // (dw2, whose sums are as long, comes behind it: its tiles are the ones in halves)
+    dense_block<false, true, true, kDenseStore, S, TERMS ? kRowTerms : kPlain, false>(g.p[0], c0, lds);
   }
 }
 
@@ -50,7 +51,7 @@ hipError_t launch_dense_grads(const DenseGemm (&p)[3], hipStream_t st) {
     blocks += (g.blocks[q] + 7) / 8 * 8;
   }
   if (blocks == 0) return hipSuccess;
-  if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
+  if (blocks > 0x7FFFFFFFLL || p[0].halves != 0) return hipErrorInvalidValue;
   const unsigned n = (unsigned)blocks;
   using dense::Big;
   using dense::Mid;

@@ -622,7 +622,8 @@ __global__ __launch_bounds__(S::NW* kWave, 2) void k_dense_few(DenseGemm p) {
 // Block b of those that share the product p (dense_blocks of them).  Blocks go round
 // the 8 XCDs: each takes a contiguous range of the tiles, in groups of 4 rows of
 // tiles, so that the blocks at work on one XCD share their operands in its L2.
-template <bool I8, bool AT, bool BT, int MODE, class S, int TERMS = kPlain>
+// HALVES: the last tiles may be those of two blocks each.
+template <bool I8, bool AT, bool BT, int MODE, class S, int TERMS = kPlain, bool HALVES = S::BN == Big::BN>
 __device__ __forceinline__ void dense_block(const DenseGemm& p, int64_t b, uint8_t* lds) {
   const int64_t tiles_m = (p.M + S::BM - 1) / S::BM;
   const int tiles_n = (p.N + S::BN - 1) / S::BN;
@@ -640,7 +641,7 @@ __device__ __forceinline__ void dense_block(const DenseGemm& p, int64_t b, uint8
   const int r = (int)(t - group * 4 * tiles_n);
   const int64_t mt = first_m + r % gm;
   const int nt = r / gm;
-  if constexpr (S::BN == Big::BN) {
+  if constexpr (HALVES) {
     if (half) {
       if constexpr (TERMS != kPlain) dense_tile_terms<AT, BT, Half, TERMS>(p, part, mt, 2 * nt + side, lds);
       else dense_tile<I8, AT, BT, MODE, Half>(p, part, mt, 2 * nt + side, lds);

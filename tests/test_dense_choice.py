@@ -3,6 +3,7 @@
 they are asked for."""
 import ctypes
 import os
+import random
 import subprocess
 
 import pytest
@@ -123,3 +124,22 @@ def test_exact_cases_reach_every_kernel(choice):
     # the loop that the long training steps run: many steps of large tiles, two terms
     c = choice.backward(6140, 4040, 1032)
     assert c["dw1"]["shape"] == c["dw2"]["shape"] == BIG and min(c["dw1"]["steps"], c["dw2"]["steps"]) > 100
+
+
+def test_halves_and_room(choice):
+    """dw1 has no tiles in halves (its kernel has no code for them), and the parts of a
+    launch fit into the workspace behind the operands."""
+    rng = random.Random(0)
+    for _ in range(300):
+        T, H, I = (int(2 ** rng.uniform(lo, hi)) for lo, hi in ((0, 14), (0, 10), (0, 9)))
+        d = M.FfnDims(8 * H, 8 * I)
+        chosen = [choice.forward(T, d.hidden, d.inter)]
+        for kind in ("f32", "bf16"):
+            for dx, weights in ((True, True), (False, True), (True, False)):
+                chosen.append(choice.backward(T, d.hidden, d.inter, kind, dx, weights))
+        room = M.ffn_workspace_query(d, T) - (T * 8 * d.inter + 255) // 256 * 256
+        for c in chosen:
+            assert c.get("dw1", {}).get("halves", 0) == 0, (T, d)
+            part = {n: (p["split"] * p["M"] * p["N"] * 4 + 255) // 256 * 256 if p["split"] > 1 else 0 for n, p in c.items()}
+            together = sum(part.get(n, 0) for n in ("dw1", "dw2", "dx"))
+            assert max([together] + [part.get(n, 0) for n in ("gate", "down", "dgate")]) <= room, (T, d)
