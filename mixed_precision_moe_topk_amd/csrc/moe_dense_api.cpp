@@ -176,7 +176,7 @@ void choose(DenseGemm& g, bool int8, bool along) {
 // first) by whichever slot is free.
 double share_out(DenseGemm (&g)[3], int shape, int64_t share) {
   int64_t blocks = 0;
-  double total = 0, joins = 0;
+  double total = 0, longest = 0, joins = 0;
   const Cost each = shape == moe::kDenseBig ? kOne[shape] : kTwo[shape];
   for (DenseGemm& q : g) {
     q.shape = shape;
@@ -186,7 +186,9 @@ double share_out(DenseGemm (&g)[3], int shape, int64_t share) {
     const int64_t n = moe::dense_tiles(q) * q.split;
     if (n == 0) continue;
     blocks += n;
-    total += (double)n * ((double)q.steps * each.step + each.fixed);
+    const double cost = (double)q.steps * each.step + each.fixed;
+    total += (double)n * cost;
+    longest = std::max(longest, cost);
     joins += join_cost(q, q.split);
   }
   int order[3];
@@ -204,7 +206,9 @@ double share_out(DenseGemm (&g)[3], int shape, int64_t share) {
     last->halves = (int32_t)std::min(moe::dense_halves(shape, blocks), moe::dense_tiles(*last) * last->split);
     return joins + run_cost(shape, blocks, (double)last->steps);
   }
-  if (blocks > 64 * slots(shape)) return joins + total / (double)slots(shape);
+  // no launch ends before its longest block does
+  const double least = std::max(longest, total / (double)slots(shape));
+  if (blocks > 64 * slots(shape)) return joins + least;
   struct Free {
     double at;
     int64_t n;
@@ -226,7 +230,7 @@ double share_out(DenseGemm (&g)[3], int shape, int64_t share) {
       int into = -1;
       for (int k = 0; k < groups; ++k)
         if (free[k].at == done) into = k;
-      if (into < 0 && groups == 8) return joins + std::max(end, total / (double)slots(shape));
+      if (into < 0 && groups == 8) return joins + std::max(end, least);
       if (into < 0) free[into = groups++] = {done, 0};
       free[into].n += take;
     }

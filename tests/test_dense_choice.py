@@ -143,3 +143,11 @@ def test_halves_and_room(choice):
             part = {n: (p["split"] * p["M"] * p["N"] * 4 + 255) // 256 * 256 if p["split"] > 1 else 0 for n, p in c.items()}
             together = sum(part.get(n, 0) for n in ("dw1", "dw2", "dx"))
             assert max([together] + [part.get(n, 0) for n in ("gate", "down", "dgate")]) <= room, (T, d)
+
+
+def test_long_sums_are_cut(choice):
+    """A few long sums among very many short ones: 16 blocks of 8192 steps ran four times as
+    long as all the others together when the estimate left the longest block out."""
+    for T in (1, 3, 64):
+        c = choice.backward(T, 4096, 1 << 18)
+        assert c["dx"]["split"] > 1 and c["dx"]["steps"] <= 2048, (T, c["dx"])
