@@ -133,14 +133,22 @@ hipError_t launch_rows(const DenseGemm& p, hipStream_t st) {
   return hipGetLastError();
 }
 
-// More rows a wave read a less often, while the blocks still reach most CUs.
+// Rows of weights a wave, where several copies of the weights are read in turn, us by 1
+// and by 2 rows:
+//   columns           2048       4096       6144  |    6400       8192       9216
+//   int8, 1024 long   3.3  3.9   4.6  4.3   6.2  6.3 |  6.9  6.3   7.6  6.4   9.3  8.3
+//   int8, 7168 long   4.9  5.9   7.3  7.6   9.7 10.7 | 10.9 10.9  11.9 12.3  14.6 14.8
+//   bf16, 1024 long (the block, gate and up included)
+//                     9.5 10.6  11.9 11.9  16.0 16.4 | 16.8 16.4  17.9 17.4  21.3 21.7
+//   bf16, 7168 long  22.7 24.6  34.4 35.0  51.3 53.4 | 53.7 53.6  63.0 63.5  73.4 76.1
+// One row up to three blocks of 8 rows a CU, which are all at work at once; from there on
+// two, which win by up to 15 % for short rows and lose up to 4 % for long ones.  Four rows
+// were not faster at any size.  Gates and ups take one unit's two rows: two units a wave
+// gained 2 to 8 % for 2304 to 2560 units of 7168 and longer, and lost 4 to 25 % elsewhere.
 template <bool I8>
 hipError_t launch_one(int mode, const DenseGemm& p, hipStream_t st) {
-  constexpr int64_t kBlocks = 224;
-  if (mode == kDenseGate)
-    return p.N / 2 >= 16 * kBlocks ? launch_rows<I8, kDenseGate, 4>(p, st) : launch_rows<I8, kDenseGate, 2>(p, st);
-  if (p.N >= 32 * kBlocks) return launch_rows<I8, kDenseStore, 4>(p, st);
-  return p.N >= 16 * kBlocks ? launch_rows<I8, kDenseStore, 2>(p, st) : launch_rows<I8, kDenseStore, 1>(p, st);
+  if (mode == kDenseGate) return launch_rows<I8, kDenseGate, 2>(p, st);
+  return p.N <= 3 * kCus * kOneWaves ? launch_rows<I8, kDenseStore, 1>(p, st) : launch_rows<I8, kDenseStore, 2>(p, st);
 }
 
 }  // namespace

@@ -136,3 +136,25 @@ def test_largest_weights(T, kind):
     """2^30 weights a matrix: every row of w1 (2^33 bytes of float32 gradients) and of w2
     counts."""
     Exact(T, 4096, 1 << 18, "powers", 4).run(kind)
+
+
+@pytest.mark.parametrize("H", [2048, 6144, 6152, 8200])
+def test_one_token(H):
+    """Either side of where a wave takes one row of weights or two."""
+    Exact(1, H, 136, "twelve bits", 5).run()
+
+
+@pytest.mark.parametrize("N", [6144, 6152, 8200])
+@pytest.mark.parametrize("K", [16, 1040, 9232])
+def test_one_token_int8(N, K):
+    import torch
+
+    import mixed_precision_moe_topk_amd as M
+
+    gen = torch.Generator(device="cuda").manual_seed(N + K)
+    rand = lambda *s: torch.randint(-128, 128, s, generator=gen, device="cuda").to(torch.int8)  # noqa: E731
+    codes, w, d = rand(1, K), rand(N, K), M.Int8Dims(K, N, "f32")
+    one, out = torch.ones(N, device="cuda"), torch.full((1, N), float("nan"), device="cuda")
+    ws = torch.empty(max(M.int8_workspace_query(d, 1), 16), dtype=torch.uint8, device="cuda")
+    M.int8_matmul(d, codes, one[:1], w, one, None, out, ws)
+    assert torch.equal(out.double(), (codes.double() @ w.double().T).float().double())
