@@ -33,9 +33,8 @@ enum DenseShape : int {
   kDenseMid = 1,  // 128 x 128, 4 waves, two blocks a CU
   kDenseLow = 2,  // 64 x 128, 4 waves, two blocks a CU; not for rows across k
   kDenseFew = 3,  // 64 x 64, 4 waves, two blocks a CU, four steps under way; both
-                  // operands along k, at most kDenseFewRows rows
+                  // operands along k, few rows (see few_rows in moe_dense_api.cpp)
 };
-constexpr int64_t kDenseFewRows = 256;
 constexpr int dense_rows(int shape) { return shape == kDenseBig ? 256 : shape == kDenseMid ? 128 : 64; }
 constexpr int dense_columns(int shape) { return shape == kDenseBig ? 256 : shape == kDenseFew ? 64 : 128; }
 

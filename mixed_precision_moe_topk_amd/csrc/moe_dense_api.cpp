@@ -121,8 +121,7 @@ moe_status check_int8(const moe_int8_dims* d, int64_t num_tokens) {
 //    64 x 64     0.24 + 4.2         0.45 + 7.5
 // a join 6.5 (with its launch on the host) + 1 for 4 MB.  (The block in bf16, T tokens
 // of 7168 x 2048, by 64 x 128, 128 and 256 rows: T = 64: 33, 35, -; 512: 86, 71, 91;
-// 2048: 266, 180, 171; with 64 x 64 among them T = 64: 30 -> 26.6, 100: 45 -> 39, 200: 52
-// still.)
+// 2048: 266, 180, 171; with 64 x 64 among them T = 64: 30 -> 26.6, 100: 45 -> 39.)
 constexpr int64_t kMinPartSteps = 4;
 using moe::kCus;
 struct Cost {
@@ -151,13 +150,28 @@ void set_parts(DenseGemm& g, int64_t steps, int64_t parts) {
   g.split = (int32_t)std::max((int64_t)1, ceil_div(steps, g.steps));
 }
 
+// Whether tiles of 64 x 64 are among the choices.  Their step in the estimate holds for
+// one or two tiles of rows; with three and four, long sums take longer than it says.
+// The block in bf16 (us, without and with them; hidden x inter, the product of that many steps in question):
+//   tokens               64          128          160          208          256
+//   gate  32 steps   17.7 17.7   20.2 17.8    19.7 17.9    20.4 18.0    21.0 17.9   (2048 x 1024)
+//   down  32         33.4 33.4   45.5 39.9    49.1 49.1    48.0 47.9    50.5 50.5   (7168 x 2048)
+//   gate  43         21.0 18.7   21.7 19.7    21.3 23.9    22.9 24.7    23.4 24.9   (2744 x 1000)
+//   gate  64         27.9 26.8   30.3 30.4    33.0 31.9    37.0 35.7    39.2 36.4   (4096 x 2048)
+//   gate  64         21.7 18.0   19.6 19.2    21.5 21.6    23.7 25.1    24.1 25.2   (4096 x 1024)
+//   gate  81         31.8 31.5   35.6 35.6    37.5 37.5    41.2 46.2    44.5 59.1   (5128 x 1368)
+//   gate 112         33.5 33.5   39.8 39.9    49.1 49.1    47.9 55.4    50.5 58.8   (7168 x 2048)
+// and in int8 56 steps (7168 to 2048) 13.5 | 10.6 at 64 tokens, 13.6 | 12.1 at 128, 14.9 |
+// 17.4 at 192.
+bool few_rows(int64_t M, int64_t steps) { return M <= 128 || (M <= 256 && steps <= 32); }
+
 // One product alone; along: both operands lie along k.
 void choose(DenseGemm& g, bool int8, bool along) {
   const int64_t steps = steps_of(g, int8);
   double best = 1e300;
   int shape = 0;
   int64_t parts = 1;
-  for (int s = 0; s < (along && g.M <= moe::kDenseFewRows ? 4 : 3); ++s) {
+  for (int s = 0; s < (along && few_rows(g.M, steps) ? 4 : 3); ++s) {
     g.shape = s;
     const int64_t tiles = std::max((int64_t)1, moe::dense_tiles(g));
     const int64_t most = std::max((int64_t)1, std::min(slots(s) / tiles, steps / kMinPartSteps));

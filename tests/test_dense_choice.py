@@ -151,3 +151,12 @@ def test_long_sums_are_cut(choice):
     for T in (1, 3, 64):
         c = choice.backward(T, 4096, 1 << 18)
         assert c["dx"]["split"] > 1 and c["dx"]["steps"] <= 2048, (T, c["dx"])
+
+
+def test_tiles_of_few_tokens(choice):
+    """Tiles of 64 x 64 up to 128 tokens, and up to 256 for sums of at most 32 steps."""
+    assert choice.forward(128, 2744, 1000)["gate"]["shape"] == FEW
+    assert choice.forward(129, 2744, 1000)["gate"]["shape"] != FEW
+    assert choice.forward(256, 2048, 1024)["gate"]["shape"] == FEW
+    assert choice.forward(256, 2056, 1024)["gate"]["shape"] != FEW
+    assert choice.forward(257, 2048, 1024)["gate"]["shape"] != FEW
