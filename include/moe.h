@@ -655,8 +655,8 @@ moe_status moe_ffn_backward(const moe_ffn_dims* dims, const void* dout, int64_t 
                             size_t workspace_bytes, hipStream_t stream);
 
 /* Rows of x (tokens, or the channels of a weight matrix) as 8-bit integers, one
- * scale a row: scales[r] = amax * (1 / 127), both rounded to float32 (a division by the
- * constant comes out so in most programs), at least 2^-126, and 1 for an all-zero
+ * scale a row: scales[r] = amax * c with c = 1 / 127 rounded to float32, rounded once
+ * more (amax / 127 as float32 or the number below), at least 2^-126, and 1 for an all-zero
  * row; codes[r] = x[r] / scales[r] rounded to the nearest integer, ties to even (of
  * the exact quotient).  A row with an infinity or NaN gets scale NaN and codes 0, so
  * that its products are NaN.

@@ -68,7 +68,8 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-// 1 / (1 + e^-g): within 4 ulp and, from the exponential's argument, 2^-24 |g|.
+// 1 / (1 + e^-g): within 4 ulp and, from the exponential's argument, 2^-24 |g|; 0 where
+// it lies below 2^-126 (the reciprocal flushes what is subnormal).
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
 // What finishing eight sums reads from memory.  Read ahead (`Ahead::load`), with

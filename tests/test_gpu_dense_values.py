@@ -84,3 +84,48 @@ def test_infinities(T, H, I, dx, kind):
             tol = err + HALF[kind] * (np.abs(want) + err)
             close(name, np.where(odd, 0, r[name]), np.where(odd, 0, want), np.where(odd, 0, tol))
     assert seen > 0
+
+
+@pytest.mark.parametrize("T, H, I", [(5, 136, 72), (300, 520, 264), (5000, 64, 72), (130, 5752, 904)])
+def test_infinities_leave_the_other_rows(T, H, I):
+    """A tile that is taken again keeps the bits of its finite sums."""
+    got = []
+    for value in (1.0, np.inf):
+        b = Block(T, H, I, seed=62)
+        b.dout[T // 2, 7] = value
+        b.forward()
+        got.append(b.backward(dx="none")["dw2"])
+    rest = np.arange(H) != 7
+    assert np.array_equal(got[0][rest], got[1][rest]) and np.isfinite(got[0]).all()
+    assert not np.isfinite(got[1][7]).any()
+
+
+def test_infinities_captured():
+    """The second round of such tiles in a graph, between replays over finite inputs."""
+    import torch
+
+    import mixed_precision_moe_topk_amd as M
+
+    T, H, I = 700, 264, 136
+    b = Block(T, H, I, seed=63)
+    f = b.forward()
+    d, x, w1, w2, saved = b.kept
+    dout = torch.from_numpy(b.dout).cuda().bfloat16()
+    new = lambda: (torch.empty(2 * I, H, device="cuda"), torch.empty(H, I, device="cuda"),  # noqa: E731
+                   torch.empty(M.ffn_workspace_query(d, T), dtype=torch.uint8, device="cuda"))
+    one, two = new(), new()
+    M.ffn_backward(d, dout, x, w1, w2, saved, *one)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        M.ffn_backward(d, dout, x, w1, w2, saved, *one)
+    for turn in range(6):
+        dout[T // 2, 7] = float("inf") if turn % 2 else 1.0
+        graph.replay()
+        M.ffn_backward(d, dout, x, w1, w2, saved, *two)
+        torch.cuda.synchronize()
+        for a, c in zip(one[:2], two[:2]):
+            assert torch.equal(a.nan_to_num(5.0, 6.0, 7.0), c.nan_to_num(5.0, 6.0, 7.0)), turn
+        assert bool(two[1].isfinite().all()) == (turn % 2 == 0)
+    assert np.isfinite(f["h2"]).all()
+    del graph
