@@ -152,7 +152,8 @@ void set_parts(DenseGemm& g, int64_t steps, int64_t parts) {
 
 // Whether tiles of 64 x 64 are among the choices.  Their step in the estimate holds for
 // one or two tiles of rows; with three and four, long sums take longer than it says.
-// The block in bf16 (us, without and with them; hidden x inter, the product of that many steps in question):
+// The block in bf16 (us, without and with them; the product in question and its steps,
+// and hidden x inter):
 //   tokens               64          128          160          208          256
 //   gate  32 steps   17.7 17.7   20.2 17.8    19.7 17.9    20.4 18.0    21.0 17.9   (2048 x 1024)
 //   down  32         33.4 33.4   45.5 39.9    49.1 49.1    48.0 47.9    50.5 50.5   (7168 x 2048)
@@ -282,7 +283,7 @@ size_t part_bytes(int64_t rows, int64_t columns, int64_t K, bool int8) {
 }
 
 moe_status run_product(int mode, DenseGemm g, bool int8, void* parts, const char* what, hipStream_t stream) {
-  // (the block of 7168 x 2048 with one token: 20.2 us, by tiles 26.5; two tokens by a
+  // (the block of 7168 x 2048 with one token: 19.2 us, by tiles 26.5; two tokens by a
   // kernel of that kind took 27.7)
   if (g.M == 1 && mode != moe::kDenseDgate)
     return moe::check_hip(moe::launch_dense_one(int8, mode, g, stream), what, stream);

@@ -16,7 +16,8 @@ hipError_t launch_dense_dgate(const DenseGemm& p, hipStream_t st) {
 // 2048, float32 gradients: dw2 beside the gradients of gate and up, then dw1 beside dx,
 // took 1098 us; the gradients of gate and up, then these three, 957, and 851 since
 // operands with one term are loaded once).  Bound by power and LDS as in
-// moe_dense_gemm.h: 701 us at 4093 tokens, 1.37 PFLOP/s with both terms counted.
+// moe_dense_gemm.h: 701 us at 4093 tokens on one card, 759 on another, 1.37 and 1.27
+// PFLOP/s with both terms counted.
 struct DenseGrads {
   DenseGemm p[3];  // dw1, dw2, dx
   int64_t first[3], blocks[3];

@@ -518,11 +518,11 @@ __device__ __forceinline__ void dense_tile_terms(const DenseGemm& p, int part, i
 // step before is loaded anew.  Narrower than Low, so that more of the CUs work without
 // parts and a join: 64 tokens of 2048 x 7168 take 11.4 us (Low in 4 parts 10.2, and 4.0
 // for the join), in int8 8.5 (Low 11.8); the block of 7168 x 2048 in int8 with 2
-// tokens 27.0 -> 23.2 us, with 64 31.4 -> 26.7.  What a CU takes in of a step's 16 KB bounds it, 0.27 us
-// alone and 0.22 by two blocks, also with 64 blocks in all.  Not better: rings of 9
-// steps (28.0 us in place of 26.6 for the block in bf16, 64 tokens; 4 steps as 5), the
-// fragments read a step ahead with halves of a step to a wave (8.6 -> 10.9), blocks that
-// begin at k of their own.
+// tokens 27.0 -> 23.2 us, with 64 31.4 -> 26.7.  What a CU takes in of a step's 16 KB
+// bounds it, 0.27 us alone and 0.22 by two blocks, also with 64 blocks in all.  Not
+// better: rings of 9 steps (28.0 us in place of 26.6 for the block in bf16, 64 tokens, the
+// same weights in every call; 4 steps as 5), the fragments read a step ahead with halves
+// of a step to a wave (8.6 -> 10.9), blocks that begin at k of their own.
 template <bool I8, int MODE, class S>
 __device__ __forceinline__ void few_tile(const DenseGemm& p, int part, int64_t mt, int nt, uint8_t* lds) {
   constexpr int NW = S::NW, BM = S::BM, BN = S::BN, WM = S::WM, WN = S::WN, ST = S::kStages;

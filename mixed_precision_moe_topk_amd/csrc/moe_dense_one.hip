@@ -5,7 +5,7 @@
 // lane), AHEAD of them under way, so that all lanes of a read lie in one row and no
 // sums meet in memory: the lanes' sums meet by shuffles.  Products are float32
 // fused multiply-adds (int8: four products to an int32).  Memory bounds it: 7168 x 4096
-// gates and ups 11.5 us (58.7 MB, 5.1 TB/s), down 2048 x 7168 8.3 us, of which some 3
+// gates and ups 11.9 us (58.7 MB, 4.9 TB/s), down 2048 x 7168 7.2 us, of which some 3
 // are the launch and the first reads.  With matrix instructions, whose lanes gather 16
 // rows a read, they took 13.9 and 10.2.
 #include <type_traits>
